@@ -19,6 +19,13 @@ from .binding import (  # noqa: F401
     ccq_bwd_chunked,
     ccq_chunk_carry_bytes,
     ccq_step_backward,
+    ccq_qk_norm_rope,
+    ccq_qk_norm_rope_backward,
+    ccq_scan,
+    ccq_scan_backward,
+    ccq_beam_select,
+    ccq_beam_reorder,
+    scan_carry_shape,
     new_chunk_carry,
     library_path,
     load_library,

@@ -31,6 +31,16 @@ EXPORTED_SYMBOLS = (
     "ccq_bwd_chunked",
     "ccq_bwd_workspace_bytes",
     "ccq_chunk_carry_bytes",
+    "ccq_qk_norm_rope",
+    "ccq_qk_norm_rope_backward",
+    "ccq_qk_backward_workspace_bytes",
+    "ccq_scan",
+    "ccq_scan_workspace_bytes",
+    "ccq_scan_backward",
+    "ccq_scan_backward_workspace_bytes",
+    "ccq_beam_select",
+    "ccq_beam_select_workspace_bytes",
+    "ccq_beam_reorder",
     "ccq_status_string",
     "ccq_abi_version",
 )
@@ -88,6 +98,79 @@ class BwdParams(ctypes.Structure):
     ]
 
 
+class QkParams(ctypes.Structure):
+    """Mirror of ``ccq_qk_params``."""
+
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("B", ctypes.c_int32), ("T", ctypes.c_int32),
+        ("H_q", ctypes.c_int32), ("H_k", ctypes.c_int32), ("d", ctypes.c_int32),
+        ("q_norm", ctypes.c_int32), ("k_norm", ctypes.c_int32), ("rot", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32), ("expand_keys", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+        ("q_stride_b", ctypes.c_int64), ("q_stride_t", ctypes.c_int64), ("q_stride_h", ctypes.c_int64),
+        ("k_stride_b", ctypes.c_int64), ("k_stride_t", ctypes.c_int64), ("k_stride_h", ctypes.c_int64),
+        ("positions", ctypes.c_void_p), ("position0", ctypes.c_int64), ("inv_freq", ctypes.c_void_p),
+        ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
+    ]
+
+
+class QkBwdParams(ctypes.Structure):
+    """Mirror of ``ccq_qk_bwd_params``."""
+
+    _fields_ = [
+        ("fwd", QkParams),
+        ("dq_out", ctypes.c_void_p), ("dk_out", ctypes.c_void_p), ("dq", ctypes.c_void_p), ("dk", ctypes.c_void_p),
+        ("dq_stride_b", ctypes.c_int64), ("dq_stride_t", ctypes.c_int64), ("dq_stride_h", ctypes.c_int64),
+        ("dk_stride_b", ctypes.c_int64), ("dk_stride_t", ctypes.c_int64), ("dk_stride_h", ctypes.c_int64),
+        ("dq_weight", ctypes.c_void_p), ("dk_weight", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class ScanParams(ctypes.Structure):
+    """Mirror of ``ccq_scan_params``."""
+
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("D", ctypes.c_int32),
+        ("complement", ctypes.c_int32),
+        ("x", ctypes.c_void_p), ("log_alpha", ctypes.c_void_p),
+        ("x_stride_b", ctypes.c_int64), ("x_stride_t", ctypes.c_int64),
+        ("la_stride_b", ctypes.c_int64), ("la_stride_t", ctypes.c_int64),
+        ("lengths", ctypes.c_void_p), ("h0", ctypes.c_void_p), ("y", ctypes.c_void_p), ("h_out", ctypes.c_void_p),
+        ("chunk_carry", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class ScanBwdParams(ctypes.Structure):
+    """Mirror of ``ccq_scan_bwd_params``."""
+
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("D", ctypes.c_int32),
+        ("complement", ctypes.c_int32),
+        ("x", ctypes.c_void_p), ("log_alpha", ctypes.c_void_p), ("dy", ctypes.c_void_p),
+        ("x_stride_b", ctypes.c_int64), ("x_stride_t", ctypes.c_int64),
+        ("la_stride_b", ctypes.c_int64), ("la_stride_t", ctypes.c_int64),
+        ("dy_stride_b", ctypes.c_int64), ("dy_stride_t", ctypes.c_int64),
+        ("lengths", ctypes.c_void_p), ("h0", ctypes.c_void_p), ("dh_out", ctypes.c_void_p),
+        ("chunk_carry", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("dlog_alpha", ctypes.c_void_p),
+        ("dh0", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class BeamParams(ctypes.Structure):
+    """Mirror of ``ccq_beam_params``."""
+
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("V", ctypes.c_int32),
+        ("M", ctypes.c_int32),
+        ("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_int64), ("scores", ctypes.c_void_p),
+        ("finished", ctypes.c_void_p), ("pad_token", ctypes.c_int32), ("token", ctypes.c_void_p),
+        ("parent", ctypes.c_void_p), ("score", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 def library_path() -> str:
     return os.environ.get("CCQ_LIBRARY", os.path.join(_HERE, "libccq.so"))
 
@@ -123,6 +206,18 @@ def load_library():
     lib.ccq_bwd_workspace_bytes.restype = ctypes.c_size_t
     lib.ccq_chunk_carry_bytes.argtypes = [i32] * 5
     lib.ccq_chunk_carry_bytes.restype = ctypes.c_size_t
+    for name, cls in (("ccq_qk_norm_rope", QkParams), ("ccq_qk_norm_rope_backward", QkBwdParams),
+                      ("ccq_scan", ScanParams), ("ccq_scan_backward", ScanBwdParams),
+                      ("ccq_beam_select", BeamParams)):
+        getattr(lib, name).argtypes = [ctypes.POINTER(cls), vp]
+        getattr(lib, name).restype = ctypes.c_int
+    for name, cls in (("ccq_qk_backward_workspace_bytes", QkBwdParams), ("ccq_scan_workspace_bytes", ScanParams),
+                      ("ccq_scan_backward_workspace_bytes", ScanBwdParams),
+                      ("ccq_beam_select_workspace_bytes", BeamParams)):
+        getattr(lib, name).argtypes = [ctypes.POINTER(cls)]
+        getattr(lib, name).restype = ctypes.c_size_t
+    lib.ccq_beam_reorder.argtypes = [i32, ctypes.POINTER(vp), ctypes.POINTER(ctypes.c_size_t), i32, i32, vp, vp]
+    lib.ccq_beam_reorder.restype = ctypes.c_int
     lib.ccq_status_string.argtypes = [i32]
     lib.ccq_status_string.restype = ctypes.c_char_p
     lib.ccq_abi_version.argtypes = []
@@ -505,3 +600,324 @@ def ccq_bwd_chunked(rule, q, k, v, log_alpha, w_lambda, b_lambda, d_o, carry_in=
     if st != 0:
         raise CcqError(st, "ccq_bwd_chunked")
     return out
+
+
+# ---------------------------------------------------------------- operators around the read step
+#
+# They run on the device of their first tensor, whichever device is current, on the given stream or
+# that device's current one; what they allocate belongs to that stream.
+
+_NORMS = {"none": 0, None: 0, "rms": 1, "l2": 2}
+MAX_REORDER_STATES = 16  # CCQ_MAX_REORDER_STATES
+
+
+class _NoContext:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NO_CONTEXT = _NoContext()
+
+
+def _place(dev, stream):
+    """Context in which a call on tensors of ``dev`` allocates and launches."""
+    import torch
+    if dev.type != "cuda":
+        raise ValueError("tensors must be device tensors")
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        return torch.cuda.stream(stream)
+    if dev.index != torch.cuda.current_device():
+        return torch.cuda.device(dev)
+    return _NO_CONTEXT
+
+
+def _check_on(name, t, dev, dtype, shape):
+    """t lies on dev, is dense and has this dtype and shape (None: absent)."""
+    if t is None:
+        return
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, is on {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _check_strided(name, t, dev, dtype, shape):
+    """As _check_on, but only the last dimension has to be dense.  Returns the other dimensions'
+    strides (0 where there is one entry, whose stride means nothing)."""
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, is on {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] != 1:
+        raise ValueError(f"{name} must be dense in its last dimension")
+    return [s if n > 1 else 0 for s, n in zip(st[:-1], shape)]
+
+
+def _call(name, params, dev):
+    import torch
+    fn = getattr(load_library(), name)
+    st = fn(params, torch._C._cuda_getCurrentRawStream(dev.index))
+    if st != 0:
+        raise CcqError(st, name)
+
+
+def _workspace(params, size_fn, workspace, dev):
+    """Points params at the given workspace, or at one allocated here; returns what to keep alive."""
+    import torch
+    if workspace is None:
+        need = int(size_fn(params))
+        if need == 0:
+            return None
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    params.workspace = workspace.data_ptr()
+    params.workspace_bytes = workspace.numel() * workspace.element_size()
+    return workspace
+
+
+def _norm_code(kind):
+    if kind not in _NORMS:
+        raise ValueError(f"unknown norm {kind!r}: 'none', 'rms' or 'l2'")
+    return _NORMS[kind]
+
+
+def _qk_params(q, k, positions, inv_freq, q_weight, k_weight, q_norm, k_norm, eps, interleaved, expand_keys,
+               position_offset, q_out, k_out):
+    import torch
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("q or k must be given")
+    if ref.dim() != 4:
+        raise ValueError("q and k are [B, T, H, d]")
+    dev, dt = ref.device, ref.dtype
+    B, T, _, d = ref.shape
+    Hq = 0 if q is None else q.shape[2]
+    Hk = 0 if k is None else k.shape[2]
+    qs = [0, 0, 0] if q is None else _check_strided("q", q, dev, dt, (B, T, Hq, d))
+    ks = [0, 0, 0] if k is None else _check_strided("k", k, dev, dt, (B, T, Hk, d))
+    _check_on("positions", positions, dev, torch.int64, (B, T))
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _check_on("inv_freq", inv_freq, dev, torch.float32, (rot // 2,))
+    _check_on("q_weight", q_weight, dev, torch.float32, (d,))
+    _check_on("k_weight", k_weight, dev, torch.float32, (d,))
+    if expand_keys and (Hk == 0 or Hq % Hk):
+        raise ValueError(f"expand_keys: {Hk} key heads do not divide {Hq} query heads")
+    _check_on("q_out", q_out, dev, dt, (B, Hq, T, d))
+    _check_on("k_out", k_out, dev, dt, (B, Hq if expand_keys else Hk, T, d))
+    return QkParams(_dtype_code(ref), B, T, Hq, Hk, d, _norm_code(q_norm), _norm_code(k_norm), rot, int(interleaved),
+                    int(expand_keys), eps, _ptr(q), _ptr(k), *qs, *ks, _ptr(positions), position_offset,
+                    _ptr(inv_freq) if rot else None, _ptr(q_weight), _ptr(k_weight), _ptr(q_out), _ptr(k_out))
+
+
+def ccq_qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=None, q_norm="rms", k_norm="l2",
+                     eps: float = 1e-6, interleaved: bool = False, expand_keys: bool = False,
+                     position_offset: int = 0, q_out=None, k_out=None, stream=None):
+    """Queries and keys of a projection made ready for the read step (see ``ccq_qk_norm_rope`` in
+    ccq.h): every head's row normalised ("rms", "l2" or "none"), weighted, rotated by its position and
+    laid out head-major.  q [B, T, H_q, d], k [B, T, H_k, d]: strided views are fine, either may be
+    None; positions [B, T] int64, or token t stands at position_offset + t; inv_freq [rot / 2] fp32, or
+    None for no rotation.  Returns (q_out [B, H_q, T, d], k_out [B, H_k, T, d], or [B, H_q, T, d] with
+    expand_keys), None in the place of an absent side."""
+    import torch
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("q or k must be given")
+    dev = ref.device
+    with _place(dev, stream):
+        B, T, _, d = ref.shape
+        if q is not None and q_out is None:
+            q_out = torch.empty((B, q.shape[2], T, d), dtype=q.dtype, device=dev)
+        if k is not None and k_out is None:
+            heads = q.shape[2] if expand_keys and q is not None else k.shape[2]
+            k_out = torch.empty((B, heads, T, d), dtype=k.dtype, device=dev)
+        p = _qk_params(q, k, positions, inv_freq, q_weight, k_weight, q_norm, k_norm, eps, interleaved, expand_keys,
+                       position_offset, q_out, k_out)
+        _call("ccq_qk_norm_rope", p, dev)
+    return q_out, k_out
+
+
+def ccq_qk_norm_rope_backward(q, k, dq_out, dk_out, positions=None, inv_freq=None, q_weight=None, k_weight=None,
+                              q_norm="rms", k_norm="l2", eps: float = 1e-6, interleaved: bool = False,
+                              position_offset: int = 0, dq=None, dk=None, workspace=None, stream=None):
+    """Gradient of ``ccq_qk_norm_rope`` (see ``ccq_qk_norm_rope_backward`` in ccq.h).  dq_out, dk_out:
+    fp32 gradients of its outputs, dense; dk_out has H_q heads if the keys were expanded.  Returns a
+    dict: dq, dk (dtype and shape of q, k, into the given views if any), dq_weight, dk_weight (fp32
+    [d], None without that weight)."""
+    import torch
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("q or k must be given")
+    dev, dt = ref.device, ref.dtype
+    lib = load_library()
+    with _place(dev, stream):
+        B, T, _, d = ref.shape
+        Hq = 0 if q is None else q.shape[2]
+        Hk = 0 if k is None else k.shape[2]
+        expand = k is not None and dk_out is not None and dk_out.shape[1] != Hk
+        f = _qk_params(q, k, positions, inv_freq, q_weight, k_weight, q_norm, k_norm, eps, interleaved, expand,
+                       position_offset, None, None)
+        out = dict(dq=None, dk=None, dq_weight=None, dk_weight=None)
+        if q is not None:
+            out["dq"] = torch.empty((B, T, Hq, d), dtype=dt, device=dev) if dq is None else dq
+        if k is not None:
+            out["dk"] = torch.empty((B, T, Hk, d), dtype=dt, device=dev) if dk is None else dk
+        for name, t, heads in (("dq_out", dq_out, Hq), ("dk_out", dk_out, Hq if expand else Hk)):
+            if (t is None) != (heads == 0):
+                raise ValueError(f"{name} is given with its input and only with it")
+            _check_on(name, t, dev, torch.float32, (B, heads, T, d))
+        qs = [0, 0, 0] if q is None else _check_strided("dq", out["dq"], dev, dt, (B, T, Hq, d))
+        ks = [0, 0, 0] if k is None else _check_strided("dk", out["dk"], dev, dt, (B, T, Hk, d))
+        if q_weight is not None:
+            out["dq_weight"] = torch.empty(d, dtype=torch.float32, device=dev)
+        if k_weight is not None:
+            out["dk_weight"] = torch.empty(d, dtype=torch.float32, device=dev)
+        p = QkBwdParams(f, _ptr(dq_out), _ptr(dk_out), _ptr(out["dq"]), _ptr(out["dk"]), *qs, *ks,
+                        _ptr(out["dq_weight"]), _ptr(out["dk_weight"]), None, 0)
+        keep = _workspace(p, lib.ccq_qk_backward_workspace_bytes, workspace, dev)  # noqa: F841
+        _call("ccq_qk_norm_rope_backward", p, dev)
+    return out
+
+
+def scan_carry_shape(x):
+    """Shape of the chunk-carry tensor of ``ccq_scan`` for inputs x [B, T, D]."""
+    B, T, D = x.shape
+    return (B, (T + 63) // 64, D)
+
+
+def ccq_scan(x, log_alpha, h0=None, h_out=None, y=None, lengths=None, complement: bool = False, chunk_carry=None,
+             workspace=None, stream=None):
+    """Gated linear recurrence h_t = exp(log_alpha_t) h_{t-1} + s_t x_t over [B, T, D] (see ``ccq_scan``
+    in ccq.h; s_t is 1, or 1 - exp(log_alpha_t) with complement).  x and log_alpha may be strided
+    views; h0, h_out [B, D] fp32 (h_out may be h0: the serving step); lengths [B] int32; chunk_carry:
+    fp32 tensor of ``scan_carry_shape(x)`` that receives the state before every 64-token chunk, for
+    ``ccq_scan_backward``.  Returns y [B, T, D] (rows at t >= length are left as they were)."""
+    import torch
+    if x.dim() != 3:
+        raise ValueError("x is [B, T, D]")
+    dev, dt = x.device, x.dtype
+    shape = B, T, D = tuple(x.shape)
+    lib = load_library()
+    with _place(dev, stream):
+        if y is None:
+            y = torch.empty(shape, dtype=dt, device=dev)
+        xs = _check_strided("x", x, dev, dt, shape)
+        gs = _check_strided("log_alpha", log_alpha, dev, dt, shape)
+        _check_on("y", y, dev, dt, shape)
+        _check_on("h0", h0, dev, torch.float32, (B, D))
+        _check_on("h_out", h_out, dev, torch.float32, (B, D))
+        _check_on("lengths", lengths, dev, torch.int32, (B,))
+        _check_on("chunk_carry", chunk_carry, dev, torch.float32, (B, (T + 63) // 64, D))
+        p = ScanParams(_dtype_code(x), B, T, D, int(complement), _ptr(x), _ptr(log_alpha), *xs, *gs, _ptr(lengths),
+                       _ptr(h0), _ptr(y), _ptr(h_out), _ptr(chunk_carry), None, 0)
+        keep = _workspace(p, lib.ccq_scan_workspace_bytes, workspace, dev)  # noqa: F841
+        _call("ccq_scan", p, dev)
+    return y
+
+
+def ccq_scan_backward(x, log_alpha, dy, h0=None, dh_out=None, lengths=None, complement: bool = False,
+                      chunk_carry=None, want_dh0: bool = False, dx=None, dlog_alpha=None, workspace=None, stream=None):
+    """Gradient of ``ccq_scan`` (see ``ccq_scan_backward`` in ccq.h).  dy [B, T, D]: gradient of y (a
+    strided view is fine); dh_out [B, D] fp32: gradient of h_out, or None; chunk_carry: what the
+    forward kept, or None to form it again.  Returns a dict: dx, dlog_alpha (dtype of x; zeros at
+    t >= length) and, with want_dh0, dh0 fp32."""
+    import torch
+    if x.dim() != 3:
+        raise ValueError("x is [B, T, D]")
+    dev, dt = x.device, x.dtype
+    shape = B, T, D = tuple(x.shape)
+    lib = load_library()
+    with _place(dev, stream):
+        out = dict(dx=torch.empty(shape, dtype=dt, device=dev) if dx is None else dx,
+                   dlog_alpha=torch.empty(shape, dtype=dt, device=dev) if dlog_alpha is None else dlog_alpha)
+        xs = _check_strided("x", x, dev, dt, shape)
+        gs = _check_strided("log_alpha", log_alpha, dev, dt, shape)
+        ys = _check_strided("dy", dy, dev, dt, shape)
+        _check_on("dx", out["dx"], dev, dt, shape)
+        _check_on("dlog_alpha", out["dlog_alpha"], dev, dt, shape)
+        _check_on("h0", h0, dev, torch.float32, (B, D))
+        _check_on("dh_out", dh_out, dev, torch.float32, (B, D))
+        _check_on("lengths", lengths, dev, torch.int32, (B,))
+        _check_on("chunk_carry", chunk_carry, dev, torch.float32, (B, (T + 63) // 64, D))
+        if want_dh0:
+            out["dh0"] = torch.empty((B, D), dtype=torch.float32, device=dev)
+        p = ScanBwdParams(_dtype_code(x), B, T, D, int(complement), _ptr(x), _ptr(log_alpha), _ptr(dy), *xs, *gs, *ys,
+                          _ptr(lengths), _ptr(h0), _ptr(dh_out), _ptr(chunk_carry), _ptr(out["dx"]),
+                          _ptr(out["dlog_alpha"]), _ptr(out.get("dh0")), None, 0)
+        keep = _workspace(p, lib.ccq_scan_backward_workspace_bytes, workspace, dev)  # noqa: F841
+        _call("ccq_scan_backward", p, dev)
+    return out
+
+
+def ccq_beam_select(logits, scores, m: int, finished=None, pad_token: int = 0, workspace=None, stream=None):
+    """One selection step of beam search (see ``ccq_beam_select`` in ccq.h).  logits [N, K, V] (rows may
+    be padded: logits[..., :V] of a wider tensor), scores [N, K] fp32, finished [N, K] bool / uint8 or
+    None.  Returns a dict: token, parent (int32 [N, m]) and score (fp32 [N, m]), best first."""
+    import torch
+    if logits.dim() != 3:
+        raise ValueError("logits is [N, K, V]")
+    dev = logits.device
+    N, K, V = logits.shape
+    lib = load_library()
+    with _place(dev, stream):
+        st = _check_strided("logits", logits, dev, logits.dtype, (N, K, V))
+        stride = st[1] if K > 1 else st[0] if N > 1 else V
+        if N > 1 and K > 1 and st[0] != K * st[1]:
+            raise ValueError("the rows of logits must be evenly spaced")
+        _check_on("scores", scores, dev, torch.float32, (N, K))
+        if finished is not None and finished.dtype == torch.bool:
+            finished = finished.view(torch.uint8)
+        _check_on("finished", finished, dev, torch.uint8, (N, K))
+        if m <= 0:
+            raise ValueError("m must be positive")
+        out = dict(token=torch.empty((N, m), dtype=torch.int32, device=dev),
+                   parent=torch.empty((N, m), dtype=torch.int32, device=dev),
+                   score=torch.empty((N, m), dtype=torch.float32, device=dev))
+        p = BeamParams(_dtype_code(logits), N, K, V, m, _ptr(logits), stride, _ptr(scores), _ptr(finished), pad_token,
+                       _ptr(out["token"]), _ptr(out["parent"]), _ptr(out["score"]), None, 0)
+        keep = _workspace(p, lib.ccq_beam_select_workspace_bytes, workspace, dev)  # noqa: F841
+        _call("ccq_beam_select", p, dev)
+    return out
+
+
+def ccq_beam_reorder(states, parent, stream=None):
+    """Moves every state's rows to the beams that continue them, in place (see ``ccq_beam_reorder`` in
+    ccq.h).  states: up to 16 dense tensors [N K, ...] of any dtype whose rows are a multiple of 4
+    bytes; parent [N, K] int32, as ``ccq_beam_select`` returns it for m = K."""
+    import torch
+    lib = load_library()
+    if not states or len(states) > MAX_REORDER_STATES:
+        raise ValueError(f"1 to {MAX_REORDER_STATES} states, got {len(states)}")
+    if parent.dim() != 2:
+        raise ValueError("parent is [N, K]")
+    dev = parent.device
+    N, K = parent.shape
+    with _place(dev, stream):
+        _check_on("parent", parent, dev, torch.int32, (N, K))
+        count = len(states)
+        ptrs, rows = (ctypes.c_void_p * count)(), (ctypes.c_size_t * count)()
+        for i, t in enumerate(states):
+            if t.device != dev:
+                raise ValueError(f"states[{i}] must be on {dev}, is on {t.device}")
+            if not t.is_contiguous() or t.dim() < 1 or t.shape[0] != N * K:
+                raise ValueError(f"states[{i}] must be contiguous with {N * K} rows")
+            ptrs[i] = t.data_ptr()
+            rows[i] = t.numel() // (N * K) * t.element_size() if N * K else 0
+        st = lib.ccq_beam_reorder(count, ptrs, rows, N, K, parent.data_ptr(),
+                                  torch._C._cuda_getCurrentRawStream(dev.index))
+        if st != 0:
+            raise CcqError(st, "ccq_beam_reorder")

@@ -154,4 +154,21 @@ hipError_t launch_gdn(const FwdArgs& a, hipStream_t stream);
 // the Gated DeltaNet segment summary kernel (its own translation unit)
 hipError_t launch_gdn_summary(const FwdArgs& a, hipStream_t stream);
 
+// Operators around the read step (one call each after validation, ccq_ops_api.cpp).
+hipError_t launch_qk(const ccq_qk_params& p, hipStream_t stream);
+size_t qk_backward_workspace_bytes(const ccq_qk_bwd_params& p);
+hipError_t launch_qk_backward(const ccq_qk_bwd_params& p, hipStream_t stream);
+size_t scan_workspace_bytes(const ccq_scan_params& p);
+hipError_t launch_scan(const ccq_scan_params& p, hipStream_t stream);
+size_t scan_backward_workspace_bytes(const ccq_scan_bwd_params& p);
+hipError_t launch_scan_backward(const ccq_scan_bwd_params& p, hipStream_t stream);
+constexpr int kBeamMaxBeams = 64;
+constexpr int kBeamMaxPicks = 64;
+constexpr int kBeamMaxChunk = 16384;  // logits of a row that one workgroup holds in registers
+constexpr int kBeamMaxLists = 4096;   // beams x chunks of a row, joined by one workgroup
+size_t beam_workspace_bytes(const ccq_beam_params& p);
+hipError_t launch_beam_select(const ccq_beam_params& p, hipStream_t stream);
+hipError_t launch_beam_reorder(int n_states, void* const* states, const size_t* row_bytes, int N, int K,
+                               const int32_t* parent, hipStream_t stream);
+
 }  // namespace ccq

@@ -327,6 +327,181 @@ int ccq_bwd_chunked(const ccq_bwd_params *p, void *hip_stream);
  * Gated DeltaNet the prefill's segment slots. */
 size_t ccq_bwd_workspace_bytes(const ccq_bwd_params *p);
 
+/* ------------------------------------------------------------------------------------------
+ * Operators around the read step.  They keep the conventions above (device pointers, nothing
+ * allocated, errors before anything is enqueued, 16-byte aligned pointers, work on hip_stream
+ * alone), with these differences: where a tensor has strides they are given in elements, the
+ * last dimension is always dense, and a stride whose bytes are not a multiple of 16 is
+ * CCQ_ERR_MISALIGNED (the logits of ccq_beam_select may start a row anywhere).  Buffers that are
+ * written must not overlap any other buffer of the call, except where an entry says so
+ * (CCQ_ERR_INVALID_ARG where the library sees it).  A workspace holds nothing between calls, but
+ * two calls that can run at the same time need one each: so do two captured graphs that can.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Norm of a query or key row x of d entries: y = x r w with the optional weight w and
+ *   CCQ_NORM_NONE: r = 1;
+ *   CCQ_NORM_RMS : r = 1 / sqrt(mean(x^2) + eps);
+ *   CCQ_NORM_L2  : r = 1 / max(|x|, 1e-12), the unit keys the read step asks for (the norm of
+ *                  CCQ_FLAG_NORMALIZE_KEYS). */
+typedef enum { CCQ_NORM_NONE = 0, CCQ_NORM_RMS = 1, CCQ_NORM_L2 = 2 } ccq_norm;
+
+/* Arguments of ccq_qk_norm_rope.  Zero-initialise, then fill in. */
+typedef struct {
+  int32_t dtype;             /* ccq_dtype of q, k, q_out, k_out                                    */
+  int32_t B, T, H_q, H_k, d; /* H_k divides H_q if expand_keys; d in {64, 128}; H_q or H_k may be 0 */
+  int32_t q_norm, k_norm;    /* ccq_norm                                                           */
+  int32_t rot;               /* leading entries of a row that are rotated: 0 .. d, a multiple of 16 */
+  int32_t interleaved;       /* 0: entry i turns with entry i + rot / 2; 1: entry 2 i with 2 i + 1  */
+  int32_t expand_keys;       /* 1: k_out has H_q heads, head h holding key head h / (H_q / H_k)     */
+  float eps;                 /* of CCQ_NORM_RMS, >= 0                                               */
+  const void *q;             /* [B, T, H_q, d], strides below; NULL when H_q == 0                   */
+  const void *k;             /* [B, T, H_k, d], strides below; NULL when H_k == 0                   */
+  int64_t q_stride_b, q_stride_t, q_stride_h; /* >= 0: part of a packed projection, for instance   */
+  int64_t k_stride_b, k_stride_t, k_stride_h;
+  const int64_t *positions;  /* [B, T], or NULL: token t stands at position0 + t                    */
+  int64_t position0;
+  const float *inv_freq;     /* [rot / 2] angle per position of every pair; NULL when rot == 0      */
+  const float *q_weight;     /* [d] or NULL (ones)                                                  */
+  const float *k_weight;     /* [d] or NULL (ones)                                                  */
+  void *q_out;               /* [B, H_q, T, d], written; may not be q                               */
+  void *k_out;               /* [B, H_k, T, d], or [B, H_q, T, d] with expand_keys, written         */
+} ccq_qk_params;
+
+/*
+ * Queries and keys of a projection, made ready for the read step in one pass: every head's row is
+ * normalised, weighted, rotated by its position (rotary embedding; the angle position * inv_freq
+ * is formed in 64 bits, so it holds at any position below 2^53) and stored head-major as
+ * ccq_fwd_chunked ([B, H, T, d]) and ccq_decode_step (T = 1: [N, H, d]) read it.  A rotation keeps
+ * lengths, so keys under CCQ_NORM_L2 without a weight are unit keys.  The arithmetic is fp32; the
+ * result is rounded once.  Either side may be absent (H_q == 0 or H_k == 0).  A value row is
+ * laid out the same way by CCQ_NORM_NONE and rot == 0.  Returns a ccq_status.
+ */
+int ccq_qk_norm_rope(const ccq_qk_params *p, void *hip_stream);
+
+/* Arguments of ccq_qk_norm_rope_backward.  Zero-initialise, then fill in. */
+typedef struct {
+  ccq_qk_params fwd;         /* the forward's arguments; q_out and k_out are not used              */
+  const float *dq_out;       /* [B, H_q, T, d] fp32: gradient of q_out, as ccq_bwd_chunked leaves it */
+  const float *dk_out;       /* fp32, the shape of k_out                                            */
+  void *dq;                  /* [B, T, H_q, d] dtype, strides below, written                        */
+  void *dk;                  /* [B, T, H_k, d] dtype, strides below, written: summed over shared heads */
+  int64_t dq_stride_b, dq_stride_t, dq_stride_h; /* no two rows may overlap                         */
+  int64_t dk_stride_b, dk_stride_t, dk_stride_h;
+  float *dq_weight;          /* [d] fp32, written (set if and only if q_weight is)                  */
+  float *dk_weight;          /* [d] fp32, written (set if and only if k_weight is)                  */
+  void *workspace;           /* ccq_qk_backward_workspace_bytes(p) bytes, or NULL when that is 0    */
+  size_t workspace_bytes;
+} ccq_qk_bwd_params;
+
+/* Gradient of ccq_qk_norm_rope: dq, dk and the weights' gradients, summed over B, T and heads in
+ * a fixed order (two calls give the same bits).  Where an L2 norm is at its floor the norm is a
+ * constant.  Returns a ccq_status. */
+int ccq_qk_norm_rope_backward(const ccq_qk_bwd_params *p, void *hip_stream);
+/* Bytes of device workspace that call needs: 0 without weights and for invalid p. */
+size_t ccq_qk_backward_workspace_bytes(const ccq_qk_bwd_params *p);
+
+/* Arguments of ccq_scan.  Zero-initialise, then fill in. */
+typedef struct {
+  int32_t dtype;             /* ccq_dtype of x, log_alpha and y                                     */
+  int32_t B, T, D;           /* D a multiple of 8                                                   */
+  int32_t complement;        /* 1: the input is scaled by 1 - alpha                                 */
+  const void *x;             /* [B, T, D], strides below                                            */
+  const void *log_alpha;     /* [B, T, D], strides below; -INFINITY starts the channel anew          */
+  int64_t x_stride_b, x_stride_t;   /* >= 0                                                         */
+  int64_t la_stride_b, la_stride_t; /* >= 0                                                         */
+  const int32_t *lengths;    /* [B] tokens of each sequence (taken into 0 .. T), or NULL: T each     */
+  const float *h0;           /* [B, D] state before the first token, or NULL: zeros                 */
+  void *y;                   /* [B, T, D] dtype, written: h_t; rows at t >= length are left as they were */
+  float *h_out;              /* [B, D] state after the last token, or NULL; may be h0 itself        */
+  float *chunk_carry;        /* NULL, or [B, ceil(T / 64), D] fp32: the state before every 64-token
+                                chunk that starts inside the sequence, for ccq_scan_backward         */
+  void *workspace;           /* ccq_scan_workspace_bytes(p) bytes, or NULL when that is 0            */
+  size_t workspace_bytes;
+} ccq_scan_params;
+
+/*
+ * Gated linear recurrence, channel by channel:
+ *   h_t = alpha_t h_{t-1} + s_t x_t,  alpha_t = exp(log_alpha_t),  s_t = 1 or 1 - alpha_t,  y_t = h_t.
+ * The state is fp32 throughout and a call continues where h0 left off, so T = 1 with h_out == h0
+ * is the serving step.  Where alpha_t is 0 the old state is dropped, whatever it holds (an
+ * infinity or NaN before it does not pass).  Rows behind a sequence's length are neither read
+ * into a result nor written.  Long sequences are cut along T and the pieces joined in a fixed
+ * order: two calls give the same bits.  Returns a ccq_status.
+ */
+int ccq_scan(const ccq_scan_params *p, void *hip_stream);
+/* Bytes of device workspace ccq_scan needs (0 if none and for invalid p): depends on dtype, B, T, D. */
+size_t ccq_scan_workspace_bytes(const ccq_scan_params *p);
+
+/* Arguments of ccq_scan_backward.  Zero-initialise, then fill in. */
+typedef struct {
+  int32_t dtype;             /* ccq_dtype of x, log_alpha, dy, dx and dlog_alpha                    */
+  int32_t B, T, D;
+  int32_t complement;
+  const void *x, *log_alpha; /* the forward's inputs, strides below                                 */
+  const void *dy;            /* [B, T, D] gradient of y, strides below                              */
+  int64_t x_stride_b, x_stride_t, la_stride_b, la_stride_t, dy_stride_b, dy_stride_t; /* >= 0        */
+  const int32_t *lengths;    /* the forward's                                                       */
+  const float *h0;           /* the forward's                                                       */
+  const float *dh_out;       /* [B, D] gradient of h_out, or NULL: zeros                            */
+  const float *chunk_carry;  /* the forward's, or NULL: recomputed                                  */
+  void *dx, *dlog_alpha;     /* [B, T, D] dtype, written; zeros at t >= length                      */
+  float *dh0;                /* [B, D], written, or NULL; may be dh_out itself                      */
+  void *workspace;           /* ccq_scan_backward_workspace_bytes(p) bytes, or NULL when that is 0   */
+  size_t workspace_bytes;
+} ccq_scan_bwd_params;
+
+/* Gradient of ccq_scan: with the adjoint a_t = dy_t + alpha_{t+1} a_{t+1} (dh_out behind the last
+ * token), dx_t = s_t a_t, dlog_alpha_t = alpha_t a_t (h_{t-1} - [complement] x_t) and
+ * dh0 = alpha_0 a_0.  States and adjoints are fp32; the states come from chunk_carry and the
+ * inputs, not from the rounded y.  Where alpha_t is 0 both products are 0.  Returns a
+ * ccq_status. */
+int ccq_scan_backward(const ccq_scan_bwd_params *p, void *hip_stream);
+size_t ccq_scan_backward_workspace_bytes(const ccq_scan_bwd_params *p);
+
+/* Arguments of ccq_beam_select.  Zero-initialise, then fill in. */
+typedef struct {
+  int32_t dtype;             /* ccq_dtype of logits                                                 */
+  int32_t N, K, V, M;        /* requests, beams of each, vocabulary, picks: K <= 64, M <= min(64, K V),
+                                K V < 2^31 and K ceil(V / 16384) <= 4096                            */
+  const void *logits;        /* [N, K, V], a row every logits_stride elements                        */
+  int64_t logits_stride;     /* >= V                                                                 */
+  const float *scores;       /* [N, K] log-probability of every beam so far                          */
+  const uint8_t *finished;   /* [N, K], non-zero: the beam is complete; or NULL: none is             */
+  int32_t pad_token;         /* 0 .. V - 1: the one token a finished beam goes on with               */
+  int32_t *token, *parent;   /* [N, M] written: the picks' tokens and the beams they continue        */
+  float *score;              /* [N, M] written: their scores                                         */
+  void *workspace;           /* ccq_beam_select_workspace_bytes(p) bytes                             */
+  size_t workspace_bytes;
+} ccq_beam_params;
+
+/*
+ * One selection step of beam search.  Continuing beam k with token v scores
+ *   scores[k] + logits[k][v] - log sum_u exp logits[k][u],
+ * and a finished beam goes on with pad_token alone, at its old score (every other token: -inf).
+ * For each request the M best of the K V continuations, best first; equal ones in order of beam,
+ * then token.  A NaN logit counts as -inf and +inf as the largest finite number; a beam whose
+ * score is -inf or NaN has only continuations at -inf, and so has a row of -inf.  The
+ * normaliser is formed so that scores of different beams compare as they would in 64 bits (its
+ * terms near the top in 64 bits, the tail in 32 with sums in 64).  Returns a ccq_status.
+ */
+int ccq_beam_select(const ccq_beam_params *p, void *hip_stream);
+size_t ccq_beam_select_workspace_bytes(const ccq_beam_params *p);
+
+/* Most states of one ccq_beam_reorder. */
+#define CCQ_MAX_REORDER_STATES 16
+
+/*
+ * Moves carried states to the beams that continue them, in place: for every state s, request i
+ * and beam j, row (i K + j) of states[s] becomes what row (i K + parent[i][j]) was.  A row is
+ * row_bytes[s] bytes, a multiple of 4: S, C, ksum and n of a decode step with N K sequences, h of
+ * ccq_scan, or anything else kept per beam.  parent is [N, K]; a parent outside 0 .. K - 1 leaves
+ * its beam as it is.  1 <= K <= 64, 1 <= n_states <= CCQ_MAX_REORDER_STATES; states and row_bytes
+ * are host arrays, read before the call returns.  Rows that stay are neither read nor written.
+ * Returns a ccq_status.
+ */
+int ccq_beam_reorder(int32_t n_states, void *const *states, const size_t *row_bytes, int32_t N, int32_t K,
+                     const int32_t *parent, void *hip_stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,180 @@
+"""ccq_beam_select and ccq_beam_reorder on the GPU against their fp64 definitions.
+
+Tokens and parents are equal; scores are rounded once from 64 bits, the normaliser's fp32 part adding
+at most 2^-24 of itself (its terms and its sums of 64 at a time round apart from each other, 64 2^-24 at
+worst of the tail's share): |error| <= 2^-24 |score| + 64 2^-24.  Reordering moves bits.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import layer
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+def _run(logits, scores, m, finished=None, pad=0, tag=""):
+    import torch
+    from curvature_conditioned_query_amd import ccq_beam_select
+    print(f"beam {tag} {tuple(logits.shape)} {logits.dtype} m={m}", flush=True)
+    out = ccq_beam_select(logits, scores, m, finished=finished, pad_token=pad)
+    again = ccq_beam_select(logits, scores, m, finished=finished, pad_token=pad)
+    t, p, s = layer.beam_select(logits.double().cpu().numpy(), scores.double().cpu().numpy(), m,
+                                None if finished is None else finished.cpu().numpy(), pad)
+    assert np.array_equal(out["parent"].cpu().numpy(), p), tag
+    assert np.array_equal(out["token"].cpu().numpy(), t), tag
+    got = out["score"].double().cpu().numpy()
+    fin = np.isfinite(s)
+    assert np.array_equal(got[~fin], s[~fin])
+    assert (np.abs(got[fin] - s[fin]) <= U * np.abs(s[fin]) + 64 * U).all()
+    assert all(torch.equal(out[n], again[n]) for n in out)
+    return out
+
+
+def _logits(N, K, V, dtype, seed, stride=None):
+    import torch
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    g = torch.Generator().manual_seed(seed)
+    x = (2.5 * torch.randn(N, 1, V, generator=g) + torch.randn(N, K, V, generator=g)).to(dt)
+    if stride:
+        wide = torch.full((N, K, stride), 1e4, dtype=dt)
+        wide[..., :V] = x
+        return wide.cuda()[..., :V], g
+    return x.cuda(), g
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,K,V,m,stride", [
+    (1, 1, 1, 1, None), (1, 4, 3, 12, None), (2, 3, 17, 5, None), (3, 2, 255, 4, 256), (1, 4, 2048, 4, None),
+    (2, 5, 2049, 10, None), (1, 8, 5003, 64, None), (5, 4, 32001, 8, None), (40, 16, 1000, 16, 1003), (1, 1, 70000, 64, None),
+    (64, 8, 9001, 16, None), (1, 64, 333, 64, None), (3, 4, 16384, 7, 16385)])
+def test_select(gpu_lib, dtype, N, K, V, m, stride):
+    import torch
+    logits, g = _logits(N, K, V, dtype, V + K, stride)
+    scores = (-4 * torch.rand(N, K, generator=g) - 3).cuda()
+    _run(logits, scores, m, tag="plain")
+    fin = torch.rand(N, K, generator=g).cuda() < 0.3
+    _run(logits, scores, m, finished=fin, pad=V // 2, tag="finished")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,m", [(100, 10), (4099, 16), (40000, 64)])
+def test_ties_go_to_the_lowest(gpu_lib, dtype, V, m):
+    """Rows of one value, of few values, rising and falling rows, equal beams."""
+    import torch
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    scores = torch.zeros(1, 3).cuda()
+    _run(torch.zeros(1, 3, V, dtype=dt).cuda(), scores, m, tag="constant")
+    g = torch.Generator().manual_seed(1)
+    _run(torch.randint(0, 3, (1, 1, V), generator=g).to(dt).expand(1, 3, V).contiguous().cuda(), scores, m, tag="three values, equal beams")
+    ramp = (torch.arange(V, dtype=torch.float64) / V * 8).to(dt).expand(1, 3, V).contiguous().cuda()
+    _run(ramp, scores, m, tag="rising")
+    _run(ramp.flip(-1).contiguous(), scores, m, tag="falling")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [50, 5000, 20011])
+@pytest.mark.parametrize("allowed", [0, 1, 3, 40])
+def test_masked_vocabulary(gpu_lib, dtype, V, allowed):
+    """Only a few tokens are allowed, down to none; the picks run out into -inf, lowest first."""
+    import torch
+    logits, g = _logits(2, 3, V, dtype, V)
+    keep = torch.randperm(V, generator=g)[:allowed].cuda()
+    x = torch.full_like(logits, -float("inf"))
+    x[..., keep] = logits[..., keep]
+    _run(x, (-torch.rand(2, 3, generator=g)).cuda(), 16, tag=f"{allowed} allowed")
+
+
+def test_lowest_finite_mask(gpu_lib):
+    """A mask of the type's lowest value: those tokens count as far away, not as absent."""
+    import torch
+    logits, g = _logits(1, 2, 3001, "f32", 8)
+    x = torch.full_like(logits, torch.finfo(torch.float32).min)
+    x[..., 7:9] = logits[..., 7:9]
+    _run(x, torch.tensor([[-1.0, -1.5]]).cuda(), 8, tag="lowest value")
+
+
+def test_nan_inf_and_dead_beams(gpu_lib):
+    import torch
+    inf, nan = float("inf"), float("nan")
+    logits, _ = _logits(1, 4, 6001, "f32", 9)
+    logits[0, 0, 5:3000] = nan
+    logits[0, 1, 17], logits[0, 1, 4000] = inf, inf
+    _run(logits, torch.tensor([[-1.0, -2.0, -3.0, -4.0]]).cuda(), 8, tag="nan and inf")
+    _run(logits, torch.tensor([[0.0, -inf, nan, -inf]]).cuda(), 12, tag="first step: one live beam")
+    _run(logits, torch.full((1, 4), -inf).cuda(), 12, tag="no live beam")
+    logits[0, 0] = nan
+    fin = torch.tensor([[0, 1, 1, 0]], dtype=torch.uint8).cuda()
+    _run(logits, torch.tensor([[-1.0, nan, -inf, -2.0]]).cuda(), 12, finished=fin, pad=3, tag="finished and nan")
+    _run(logits, torch.tensor([[-1.0, -5.0, -0.1, -inf]]).cuda(), 30, finished=torch.ones_like(fin), pad=20, tag="all finished")
+
+
+def test_peaked_rows_where_few_terms_carry_the_sum(gpu_lib):
+    """Rows with one token far above, and rows whose large logits all lie on one thread."""
+    import torch
+    logits, g = _logits(4, 4, 40003, "f32", 10)
+    logits[:, :, 12345] += 30.0
+    logits[1, :, 8 : 8 + 4] += 25.0
+    logits[2, :, 2048 * torch.arange(19)] += 20.0
+    _run(logits, (-torch.rand(4, 4, generator=g)).cuda(), 32, tag="peaked")
+
+
+@pytest.mark.parametrize("K", [1, 2, 3, 4, 5, 8, 13, 16, 17, 40, 64])
+def test_reorder(gpu_lib, K):
+    """States of many row sizes and types, moved in place by every kind of parents."""
+    import torch
+    from curvature_conditioned_query_amd import ccq_beam_reorder
+    print(f"reorder K={K}", flush=True)
+    N = 3
+    g = torch.Generator().manual_seed(K)
+    make = lambda *shape: torch.randn(N * K, *shape, generator=g).cuda()  # noqa: E731
+    states = [make(2, 16, 16), make(1), make(5, 3), make(4097), torch.randint(0, 1 << 40, (N * K, 3), generator=g).cuda(),
+              make(2, 6).to(torch.bfloat16), torch.randint(0, 256, (N * K, 8), generator=g).to(torch.uint8).cuda()]
+    for kind in ("random", "same", "all one", "cycle", "outside"):
+        parent = {"random": torch.randint(0, K, (N, K), generator=g), "same": torch.arange(K).expand(N, K),
+                  "all one": torch.full((N, K), K // 2), "cycle": (torch.arange(K) + 1).remainder(K).expand(N, K),
+                  "outside": torch.randint(-2, K + 2, (N, K), generator=g)}[kind].to(torch.int32).contiguous()
+        want = [torch.from_numpy(layer.beam_reorder(s.float().cpu().numpy() if s.dtype == torch.bfloat16 else s.cpu().numpy(),
+                                                    parent.numpy())) for s in states]
+        ccq_beam_reorder(states, parent.cuda())
+        for s, w in zip(states, want):
+            assert torch.equal(s.cpu().to(w.dtype), w), kind
+
+
+def test_reorder_leaves_neighbours_alone(gpu_lib):
+    import torch
+    from curvature_conditioned_query_amd import ccq_beam_reorder
+    buf = torch.randn(12, 1000, device="cuda")
+    keep = buf.clone()
+    ccq_beam_reorder([buf[4:8]], torch.tensor([[1, 0], [1, 1]], dtype=torch.int32, device="cuda"))
+    assert torch.equal(buf[:4], keep[:4]) and torch.equal(buf[8:], keep[8:])
+    assert torch.equal(buf[4:8], keep[[5, 4, 7, 7]])
+
+
+def test_other_stream_and_replayed_capture(gpu_lib):
+    import torch
+    from curvature_conditioned_query_amd import ccq_beam_reorder, ccq_beam_select
+    logits, g = _logits(3, 4, 9000, "bf16", 12)
+    scores = -torch.rand(3, 4, generator=g).cuda()
+    state, fresh = torch.randn(12, 700, device="cuda"), torch.randn(12, 700, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    want, got = ccq_beam_select(logits, scores, 4), ccq_beam_select(logits, scores, 4, stream=side)
+    side.synchronize()
+    assert all(torch.equal(want[n], got[n]) for n in want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = ccq_beam_select(logits, scores, 4)
+        ccq_beam_reorder([state], out["parent"])
+    for _ in range(4):
+        logits.copy_(torch.randn(logits.shape, device="cuda"))
+        want = ccq_beam_select(logits, scores, 4)
+        state.copy_(fresh)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(want[n], out[n]) for n in want)
+        rows = (torch.arange(3, device="cuda")[:, None] * 4 + want["parent"]).flatten().long()
+        assert torch.equal(state, fresh[rows])

@@ -1,0 +1,234 @@
+"""ccq_scan and its gradient on the GPU against their token-by-token fp64 definitions.
+
+Tolerances.  u = 2^-24.  A step of the recurrence rounds the gate (exp, within 4 u), the product, the
+scaled input (at most 4 u) and the sum: under 10 u of alpha_t A_{t-1} + |s_t x_t|, A the recurrence of
+the absolute values; an error made once is carried on by the gates, as the oracle's majorant E carries
+it.  Pieces that are joined multiply their gates and then the state, which rounds each gate's product
+once: the same bound a step.  So |error| <= 10 u E, and half a step of the stored type (2^-8 of the
+value for bf16).  The gradient has the same bound with its own majorants, twice over where an adjoint
+meets a state (20 u).
+"""
+
+import numpy as np
+import pytest
+
+from oracle import layer
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+STEP = {"bf16": 2.0 ** -8, "f32": 0.0}
+
+
+def _np(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def _check(got, want, size, dtype, units, tag):
+    got = _np(got)
+    live = ~np.isnan(want)
+    err = np.abs(got - want)[live]
+    tol = (units * U * size + STEP[dtype] * (np.abs(want) + units * U * size) + 1e-37)[live]
+    assert not (err > tol).any(), f"{tag}: worst {np.max(err / tol):.2f} of the tolerance"
+
+
+def _make(dtype, B, T, D, seed, decay=1 / 8, h0=True, lengths=None):
+    import torch
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(B, T, D, generator=g).to(dt).cuda()
+    la = (torch.nn.functional.logsigmoid(torch.randn(B, T, D, generator=g)) * decay).to(dt).cuda()
+    h = torch.randn(B, D, generator=g).cuda() if h0 else None
+    n = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    return x, la, h, n
+
+
+def _both(dtype, x, la, h0, n, complement, keep=True, tag=""):
+    """Forward with its chunk carries, and the gradient from them and without them."""
+    import torch
+    from curvature_conditioned_query_amd import ccq_scan, ccq_scan_backward, scan_carry_shape
+    B, T, D = x.shape
+    y = torch.full((B, T, D), 7.0, dtype=x.dtype, device="cuda")
+    h = torch.empty(B, D, device="cuda")
+    carry = torch.empty(scan_carry_shape(x), device="cuda")
+    assert ccq_scan(x, la, h0=h0, h_out=h, y=y, lengths=n, complement=complement, chunk_carry=carry) is y
+    lens = None if n is None else n.tolist()
+    hs, last, es, last_err = layer.scan(_np(x), _np(la), _np(h0), lens, complement)
+    _check(y, hs, es, dtype, 10, tag + "y")
+    assert (y[torch.from_numpy(np.isnan(hs)).cuda()] == 7.0).all(), "a row behind its length was written"
+    _check(h, last, last_err, "f32", 10, tag + "h")
+    for c in range(carry.shape[1]):
+        for b in range(B):
+            if 64 * c < (T if lens is None else lens[b]):
+                want = hs[b, 64 * c - 1] if c else (np.zeros(D) if h0 is None else _np(h0)[b])
+                size = es[b, 64 * c - 1] if c else np.zeros(D)
+                _check(carry[b, c], want, size, "f32", 10, tag + "carry")
+    g = torch.Generator().manual_seed(99)
+    dy = torch.randn(B, T, D, generator=g).to(x.dtype).cuda()
+    dh = torch.randn(B, D, generator=g).cuda()
+    want = layer.scan_backward(_np(x), _np(la), _np(dy), _np(h0), _np(dh), lens, complement)
+    for given in (carry, None):
+        out = ccq_scan_backward(x, la, dy, h0=h0, dh_out=dh, lengths=n, complement=complement, chunk_carry=given, want_dh0=True)
+        for i, name in enumerate(("dx", "dlog_alpha", "dh0")):
+            _check(out[name], want[i], want[3 + i], "f32" if name == "dh0" else dtype, 20, f"{tag}{name} kept={given is not None} ")
+    return y, h
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("complement", [False, True])
+@pytest.mark.parametrize("B,T,D", [(1, 1, 8), (3, 2, 24), (2, 63, 64), (1, 64, 72), (2, 65, 200), (1, 127, 128), (1, 257, 8),
+                                   (2, 513, 136), (1, 1500, 64)])
+def test_forward_and_backward(gpu_lib, dtype, complement, B, T, D):
+    print(f"scan {dtype} complement={complement} B{B} T{T} D{D}", flush=True)
+    x, la, h0, _ = _make(dtype, B, T, D, 1 + T)
+    _both(dtype, x, la, h0, None, complement)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,lengths", [(300, [0, 1, 300, 64, 65]), (1100, [1100, 255, 256, 257, 1024]), (70, [-5, 99, 70, 2, 0])])
+def test_lengths(gpu_lib, dtype, T, lengths):
+    """Empty sequences, single tokens, ends at and beside a piece's end, lengths outside 0 .. T."""
+    print(f"scan lengths {dtype} T{T} {lengths}", flush=True)
+    x, la, h0, n = _make(dtype, len(lengths), T, 40, 5, lengths=lengths)
+    for b, k in enumerate(lengths):
+        x[b, max(0, k):] = float("nan")
+        la[b, max(0, k):] = float("inf")
+    _both(dtype, x, la, h0, n, True)
+
+
+@pytest.mark.parametrize("decay", [1e-5, 20.0])
+def test_slow_and_fast_gates(gpu_lib, decay):
+    """Gates next to 1 (nothing is lost over the whole length) and gates that forget within a token."""
+    x, la, h0, _ = _make("f32", 1, 900, 64, 6, decay=decay)
+    _both("f32", x, la, h0, None, False)
+    _both("f32", x, la, h0, None, True)
+
+
+@pytest.mark.parametrize("where", [0, 1, 100, 255, 256, 700])
+def test_reset_drops_what_came_before(gpu_lib, where):
+    """log_alpha = -inf at one token: NaN and infinities before it do not pass, in no direction."""
+    import torch
+    from curvature_conditioned_query_amd import ccq_scan, ccq_scan_backward
+    x, la, h0, _ = _make("f32", 2, 800, 64, 7)
+    la[:, where] = -float("inf")
+    want = ccq_scan(x[:, where:], la[:, where:])
+    dy, dh = torch.randn_like(x), torch.randn(2, 64, device="cuda")
+    clean = ccq_scan_backward(x, la, dy, h0=h0, dh_out=dh, want_dh0=True)
+    x[:, :where] = float("nan")
+    h0[:] = float("inf")
+    y = ccq_scan(x, la, h0=h0)
+    assert torch.isfinite(y[:, where:]).all()
+    hs, _, es, _ = layer.scan(_np(x[:, where:]), _np(la[:, where:]), None, None, False)
+    _check(y[:, where:], hs, es, "f32", 10, "y")
+    _check(want, hs, es, "f32", 10, "y alone")
+    out = ccq_scan_backward(x, la, dy, h0=h0, dh_out=dh, want_dh0=True)
+    for name in ("dx", "dlog_alpha"):
+        assert torch.isfinite(out[name][:, where:]).all()
+    assert (out["dlog_alpha"][:, where] == 0).all()
+    assert torch.equal(out["dx"], clean["dx"])  # the adjoint does not see the states
+    if where == 0:
+        assert (out["dh0"] == 0).all()
+
+
+def test_an_infinity_or_nan_stays_until_a_reset(gpu_lib):
+    import torch
+    from curvature_conditioned_query_amd import ccq_scan
+    x, la, h0, _ = _make("f32", 1, 1000, 64, 8, decay=2.0)
+    x[0, 3, 0], x[0, 5, 1] = float("inf"), float("nan")
+    y = ccq_scan(x, la, h0=h0)
+    assert (y[0, 3:, 0] == float("inf")).all() and y[0, 5:, 1].isnan().all() and torch.isfinite(y[0, :, 2:]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_strided_inputs(gpu_lib, dtype):
+    """Parts of a packed projection, a time-major tensor, and inputs shared by all sequences (stride 0)."""
+    import torch
+    from curvature_conditioned_query_amd import ccq_scan, ccq_scan_backward
+    B, T, D = 2, 90, 48
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    packed = torch.randn(B, T, 3 * D).to(dt).cuda()
+    x = packed[..., D : 2 * D]
+    la = -torch.rand(T, B, D).to(dt).cuda().transpose(0, 1)
+    assert torch.equal(ccq_scan(x, la), ccq_scan(x.contiguous(), la.contiguous()))
+    one = -torch.rand(1, T, D).to(dt).cuda().expand(B, T, D)
+    dy = packed[..., 2 * D :]
+    a, b = ccq_scan_backward(x, one, dy), ccq_scan_backward(x.contiguous(), one.contiguous(), dy.contiguous())
+    assert torch.equal(a["dx"], b["dx"]) and torch.equal(a["dlog_alpha"], b["dlog_alpha"])
+
+
+def test_steps_continue_a_prefill_in_place(gpu_lib):
+    import torch
+    from curvature_conditioned_query_amd import ccq_scan
+    x, la, h0, _ = _make("f32", 3, 131, 64, 9)
+    hs, _, es, _ = layer.scan(_np(x), _np(la), _np(h0), None, True)
+    h = h0.clone()
+    _check(ccq_scan(x[:, :100], la[:, :100], h0=h, h_out=h, complement=True), hs[:, :100], es[:, :100], "f32", 10, "prefill")
+    for t in range(100, 131):
+        y = ccq_scan(x[:, t : t + 1], la[:, t : t + 1], h0=h, h_out=h, complement=True)
+        _check(y, hs[:, t : t + 1], es[:, t : t + 1], "f32", 10, f"step {t}")
+        assert torch.equal(y[:, 0], h)
+
+
+def test_many_sequences_and_channels_run_again_alike(gpu_lib):
+    """A size that is cut along T and over many workgroups: bit for bit the same twice, forward and back,
+    and right at sampled channels."""
+    import torch
+    from curvature_conditioned_query_amd import ccq_scan, ccq_scan_backward
+    x, la, h0, _ = _make("bf16", 2, 5000, 1032, 10)
+    h = torch.empty_like(h0)
+    y = ccq_scan(x, la, h0=h0, h_out=h)
+    dy = torch.randn(x.shape, generator=torch.Generator().manual_seed(1)).to(x.dtype).cuda()
+    out = ccq_scan_backward(x, la, dy, h0=h0, want_dh0=True)
+    for _ in range(2):
+        assert torch.equal(y, ccq_scan(x, la, h0=h0))
+        more = ccq_scan_backward(x, la, dy, h0=h0, want_dh0=True)
+        assert all(torch.equal(out[n], more[n]) for n in out)
+    at = [0, 7, 63, 64, 512, 1024, 1031]
+    hs, last, es, le = layer.scan(_np(x[..., at]), _np(la[..., at]), _np(h0[:, at]), None, False)
+    _check(y[..., at], hs, es, "bf16", 10, "y")
+    _check(h[:, at], last, le, "f32", 10, "h")
+    want = layer.scan_backward(_np(x[..., at]), _np(la[..., at]), _np(dy[..., at]), _np(h0[:, at]), None, None, False)
+    _check(out["dx"][..., at], want[0], want[3], "bf16", 20, "dx")
+    _check(out["dlog_alpha"][..., at], want[1], want[4], "bf16", 20, "dlog_alpha")
+    _check(out["dh0"][:, at], want[2], want[5], "f32", 20, "dh0")
+
+
+@pytest.mark.parametrize("T", [1, 700])
+def test_other_stream_and_replayed_capture(gpu_lib, T):
+    import torch
+    from curvature_conditioned_query_amd import ccq_scan, ccq_scan_backward
+    x, la, h0, _ = _make("bf16", 2, T, 256, 11)
+    dy = torch.randn_like(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    want = ccq_scan(x, la, h0=h0)
+    got = ccq_scan(x, la, h0=h0, stream=side)
+    side.synchronize()
+    assert torch.equal(want, got)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = ccq_scan(x, la, h0=h0)
+        out = ccq_scan_backward(x, la, dy, h0=h0, want_dh0=True)
+    for _ in range(4):
+        x.copy_(torch.randn_like(x))
+        want, back = ccq_scan(x, la, h0=h0), ccq_scan_backward(x, la, dy, h0=h0, want_dh0=True)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(want, y) and all(torch.equal(back[n], out[n]) for n in out)
+
+
+def test_two_streams_at_once(gpu_lib):
+    """Calls in flight together, each with its own workspace, do not see each other."""
+    import torch
+    from curvature_conditioned_query_amd import ccq_scan
+    sets = [_make("bf16", 2, 3000, 512, 20 + i) for i in range(4)]
+    want = [ccq_scan(x, la, h0=h0) for x, la, h0, _ in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(5):
+        got = [ccq_scan(x, la, h0=h0, stream=s) for s, (x, la, h0, _) in zip(streams, sets)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
