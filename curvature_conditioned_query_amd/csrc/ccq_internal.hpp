@@ -158,6 +158,7 @@ hipError_t launch_gdn_summary(const FwdArgs& a, hipStream_t stream);
 hipError_t launch_qk(const ccq_qk_params& p, hipStream_t stream);
 size_t qk_backward_workspace_bytes(const ccq_qk_bwd_params& p);
 hipError_t launch_qk_backward(const ccq_qk_bwd_params& p, hipStream_t stream);
+bool scan_grid_fits(int B, int T, int D);  // whether the sizes' tiles can be one launch
 size_t scan_workspace_bytes(const ccq_scan_params& p);
 hipError_t launch_scan(const ccq_scan_params& p, hipStream_t stream);
 size_t scan_backward_workspace_bytes(const ccq_scan_bwd_params& p);

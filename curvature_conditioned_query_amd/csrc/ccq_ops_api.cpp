@@ -166,6 +166,7 @@ int validate_qk_backward(const ccq_qk_bwd_params* p) {
 int scan_sizes(int dtype, int B, int T, int D, int complement) {
   if (bad_dtype(dtype) || B <= 0 || T <= 0 || D <= 0 || (complement & ~1)) return CCQ_ERR_INVALID_ARG;
   if (D % 8 != 0 || D > (1 << 24) || (long long)B * T > (1LL << 30) || (long long)B * D > 0x7fffffffLL) return CCQ_ERR_UNSUPPORTED;
+  if (!ccq::scan_grid_fits(B, T, D)) return CCQ_ERR_UNSUPPORTED;
   return CCQ_OK;
 }
 size_t scan_carry_bytes(int B, int T, int D) { return (size_t)B * ((T + 63) / 64) * D * 4; }

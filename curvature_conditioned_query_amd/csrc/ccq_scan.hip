@@ -2,7 +2,7 @@
 //
 // A few operations an element: memory is the bound, so every input is read once.  A run of tokens acts
 // on the state as h -> P h + q (P the product of its gates, q what the run adds), and runs compose:
-// (P1, q1) then (P2, q2) is (P1 P2, P2 q1 + q2).  A workgroup takes a tile of 128 tokens by 64 channels
+// (P1, q1) then (P2, q2) is (P1 P2, P2 q1 + q2).  A workgroup takes a tile of 128 tokens by 128 channels
 // into registers (a thread: four tokens of eight channels, one 16-byte load each in bf16), folds its
 // tokens, joins the threads' pairs in LDS, and publishes the tile's pair; the state before the tile is
 // the fold of the pairs of the tiles before it, and the tile's tokens are then walked again, from
@@ -10,10 +10,13 @@
 // still read once: about 1/2 of the traffic of a pass that sums up the pieces before the pass that
 // writes them would be spent on reading twice.
 //
+// A row of a tile is 256 bytes (bf16): read two, write one of that shape reaches 5.3 TB/s, where rows of
+// 128 bytes reach 4.8; past the caches (non-temporal), which a single use has no use for, 6.0 and 5.4.
+//
 // Waiting.  A tile's pair depends on its own inputs alone and is published before its workgroup waits
-// for any other, and tiles are handed out by a counter in the order of the recurrence, so whatever a
-// workgroup waits for is already being worked on by one that waits for nothing first.  The folds go
-// in a fixed order (16 or 64 tiles make a group, whose last tile publishes the group's pair), so two
+// for any other, and each column's tiles are handed out by a counter in the order of the recurrence, so
+// whatever a workgroup waits for is already being worked on by one that waits for nothing first.  The folds go
+// in a fixed order (16 tiles make a group, whose last tile publishes the group's pair), so two
 // calls give the same bits.  A wait gives up after about a second and leaves NaN: only a workspace
 // that another call is writing can bring that about.
 //
@@ -28,14 +31,26 @@
 namespace ccq {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = 4;
-constexpr int kChunk = 64;              // tokens between kept states
-constexpr int kCols = 64;               // channels of a tile: one lane each where pairs are joined
-constexpr int kRun = 4;                 // tokens of a thread
-constexpr int kRuns = 8;                // runs of a wave, one behind the other
-constexpr int kTile = kRun * kRuns * kWaves;  // tokens of a tile
-static_assert(kTile % kChunk == 0, "tiles start at a kept state");
+constexpr int kThreads = 512;      // of a tile
+constexpr int kStepThreads = 256;  // of the kernels without tiles
+constexpr int kChunk = 64;         // tokens between kept states
+constexpr int kCols = 128;         // channels of a tile
+constexpr int kOct = kCols / 8;    // threads side by side: eight channels each
+constexpr int kRuns = kThreads / kOct;  // runs of a tile, one behind the other
+constexpr int kParts = kThreads / kCols;  // threads that share a channel where pairs are joined
+constexpr int kPartRuns = kRuns / kParts;
+constexpr int kGroup = 16;  // tiles of a group
+// Tokens of a thread: 32 to 64 registers of inputs.
+template <typename T, bool BACK>
+struct Run {
+  static constexpr int n = sizeof(T) == 4 && BACK ? 2 : 4;
+  static constexpr int tile = n * kRuns;  // tokens of a tile
+  static_assert(tile % kChunk == 0, "tiles start at a kept state");
+};
+inline int tile_tokens(int dtype, bool back) {
+  return dtype == CCQ_DTYPE_BF16 ? (back ? Run<__bf16, true>::tile : Run<__bf16, false>::tile)
+                                 : (back ? Run<float, true>::tile : Run<float, false>::tile);
+}
 
 __device__ __forceinline__ int sequence_length(const int32_t* lengths, int b, int T) {
   return lengths ? min(max(lengths[b], 0), T) : T;
@@ -43,14 +58,16 @@ __device__ __forceinline__ int sequence_length(const int32_t* lengths, int b, in
 
 // ---------------------------------------------------------------- gates
 
-// alpha = exp(g) to about 2 units in the last place; 0 below about -87.  The hardware's 2^p takes the
-// rounded product p = g log2(e), whose rounding, up to |p| / 2 units of the result, is made good to first
-// order.
+// alpha = exp(g); 0 below about -87.  The hardware's 2^p takes the rounded product p = g log2(e), whose
+// rounding is worth up to |g| 2^-24 of the result.  For fp32 inputs it is made good to first order, which
+// leaves about 2 units in the last place; bf16 inputs stand for values 2^-9 |g| apart, and go without.
+template <typename T>
 __device__ __forceinline__ float gate(float g) {
   constexpr float hi = 1.44269502162933349609f, lo = 1.92596299112661746887e-8f, ln2 = 0.693147180559945f;
   const float p = g * hi;
-  const float rest = fmaf(g, lo, fmaf(g, hi, -p));
   const float a = __builtin_amdgcn_exp2f(p);
+  if constexpr (sizeof(T) == 2) return a;
+  const float rest = fmaf(g, lo, fmaf(g, hi, -p));
   return fabsf(p) < 127.f ? fmaf(a, rest * ln2, a) : a;  // beyond: 0, infinity or NaN
 }
 
@@ -66,12 +83,31 @@ __device__ __forceinline__ float one_minus(float g, float alpha) {
   return fabsf(g) < 0.25f ? -g * s : 1.f - alpha;
 }
 
-// alpha h, and alpha h + u, with 0 h = 0 for every h.
-__device__ __forceinline__ float gated(float alpha, float h) { return alpha == 0.f ? 0.f : alpha * h; }
-__device__ __forceinline__ float step(float alpha, float h, float u) { return alpha == 0.f ? u : fmaf(alpha, h, u); }
+// alpha h, and alpha h + u; with RESETS 0 h = 0 for every h.  Where no gate of a wave is 0, as is the
+// rule, its walks go without that test, a third of their operations.
+template <bool RESETS>
+__device__ __forceinline__ float gated(float alpha, float h) {
+  return RESETS && alpha == 0.f ? 0.f : alpha * h;
+}
+template <bool RESETS>
+__device__ __forceinline__ float step(float alpha, float h, float u) {
+  return RESETS && alpha == 0.f ? u : fmaf(alpha, h, u);
+}
+// The state behind a token.  With the complement scale, alpha h + (1 - alpha) x: EXACT from 1 - alpha formed
+// to its last place, as an fp32 result needs; else as x + alpha (h - x), which rounds at the size of x, for
+// the few tokens between a state so formed and results stored in bf16.
+template <bool RESETS, bool COMPLEMENT, bool EXACT>
+__device__ __forceinline__ float advance(float alpha, float g, float h, float x) {
+  if constexpr (!COMPLEMENT) return step<RESETS>(alpha, h, x);
+  if constexpr (EXACT) return step<RESETS>(alpha, h, x * one_minus(g, alpha));
+  return step<RESETS>(alpha, h - x, x);
+}
 
 // The product of a run's gates, one more of them.
-__device__ __forceinline__ float gates_product(float P, float alpha) { return alpha == 0.f ? -0.f : P * alpha; }
+template <bool RESETS>
+__device__ __forceinline__ float gates_product(float P, float alpha) {
+  return RESETS && alpha == 0.f ? -0.f : P * alpha;
+}
 
 // ---------------------------------------------------------------- runs
 
@@ -117,25 +153,86 @@ __device__ __forceinline__ void store8(__bf16* p, const float (&x)[8]) {
   *reinterpret_cast<bf16x8*>(p) = a;
 }
 
+// The stored form, so that a thread's loads are all under way before the first is waited for: eight
+// channels in words of kPer.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+template <typename T>
+struct Raw8 {
+  static constexpr int kPer = 4 / (int)sizeof(T), kWords = 8 / kPer;
+  unsigned w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < kWords; i += 4) {
+      const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + i * kPer));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[i + j] = v[j];
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int i = 0; i < kWords; i += 4)
+      __builtin_nontemporal_store(u32x4{w[i], w[i + 1], w[i + 2], w[i + 3]}, reinterpret_cast<u32x4*>(p + i * kPer));
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+  }
+  // channel e of word i
+  __device__ __forceinline__ float get(int i, int e) const {
+    if constexpr (kPer == 1) return __uint_as_float(w[i]);
+    return __uint_as_float(e ? w[i] & 0xffff0000u : w[i] << 16);
+  }
+  __device__ __forceinline__ void set(int i, const float (&x)[kPer]) {
+    if constexpr (kPer == 1) w[i] = __float_as_uint(x[0]);
+    else w[i] = __builtin_bit_cast(unsigned, bf16x2{(__bf16)x[0], (__bf16)x[1]});
+  }
+};
+
+// Behind the end of a sequence: gates of 1 and inputs of 0, so nothing changes.
+template <typename R, int N>
+__device__ __forceinline__ void clear_from(R (&raw)[N], int live) {
+#pragma unroll
+  for (int r = 0; r < N; ++r)
+    if (r >= live) raw[r].clear();
+}
+
+// Makes word i of a run new to the compiler once `done` is known: without this it forms all of a run's
+// gates before it folds the first, or keeps them for the walk, and neither fits the registers.
+template <typename R, int N>
+__device__ __forceinline__ void in_turn(R (&raw)[N], int i, float done) {
+#pragma unroll
+  for (int r = 0; r < N; ++r) asm volatile("" : "+v"(raw[r].w[i]) : "v"(done));
+}
+
+// A thread's run of one input: token t0 on, eight channels from c0 on.  Every load is made, at a row and
+// column inside the tensor; what lies outside the sequence is cleared later.
+template <typename T, int RUN>
+__device__ __forceinline__ void load_run(Raw8<T> (&raw)[RUN], const void* base, int64_t stride_b, int64_t stride_t, int b,
+                                         int t0, int c0, int T_max, int D) {
+  const T* p = static_cast<const T*>(base) + b * stride_b + min(c0, D - 8);
+#pragma unroll
+  for (int r = 0; r < RUN; ++r) raw[r].load(p + (int64_t)min(t0 + r, T_max - 1) * stride_t);
+}
+
 // ---------------------------------------------------------------- tiles
 
-// The tiles of a call, in the order of the recurrence: all (sequence, 64 channels) columns of the first
-// tokens, then of the next.  The workspace holds a counter, a pair for every tile and channel, and one
-// for every group of tiles.
+// The tiles of a call: (sequence, 128 channels) columns of `segments` tiles.  Counter k hands out the
+// tiles of columns k, k + kCounters, ... in the order of the recurrence: all of the first tokens, then of
+// the next.  One counter for all took 4.4 ns a tile, 18 of 78 us at B4 T4096 D2048 with 4096 tiles.  The
+// workspace holds the counters, a pair for every tile and channel, and one for every group of tiles.
+constexpr int kCounters = 16;
+constexpr int kCounterStride = 32;  // words: a cache line each
 struct Tiles {
-  int columns;   // B ceil(D / 64)
-  int per_row;   // ceil(D / 64)
-  int segments;  // ceil(T / kTile)
-  int group;     // segments of a group
-  unsigned* counter;
-  uint64_t* pairs;   // [segments][columns][64]
-  uint64_t* groups;  // [segments / group][columns][64]
+  int columns;   // B ceil(D / 128)
+  int per_row;   // ceil(D / 128)
+  int segments;  // ceil(T / tile)
+  unsigned* counters;
+  uint64_t* pairs;   // [segments][columns][128]
+  uint64_t* groups;  // [segments / kGroup][columns][128]
 };
-constexpr size_t kCounterBytes = 256;
+constexpr size_t kCounterBytes = kCounters * kCounterStride * 4;
 
-__host__ __device__ inline int group_of(int segments) { return segments <= 256 ? 16 : 64; }
-
-constexpr uint64_t kEmpty = ~(uint64_t)0;  // no pair: the half of P is a NaN that is never published
+// No pair: all ones; the half of P is then a NaN that is never published.
 
 __device__ __forceinline__ void publish(uint64_t* at, Pair r) {
   if (r.P != r.P) r.P = __int_as_float(0x7fc00000);
@@ -146,151 +243,286 @@ __device__ __forceinline__ Pair unpack(uint64_t word) {
   return Pair{__uint_as_float((unsigned)word), __uint_as_float((unsigned)(word >> 32))};
 }
 
-// The fold of n published pairs, `stride` words apart.  Every lane of the wave waits with the others.
-__device__ Pair fold_published(const uint64_t* from, int n, size_t stride) {
+// The fold of n published pairs, `stride` words apart.  The wave waits as one.
+template <int BATCH>
+__device__ __forceinline__ Pair fold_published(const uint64_t* from, int lane, int n, size_t stride) {
   Pair acc{1.f, 0.f};
   int polls = 0;
-  for (int i = 0; i < n; i += 8) {
-    uint64_t w[8];
-    bool empty;
-    do {
-      empty = false;
+  for (int i = 0; i < n; i += BATCH) {
+    uint64_t w[BATCH];
+    for (;;) {
+      bool empty = false;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        w[j] = __hip_atomic_load(from + (size_t)min(i + j, n - 1) * stride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      for (int j = 0; j < BATCH; ++j)
+        w[j] = __hip_atomic_load(from + (size_t)min(i + j, n - 1) * stride + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) empty |= (unsigned)w[j] == 0xffffffffu;
-      if (__any(empty)) {
-        if (++polls > (1 << 19)) return Pair{-0.f, __int_as_float(0x7fc00000)};
-        __builtin_amdgcn_s_sleep(1);
-      }
-    } while (__any(empty));
+      for (int j = 0; j < BATCH; ++j) empty |= (unsigned)w[j] == 0xffffffffu;
+      if (!__any(empty)) break;
+      if (++polls > (1 << 19)) return Pair{-0.f, __int_as_float(0x7fc00000)};
+      __builtin_amdgcn_s_sleep(1);
+    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < BATCH; ++j)
       if (i + j < n) acc = then(acc, unpack(w[j]));
   }
   return acc;
 }
 
-// The state before segment s of a column (lane = channel), from the pairs published so far; own: the
-// segment's pair, which has been published; the last segment of a group publishes the group's.
-__device__ float state_before(const Tiles& t, int s, int column, int lane, const Pair& own) {
-  const size_t stride = (size_t)t.columns * kCols, at = (size_t)column * kCols + lane;
-  const int g = s / t.group, first = g * t.group;
-  const Pair here = fold_published(t.pairs + (size_t)first * stride + at, s - first, stride);
-  if (s == first + t.group - 1) publish(t.groups + (size_t)g * stride + at, then(here, own));
-  const Pair earlier = fold_published(t.groups + at, g, stride);
-  return through(earlier.q, here);  // segment 0's pair holds the state before it and drops what it is given
+// Pairs of a channel, a part a thread.
+typedef Pair Parts[kParts][kCols];
+__device__ __forceinline__ Pair fold_parts(const Parts& parts, int ch) {
+  Pair all = parts[0][ch];
+#pragma unroll
+  for (int i = 1; i < kParts; ++i) all = then(all, parts[i][ch]);
+  return all;
 }
 
-__global__ __launch_bounds__(kThreads) void scan_clear_kernel(Tiles t, size_t words) {
-  if (blockIdx.x == 0 && threadIdx.x == 0) *t.counter = 0;
-  for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < words; i += (size_t)gridDim.x * kThreads)
-    t.pairs[i] = kEmpty;
-}
-
-// This workgroup's tile: by the counter where workgroups wait for one another.
-__device__ __forceinline__ unsigned next_tile(const Tiles& t, unsigned* shared) {
-  if (t.segments == 1) return blockIdx.x;
-  if (threadIdx.x == 0) *shared = __hip_atomic_fetch_add(t.counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// The state before segment s > 0 of a column, for channel ch: the threads that share the channel (part 0 ..
+// kParts - 1) fold a part of the pairs each.  own: the segment's pair, which part 0 has published; the
+// last segment of a group publishes the group's.  All threads take part.
+__device__ __forceinline__ float state_before(const Tiles& t, int s, int column, int part, int half, int lane,
+                                              const Parts& own, Parts& parts) {
+  const size_t stride = (size_t)t.columns * kCols, at = (size_t)column * kCols + 64 * half;
+  const int ch = 64 * half + lane, g = s / kGroup, first = g * kGroup, inside = s - first;
+  Pair here{1.f, 0.f};
+  if (inside > 0) {
+    constexpr int share = kGroup / kParts;
+    const int from = part * share;
+    parts[part][ch] =
+        fold_published<share>(t.pairs + (size_t)(first + from) * stride + at, lane, min(share, inside - from), stride);
+    __syncthreads();
+    here = fold_parts(parts, ch);
+  }
+  if (inside == kGroup - 1 && part == 0) publish(t.groups + (size_t)g * stride + at + lane, then(here, fold_parts(own, ch)));
+  if (g == 0) return here.q;  // segment 0's pair holds the state before it and drops what it is given
+  const int share = (g + kParts - 1) / kParts, from = part * share;
+  if (inside > 0) __syncthreads();
+  parts[part][ch] = fold_published<4>(t.groups + (size_t)from * stride + at, lane, min(share, g - from), stride);
   __syncthreads();
-  return *shared;
+  return through(fold_parts(parts, ch).q, here);
+}
+
+__global__ __launch_bounds__(kStepThreads) void scan_clear_kernel(Tiles t, size_t words) {
+  if (blockIdx.x == 0 && threadIdx.x < kCounters) t.counters[threadIdx.x * kCounterStride] = 0;
+  // words come 128 at a time
+  for (size_t i = ((size_t)blockIdx.x * kStepThreads + threadIdx.x) * 2; i < words; i += (size_t)gridDim.x * kStepThreads * 2)
+    *reinterpret_cast<u32x4*>(t.pairs + i) = u32x4{~0u, ~0u, ~0u, ~0u};
+}
+
+// A thread's run of tokens, from the stored inputs: folded to its pairs, and walked from the state before
+// it.  Folding tells whether a gate is 0 (or the product too small to tell): then it is done again with
+// that in mind.  The gates are formed each time: keeping them would take 64 registers, and the registers decide how
+// many loads a CU has under way.
+template <bool RESETS, bool COMPLEMENT, typename T, int RUN>
+__device__ __forceinline__ bool fold_run(Raw8<T> (&g_raw)[RUN], Raw8<T> (&x_raw)[RUN], Pair (&out)[8]) {
+  constexpr int PER = Raw8<T>::kPer;
+  bool zero = false;
+#pragma unroll
+  for (int i = 0; i < Raw8<T>::kWords; ++i) {
+    in_turn(g_raw, i, i ? out[i * PER - 1].q : 0.f);
+    in_turn(x_raw, i, i ? out[i * PER - 1].q : 0.f);
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      Pair r{1.f, 0.f};
+#pragma unroll
+      for (int t = 0; t < RUN; ++t) {
+        const float g = g_raw[t].get(i, e), x = x_raw[t].get(i, e), a = gate<T>(g);
+        r.q = advance<RESETS, COMPLEMENT, true>(a, g, r.q, x);
+        r.P = t == 0 && !RESETS ? a : gates_product<RESETS>(r.P, a);
+      }
+      zero |= r.P == 0.f;
+      out[i * PER + e] = r;
+    }
+  }
+  return zero;
+}
+// From the states before the run to the stored states, in the place of the inputs.
+template <bool RESETS, bool COMPLEMENT, typename T, int RUN>
+__device__ __forceinline__ void walk_run(Raw8<T> (&g_raw)[RUN], Raw8<T> (&x_raw)[RUN], const Pair* starts) {
+  constexpr int PER = Raw8<T>::kPer;
+  float done = 0.f;
+#pragma unroll
+  for (int i = 0; i < Raw8<T>::kWords; ++i) {
+    in_turn(g_raw, i, done);
+    in_turn(x_raw, i, done);
+    float h[RUN][PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      float state = starts[i * PER + e].P;
+#pragma unroll
+      for (int t = 0; t < RUN; ++t) {
+        const float g = g_raw[t].get(i, e), x = x_raw[t].get(i, e), a = gate<T>(g);
+        h[t][e] = state = advance<RESETS, COMPLEMENT, sizeof(T) == 4>(a, g, state, x);
+      }
+      done = state;
+    }
+#pragma unroll
+    for (int t = 0; t < RUN; ++t) x_raw[t].set(i, h[t]);
+  }
+}
+
+// This workgroup's tile: its place in the order of the recurrence and its column.
+struct Place {
+  int order, column;
+};
+__device__ __forceinline__ Place next_tile(const Tiles& t, unsigned* shared) {
+  if (t.segments == 1) return Place{0, (int)blockIdx.x};
+  const unsigned k = (blockIdx.x % (unsigned)t.columns) % kCounters;
+  const unsigned share = ((unsigned)t.columns - k + kCounters - 1) / kCounters;  // the counter's columns
+  if (threadIdx.x == 0)
+    *shared = __hip_atomic_fetch_add(t.counters + k * kCounterStride, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  const unsigned i = __builtin_amdgcn_readfirstlane(*shared), order = i / share;
+  return Place{(int)order, (int)(k + kCounters * (i - order * share))};
 }
 
 template <typename T, bool COMPLEMENT>
-__global__ __launch_bounds__(kThreads) void scan_tile_kernel(ccq_scan_params p, Tiles tiles) {
+__global__ __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : COMPLEMENT ? 4 : 6) void scan_tile_kernel(ccq_scan_params p, Tiles tiles) {
+  constexpr int RUN = Run<T, false>::n, TILE = Run<T, false>::tile;
   __shared__ unsigned ticket;
-  __shared__ __align__(16) Pair runs[kWaves][kRuns][kCols];   // every run's pair
-  __shared__ __align__(16) float starts[kWaves][kRuns][kCols];  // the state before every run
-  __shared__ Pair wave_pair[kWaves][kCols];
-  __shared__ float tile_start[kCols];
-  const unsigned tile = next_tile(tiles, &ticket);
-  const int s = (int)(tile / (unsigned)tiles.columns), column = (int)(tile - (unsigned)s * tiles.columns);
+  __shared__ __align__(16) Pair runs[kRuns][kCols];  // every run's pair, and then the state before it
+  __shared__ Parts own, parts;
+  const Place place = next_tile(tiles, &ticket);
+  const int s = place.order, column = place.column;
   const int b = column / tiles.per_row, c_tile = (column - b * tiles.per_row) * kCols;
   const int n = sequence_length(p.lengths, b, p.T);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, oct = lane & 7, run = lane >> 3;
-  const int t_wave = s * kTile + wave * kRun * kRuns, t0 = t_wave + run * kRun, c0 = c_tile + 8 * oct;
+  // where tokens are held: run and eight channels
+  const int run = threadIdx.x / kOct, oct = threadIdx.x % kOct;
+  const int t0 = s * TILE + run * RUN, c0 = c_tile + 8 * oct;
+  // where pairs are joined: part and channel
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int part = wave / (kCols / 64), half = wave % (kCols / 64), ch = 64 * half + lane, c = c_tile + ch;
 
-  float a[kRun][8], u[kRun][8];
-  {
-    const T* g = static_cast<const T*>(p.log_alpha) + b * p.la_stride_b + c0;
-    const T* x = static_cast<const T*>(p.x) + b * p.x_stride_b + c0;
-#pragma unroll
-    for (int r = 0; r < kRun; ++r) {
-      if (t0 + r < n && c0 < p.D) {
-        load8(g + (int64_t)(t0 + r) * p.la_stride_t, a[r]);
-        load8(x + (int64_t)(t0 + r) * p.x_stride_t, u[r]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a[r][e] = u[r][e] = 0.f;  // the state stays as it is
-      }
-    }
+  Raw8<T> g_raw[RUN], x_raw[RUN];
+  load_run(g_raw, p.log_alpha, p.la_stride_b, p.la_stride_t, b, t0, c0, p.T, p.D);
+  load_run(x_raw, p.x, p.x_stride_b, p.x_stride_t, b, t0, c0, p.T, p.D);
+  if ((s + 1) * TILE > n) {
+    clear_from(g_raw, n - t0);
+    clear_from(x_raw, n - t0);
   }
   Pair mine[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) mine[e] = Pair{1.f, 0.f};
-#pragma unroll
-  for (int r = 0; r < kRun; ++r) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float g = a[r][e], alpha = gate(g);
-      if constexpr (COMPLEMENT) u[r][e] *= one_minus(g, alpha);
-      a[r][e] = alpha;
-      mine[e].q = step(alpha, mine[e].q, u[r][e]);
-      mine[e].P = gates_product(mine[e].P, alpha);
-    }
-  }
+  const bool resets = __any(fold_run<false, COMPLEMENT>(g_raw, x_raw, mine));
+  if (resets) fold_run<true, COMPLEMENT>(g_raw, x_raw, mine);
 #pragma unroll
   for (int e = 0; e < 8; e += 2)
-    *reinterpret_cast<f32x4*>(&runs[wave][run][8 * oct + e]) = f32x4{mine[e].P, mine[e].q, mine[e + 1].P, mine[e + 1].q};
+    *reinterpret_cast<f32x4*>(&runs[run][8 * oct + e]) = f32x4{mine[e].P, mine[e].q, mine[e + 1].P, mine[e + 1].q};
   __syncthreads();
-  // a lane takes a channel: the pairs in front of each of its wave's runs
-  Pair before[kRuns], sum{1.f, 0.f};
+  Pair sum{1.f, 0.f};
 #pragma unroll
-  for (int r = 0; r < kRuns; ++r) {
-    before[r] = sum;
-    sum = then(sum, runs[wave][r][lane]);
+  for (int r = 0; r < kPartRuns; ++r) sum = then(sum, runs[part * kPartRuns + r][ch]);
+  float start = 0.f;
+  if (s == 0) {
+    start = p.h0 && c < p.D ? p.h0[(size_t)b * p.D + c] : 0.f;
+    if (part == 0) sum = Pair{-0.f, through(start, sum)};  // holds the state before it
   }
-  wave_pair[wave][lane] = sum;
+  own[part][ch] = sum;
   __syncthreads();
-  const int c = c_tile + lane;
-  if (wave == 0) {
-    Pair all = wave_pair[0][lane];
+  if (part == 0 && tiles.segments > 1)
+    publish(tiles.pairs + ((size_t)s * tiles.columns + column) * kCols + ch, fold_parts(own, ch));
+  if (s > 0) start = state_before(tiles, s, column, part, half, lane, own, parts);
+  float h = start;
+  for (int i = 0; i < part; ++i) h = through(h, own[i][ch]);
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) all = then(all, wave_pair[w][lane]);
-    float start = 0.f;
-    if (s == 0) {
-      start = p.h0 && c < p.D ? p.h0[(size_t)b * p.D + c] : 0.f;
-      all = Pair{-0.f, through(start, all)};
-    }
-    if (tiles.segments > 1) {
-      publish(tiles.pairs + ((size_t)s * tiles.columns + column) * kCols + lane, all);
-      if (s > 0) start = state_before(tiles, s, column, lane, all);
-    }
-    tile_start[lane] = start;
-    if (p.h_out && s == tiles.segments - 1 && c < p.D) p.h_out[(size_t)b * p.D + c] = through(start, all);
-  }
-  __syncthreads();
-  float h = tile_start[lane];
-  for (int w = 0; w < wave; ++w) h = through(h, wave_pair[w][lane]);
-#pragma unroll
-  for (int r = 0; r < kRuns; ++r) {
-    const float start = through(h, before[r]);
-    starts[wave][r][lane] = start;
-    const int t = t_wave + r * kRun;
+  for (int r = 0; r < kPartRuns; ++r) {
+    const Pair pair = runs[part * kPartRuns + r][ch];
+    runs[part * kPartRuns + r][ch].P = h;
+    const int t = s * TILE + (part * kPartRuns + r) * RUN;
     if (p.chunk_carry && t % kChunk == 0 && t < n && c < p.D)
-      p.chunk_carry[((size_t)b * ((p.T + kChunk - 1) / kChunk) + t / kChunk) * p.D + c] = start;
+      p.chunk_carry[((size_t)b * ((p.T + kChunk - 1) / kChunk) + t / kChunk) * p.D + c] = h;
+    h = through(h, pair);
   }
+  if (p.h_out && s == tiles.segments - 1 && part == kParts - 1 && c < p.D) p.h_out[(size_t)b * p.D + c] = h;
   __syncthreads();
   if (p.y == nullptr || c0 >= p.D) return;
-  float state[8];
-  load8(&starts[wave][run][8 * oct], state);
+  if (resets) walk_run<true, COMPLEMENT>(g_raw, x_raw, &runs[run][8 * oct]);
+  else walk_run<false, COMPLEMENT>(g_raw, x_raw, &runs[run][8 * oct]);
   T* y = static_cast<T*>(p.y) + ((size_t)b * p.T + t0) * p.D + c0;
 #pragma unroll
-  for (int r = 0; r < kRun; ++r) {
+  for (int r = 0; r < RUN; ++r)
+    if (t0 + r < n) x_raw[r].store(y + (size_t)r * p.D);
+}
+
+// A thread's run for the gradient: the state's pair and the adjoint's q; then both walked.
+template <bool RESETS, bool COMPLEMENT, typename T, int RUN>
+__device__ __forceinline__ bool fold_run_back(Raw8<T> (&g_raw)[RUN], Raw8<T> (&x_raw)[RUN],
+                                              Raw8<T> (&d_raw)[RUN], Pair (&out)[8], float (&q)[8]) {
+  constexpr int PER = Raw8<T>::kPer;
+  bool zero = false;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) state[e] = step(a[r][e], state[e], u[r][e]);
-    if (t0 + r < n) store8(y + (size_t)r * p.D, state);
+  for (int i = 0; i < Raw8<T>::kWords; ++i) {
+    in_turn(g_raw, i, i ? q[i * PER - 1] : 0.f);
+    in_turn(x_raw, i, i ? q[i * PER - 1] : 0.f);
+    in_turn(d_raw, i, i ? q[i * PER - 1] : 0.f);
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      float a[RUN], adj = 0.f;
+      Pair r{1.f, 0.f};
+#pragma unroll
+      for (int t = 0; t < RUN; ++t) {
+        const float g = g_raw[t].get(i, e), x = x_raw[t].get(i, e);
+        a[t] = gate<T>(g);
+        r.q = advance<RESETS, COMPLEMENT, sizeof(T) == 4>(a[t], g, r.q, x);
+        r.P = t == 0 && !RESETS ? a[t] : gates_product<RESETS>(r.P, a[t]);
+      }
+#pragma unroll
+      for (int t = RUN - 1; t >= 0; --t) adj = gated<RESETS>(a[t], adj + d_raw[t].get(i, e));
+      zero |= r.P == 0.f;
+      out[i * PER + e] = r;
+      q[i * PER + e] = adj;
+    }
+  }
+  return zero;
+}
+// (1 - alpha) full for a bf16 result, from alpha full: their difference, or for gates next to 1, where it
+// would be all rounding, -(g + g^2 / 2) full (each within 2^-16 of the result).
+__device__ __forceinline__ float less(float g, float full, float scaled) {
+  return fabsf(g) < 1.f / 256.f ? -g * fmaf(0.5f, g, 1.f) * full : full - scaled;
+}
+// From the states before the run and the adjoints behind it (P, q of `ends`) to the stored gradients: the
+// input's in the place of x_raw, log_alpha's in the place of g_raw.
+template <bool RESETS, bool COMPLEMENT, typename T, int RUN>
+__device__ __forceinline__ void walk_run_back(Raw8<T> (&g_raw)[RUN], Raw8<T> (&x_raw)[RUN],
+                                              Raw8<T> (&d_raw)[RUN], const Pair* ends) {
+  constexpr int PER = Raw8<T>::kPer;
+  float done = 0.f;
+#pragma unroll
+  for (int i = 0; i < Raw8<T>::kWords; ++i) {
+    in_turn(g_raw, i, done);
+    in_turn(x_raw, i, done);
+    in_turn(d_raw, i, done);
+    float ox[RUN][PER], og[RUN][PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      float h = ends[i * PER + e].P, adj = ends[i * PER + e].q;
+      float a[RUN], s[RUN], of[RUN];  // of: what log_alpha's gradient takes: the state before, less the input
+#pragma unroll
+      for (int t = 0; t < RUN; ++t) {
+        const float g = g_raw[t].get(i, e), x = x_raw[t].get(i, e);
+        a[t] = gate<T>(g);
+        of[t] = COMPLEMENT ? h - x : h;
+        if constexpr (COMPLEMENT && sizeof(T) == 4) {
+          s[t] = one_minus(g, a[t]);
+          h = step<RESETS>(a[t], h, s[t] * x);
+        } else {
+          h = advance<RESETS, COMPLEMENT, false>(a[t], g, h, x);
+        }
+      }
+#pragma unroll
+      for (int t = RUN - 1; t >= 0; --t) {
+        const float full = adj + d_raw[t].get(i, e);
+        adj = gated<RESETS>(a[t], full);
+        if constexpr (!COMPLEMENT) ox[t][e] = full;
+        else if constexpr (sizeof(T) == 4) ox[t][e] = s[t] * full;
+        else ox[t][e] = less(g_raw[t].get(i, e), full, a[t] * full);
+        og[t][e] = RESETS ? gated<RESETS>(a[t], full * of[t]) : adj * of[t];
+      }
+      done = adj;
+    }
+#pragma unroll
+    for (int t = 0; t < RUN; ++t) {
+      x_raw[t].set(i, ox[t]);
+      g_raw[t].set(i, og[t]);
+    }
   }
 }
 
@@ -298,160 +530,105 @@ __global__ __launch_bounds__(kThreads) void scan_tile_kernel(ccq_scan_params p, 
 // alpha (d + dy) in front of it, so a run acts on it as d -> P d + q with the run's own product of gates.
 // The states are walked forward again, from the state kept before the tile.
 template <typename T, bool COMPLEMENT>
-__global__ __launch_bounds__(kThreads) void scan_backward_tile_kernel(ccq_scan_bwd_params p, const float* carry,
-                                                                      Tiles tiles) {
+__global__ __launch_bounds__(kThreads, 4) void scan_backward_tile_kernel(ccq_scan_bwd_params p, const float* carry,
+                                                                         Tiles tiles) {
+  constexpr int RUN = Run<T, true>::n, TILE = Run<T, true>::tile;
   __shared__ unsigned ticket;
-  __shared__ __align__(16) Pair runs[kWaves][kRuns][kCols];
-  __shared__ __align__(16) float back[kWaves][kRuns][kCols];  // q of every run for the adjoint
-  __shared__ Pair wave_pair[kWaves][kCols];
-  __shared__ float wave_back[kWaves][kCols];
-  __shared__ float tile_end[kCols];  // adjoint behind the tile
-  const unsigned tile = next_tile(tiles, &ticket);
-  const int order = (int)(tile / (unsigned)tiles.columns), column = (int)(tile - (unsigned)order * tiles.columns);
-  const int s = tiles.segments - 1 - order;
+  __shared__ __align__(16) Pair runs[kRuns][kCols];   // every run's pair; then state before it, adjoint behind it
+  __shared__ __align__(16) float back[kRuns][kCols];  // q of every run for the adjoint
+  __shared__ Parts ahead, own, parts;                 // own: for the adjoint, the tile's last part first
+  const Place place = next_tile(tiles, &ticket);
+  const int order = place.order, column = place.column, s = tiles.segments - 1 - order;
   const int b = column / tiles.per_row, c_tile = (column - b * tiles.per_row) * kCols;
   const int n = sequence_length(p.lengths, b, p.T);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, oct = lane & 7, run = lane >> 3;
-  const int t0 = s * kTile + wave * kRun * kRuns + run * kRun, c0 = c_tile + 8 * oct, c = c_tile + lane;
+  const int run = threadIdx.x / kOct, oct = threadIdx.x % kOct;
+  const int t0 = s * TILE + run * RUN, c0 = c_tile + 8 * oct;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int part = wave / (kCols / 64), half = wave % (kCols / 64), ch = 64 * half + lane, c = c_tile + ch;
 
-  float a[kRun][8], u[kRun][8], dy[kRun][8], sc[COMPLEMENT ? kRun : 1][8];
+  Raw8<T> g_raw[RUN], x_raw[RUN], d_raw[RUN];
+  load_run(g_raw, p.log_alpha, p.la_stride_b, p.la_stride_t, b, t0, c0, p.T, p.D);
+  load_run(x_raw, p.x, p.x_stride_b, p.x_stride_t, b, t0, c0, p.T, p.D);
+  load_run(d_raw, p.dy, p.dy_stride_b, p.dy_stride_t, b, t0, c0, p.T, p.D);
+  float h = 0.f;  // state before the tile
+  if (s * TILE < n && c < p.D)
+    h = carry[((size_t)b * ((p.T + kChunk - 1) / kChunk) + s * (TILE / kChunk)) * p.D + c];
+  if ((s + 1) * TILE > n) {
+    clear_from(g_raw, n - t0);
+    clear_from(x_raw, n - t0);
+    clear_from(d_raw, n - t0);
+  }
+  bool resets;
   {
-    const T* g = static_cast<const T*>(p.log_alpha) + b * p.la_stride_b + c0;
-    const T* x = static_cast<const T*>(p.x) + b * p.x_stride_b + c0;
-    const T* d = static_cast<const T*>(p.dy) + b * p.dy_stride_b + c0;
+    Pair mine[8];
+    float q[8];
+    resets = __any(fold_run_back<false, COMPLEMENT>(g_raw, x_raw, d_raw, mine, q));
+    if (resets) fold_run_back<true, COMPLEMENT>(g_raw, x_raw, d_raw, mine, q);
 #pragma unroll
-    for (int r = 0; r < kRun; ++r) {
-      if (t0 + r < n && c0 < p.D) {
-        load8(g + (int64_t)(t0 + r) * p.la_stride_t, a[r]);
-        load8(x + (int64_t)(t0 + r) * p.x_stride_t, u[r]);
-        load8(d + (int64_t)(t0 + r) * p.dy_stride_t, dy[r]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a[r][e] = u[r][e] = dy[r][e] = 0.f;
-      }
-    }
-  }
-  float h_tile = 0.f;  // state before the tile
-  if (s * kTile < n && c < p.D)
-    h_tile = carry[((size_t)b * ((p.T + kChunk - 1) / kChunk) + s * (kTile / kChunk)) * p.D + c];
-
-  Pair mine[8];
-  float q[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    mine[e] = Pair{1.f, 0.f};
-    q[e] = 0.f;
-  }
-#pragma unroll
-  for (int r = 0; r < kRun; ++r) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float g = a[r][e], alpha = gate(g);
-      a[r][e] = alpha;
-      float in = u[r][e];
-      if constexpr (COMPLEMENT) {
-        sc[r][e] = one_minus(g, alpha);
-        in *= sc[r][e];
-      }
-      mine[e].q = step(alpha, mine[e].q, in);
-      mine[e].P = gates_product(mine[e].P, alpha);
-    }
-  }
-#pragma unroll
-  for (int r = kRun - 1; r >= 0; --r) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) q[e] = gated(a[r][e], q[e] + dy[r][e]);
-  }
-#pragma unroll
-  for (int e = 0; e < 8; e += 2)
-    *reinterpret_cast<f32x4*>(&runs[wave][run][8 * oct + e]) = f32x4{mine[e].P, mine[e].q, mine[e + 1].P, mine[e + 1].q};
-  store8(&back[wave][run][8 * oct], q);
-  __syncthreads();
-  // a lane takes a channel: the pairs in front of each of its wave's runs, and behind each for the adjoint
-  Pair before[kRuns], behind[kRuns], sum{1.f, 0.f}, rsum{1.f, 0.f};
-#pragma unroll
-  for (int r = 0; r < kRuns; ++r) {
-    before[r] = sum;
-    sum = then(sum, runs[wave][r][lane]);
-  }
-#pragma unroll
-  for (int r = kRuns - 1; r >= 0; --r) {
-    behind[r] = rsum;
-    rsum = then(rsum, Pair{runs[wave][r][lane].P, back[wave][r][lane]});
-  }
-  wave_pair[wave][lane] = sum;
-  wave_back[wave][lane] = rsum.q;
-  __syncthreads();
-  if (wave == 0) {
-    Pair all{1.f, 0.f};
-#pragma unroll
-    for (int w = kWaves - 1; w >= 0; --w) all = then(all, Pair{wave_pair[w][lane].P, wave_back[w][lane]});
-    float end = 0.f;
-    if (order == 0) {
-      end = p.dh_out && c < p.D ? p.dh_out[(size_t)b * p.D + c] : 0.f;
-      all = Pair{-0.f, through(end, all)};
-    }
-    if (tiles.segments > 1) {
-      publish(tiles.pairs + ((size_t)order * tiles.columns + column) * kCols + lane, all);
-      if (order > 0) end = state_before(tiles, order, column, lane, all);
-    }
-    tile_end[lane] = end;
-    if (p.dh0 && s == 0 && c < p.D) p.dh0[(size_t)b * p.D + c] = through(end, all);
+    for (int e = 0; e < 8; e += 2)
+      *reinterpret_cast<f32x4*>(&runs[run][8 * oct + e]) = f32x4{mine[e].P, mine[e].q, mine[e + 1].P, mine[e + 1].q};
+    store8(&back[run][8 * oct], q);
   }
   __syncthreads();
-  float h = h_tile, d = tile_end[lane];
-  for (int w = 0; w < wave; ++w) h = through(h, wave_pair[w][lane]);
-  for (int w = kWaves - 1; w > wave; --w) d = through(d, Pair{wave_pair[w][lane].P, wave_back[w][lane]});
-  // every run's state in front of it and adjoint behind it, where its pair stood
+  Pair sum{1.f, 0.f}, rsum{1.f, 0.f};
 #pragma unroll
-  for (int r = 0; r < kRuns; ++r) runs[wave][r][lane] = Pair{through(h, before[r]), through(d, behind[r])};
+  for (int r = 0; r < kPartRuns; ++r) sum = then(sum, runs[part * kPartRuns + r][ch]);
+#pragma unroll
+  for (int r = kPartRuns - 1; r >= 0; --r)
+    rsum = then(rsum, Pair{runs[part * kPartRuns + r][ch].P, back[part * kPartRuns + r][ch]});
+  float end = 0.f;
+  if (order == 0) {
+    end = p.dh_out && c < p.D ? p.dh_out[(size_t)b * p.D + c] : 0.f;
+    if (part == kParts - 1) rsum = Pair{-0.f, through(end, rsum)};
+  }
+  ahead[part][ch] = sum;
+  own[kParts - 1 - part][ch] = rsum;
+  __syncthreads();
+  if (part == 0 && tiles.segments > 1)
+    publish(tiles.pairs + ((size_t)order * tiles.columns + column) * kCols + ch, fold_parts(own, ch));
+  if (order > 0) end = state_before(tiles, order, column, part, half, lane, own, parts);
+  float d = end;
+  for (int i = 0; i < kParts - 1 - part; ++i) d = through(d, own[i][ch]);
+  for (int i = 0; i < part; ++i) h = through(h, ahead[i][ch]);
+#pragma unroll
+  for (int r = kPartRuns - 1; r >= 0; --r) {
+    float& q = back[part * kPartRuns + r][ch];
+    const float next = through(d, Pair{runs[part * kPartRuns + r][ch].P, q});
+    q = d;
+    d = next;
+  }
+  if (p.dh0 && s == 0 && part == 0 && c < p.D) p.dh0[(size_t)b * p.D + c] = d;
+#pragma unroll
+  for (int r = 0; r < kPartRuns; ++r) {
+    const Pair pair = runs[part * kPartRuns + r][ch];
+    runs[part * kPartRuns + r][ch] = Pair{h, back[part * kPartRuns + r][ch]};
+    h = through(h, pair);
+  }
   __syncthreads();
   if (c0 >= p.D) return;
-  float state[8], adj[8];
-#pragma unroll
-  for (int e = 0; e < 8; e += 2) {
-    const f32x4 v = *reinterpret_cast<const f32x4*>(&runs[wave][run][8 * oct + e]);
-    state[e] = v[0];
-    adj[e] = v[1];
-    state[e + 1] = v[2];
-    adj[e + 1] = v[3];
-  }
-  // u becomes what log_alpha's gradient takes from each token: the state before it, less the input
-#pragma unroll
-  for (int r = 0; r < kRun; ++r) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float x = u[r][e];
-      u[r][e] = COMPLEMENT ? state[e] - x : state[e];
-      state[e] = step(a[r][e], state[e], COMPLEMENT ? sc[r][e] * x : x);
-    }
+  const Pair* ends = &runs[run][8 * oct];
+  if (resets) walk_run_back<true, COMPLEMENT>(g_raw, x_raw, d_raw, ends);
+  else walk_run_back<false, COMPLEMENT>(g_raw, x_raw, d_raw, ends);
+  if ((s + 1) * TILE > n) {
+    clear_from(g_raw, n - t0);
+    clear_from(x_raw, n - t0);
   }
   const size_t at = ((size_t)b * p.T + t0) * p.D + c0;
-  T* dx = static_cast<T*>(p.dx) + at;
-  T* dg = static_cast<T*>(p.dlog_alpha) + at;
+  T *dx = static_cast<T*>(p.dx) + at, *dg = static_cast<T*>(p.dlog_alpha) + at;
 #pragma unroll
-  for (int r = kRun - 1; r >= 0; --r) {
-    const bool live = t0 + r < n;
-    float ox[8], og[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float full = adj[e] + dy[r][e];
-      ox[e] = live ? (COMPLEMENT ? sc[r][e] * full : full) : 0.f;
-      adj[e] = gated(a[r][e], full);
-      og[e] = live ? gated(a[r][e], full * u[r][e]) : 0.f;
-    }
+  for (int r = 0; r < RUN; ++r) {
     if (t0 + r < p.T) {
-      store8(dx + (size_t)r * p.D, ox);
-      store8(dg + (size_t)r * p.D, og);
+      x_raw[r].store(dx + (size_t)r * p.D);
+      g_raw[r].store(dg + (size_t)r * p.D);
     }
   }
 }
 
 // A few tokens: eight channels a thread, one token behind the other.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void scan_step_kernel(ccq_scan_params p) {
+__global__ __launch_bounds__(kStepThreads) void scan_step_kernel(ccq_scan_params p) {
   const int per_row = p.D / 8;
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int64_t i = (int64_t)blockIdx.x * kStepThreads + threadIdx.x;
   if (i >= (int64_t)p.B * per_row) return;
   const int b = (int)(i / per_row), c = 8 * (int)(i - (int64_t)b * per_row);
   const int n = sequence_length(p.lengths, b, p.T);
@@ -467,8 +644,8 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(ccq_scan_params p) 
     load8(x + t * p.x_stride_t, xt);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float alpha = gate(gt[e]);
-      h[e] = step(alpha, h[e], p.complement ? xt[e] * one_minus(gt[e], alpha) : xt[e]);
+      const float alpha = gate<T>(gt[e]);
+      h[e] = step<true>(alpha, h[e], p.complement ? xt[e] * one_minus(gt[e], alpha) : xt[e]);
     }
     store8(y + (int64_t)t * p.D, h);
   }
@@ -477,31 +654,30 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(ccq_scan_params p) 
 
 // ---------------------------------------------------------------- launches
 
-Tiles tiles_of(int B, int T, int D, void* workspace) {
+Tiles tiles_of(int dtype, bool back, int B, int T, int D, void* workspace) {
   Tiles t{};
   t.per_row = (D + kCols - 1) / kCols;
   t.columns = B * t.per_row;
-  t.segments = (T + kTile - 1) / kTile;
-  t.group = group_of(t.segments);
-  t.counter = static_cast<unsigned*>(workspace);
+  t.segments = (T - 1) / tile_tokens(dtype, back) + 1;
+  t.counters = static_cast<unsigned*>(workspace);
   t.pairs = reinterpret_cast<uint64_t*>(static_cast<unsigned char*>(workspace) + kCounterBytes);
   t.groups = t.pairs + (size_t)t.segments * t.columns * kCols;
   return t;
 }
-size_t tile_words(int B, int T, int D) {
-  const size_t segments = (size_t)((T + kTile - 1) / kTile);
+size_t tile_words(int dtype, bool back, int B, int T, int D) {
+  const size_t segments = (size_t)((T - 1) / tile_tokens(dtype, back) + 1);
   if (segments == 1) return 0;
-  return (segments + segments / group_of((int)segments)) * B * ((D + kCols - 1) / kCols) * kCols;
+  return (segments + segments / kGroup) * B * ((D + kCols - 1) / kCols) * kCols;
 }
-size_t tile_bytes(int B, int T, int D) {
-  const size_t words = tile_words(B, T, D);
+size_t tile_bytes(int dtype, bool back, int B, int T, int D) {
+  const size_t words = tile_words(dtype, back, B, T, D);
   return words ? kCounterBytes + words * sizeof(uint64_t) : 0;
 }
 
 hipError_t clear_tiles(const Tiles& t, size_t words, hipStream_t stream) {
   if (words == 0) return hipSuccess;
-  const size_t blocks = (words + kThreads * 4 - 1) / (kThreads * 4);
-  scan_clear_kernel<<<(unsigned)(blocks < 1024 ? blocks : 1024), kThreads, 0, stream>>>(t, words);
+  const size_t blocks = (words + kStepThreads * 4 - 1) / (kStepThreads * 4);
+  scan_clear_kernel<<<(unsigned)(blocks < 1024 ? blocks : 1024), kStepThreads, 0, stream>>>(t, words);
   return hipGetLastError();
 }
 
@@ -509,8 +685,8 @@ hipError_t clear_tiles(const Tiles& t, size_t words, hipStream_t stream) {
 constexpr int kMostSteps = 8;
 
 hipError_t launch_tiles(const ccq_scan_params& p, void* workspace, hipStream_t stream) {
-  const Tiles t = tiles_of(p.B, p.T, p.D, workspace);
-  const hipError_t e = clear_tiles(t, tile_words(p.B, p.T, p.D), stream);
+  const Tiles t = tiles_of(p.dtype, false, p.B, p.T, p.D, workspace);
+  const hipError_t e = clear_tiles(t, tile_words(p.dtype, false, p.B, p.T, p.D), stream);
   if (e != hipSuccess) return e;
   const unsigned grid = (unsigned)((int64_t)t.columns * t.segments);
   if (p.dtype == CCQ_DTYPE_BF16) {
@@ -523,32 +699,42 @@ hipError_t launch_tiles(const ccq_scan_params& p, void* workspace, hipStream_t s
   return hipGetLastError();
 }
 
+// The gradient's tiles and, where the states are formed again, the forward's before them.
+size_t tile_space(const ccq_scan_bwd_params& p) {
+  const size_t back = tile_bytes(p.dtype, true, p.B, p.T, p.D);
+  const size_t ahead = p.chunk_carry ? 0 : tile_bytes(p.dtype, false, p.B, p.T, p.D);
+  return back > ahead ? back : ahead;
+}
 size_t carry_bytes(int B, int T, int D) {
   return ((size_t)B * ((T + kChunk - 1) / kChunk) * D * 4 + 255) / 256 * 256;
 }
 
 }  // namespace
 
-size_t scan_workspace_bytes(const ccq_scan_params& p) { return p.T <= kMostSteps ? 0 : tile_bytes(p.B, p.T, p.D); }
+bool scan_grid_fits(int B, int T, int D) {
+  const int64_t columns = (int64_t)B * ((D + kCols - 1) / kCols), segments = (T - 1) / Run<float, true>::tile + 1;  // the smaller tile
+  return columns * segments <= 0x7fffffff;
+}
+
+size_t scan_workspace_bytes(const ccq_scan_params& p) { return p.T <= kMostSteps ? 0 : tile_bytes(p.dtype, false, p.B, p.T, p.D); }
 
 hipError_t launch_scan(const ccq_scan_params& p, hipStream_t stream) {
   if (p.T > kMostSteps) return launch_tiles(p, p.workspace, stream);
-  const unsigned grid = (unsigned)(((int64_t)p.B * (p.D / 8) + kThreads - 1) / kThreads);
-  if (p.dtype == CCQ_DTYPE_BF16) scan_step_kernel<__bf16><<<grid, kThreads, 0, stream>>>(p);
-  else scan_step_kernel<float><<<grid, kThreads, 0, stream>>>(p);
+  const unsigned grid = (unsigned)(((int64_t)p.B * (p.D / 8) + kStepThreads - 1) / kStepThreads);
+  if (p.dtype == CCQ_DTYPE_BF16) scan_step_kernel<__bf16><<<grid, kStepThreads, 0, stream>>>(p);
+  else scan_step_kernel<float><<<grid, kStepThreads, 0, stream>>>(p);
   return hipGetLastError();
 }
 
 size_t scan_backward_workspace_bytes(const ccq_scan_bwd_params& p) {
-  return tile_bytes(p.B, p.T, p.D) + (p.chunk_carry ? 0 : carry_bytes(p.B, p.T, p.D));
+  return tile_space(p) + (p.chunk_carry ? 0 : carry_bytes(p.B, p.T, p.D));
 }
 
 hipError_t launch_scan_backward(const ccq_scan_bwd_params& p, hipStream_t stream) {
   const float* carry = p.chunk_carry;
-  const size_t tile_space = tile_bytes(p.B, p.T, p.D);
-  if (carry == nullptr) {
+    if (carry == nullptr) {
     // the forward once more, for its kept states alone
-    float* kept = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + tile_space);
+    float* kept = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + tile_space(p));
     ccq_scan_params f{};
     f.dtype = p.dtype;
     f.B = p.B;
@@ -568,8 +754,8 @@ hipError_t launch_scan_backward(const ccq_scan_bwd_params& p, hipStream_t stream
     if (e != hipSuccess) return e;
     carry = kept;
   }
-  const Tiles t = tiles_of(p.B, p.T, p.D, p.workspace);
-  const hipError_t e = clear_tiles(t, tile_words(p.B, p.T, p.D), stream);
+  const Tiles t = tiles_of(p.dtype, true, p.B, p.T, p.D, p.workspace);
+  const hipError_t e = clear_tiles(t, tile_words(p.dtype, true, p.B, p.T, p.D), stream);
   if (e != hipSuccess) return e;
   const unsigned grid = (unsigned)((int64_t)t.columns * t.segments);
   if (p.dtype == CCQ_DTYPE_BF16) {

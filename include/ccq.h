@@ -424,7 +424,8 @@ typedef struct {
  *   h_t = alpha_t h_{t-1} + s_t x_t,  alpha_t = exp(log_alpha_t),  s_t = 1 or 1 - alpha_t,  y_t = h_t.
  * The state is fp32 throughout and a call continues where h0 left off, so T = 1 with h_out == h0
  * is the serving step.  Where alpha_t is 0 the old state is dropped, whatever it holds (an
- * infinity or NaN before it does not pass).  Rows behind a sequence's length are neither read
+ * infinity or NaN before it does not pass); alpha_t is 0 for log_alpha_t below about -87.  (With
+ * the complement scale an infinite input may give NaN instead of itself.)  Rows behind a sequence's length are neither read
  * into a result nor written.  Long sequences are cut along T and the pieces joined in a fixed
  * order: two calls give the same bits.  Returns a ccq_status.
  */
