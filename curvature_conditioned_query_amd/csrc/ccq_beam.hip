@@ -404,10 +404,10 @@ __device__ __forceinline__ void move_columns(unsigned char* base, size_t row, si
   W v[KMAX];
 #pragma unroll
   for (int j = 0; j < KMAX; ++j)
-    if (j < K && par[j] != j) v[j] = *reinterpret_cast<const W*>(base + (size_t)par[j] * row + off);
+    if (j < K && par[j] != j) v[j] = __builtin_nontemporal_load(reinterpret_cast<const W*>(base + (size_t)par[j] * row + off));
 #pragma unroll
   for (int j = 0; j < KMAX; ++j)
-    if (j < K && par[j] != j) *reinterpret_cast<W*>(base + (size_t)j * row + off) = v[j];
+    if (j < K && par[j] != j) __builtin_nontemporal_store(v[j], reinterpret_cast<W*>(base + (size_t)j * row + off));
 }
 
 template <int KMAX>

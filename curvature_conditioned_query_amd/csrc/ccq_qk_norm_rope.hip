@@ -5,10 +5,12 @@
 // Everything is a few operations an element, so both directions are bound by memory: a row is read
 // once and written once.  A row lies on d / 8 lanes, eight entries (16 bytes of bf16) a lane; 256
 // threads hold 256 / (d / 8) tokens, each thread the same eight entries of one token, and walk over
-// that token's heads.  The angles depend on token and entry alone, so a thread forms its eight
-// cosines and sines once, in registers, for all heads it visits.  Consecutive tokens of a workgroup
-// are consecutive rows of the head-major side, consecutive heads are consecutive rows of the
-// projection, so both sides move whole cache lines.
+// that token's heads, queries and then keys, a few rows' loads ahead.  The angles depend on token and
+// entry alone: a workgroup forms each cosine and sine once, in LDS, and a thread takes its eight into
+// registers for all heads it visits (formed by every thread for itself and for queries and keys apart
+// they were about 5 of 56 us of the prefill).  Consecutive tokens of a workgroup are consecutive rows of
+// the head-major side, consecutive heads are consecutive rows of the projection, so both sides move
+// whole cache lines.
 #include "ccq_device.hpp"
 #include "ccq_internal.hpp"
 
@@ -16,31 +18,58 @@ namespace ccq {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kAhead = 8;      // rows a thread loads at a time
+constexpr int kBackAhead = 4;  // and of the gradient, whose rows are three times as wide
 constexpr float kL2Floor = 1e-12f;
 
-// Eight consecutive entries of a row.
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    x[e] = a[e];
-    x[4 + e] = b[e];
+// Rows are read past the caches, being read once.  The gradient, whose rows leave as they came, is also
+// written past them (101 against 108 us at the prefill's size, before the workgroups were halved); the forward, whose rows part by head, is
+// not: its caches gather the rows of a head (53 against 59 us).
+// Eight entries as they are stored, so that several rows' loads are under way at a time.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+  f32x4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
+    b = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p + 4));
   }
-}
-__device__ __forceinline__ void load8(const __bf16* p, float (&x)[8]) {
-  const bf16x8 a = *reinterpret_cast<const bf16x8*>(p);
+  __device__ __forceinline__ void get(float (&x)[8]) const {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = (float)a[e];
+    for (int e = 0; e < 4; ++e) {
+      x[e] = a[e];
+      x[4 + e] = b[e];
+    }
+  }
+};
+template <>
+struct Raw8<__bf16> {
+  bf16x8 a;
+  __device__ __forceinline__ void load(const __bf16* p) { a = __builtin_nontemporal_load(reinterpret_cast<const bf16x8*>(p)); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = (float)a[e];
+  }
+};
+
+// STREAM: past the caches.
+template <bool STREAM, typename V>
+__device__ __forceinline__ void store_vec(V v, V* p) {
+  if constexpr (STREAM) __builtin_nontemporal_store(v, p);
+  else *p = v;
 }
+template <bool STREAM>
 __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  *reinterpret_cast<f32x4*>(p) = f32x4{x[0], x[1], x[2], x[3]};
-  *reinterpret_cast<f32x4*>(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
+  store_vec<STREAM>(f32x4{x[0], x[1], x[2], x[3]}, reinterpret_cast<f32x4*>(p));
+  store_vec<STREAM>(f32x4{x[4], x[5], x[6], x[7]}, reinterpret_cast<f32x4*>(p + 4));
 }
+template <bool STREAM>
 __device__ __forceinline__ void store8(__bf16* p, const float (&x)[8]) {
   bf16x8 a;
 #pragma unroll
   for (int e = 0; e < 8; ++e) a[e] = (__bf16)x[e];
-  *reinterpret_cast<bf16x8*>(p) = a;
+  store_vec<STREAM>(a, reinterpret_cast<bf16x8*>(p));
 }
 
 // The rotation of a thread's eight entries: out_e = x_e c_e + partner_e s_e, s_e carrying the sign.
@@ -51,44 +80,64 @@ struct Turn {
 
 // The angle is formed in 64 bits and in turns, reduced to [-1/2, 1/2] there, so a far position loses
 // nothing; sine and cosine of the remainder are fp32.
-__device__ __forceinline__ void turn_sincos(double position, float inv_freq, float* sn, float* cs) {
+__device__ __forceinline__ float2 turn_sincos(double position, float inv_freq) {
   constexpr double kInvTwoPi = 0.15915494309189533577;
   const double t = position * ((double)inv_freq * kInvTwoPi);
-  const float r = (float)(t - rint(t));
-  sincospif(2.f * r, sn, cs);
+  float2 r;
+  sincospif(2.f * (float)(t - rint(t)), &r.y, &r.x);
+  return r;
 }
 
-__device__ __forceinline__ Turn make_turn(const ccq_qk_params& p, int lane, int row_lane, int64_t position) {
-  Turn u;
-  u.partner = lane;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    u.c[e] = 1.f;
-    u.s[e] = 0.f;
-  }
-  const int i0 = 8 * row_lane, half = p.rot / 2;
-  if (i0 < p.rot) {
-    const double pos = (double)position;
-    if (p.interleaved) {
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        turn_sincos(pos, p.inv_freq[(i0 + e) >> 1], &u.s[e + 1], &u.c[e]);
-        u.c[e + 1] = u.c[e];
-        u.s[e] = -u.s[e + 1];
-      }
-    } else {
-      const bool low = i0 < half;
-      u.partner = low ? lane + half / 8 : lane - half / 8;
-      const float* f = p.inv_freq + (low ? i0 : i0 - half);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        turn_sincos(pos, f[e], &u.s[e], &u.c[e]);
-        if (low) u.s[e] = -u.s[e];
+// Cosine (x) and sine (y) of every pair of the workgroup's tokens.
+template <int D>
+struct Angles {
+  static constexpr int TOK = kThreads / (D / 8), PAIRS = D / 2;
+  float2 a[TOK][PAIRS];
+
+  // All threads; tokens from `first` on, those past the last as the last.
+  __device__ __forceinline__ void form(const ccq_qk_params& p, int first, int tokens) {
+    const int pairs = p.rot / 2;
+    for (int i = threadIdx.x; i < TOK * PAIRS; i += kThreads) {
+      const int tok = i / PAIRS, k = i % PAIRS;
+      if (k < pairs) {
+        const int bt = min(first + tok, tokens - 1);
+        const int64_t position = p.positions ? p.positions[bt] : p.position0 + bt % p.T;
+        a[tok][k] = turn_sincos((double)position, p.inv_freq[k]);
       }
     }
   }
-  return u;
-}
+  __device__ __forceinline__ Turn take(const ccq_qk_params& p, int tok, int row_lane, int lane) const {
+    Turn u;
+    u.partner = lane;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      u.c[e] = 1.f;
+      u.s[e] = 0.f;
+    }
+    const int i0 = 8 * row_lane, half = p.rot / 2;
+    if (i0 < p.rot) {
+      if (p.interleaved) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float2 v = a[tok][(i0 + e) >> 1];
+          u.c[e] = u.c[e + 1] = v.x;
+          u.s[e] = -v.y;
+          u.s[e + 1] = v.y;
+        }
+      } else {
+        const bool low = i0 < half;
+        u.partner = low ? lane + half / 8 : lane - half / 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 v = a[tok][(low ? i0 : i0 - half) + e];
+          u.c[e] = v.x;
+          u.s[e] = low ? -v.y : v.y;
+        }
+      }
+    }
+    return u;
+  }
+};
 
 // x turned by u, or back (the transpose, which is the inverse).  Every lane of a row takes part.
 template <bool BACK>
@@ -113,202 +162,264 @@ __device__ __forceinline__ float row_scale(float sumsq, int kind, float inv_d, f
   return 1.f;
 }
 
-// The heads of one workgroup: `per` heads of the queries, or of the keys behind them.
-struct HeadRange {
-  int begin, end;
-  bool keys;
+// One side of a call: queries or keys.
+struct Side {
+  const void* in;
+  int64_t sb, st, sh;
+  const float* w;
+  void* out;
+  int norm, copies, heads_out;
 };
-__device__ __forceinline__ HeadRange head_range(const ccq_qk_params& p, int part, int per) {
-  const int parts_q = (p.H_q + per - 1) / per;
-  HeadRange h;
-  h.keys = part >= parts_q;
-  h.begin = (h.keys ? part - parts_q : part) * per;
-  h.end = min(h.begin + per, h.keys ? p.H_k : p.H_q);
-  return h;
+__device__ __forceinline__ Side side_of(const ccq_qk_params& p, bool keys) {
+  Side s;
+  s.in = keys ? p.k : p.q;
+  s.sb = keys ? p.k_stride_b : p.q_stride_b;
+  s.st = keys ? p.k_stride_t : p.q_stride_t;
+  s.sh = keys ? p.k_stride_h : p.q_stride_h;
+  s.w = keys ? p.k_weight : p.q_weight;
+  s.out = keys ? p.k_out : p.q_out;
+  s.norm = keys ? p.k_norm : p.q_norm;
+  s.copies = keys && p.expand_keys ? p.H_q / p.H_k : 1;
+  s.heads_out = keys ? p.H_k * s.copies : p.H_q;
+  return s;
+}
+__device__ __forceinline__ void load_weight(const float* w, int row_lane, float (&wt)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) wt[e] = 1.f;
+  if (w) {
+    Raw8<float> raw;
+    raw.load(w + 8 * row_lane);
+    raw.get(wt);
+  }
 }
 
+// A workgroup's heads: `per` of the queries' and keys' together, from blockIdx.y per on.
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void qk_forward_kernel(ccq_qk_params p, int per) {
   constexpr int LPR = D / 8, TOK = kThreads / LPR;
-  const int lane = threadIdx.x & 63, rl = threadIdx.x % LPR;
-  const int tokens = p.B * p.T;
-  const int tok = blockIdx.x * TOK + threadIdx.x / LPR;
-  const bool live = tok < tokens;
-  const int bt = live ? tok : tokens - 1;
+  __shared__ Angles<D> angles;
+  const int lane = threadIdx.x & 63, rl = threadIdx.x % LPR, row = threadIdx.x / LPR;
+  const int tokens = p.B * p.T, first = blockIdx.x * TOK;
+  const bool live = first + row < tokens;
+  const int bt = live ? first + row : tokens - 1;
   const int b = bt / p.T, t = bt - b * p.T;
-  const HeadRange hr = head_range(p, blockIdx.y, per);
-  const int64_t position = p.positions ? p.positions[bt] : p.position0 + t;
-  const Turn u = make_turn(p, lane, rl, position);
+  if (p.rot) angles.form(p, first, tokens);
+  __syncthreads();
+  const Turn u = angles.take(p, row, rl, lane);
 
-  const T* in = static_cast<const T*>(hr.keys ? p.k : p.q) + 8 * rl;
-  in += hr.keys ? b * p.k_stride_b + t * p.k_stride_t : b * p.q_stride_b + t * p.q_stride_t;
-  const int64_t step = hr.keys ? p.k_stride_h : p.q_stride_h;
-  const float* w = hr.keys ? p.k_weight : p.q_weight;
-  const int kind = hr.keys ? p.k_norm : p.q_norm;
-  const int copies = hr.keys && p.expand_keys ? p.H_q / p.H_k : 1;
-  const int heads_out = hr.keys ? p.H_k * copies : p.H_q;
-  T* out = static_cast<T*>(hr.keys ? p.k_out : p.q_out) + 8 * rl;
-
-  float wt[8];
+  const int from = blockIdx.y * per, to = min(from + per, p.H_q + p.H_k);
+  for (int side = 0; side < 2; ++side) {
+    const int begin = side ? max(from - p.H_q, 0) : from, end = side ? to - p.H_q : min(to, p.H_q);
+    if (begin >= end) continue;
+    const Side s = side_of(p, side != 0);
+    const T* in = static_cast<const T*>(s.in) + b * s.sb + t * s.st + 8 * rl;
+    T* out = static_cast<T*>(s.out) + (((int64_t)b * s.heads_out) * p.T + t) * D + 8 * rl;
+    const int64_t out_step = (int64_t)p.T * D;
+    float wt[8];
+    load_weight(s.w, rl, wt);
+    for (int h0 = begin; h0 < end; h0 += kAhead) {
+      Raw8<T> raw[kAhead];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) wt[e] = 1.f;
-  if (w) load8(w + 8 * rl, wt);
-
-  for (int h = hr.begin; h < hr.end; ++h) {
-    float x[8];
-    load8(in + h * step, x);
-    if (kind != CCQ_NORM_NONE) {
-      float ss = 0.f;
+      for (int i = 0; i < kAhead; ++i) raw[i].load(in + min(h0 + i, end - 1) * s.sh);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
-      const float r = row_scale(group_sum<LPR>(ss), kind, 1.f / D, p.eps);
+      for (int i = 0; i < kAhead; ++i) {
+        const int h = h0 + i;
+        if (h >= end) break;
+        float x[8];
+        raw[i].get(x);
+        if (s.norm != CCQ_NORM_NONE) {
+          float ss = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= r;
-    }
+          for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
+          const float r = row_scale(group_sum<LPR>(ss), s.norm, 1.f / D, p.eps);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= wt[e];
-    turn<false>(x, u, p);
-    if (live) {
-      for (int c = 0; c < copies; ++c)
-        store8(out + (((int64_t)b * heads_out + h * copies + c) * p.T + t) * D, x);
+          for (int e = 0; e < 8; ++e) x[e] *= r;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= wt[e];
+        turn<false>(x, u, p);
+        if (live) {
+          for (int c = 0; c < s.copies; ++c) store8<false>(out + (h * s.copies + c) * out_step, x);
+        }
+      }
     }
   }
 }
 
 // Gradient.  With z the gradient of the row turned back and summed over the heads that share it,
 //   dx = w z r - x r^3 (sum w z x) / (d or 1),  dw = sum of z x r over rows,
-// the second term of dx absent without a norm and where an L2 norm is at its floor.
+// the second term of dx absent without a norm and where an L2 norm is at its floor.  The weights'
+// gradients gather in registers over a workgroup's rows; workgroups go on from tile to tile, so that
+// few parts are left to be summed.
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void qk_backward_kernel(ccq_qk_bwd_params q, int per, float* partial) {
   constexpr int LPR = D / 8, TOK = kThreads / LPR;
+  __shared__ union {
+    Angles<D> angles;
+    float red[TOK][D];
+  } lds;
   const ccq_qk_params& p = q.fwd;
-  const int lane = threadIdx.x & 63, rl = threadIdx.x % LPR;
+  const int lane = threadIdx.x & 63, rl = threadIdx.x % LPR, row = threadIdx.x / LPR;
   const int tokens = p.B * p.T;
-  const HeadRange hr = head_range(p, blockIdx.y, per);
-  const T* in0 = static_cast<const T*>(hr.keys ? p.k : p.q) + 8 * rl;
-  const float* g0 = (hr.keys ? q.dk_out : q.dq_out) + 8 * rl;
-  T* out0 = static_cast<T*>(hr.keys ? q.dk : q.dq) + 8 * rl;
-  const int64_t sb = hr.keys ? p.k_stride_b : p.q_stride_b, st = hr.keys ? p.k_stride_t : p.q_stride_t,
-                sh = hr.keys ? p.k_stride_h : p.q_stride_h;
-  const int64_t ob = hr.keys ? q.dk_stride_b : q.dq_stride_b, ot = hr.keys ? q.dk_stride_t : q.dq_stride_t,
-                oh = hr.keys ? q.dk_stride_h : q.dq_stride_h;
-  const float* w = hr.keys ? p.k_weight : p.q_weight;
-  const int kind = hr.keys ? p.k_norm : p.q_norm;
-  const int copies = hr.keys && p.expand_keys ? p.H_q / p.H_k : 1;
-  const int heads_out = hr.keys ? p.H_k * copies : p.H_q;
-
-  float wt[8], dw[8];
+  const int from = blockIdx.y * per, to = min(from + per, p.H_q + p.H_k);
+  float dw[2][8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    wt[e] = 1.f;
-    dw[e] = 0.f;
-  }
-  if (w) load8(w + 8 * rl, wt);
+  for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.f;
 
-  for (int tile = blockIdx.x; tile * TOK < tokens; tile += gridDim.x) {
-    const int tok = tile * TOK + threadIdx.x / LPR;
-    const bool live = tok < tokens;
-    const int bt = live ? tok : tokens - 1;
+  for (int first = blockIdx.x * TOK; first < tokens; first += gridDim.x * TOK) {
+    const bool live = first + row < tokens;
+    const int bt = live ? first + row : tokens - 1;
     const int b = bt / p.T, t = bt - b * p.T;
-    const int64_t position = p.positions ? p.positions[bt] : p.position0 + t;
-    const Turn u = make_turn(p, lane, rl, position);
-    for (int h = hr.begin; h < hr.end; ++h) {
-      float x[8], z[8];
-      load8(in0 + b * sb + t * st + h * sh, x);
-      load8(g0 + (((int64_t)b * heads_out + h * copies) * p.T + t) * D, z);
-      for (int c = 1; c < copies; ++c) {
-        float more[8];
-        load8(g0 + (((int64_t)b * heads_out + h * copies + c) * p.T + t) * D, more);
+    __syncthreads();
+    if (p.rot) lds.angles.form(p, first, tokens);
+    __syncthreads();
+    const Turn u = lds.angles.take(p, row, rl, lane);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] += more[e];
-      }
-      turn<true>(z, u, p);
-      float ss = 0.f, dot = 0.f;
+    for (int side = 0; side < 2; ++side) {
+      const int begin = side ? max(from - p.H_q, 0) : from, end = side ? to - p.H_q : min(to, p.H_q);
+      if (begin >= end) continue;
+      const Side s = side_of(p, side != 0);
+      const T* in = static_cast<const T*>(s.in) + b * s.sb + t * s.st + 8 * rl;
+      const float* grad = (side ? q.dk_out : q.dq_out) + (((int64_t)b * s.heads_out) * p.T + t) * D + 8 * rl;
+      const int64_t grad_step = (int64_t)p.T * D;
+      T* out = static_cast<T*>(side ? q.dk : q.dq) + b * (side ? q.dk_stride_b : q.dq_stride_b) +
+               t * (side ? q.dk_stride_t : q.dq_stride_t) + 8 * rl;
+      const int64_t oh = side ? q.dk_stride_h : q.dq_stride_h;
+      float wt[8];
+      load_weight(s.w, rl, wt);
+      auto gradient = [&](const Raw8<T>& x_raw, float (&z)[8], int h) {
+        float x[8];
+        x_raw.get(x);
+        turn<true>(z, u, p);
+        float ss = 0.f, dot = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        ss += x[e] * x[e];
-        dot += wt[e] * z[e] * x[e];
-      }
-      float r = 1.f, pull = 0.f;
-      if (kind != CCQ_NORM_NONE) {
-        ss = group_sum<LPR>(ss);
-        dot = group_sum<LPR>(dot);
-        r = row_scale(ss, kind, 1.f / D, p.eps);
-        if (kind == CCQ_NORM_RMS) pull = r * r * r * dot * (1.f / D);
-        else if (sqrtf(ss) > kL2Floor) pull = r * r * r * dot;
-      }
-      if (live) {
+        for (int e = 0; e < 8; ++e) {
+          ss += x[e] * x[e];
+          dot += wt[e] * z[e] * x[e];
+        }
+        float r = 1.f, pull = 0.f;
+        if (s.norm != CCQ_NORM_NONE) {
+          ss = group_sum<LPR>(ss);
+          dot = group_sum<LPR>(dot);
+          r = row_scale(ss, s.norm, 1.f / D, p.eps);
+          if (s.norm == CCQ_NORM_RMS) pull = r * r * r * dot * (1.f / D);
+          else if (sqrtf(ss) > kL2Floor) pull = r * r * r * dot;
+        }
+        if (live) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dw[e] += z[e] * x[e] * r;
+          for (int e = 0; e < 8; ++e) dw[side][e] += z[e] * x[e] * r;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = wt[e] * z[e] * r - x[e] * pull;
-        store8(out0 + b * ob + t * ot + h * oh, x);
+          for (int e = 0; e < 8; ++e) x[e] = wt[e] * z[e] * r - x[e] * pull;
+          store8<true>(out + h * oh, x);
+        }
+      };
+      if (s.copies == 1) {
+        for (int h0 = begin; h0 < end; h0 += kBackAhead) {
+          Raw8<T> x_raw[kBackAhead];
+          Raw8<float> z_raw[kBackAhead];
+#pragma unroll
+          for (int i = 0; i < kBackAhead; ++i) {
+            const int h = min(h0 + i, end - 1);
+            x_raw[i].load(in + h * s.sh);
+            z_raw[i].load(grad + h * grad_step);
+          }
+#pragma unroll
+          for (int i = 0; i < kBackAhead; ++i) {
+            if (h0 + i >= end) break;
+            float z[8];
+            z_raw[i].get(z);
+            gradient(x_raw[i], z, h0 + i);
+          }
+        }
+      } else {
+        for (int h = begin; h < end; ++h) {
+          Raw8<T> x_raw;
+          x_raw.load(in + h * s.sh);
+          float z[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z[e] = 0.f;
+          for (int c0 = 0; c0 < s.copies; c0 += kBackAhead) {
+            Raw8<float> z_raw[kBackAhead];
+#pragma unroll
+            for (int i = 0; i < kBackAhead; ++i) z_raw[i].load(grad + (h * s.copies + min(c0 + i, s.copies - 1)) * grad_step);
+#pragma unroll
+            for (int i = 0; i < kBackAhead; ++i) {
+              if (c0 + i >= s.copies) break;
+              float more[8];
+              z_raw[i].get(more);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) z[e] += more[e];
+            }
+          }
+          gradient(x_raw, z, h);
+        }
       }
     }
   }
-  if (!w) return;
-  // the workgroup's part of the weight gradient, summed over its tokens in a fixed order
-  __shared__ float red[TOK][D];
+  // the workgroup's part of the weight gradients, summed over its tokens in a fixed order
+  const int parts = gridDim.x * gridDim.y, part = blockIdx.y * gridDim.x + blockIdx.x;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) red[threadIdx.x / LPR][8 * rl + e] = dw[e];
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float s = 0.f;
-    for (int i = 0; i < TOK; ++i) s += red[i][threadIdx.x];
-    partial[((size_t)blockIdx.y * gridDim.x + blockIdx.x) * D + threadIdx.x] = s;
+  for (int side = 0; side < 2; ++side) {
+    if (!(side ? p.k_weight : p.q_weight)) continue;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) lds.red[row][8 * rl + e] = dw[side][e];
+    __syncthreads();
+    if (threadIdx.x < D) {
+      float s = 0.f;
+      for (int i = 0; i < TOK; ++i) s += lds.red[i][threadIdx.x];
+      partial[((size_t)side * parts + part) * D + threadIdx.x] = s;
+    }
   }
 }
 
-// dq_weight (blockIdx.y 0) and dk_weight (1): sums of the workgroups' parts, 32 columns a workgroup.
-__global__ __launch_bounds__(kThreads) void qk_weight_kernel(const float* partial, int d, int parts_q, int parts_k,
-                                                             float* dq_weight, float* dk_weight) {
+// dq_weight (blockIdx.y 0) and dk_weight (1): sums of the workgroups' parts, 16 columns a workgroup, 64
+// rows at a time, so that a thread adds few parts, in a fixed order, with their loads under way together.
+constexpr int kWeightThreads = 1024, kWeightCols = 16, kWeightRows = kWeightThreads / kWeightCols;
+__global__ __launch_bounds__(kWeightThreads) void qk_weight_kernel(const float* partial, int d, int parts, float* dq_weight,
+                                                                   float* dk_weight) {
   const bool keys = blockIdx.y != 0;
   float* out = keys ? dk_weight : dq_weight;
   if (out == nullptr) return;
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), row = threadIdx.x >> 5;
-  const float* src = partial + (keys ? (size_t)parts_q * d : 0);
-  const int n = keys ? parts_k : parts_q;
+  const int col = threadIdx.x % kWeightCols, row = threadIdx.x / kWeightCols;
+  const float* src = partial + (keys ? (size_t)parts * d : 0) + blockIdx.x * kWeightCols + col;
   float s = 0.f;
-  for (int i = row; i < n; i += kThreads / 32) s += src[(size_t)i * d + col];
-  __shared__ float red[kThreads / 32][32];
-  red[row][threadIdx.x & 31] = s;
+#pragma unroll 8
+  for (int i = row; i < parts; i += kWeightRows) s += src[(size_t)i * d];
+  __shared__ float red[kWeightRows][kWeightCols];
+  red[row][col] = s;
   __syncthreads();
   if (row == 0) {
-#pragma unroll
-    for (int i = 1; i < kThreads / 32; ++i) s += red[i][threadIdx.x];
-    out[col] = s;
+    for (int i = 1; i < kWeightRows; ++i) s += red[i][col];
+    out[blockIdx.x * kWeightCols + col] = s;
   }
 }
 
-// How many heads a workgroup walks over: all of a token's heads share its angles, but the chip wants
-// about 2048 workgroups.
-int heads_per_group(const ccq_qk_params& p, int tiles) {
-  const int most = p.H_q > p.H_k ? p.H_q : p.H_k;
-  int per = most;
-  while (per > 1 && (long long)tiles * ((p.H_q + per - 1) / per + (p.H_k + per - 1) / per) < 2048) per = (per + 1) / 2;
-  return per;
-}
 int tokens_per_tile(const ccq_qk_params& p) { return kThreads / (p.d / 8); }
 int tiles_of(const ccq_qk_params& p) { return (p.B * p.T - 1) / tokens_per_tile(p) + 1; }
 
-struct BackwardGrid {
-  int per, x, parts_q, parts_k;
-};
-BackwardGrid backward_grid(const ccq_qk_params& p) {
-  BackwardGrid g;
-  const int tiles = tiles_of(p);
-  g.per = heads_per_group(p, tiles);
-  g.parts_q = (p.H_q + g.per - 1) / g.per;
-  g.parts_k = (p.H_k + g.per - 1) / g.per;
-  g.x = tiles < 1024 ? tiles : 1024;
-  return g;
+// Heads that a workgroup walks over: all, sharing the angles, where that leaves 1024 workgroups, four for
+// each CU; else fewer.
+int heads_per_group(const ccq_qk_params& p, int tiles) {
+  const int all = p.H_q + p.H_k;
+  int per = all;
+  while (per > 1 && (long long)tiles * ((all + per - 1) / per) < 1024) per = (per + 1) / 2;
+  return per;
 }
+
+dim3 grid_of(const ccq_qk_params& p, int per, int most) {
+  const int tiles = tiles_of(p);
+  return dim3(tiles < most ? tiles : most, (p.H_q + p.H_k + per - 1) / per);
+}
+// The gradient's workgroups along the tokens: two for each CU, going on from tile to tile (92 us at the
+// prefill's size; with 1024, of which 768 run at a time, 101).
+constexpr int kBackGroups = 512;
 
 }  // namespace
 
 hipError_t launch_qk(const ccq_qk_params& p, hipStream_t stream) {
-  const int tiles = tiles_of(p), per = heads_per_group(p, tiles);
-  const dim3 grid(tiles, (p.H_q + per - 1) / per + (p.H_k + per - 1) / per);
+  const int per = heads_per_group(p, tiles_of(p));
+  const dim3 grid = grid_of(p, per, 0x7fffffff);
   if (p.dtype == CCQ_DTYPE_BF16) {
     if (p.d == 128) qk_forward_kernel<__bf16, 128><<<grid, kThreads, 0, stream>>>(p, per);
     else qk_forward_kernel<__bf16, 64><<<grid, kThreads, 0, stream>>>(p, per);
@@ -322,26 +433,26 @@ hipError_t launch_qk(const ccq_qk_params& p, hipStream_t stream) {
 size_t qk_backward_workspace_bytes(const ccq_qk_bwd_params& q) {
   const ccq_qk_params& p = q.fwd;
   if (!p.q_weight && !p.k_weight) return 0;
-  const BackwardGrid g = backward_grid(p);
-  return (size_t)g.x * (g.parts_q + g.parts_k) * p.d * 4;
+  const dim3 grid = grid_of(p, heads_per_group(p, tiles_of(p)), kBackGroups);
+  return (size_t)grid.x * grid.y * 2 * p.d * 4;
 }
 
 hipError_t launch_qk_backward(const ccq_qk_bwd_params& q, hipStream_t stream) {
   const ccq_qk_params& p = q.fwd;
-  const BackwardGrid g = backward_grid(p);
-  const dim3 grid(g.x, g.parts_q + g.parts_k);
+  const int per = heads_per_group(p, tiles_of(p));
+  const dim3 grid = grid_of(p, per, kBackGroups);
   float* part = static_cast<float*>(q.workspace);
   if (p.dtype == CCQ_DTYPE_BF16) {
-    if (p.d == 128) qk_backward_kernel<__bf16, 128><<<grid, kThreads, 0, stream>>>(q, g.per, part);
-    else qk_backward_kernel<__bf16, 64><<<grid, kThreads, 0, stream>>>(q, g.per, part);
+    if (p.d == 128) qk_backward_kernel<__bf16, 128><<<grid, kThreads, 0, stream>>>(q, per, part);
+    else qk_backward_kernel<__bf16, 64><<<grid, kThreads, 0, stream>>>(q, per, part);
   } else {
-    if (p.d == 128) qk_backward_kernel<float, 128><<<grid, kThreads, 0, stream>>>(q, g.per, part);
-    else qk_backward_kernel<float, 64><<<grid, kThreads, 0, stream>>>(q, g.per, part);
+    if (p.d == 128) qk_backward_kernel<float, 128><<<grid, kThreads, 0, stream>>>(q, per, part);
+    else qk_backward_kernel<float, 64><<<grid, kThreads, 0, stream>>>(q, per, part);
   }
-  hipError_t e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || (!p.q_weight && !p.k_weight)) return e;
-  qk_weight_kernel<<<dim3(p.d / 32, 2), kThreads, 0, stream>>>(part, p.d, g.x * g.parts_q, g.x * g.parts_k, q.dq_weight,
-                                                              q.dk_weight);
+  qk_weight_kernel<<<dim3(p.d / kWeightCols, 2), kWeightThreads, 0, stream>>>(part, p.d, (int)(grid.x * grid.y),
+                                                                             q.dq_weight, q.dk_weight);
   return hipGetLastError();
 }
 
