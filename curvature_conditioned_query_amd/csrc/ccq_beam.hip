@@ -1,19 +1,22 @@
 // Beam search: the best continuations of every request over its beams and the vocabulary, and the
 // reordering of the states that the beams carry.
 //
-// Selection reads the logits once.  beam_rows_kernel gives a workgroup one chunk of one beam's row,
-// held in registers (up to 64 logits a thread): it leaves the chunk's M best logits, in order, and its
-// part of the normaliser sum exp(x - m).  beam_join_kernel, one workgroup a request, joins the parts
-// into each beam's normaliser and picks the M best continuations out of the chunks' lists.
+// Selection reads the logits once.  beam_rows_kernel gives a workgroup a stretch of one beam's row: it
+// leaves the stretch's M best logits, in order, and its part of the normaliser sum exp(x - top).
+// beam_join_kernel, one workgroup a request, joins the parts into each beam's normaliser and picks the M
+// best continuations out of the stretches' lists.
 //
-// Picking M of 16384 needs no sort: with every thread's own maximum known, the M-th best of those
-// maxima is a bound that at least M logits reach, and a logit that reaches it lies on one of the M
-// threads whose maximum does, so at most 64 M logits are left to be ranked (a few more than M in
-// earnest).  Ties go to the lowest token throughout: the bound is a pair (logit, token).
+// Picking M of many needs no sort.  A workgroup goes through its stretch in pieces held in registers (32
+// logits a thread).  In the first, the (M / 4 + 1)-th best of each wave's thread maxima is found; at least
+// M logits reach the least of the four, the bound, and few lie above it.  Those, and in the later pieces
+// whatever lies above the bound, go into a list of their wave's own, in no order, without a word between
+// the waves; a list that fills up (a row that rises, a mask over the first tokens) is thinned to its M best,
+// which raise the wave's bound.  Should fewer than M logits lie above the bound, as in a row of few values
+// or under a mask that leaves few tokens, the lowest tokens at the bound itself are looked up at the end.
 //
 // Scores of different beams meet in the comparison, so the normaliser has to be good to more than
-// fp32: the logits that reach the bound, which carry most of a peaked distribution, are left out of the
-// fp32 sum and added in 64 bits, and the threads' sums of the rest are joined in 64 bits.
+// fp32: the candidates, which carry most of a peaked distribution, are left out of the fp32 sum and added
+// in 64 bits, and the threads' sums of the rest, 2^(x log2(e) - c), are joined in 64 bits.
 #include <float.h>
 
 #include "ccq_device.hpp"
@@ -25,15 +28,15 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 
-// The workspace: a part of the normaliser and a list of M logits for every (row, chunk).
+// The workspace: a part of the normaliser and a list of M logits for every (row, stretch).
 struct Part {
-  double sum;  // sum of exp(x - top) over the chunk
+  double sum;  // sum of exp(x - top) over the stretch
   float top;   // its largest logit
   int pad;
 };
 struct Pick {
   float logit;
-  int token;  // -1: the chunk has no more
+  int token;  // -1: the stretch has no more
 };
 
 struct BeamWork {
@@ -57,11 +60,7 @@ __device__ __forceinline__ float wave_max(float x) {
 // finite number.
 __device__ __forceinline__ float as_counted(float x) { return fminf(fmaxf(x, -INFINITY), FLT_MAX); }
 
-// exp(d) for d <= 0, fp32, with the product by log2(e) good to more than its rounding.
-__device__ __forceinline__ float exp_tail(float d) {
-  constexpr float hi = 1.44269502162933349609f, lo = 1.92596299112661746887e-8f;  // log2(e) in two parts
-  return __builtin_amdgcn_exp2f(__builtin_fmaf(d, hi, d * lo));
-}
+constexpr float kLog2e = 1.44269502162933349609f;
 
 // A row's beam: 0 goes on, 1 finished, 2 dead (its score is -inf or NaN).
 __device__ __forceinline__ int beam_kind(const ccq_beam_params& p, int row) {
@@ -75,22 +74,228 @@ __device__ __forceinline__ int beam_kind(const ccq_beam_params& p, int row) {
 // to get equal normalisers to the last bit, or their ties would fall either way.
 typedef bf16x8 bf16x8_any __attribute__((aligned(2)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
+template <typename T>
+struct Any;
+template <>
+struct Any<__bf16> {
+  typedef bf16x8_any type;
+};
+template <>
+struct Any<float> {
+  typedef f32x4_any type;
+};
 
-// Elements of the chunk that thread `tid` holds: E of them, in vectors of VE, vector j from token
-// (j 256 + tid) VE of the chunk on.
+// A thread's logits of a piece as they are stored: vectors of 16 bytes, 256 vectors apart.
+template <typename T, int NV>
+struct Raw {
+  static constexpr int VE = 16 / sizeof(T);
+  typedef typename Any<T>::type V;
+  V v[NV];
+  // From token `first` on, of the piece that begins at token `at`.
+  __device__ __forceinline__ void load(const T* src, int first, int at, int V_all) {
+    if (at + kThreads * VE * NV <= V_all) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) v[j] = __builtin_nontemporal_load(reinterpret_cast<const V*>(src + first + j * (kThreads * VE)));
+      return;
+    }
+    // the row ends in this piece: vectors inside it, then the one across its end
+    if (V_all >= VE) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        v[j] = *reinterpret_cast<const V*>(src + min(first + j * (kThreads * VE), V_all - VE));
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int v0 = first + j * (kThreads * VE);
+      if (v0 < V_all && v0 + VE > V_all) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) v[j][e] = src[min(v0 + e, V_all - 1)];
+      }
+    }
+  }
+  // Logits g .. g + 7 of the thread; -inf behind the row.
+  __device__ __forceinline__ void get(float (&x)[8], int g, int first, bool whole, int V_all) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = (float)v[(g + i) / VE][(g + i) % VE];
+    if (!whole) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (first + (g + i) / VE * (kThreads * VE) + (g + i) % VE >= V_all) x[i] = -INFINITY;
+    }
+  }
+};
+
+// Sorts 64 lanes' values, the largest first.
+__device__ __forceinline__ float sort_lanes(float v, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 64; size *= 2) {
+#pragma unroll
+    for (int gap = size / 2; gap > 0; gap /= 2) {
+      const float o = __shfl_xor(v, gap, 64);
+      const bool larger = ((lane & gap) == 0) == ((lane & size) == 0 || size == 64);
+      v = larger ? fmaxf(v, o) : fminf(v, o);
+    }
+  }
+  return v;
+}
+
+// Whether logit a at token va comes before b at vb.
+__device__ __forceinline__ bool before(float a, int va, float b, int vb) { return a > b || (a == b && va < vb); }
+
+// The part and the picks of a stretch with NaN or +inf among its logits, which count as as_counted() says: one
+// pass through memory for each pick, all of the sum in 64 bits.  shared: room for 8 words.
+template <typename T>
+__device__ __attribute__((noinline)) void careful_stretch(const T* src, int begin, int end, int M, Pick* picks, Part* part,
+                                                          float* shared) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int* tokens = reinterpret_cast<int*>(shared) + kWaves;
+  float x0 = INFINITY, top = -INFINITY;  // the pick before: everything comes after +inf
+  int v0 = -1;
+  for (int m = 0; m < M; ++m) {
+    float x = -INFINITY;
+    int v = 0x7fffffff;
+    for (int i = begin + (int)threadIdx.x; i < end; i += kThreads) {
+      const float o = as_counted(to_f32(src[i]));
+      if (before(x0, v0, o, i) && before(o, i, x, v)) {
+        x = o;
+        v = i;
+      }
+    }
+    for (int off = 32; off > 0; off >>= 1) {
+      const float ox = __shfl_xor(x, off, 64);
+      const int ov = __shfl_xor(v, off, 64);
+      if (before(ox, ov, x, v)) {
+        x = ox;
+        v = ov;
+      }
+    }
+    __syncthreads();
+    if (lane == 0) {
+      shared[wave] = x;
+      tokens[wave] = v;
+    }
+    __syncthreads();
+    x = shared[0];
+    v = tokens[0];
+    for (int w = 1; w < kWaves; ++w)
+      if (before(shared[w], tokens[w], x, v)) {
+        x = shared[w];
+        v = tokens[w];
+      }
+    if (m == 0) top = x;
+    if (threadIdx.x == 0) picks[m] = v == 0x7fffffff ? Pick{-INFINITY, -1} : Pick{x, v};
+    x0 = x;
+    v0 = v;
+  }
+  double s = 0.0;
+  if (top > -INFINITY)
+    for (int i = begin + (int)threadIdx.x; i < end; i += kThreads) s += exp((double)as_counted(to_f32(src[i])) - (double)top);
+  s = wave_sum(s);
+  double* sums = reinterpret_cast<double*>(shared);
+  __syncthreads();
+  if (lane == 0) sums[wave] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) *part = Part{(sums[0] + sums[1]) + (sums[2] + sums[3]), top, 0};
+}
+
+// Picks n .. M - 1: the lowest tokens at `value`.
+template <typename T>
+__device__ __attribute__((noinline)) void fill_picks(const T* src, int begin, int end, float value, int n, int M, Pick* picks,
+                                                     int* counts) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int at = begin; at < end && n < M; at += kThreads) {
+    const int i = at + (int)threadIdx.x;
+    const bool is = i < end && to_f32(src[i]) == value;
+    const uint64_t all = __ballot(is);
+    if (lane == 0) counts[wave] = __popcll(all);
+    __syncthreads();
+    int to = n + __popcll(all & ((1ull << lane) - 1));
+    for (int w = 0; w < kWaves; ++w) {
+      if (w < wave) to += counts[w];
+      n += counts[w];
+    }
+    if (is && to < M) picks[to] = Pick{value, i};
+    __syncthreads();
+  }
+  for (int i = n + (int)threadIdx.x; i < M; i += kThreads) picks[i] = Pick{-INFINITY, -1};
+}
+
+// A logit and its token as one number: the greater comes first.
+__device__ __forceinline__ uint64_t to_key(float x, int token) {
+  const unsigned b = __float_as_uint(x + 0.f);  // -0 ties with 0
+  return (uint64_t)((int)b < 0 ? ~b : b | 0x80000000u) << 32 | (unsigned)~token;
+}
+__device__ __forceinline__ float key_logit(uint64_t key) {
+  const unsigned b = (unsigned)(key >> 32);
+  return __uint_as_float((int)b < 0 ? b & 0x7fffffffu : ~b);
+}
+__device__ __forceinline__ int key_token(uint64_t key) { return (int)~(unsigned)key; }
+
+// How many of n keys are greater; behind them stand seven that are 0, the least there is.
+__device__ __forceinline__ int count_greater(const uint64_t* keys, int n, uint64_t mine) {
+  int r = 0;
+  for (int j = 0; j < n; j += 8) {
+    uint64_t k[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) k[i] = keys[j + i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r += k[i] > mine ? 1 : 0;
+  }
+  return r;
+}
+
+// A wave's candidates in LDS, in the order they were found.  Before a group of eight logits a lane is looked
+// at, there is room for all of them.
+constexpr int kGroup = 8;
+constexpr int kHeld = 64 * kGroup + 128;
+struct Held {
+  uint64_t key[kHeld + 8];
+};
+struct Best {
+  uint64_t key[64];
+};
+__device__ __forceinline__ void wave_fence() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Thins a wave's n candidates to the M best, in order.  The others are added to gone, which counts from ref.
+__device__ __forceinline__ void thin(Held& held, Best& best, int n, int M, double& gone, float& ref) {
+  const int lane = threadIdx.x & 63;
+  if (lane < 8) held.key[n + lane] = 0;
+  wave_fence();
+  float highest = -INFINITY;
+  for (int i = lane; i < n; i += 64) highest = fmaxf(highest, key_logit(held.key[i]));
+  highest = wave_max(highest);
+  if (ref > -INFINITY) gone *= exp((double)ref - (double)highest);
+  ref = highest;
+  for (int i = lane; i < n; i += 64) {
+    const uint64_t key = held.key[i];
+    const int r = count_greater(held.key, n, key);
+    if (r < M) best.key[r] = key;
+    else gone += exp((double)key_logit(key) - (double)highest);
+  }
+  wave_fence();
+  if (lane < M) held.key[lane] = best.key[lane];
+  wave_fence();
+}
+
+// Tokens of a piece: 256 threads hold E each, in vectors of VE, vector j from token (j 256 + tid) VE of the
+// piece on.  The logits are taken as they come: a NaN shows in the sum and +inf among the candidates, and a
+// stretch that has one is left to careful_stretch.
 template <typename T, int E>
-__global__ __launch_bounds__(kThreads) void beam_rows_kernel(ccq_beam_params p, int chunks, BeamWork work) {
-  constexpr int VE = 16 / sizeof(T), NV = E / VE;
-  extern __shared__ __align__(16) unsigned char dyn[];  // candidates: M E logits, M E tokens, M E logits in order
-  __shared__ __align__(16) float best[kWaves][64];
-  __shared__ float bound_value;
-  __shared__ unsigned bound_token;
-  __shared__ int above[kWaves], equal[kWaves], found;
-  __shared__ double sums[kWaves];
-  __shared__ unsigned firsts[kThreads];
+__global__ __launch_bounds__(kThreads) void beam_rows_kernel(ccq_beam_params p, int stretches, int pieces, BeamWork work) {
+  constexpr int VE = 16 / sizeof(T), NV = E / VE, G = kGroup;  // a group of logits has a maximum of its own
+  constexpr int PIECE = kThreads * E;
+  __shared__ __align__(16) Held held[kWaves];
+  __shared__ Best best[kWaves];
+  __shared__ __align__(16) float few[8];
+  __shared__ float bounds[kWaves], tops[kWaves], mosts[kWaves], refs[kWaves];
+  __shared__ int counts[kWaves];
+  __shared__ double sums[kWaves], gones[kWaves], helds[kWaves];
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, M = p.M;
-  const int row = blockIdx.x / chunks, chunk = blockIdx.x - row * chunks;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), M = p.M;
+  const int row = blockIdx.x / stretches, stretch = blockIdx.x - row * stretches;
   const size_t list = blockIdx.x;
   Pick* picks = work.picks + list * M;
 
@@ -99,7 +304,7 @@ __global__ __launch_bounds__(kThreads) void beam_rows_kernel(ccq_beam_params p, 
     // a finished beam's one continuation and then, as a dead beam's, tokens in order at -inf
     for (int i = tid; i < M; i += kThreads) {
       Pick k{-INFINITY, -1};
-      if (chunk == 0) {
+      if (stretch == 0) {
         if (kind == 2) k.token = i;
         else if (i == 0) k = Pick{0.f, p.pad_token};
         else k.token = i - 1 < p.pad_token ? i - 1 : i;
@@ -112,135 +317,130 @@ __global__ __launch_bounds__(kThreads) void beam_rows_kernel(ccq_beam_params p, 
   }
 
   const T* src = static_cast<const T*>(p.logits) + (int64_t)row * p.logits_stride;
-  // token of the thread's first element: the rest follow by constants
-  const int first = chunk * (kThreads * E) + tid * VE;
-  float x[E];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int v0 = first + j * (kThreads * VE);
-    if (v0 + VE <= p.V) {
-      if constexpr (sizeof(T) == 2) {
-        const bf16x8 a = *reinterpret_cast<const bf16x8_any*>(src + v0);
-#pragma unroll
-        for (int e = 0; e < VE; ++e) x[j * VE + e] = as_counted((float)a[e]);
-      } else {
-        const f32x4 a = *reinterpret_cast<const f32x4_any*>(src + v0);
-#pragma unroll
-        for (int e = 0; e < VE; ++e) x[j * VE + e] = as_counted(a[e]);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < VE; ++e)
-        x[j * VE + e] = v0 + e < p.V ? as_counted(to_f32(src[v0 + e])) : -INFINITY;
-    }
-  }
-  float mine = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < E; ++i) mine = fmaxf(mine, x[i]);
-
-  // the M best thread maxima of each wave, in order
-  int rank = 0;
-#pragma unroll 8
-  for (int i = 0; i < 64; ++i) {
-    const float o = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine), i));
-    rank += (o > mine || (o == mine && i < lane)) ? 1 : 0;
-  }
-  best[wave][rank] = mine;
-  if (tid == 0) found = 0;
-  __syncthreads();
-  // the M-th best of all: every wave's lists, an entry a thread
-  const float top = fmaxf(fmaxf(best[0][0], best[1][0]), fmaxf(best[2][0], best[3][0]));
-  if (lane < M) {
-    const float v = best[wave][lane];
-    int r = lane;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      if (w == wave) continue;
-      for (int i = 0; i < M; ++i) {
-        const float o = best[w][i];
-        r += (o > v || (o == v && w < wave)) ? 1 : 0;
-      }
-    }
-    if (r == M - 1) bound_value = v;
-  }
-  __syncthreads();
-  const float bound = bound_value;
-  const uint64_t gt = __ballot(mine > bound), eq = __ballot(mine == bound);
-  if (lane == 0) {
-    above[wave] = __popcll(gt);
-    equal[wave] = __popcll(eq);
-  }
-  __syncthreads();
-  const int want = M - (above[0] + above[1] + above[2] + above[3]);  // threads at the bound that are needed
-  unsigned last = 0xffffffffu;
-  if (equal[0] + equal[1] + equal[2] + equal[3] > want) {
-    // more threads sit at the bound than are needed: those whose first such token is lowest
-    unsigned f = 0xffffffffu;
-    if (mine == bound) {
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const int v = first + (i / VE) * (kThreads * VE) + i % VE;
-        if (x[i] == bound && v < p.V) f = min(f, (unsigned)v);
-      }
-    }
-    firsts[tid] = f;
-    if (tid == 0) bound_token = 0xffffffffu;
-    __syncthreads();
-    if (f != 0xffffffffu) {
-      int r = 0;
-      for (int i = 0; i < kThreads; ++i) r += firsts[i] < f ? 1 : 0;
-      if (r == want - 1) bound_token = f;
-    }
-    __syncthreads();
-    last = bound_token;
-  }
-
-  float* cand_x = reinterpret_cast<float*>(dyn);
-  int* cand_v = reinterpret_cast<int*>(cand_x + M * E);
-  float* in_order = reinterpret_cast<float*>(cand_v + M * E);
-  if (mine >= bound) {
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int v = first + (i / VE) * (kThreads * VE) + i % VE;
-      if (v < p.V && (x[i] > bound || (x[i] == bound && (unsigned)v <= last))) {
-        const int at = atomicAdd(&found, 1);
-        cand_x[at] = x[i];
-        cand_v[at] = v;
-        x[i] = -INFINITY;  // not in the fp32 sum
-      }
-    }
-  }
+  const int begin = stretch * pieces * PIECE, end = min(p.V, begin + pieces * PIECE);
+  Raw<T, NV> ahead;
+  ahead.load(src, begin + tid * VE, begin, p.V);
+  float bound = -INFINITY;  // candidates lie above it
+  float top = -INFINITY;    // the sum of the others counts from here
   float part = 0.f;
-  if (top > -INFINITY) {
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < E; ++i) s[i & 3] += exp_tail(x[i] - top);
-    part = (s[0] + s[1]) + (s[2] + s[3]);
-  }
-  const double total = wave_sum((double)part);
-  if (lane == 0) sums[wave] = total;
-  __syncthreads();
+  double gone = 0.0;        // of candidates that were thinned out, counted from ref
+  float ref = -INFINITY;
+  int n = 0;                // candidates of the wave
 
-  const int n = found;
-  for (int i = tid; i < n; i += kThreads) {
-    const float v = cand_x[i];
-    const int token = cand_v[i];
-    int r = 0;
-    for (int j = 0; j < n; ++j) {
-      const float o = cand_x[j];
-      r += (o > v || (o == v && cand_v[j] < token)) ? 1 : 0;
+  for (int at = begin; at < end; at += PIECE) {
+    const int first = at + tid * VE;  // token of the thread's first logit: the rest follow by constants
+    const bool whole = at + PIECE <= p.V;
+    const Raw<T, NV> raw = ahead;
+    if (at + PIECE < end) ahead.load(src, first + PIECE, at + PIECE, p.V);
+    if (at == begin) {
+      float mine = -INFINITY;
+#pragma unroll
+      for (int g = 0; g < E; g += G) {
+        float x[G];
+        raw.get(x, g, first, whole, p.V);
+#pragma unroll
+        for (int i = 0; i < G; ++i) mine = fmaxf(mine, x[i]);
+      }
+      const float sorted = sort_lanes(mine, lane);
+      if (lane == 0) tops[wave] = sorted;
+      if (lane == (M + kWaves - 1) / kWaves) bounds[wave] = sorted;
+      __syncthreads();
+      bound = fminf(fminf(bounds[0], bounds[1]), fminf(bounds[2], bounds[3]));
+      top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
     }
-    in_order[r] = v;
-    if (r < M) picks[r] = Pick{v, token};
+    float higher = bound;  // for the pieces to come: this one's later groups hold tokens on either side of a tie
+    const float c = top * kLog2e;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int g = 0; g < E; g += G) {
+      float x[G];
+      raw.get(x, g, first, whole, p.V);
+      float most = x[0];
+#pragma unroll
+      for (int i = 1; i < G; ++i) most = fmaxf(most, x[i]);
+      if (__any(most > bound)) {
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          const uint64_t all = __ballot(x[i] > bound);
+          if (all == 0) continue;
+          if (x[i] > bound) {
+            const int to = n + __popcll(all & ((1ull << lane) - 1));
+            held[wave].key[to] = to_key(x[i], first + (g + i) / VE * (kThreads * VE) + (g + i) % VE);
+            x[i] = -INFINITY;  // not in the fp32 sum
+          }
+          n += __popcll(all);
+        }
+        if (n > kHeld - 64 * G) {
+          thin(held[wave], best[wave], n, M, gone, ref);
+          n = M;
+          higher = key_logit(held[wave].key[M - 1]);
+        }
+      }
+      if (fabsf(top) < 1e30f) {
+#pragma unroll
+        for (int i = 0; i < G; ++i) sum[i & 3] += __builtin_amdgcn_exp2f(fmaf(x[i], kLog2e, -c));
+      } else if (top > -INFINITY) {
+#pragma unroll
+        for (int i = 0; i < G; ++i) sum[i & 3] += __builtin_amdgcn_exp2f((x[i] - top) * kLog2e);
+      } else {
+        // nothing above -inf in the first piece, and no sum to show a NaN
+#pragma unroll
+        for (int i = 0; i < G; ++i) sum[0] = x[i] != x[i] ? x[i] : sum[0];
+      }
+    }
+    part += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    bound = higher;
   }
-  for (int i = n + tid; i < M; i += kThreads) picks[i] = Pick{-INFINITY, -1};
-  __syncthreads();
-  if (wave == 0) {
+  bool careful = part != part || top == INFINITY;
+  if (lane < 8) held[wave].key[n + lane] = 0;
+  wave_fence();
+  float most = -INFINITY;  // of the wave's candidates
+  for (int i = lane; i < n; i += 64) most = fmaxf(most, key_logit(held[wave].key[i]));
+  most = wave_max(most);
+  careful |= most == INFINITY;
+  double own = 0.0;  // the candidates' part of the sum, counted from most
+  for (int i = lane; i < n; i += 64) own += exp((double)key_logit(held[wave].key[i]) - (double)most);
+  own = wave_sum(own);
+  // c is the rounded top log2(e): its rounding is a factor of all terms
+  double total = top > -INFINITY ? (double)part : 0.0;
+  if (fabsf(top) < 1e30f) total *= exp((double)(top * kLog2e) * 0.69314718055994530942 - (double)top);
+  total = wave_sum(total);
+  gone = wave_sum(gone);
+  if (lane == 0) {
+    sums[wave] = total;
+    gones[wave] = gone;
+    refs[wave] = ref;
+    counts[wave] = n;
+    helds[wave] = own;
+    mosts[wave] = most;
+  }
+  if (__syncthreads_or(careful)) {
+    careful_stretch(src, begin, end, M, picks, work.parts + list, few);
+    return;
+  }
+  // all waves' candidates in order: a lane's against every other
+  for (int i = lane; i < n; i += 64) {
+    const uint64_t key = held[wave].key[i];
+    int r = 0;
+    for (int w = 0; w < kWaves; ++w) r += count_greater(held[w].key, counts[w], key);
+    if (r < M) picks[r] = Pick{key_logit(key), key_token(key)};
+  }
+  const int m = counts[0] + counts[1] + counts[2] + counts[3];
+  if (tid == 0) {
+    const float highest = fmaxf(fmaxf(fmaxf(mosts[0], mosts[1]), fmaxf(mosts[2], mosts[3])), top);
     double s = 0.0;
-    if (top > -INFINITY)
-      for (int i = lane; i < n; i += 64) s += exp((double)in_order[i] - (double)top);
-    s = wave_sum(s);
-    if (lane == 0) work.parts[list] = Part{s + ((sums[0] + sums[1]) + (sums[2] + sums[3])), top, 0};
+    if (highest > -INFINITY) {
+      if (top > -INFINITY) s = ((sums[0] + sums[1]) + (sums[2] + sums[3])) * exp((double)top - (double)highest);
+      for (int w = 0; w < kWaves; ++w) {
+        if (counts[w]) s += helds[w] * exp((double)mosts[w] - (double)highest);
+        if (refs[w] > -INFINITY) s += gones[w] * exp((double)refs[w] - (double)highest);
+      }
+    }
+    work.parts[list] = Part{s, highest, 0};
+  }
+  if (m < M) {
+    __syncthreads();
+    fill_picks(src, begin, end, bound, m, M, picks, counts);
   }
 }
 
@@ -252,16 +452,31 @@ struct BeamBase {
 };
 __device__ __forceinline__ double pick_total(const Pick& k, const BeamBase& b) {
   if (b.kind == 2 || !(k.logit > -INFINITY)) return -INFINITY;
-  return b.rest + ((double)k.logit - b.top);
+  return b.rest + ((double)k.logit - b.top) + 0.0;  // never -0, which orders below 0
 }
 
-__global__ __launch_bounds__(kThreads) void beam_join_kernel(ccq_beam_params p, int chunks, BeamWork work) {
-  extern __shared__ __align__(16) unsigned char dyn[];  // heads' totals, then candidates: totals and places
+// A total as an unsigned number of the same order.
+__device__ __forceinline__ uint64_t order_key(double x) {
+  const uint64_t b = (uint64_t)__double_as_longlong(x);
+  return (int64_t)b < 0 ? ~b : b | 0x8000000000000000ull;
+}
+
+__device__ __forceinline__ double key_order(uint64_t key) {
+  return __longlong_as_double((long long)((int64_t)key < 0 ? key & 0x7fffffffffffffffull : ~key));
+}
+
+// Picks M of a request's lists: eight bits at a time of the total and then of the place, the continuations
+// that agree with the M-th best so far are counted by their next digit, until few enough are left with those
+// above them to be ranked by counting.
+constexpr int kRanked = 128;
+__global__ __launch_bounds__(kThreads) void beam_join_kernel(ccq_beam_params p, int stretches, BeamWork work) {
   __shared__ BeamBase base[kBeamMaxBeams];
-  __shared__ double bound_total;
-  __shared__ int bound_list, found;
+  __shared__ int bins[256];
+  __shared__ int digit, above, inside, found;
+  __shared__ uint64_t keys[kRanked + 4];
+  __shared__ unsigned places[kRanked + 4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = blockIdx.x, K = p.K, M = p.M;
-  const int lists = K * chunks;
+  const int lists = K * stretches, entries = lists * M;
   const Part* parts = work.parts + (size_t)n * lists;
   const Pick* picks = work.picks + (size_t)n * lists * M;
 
@@ -271,12 +486,12 @@ __global__ __launch_bounds__(kThreads) void beam_join_kernel(ccq_beam_params p, 
     BeamBase b{score > -INFINITY ? score : -INFINITY, 0.0, kind};  // NaN counts as -inf
     if (kind == 0) {
       float top = -INFINITY;
-      for (int c = lane; c < chunks; c += 64) top = fmaxf(top, parts[k * chunks + c].top);
+      for (int c = lane; c < stretches; c += 64) top = fmaxf(top, parts[k * stretches + c].top);
       top = wave_max(top);
       double s = 0.0;
       if (top > -INFINITY)
-        for (int c = lane; c < chunks; c += 64) {
-          const Part q = parts[k * chunks + c];
+        for (int c = lane; c < stretches; c += 64) {
+          const Part q = parts[k * stretches + c];
           if (q.top > -INFINITY) s += q.sum * exp((double)q.top - (double)top);
         }
       s = wave_sum(s);
@@ -287,102 +502,138 @@ __global__ __launch_bounds__(kThreads) void beam_join_kernel(ccq_beam_params p, 
     }
     if (lane == 0) base[k] = b;
   }
-  if (tid == 0) {
-    found = 0;
-    bound_total = -INFINITY;
-    bound_list = lists;  // every list, unless there are more than M
-  }
+  if (tid == 0) found = 0;
   __syncthreads();
 
-  if (lists > M) {
-    double* heads = reinterpret_cast<double*>(dyn);
-    for (int i = tid; i < lists; i += kThreads) {
-      const Pick k = picks[(size_t)i * M];
-      heads[i] = k.token < 0 ? -INFINITY : pick_total(k, base[i / chunks]);
+  auto entry = [&](int i, double& total, unsigned& place) {
+    const Pick q = picks[i];
+    const int k = i / (M * stretches);
+    total = pick_total(q, base[k]);
+    place = (unsigned)k * (unsigned)p.V + (unsigned)q.token;
+    return q.token >= 0;
+  };
+  uint64_t high = 0;  // the digits of the M-th best known so far: of the total, and of the place's complement
+  unsigned low = 0;
+  int step = 0, more = 0, left = entries;  // digits known, continuations above them, those that agree
+  while (more + left > kRanked) {
+    bins[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < entries; i += kThreads) {
+      double total;
+      unsigned place;
+      if (!entry(i, total, place)) continue;
+      const uint64_t key = order_key(total);
+      int d = -1;
+      if (step < 8) {
+        if (step == 0 || (key >> (64 - 8 * step)) == (high >> (64 - 8 * step))) d = (int)(key >> (56 - 8 * step)) & 255;
+      } else if (key == high) {
+        const unsigned at = ~place;
+        if (step == 8 || (at >> (96 - 8 * step)) == (low >> (96 - 8 * step))) d = (int)(at >> (88 - 8 * step)) & 255;
+      }
+      if (d >= 0) atomicAdd(&bins[d], 1);
     }
     __syncthreads();
-    double bt = 0.0;
-    int bl = -1;
-    for (int i = tid; i < lists; i += kThreads) {
-      const double v = heads[i];
-      int r = 0;
-      for (int j = 0; j < lists; ++j) {
-        const double o = heads[j];
-        r += (o > v || (o == v && j < i)) ? 1 : 0;
+    if (wave == 0) {
+      // lane 0 holds the four highest bins
+      int four = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) four += bins[255 - 4 * lane - j];
+      int sum = four;
+      for (int off = 1; off < 64; off <<= 1) {
+        const int o = __shfl_up(sum, off, 64);
+        if (lane >= off) sum += o;
       }
-      if (r == M - 1) {
-        bt = v;
-        bl = i;
+      const int want = M - more, before_me = sum - four;
+      if (before_me < want && sum >= want) {
+        int up = before_me, j = 0;
+        for (; j < 3 && up + bins[255 - 4 * lane - j] < want; ++j) up += bins[255 - 4 * lane - j];
+        digit = 255 - 4 * lane - j;
+        above = up;
+        inside = bins[255 - 4 * lane - j];
       }
     }
-    if (bl >= 0) {
-      bound_total = bt;
-      bound_list = bl;
-    }
+    __syncthreads();
+    if (step < 8) high |= (uint64_t)digit << (56 - 8 * step);
+    else low |= (unsigned)digit << (88 - 8 * step);
+    more += above;
+    left = inside;
+    ++step;
     __syncthreads();
   }
 
-  // the lists' entries that reach the bound: those of at most M lists
-  const double bt = bound_total;
-  const int bl = bound_list;
-  double* totals = reinterpret_cast<double*>(dyn);
-  unsigned* places = reinterpret_cast<unsigned*>(totals + M * M);
-  for (int i = tid; i < lists * M; i += kThreads) {
-    const int list = i / M, k = list / chunks;
-    const Pick q = picks[i];
-    if (q.token < 0) continue;
-    const double v = pick_total(q, base[k]);
-    if (v > bt || (v == bt && list <= bl)) {
+  for (int i = tid; i < entries; i += kThreads) {
+    double total;
+    unsigned place;
+    if (!entry(i, total, place)) continue;
+    const uint64_t key = order_key(total);
+    bool in = true;
+    if (step > 0) {
+      const int bits = step < 8 ? 64 - 8 * step : 0;
+      in = (key >> bits) >= (high >> bits);
+      if (step > 8 && key == high) in = (~place >> (96 - 8 * step)) >= (low >> (96 - 8 * step));
+    }
+    if (in) {
       const int at = atomicAdd(&found, 1);
-      totals[at] = v;
-      places[at] = (unsigned)k * (unsigned)p.V + (unsigned)q.token;
+      keys[at] = key;
+      places[at] = place;
     }
   }
   __syncthreads();
   const int c = found;
-  for (int i = tid; i < c; i += kThreads) {
-    const double v = totals[i];
-    const unsigned place = places[i];
+  if (tid < 4) keys[c + tid] = 0;  // the least there is
+  __syncthreads();
+  if (tid < c) {
+    const uint64_t key = keys[tid];
+    const unsigned place = places[tid];
     int r = 0;
-    for (int j = 0; j < c; ++j) {
-      const double o = totals[j];
-      r += (o > v || (o == v && places[j] < place)) ? 1 : 0;
+    for (int j = 0; j < c; j += 4) {
+      uint64_t k[4];
+      unsigned at[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        k[i] = keys[j + i];
+        at[i] = places[j + i];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r += (int)(k[i] > key) | ((int)(k[i] == key) & (int)(at[i] < place));
     }
     if (r < M) {
       const size_t at = (size_t)n * M + r;
       p.parent[at] = (int)(place / (unsigned)p.V);
       p.token[at] = (int)(place % (unsigned)p.V);
-      p.score[at] = (float)v;
+      p.score[at] = (float)key_order(key);
     }
   }
 }
 
 struct BeamShape {
-  int per_thread, chunks;
+  int per_thread, pieces, stretches;  // logits a thread holds, pieces of a stretch, stretches of a row
 };
 
-// Logits a thread holds: 64 where that leaves 512 workgroups, fewer for few rows, where the time is
-// the latency of one workgroup.
+// 32 logits a thread and as many stretches a row as make 1024 workgroups, four for each CU; with few rows,
+// where the time is the latency of one workgroup, 8 logits a thread.
 BeamShape beam_shape(const ccq_beam_params& p) {
-  BeamShape s{64, 0};
-  for (;; s.per_thread /= 2) {
-    const long long chunk = (long long)kThreads * s.per_thread;
-    s.chunks = (int)((p.V + chunk - 1) / chunk);
-    if (s.per_thread == 8 || (long long)p.N * p.K * s.chunks >= 512 || p.K * (long long)s.chunks * 2 > kBeamMaxLists)
-      return s;
-  }
+  const long long rows = (long long)p.N * p.K;
+  BeamShape s;
+  const long long quarter = (p.V + kThreads * 32 - 1) / (kThreads * 32);
+  s.per_thread = rows * quarter < 256 ? 8 : 32;
+  const long long whole = (p.V + (long long)kThreads * s.per_thread - 1) / (kThreads * s.per_thread);  // pieces of a row
+  long long want = (1024 + rows - 1) / rows;
+  if (want > whole) want = whole;
+  if (want * p.K > kBeamMaxLists) want = kBeamMaxLists / p.K;
+  s.pieces = (int)((whole + want - 1) / want);
+  s.stretches = (int)((whole + s.pieces - 1) / s.pieces);
+  return s;
 }
 
 template <typename T, int E>
 void launch_rows(const ccq_beam_params& p, const BeamShape& s, BeamWork w, hipStream_t stream) {
-  beam_rows_kernel<T, E><<<(unsigned)(p.N * p.K * s.chunks), kThreads, (size_t)p.M * E * 12, stream>>>(p, s.chunks, w);
+  beam_rows_kernel<T, E><<<(unsigned)(p.N * p.K * s.stretches), kThreads, 0, stream>>>(p, s.stretches, s.pieces, w);
 }
 
 template <typename T>
 void launch_rows_of(const ccq_beam_params& p, const BeamShape& s, BeamWork w, hipStream_t stream) {
-  if (s.per_thread == 64) launch_rows<T, 64>(p, s, w, stream);
-  else if (s.per_thread == 32) launch_rows<T, 32>(p, s, w, stream);
-  else if (s.per_thread == 16) launch_rows<T, 16>(p, s, w, stream);
+  if (s.per_thread == 32) launch_rows<T, 32>(p, s, w, stream);
   else launch_rows<T, 8>(p, s, w, stream);
 }
 
@@ -439,21 +690,20 @@ __global__ __launch_bounds__(kThreads) void beam_reorder_kernel(ReorderArgs a, u
 }  // namespace
 
 size_t beam_workspace_bytes(const ccq_beam_params& p) {
-  const size_t lists = (size_t)p.N * p.K * beam_shape(p).chunks;
+  const size_t lists = (size_t)p.N * p.K * beam_shape(p).stretches;
   return parts_bytes(lists) + lists * p.M * sizeof(Pick);
 }
 
 hipError_t launch_beam_select(const ccq_beam_params& p, hipStream_t stream) {
   const BeamShape s = beam_shape(p);
-  const size_t lists = (size_t)p.N * p.K * s.chunks;
+  const size_t lists = (size_t)p.N * p.K * s.stretches;
   unsigned char* ws = static_cast<unsigned char*>(p.workspace);
   const BeamWork w{reinterpret_cast<Part*>(ws), reinterpret_cast<Pick*>(ws + parts_bytes(lists))};
   if (p.dtype == CCQ_DTYPE_BF16) launch_rows_of<__bf16>(p, s, w, stream);
   else launch_rows_of<float>(p, s, w, stream);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const size_t heads = p.K * s.chunks > p.M ? (size_t)p.K * s.chunks * 8 : 0, cands = (size_t)p.M * p.M * 12;
-  beam_join_kernel<<<p.N, kThreads, heads > cands ? heads : cands, stream>>>(p, s.chunks, w);
+  beam_join_kernel<<<p.N, kThreads, 0, stream>>>(p, s.stretches, w);
   return hipGetLastError();
 }
 
