@@ -605,7 +605,8 @@ def ccq_bwd_chunked(rule, q, k, v, log_alpha, w_lambda, b_lambda, d_o, carry_in=
 # ---------------------------------------------------------------- operators around the read step
 #
 # They run on the device of their first tensor, whichever device is current, on the given stream or
-# that device's current one; what they allocate belongs to that stream.
+# that device's current one; what they allocate belongs to that stream.  A call on a few tokens takes the
+# GPU a few microseconds, so the checks here are kept short.
 
 _NORMS = {"none": 0, None: 0, "rms": 1, "l2": 2}
 MAX_REORDER_STATES = 16  # CCQ_MAX_REORDER_STATES
@@ -619,109 +620,132 @@ class _NoContext:
         return False
 
 
-_NO_CONTEXT = _NoContext()
+class _Ops:
+    """What every call below looks up, once: torch, its dtypes, and the library's functions."""
+
+    def __init__(self):
+        import torch
+        lib = load_library()
+        self.torch, self.empty = torch, torch.empty
+        self.f32, self.i32, self.i64, self.u8 = torch.float32, torch.int32, torch.int64, torch.uint8
+        self.codes = {torch.float32: CCQ_DTYPE_F32, torch.bfloat16: CCQ_DTYPE_BF16}
+        self.current_device, self.raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        self.nowhere = _NoContext()
+        for name in ("qk_norm_rope", "qk_norm_rope_backward", "scan", "scan_backward", "beam_select", "beam_reorder",
+                     "qk_backward_workspace_bytes", "scan_workspace_bytes", "scan_backward_workspace_bytes",
+                     "beam_select_workspace_bytes"):
+            setattr(self, name, getattr(lib, "ccq_" + name))
+
+    def dtype_code(self, t):
+        code = self.codes.get(t.dtype)
+        if code is None:
+            raise TypeError(f"unsupported tensor dtype {t.dtype}")
+        return code
+
+    def place(self, dev, stream):
+        """Context in which a call on tensors of ``dev`` allocates and launches."""
+        if dev.type != "cuda":
+            raise ValueError("tensors must be device tensors")
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+            return self.torch.cuda.stream(stream)
+        if dev.index != self.current_device():
+            return self.torch.cuda.device(dev)
+        return self.nowhere
 
 
-def _place(dev, stream):
-    """Context in which a call on tensors of ``dev`` allocates and launches."""
-    import torch
-    if dev.type != "cuda":
-        raise ValueError("tensors must be device tensors")
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-        return torch.cuda.stream(stream)
-    if dev.index != torch.cuda.current_device():
-        return torch.cuda.device(dev)
-    return _NO_CONTEXT
+_OPS = None
 
 
-def _check_on(name, t, dev, dtype, shape):
-    """t lies on dev, is dense and has this dtype and shape (None: absent)."""
+def _ops():
+    global _OPS
+    if _OPS is None:
+        _OPS = _Ops()
+    return _OPS
+
+
+def _refuse(name, t, dev, dtype, shape, layout):
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, is on {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be {layout}")
+
+
+def _dense(name, t, dev, dtype, shape):
+    """The address of t, which lies on dev, is dense and has this dtype and shape (None: absent)."""
     if t is None:
-        return
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, is on {t.device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+        return None
+    if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        _refuse(name, t, dev, dtype, shape, "contiguous")
+    return t.data_ptr()
 
 
-def _check_strided(name, t, dev, dtype, shape):
-    """As _check_on, but only the last dimension has to be dense.  Returns the other dimensions'
-    strides (0 where there is one entry, whose stride means nothing)."""
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, is on {t.device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+def _strided(name, t, dev, dtype, shape):
+    """The strides of t, as _dense but dense in its last dimension alone: 0 for the others where there is
+    one entry, whose stride means nothing."""
     st = t.stride()
-    if st[-1] != 1 and shape[-1] != 1:
-        raise ValueError(f"{name} must be dense in its last dimension")
+    if t.shape != shape or t.dtype != dtype or t.device != dev or (st[-1] != 1 and shape[-1] != 1):
+        _refuse(name, t, dev, dtype, shape, "dense in its last dimension")
     return [s if n > 1 else 0 for s, n in zip(st[:-1], shape)]
 
 
-def _call(name, params, dev):
-    import torch
-    fn = getattr(load_library(), name)
-    st = fn(params, torch._C._cuda_getCurrentRawStream(dev.index))
+def _launch(ops, name, fn, params, dev, size_fn=None, workspace=None):
+    """Calls fn, with the workspace that it asks for: the given one, or one allocated here.  The library
+    reads its size from the arguments alone, so it is asked first only where one is needed."""
+    keep = workspace
+    if size_fn is not None:
+        if workspace is None:
+            need = size_fn(params)
+            if need:
+                keep = ops.empty(need, dtype=ops.u8, device=dev)
+                params.workspace = keep.data_ptr()
+                params.workspace_bytes = need
+        else:
+            if workspace.device != dev or not workspace.is_contiguous():
+                raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+            params.workspace = workspace.data_ptr()
+            params.workspace_bytes = workspace.numel() * workspace.element_size()
+    st = fn(params, ops.raw_stream(dev.index))
     if st != 0:
-        raise CcqError(st, name)
+        raise CcqError(st, "ccq_" + name)
+    return keep
 
 
-def _workspace(params, size_fn, workspace, dev):
-    """Points params at the given workspace, or at one allocated here; returns what to keep alive."""
-    import torch
-    if workspace is None:
-        need = int(size_fn(params))
-        if need == 0:
-            return None
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    params.workspace = workspace.data_ptr()
-    params.workspace_bytes = workspace.numel() * workspace.element_size()
-    return workspace
-
-
-def _norm_code(kind):
-    if kind not in _NORMS:
-        raise ValueError(f"unknown norm {kind!r}: 'none', 'rms' or 'l2'")
-    return _NORMS[kind]
-
-
-def _qk_params(q, k, positions, inv_freq, q_weight, k_weight, q_norm, k_norm, eps, interleaved, expand_keys,
+def _qk_params(ops, q, k, dev, positions, inv_freq, q_weight, k_weight, q_norm, k_norm, eps, interleaved, expand_keys,
                position_offset, q_out, k_out):
-    import torch
     ref = q if q is not None else k
-    if ref is None:
-        raise ValueError("q or k must be given")
-    if ref.dim() != 4:
-        raise ValueError("q and k are [B, T, H, d]")
-    dev, dt = ref.device, ref.dtype
+    dt = ref.dtype
     B, T, _, d = ref.shape
-    Hq = 0 if q is None else q.shape[2]
-    Hk = 0 if k is None else k.shape[2]
-    qs = [0, 0, 0] if q is None else _check_strided("q", q, dev, dt, (B, T, Hq, d))
-    ks = [0, 0, 0] if k is None else _check_strided("k", k, dev, dt, (B, T, Hk, d))
-    _check_on("positions", positions, dev, torch.int64, (B, T))
-    rot = 0
-    if inv_freq is not None:
-        rot = 2 * inv_freq.numel()
-        _check_on("inv_freq", inv_freq, dev, torch.float32, (rot // 2,))
-    _check_on("q_weight", q_weight, dev, torch.float32, (d,))
-    _check_on("k_weight", k_weight, dev, torch.float32, (d,))
+    Hq = Hk = 0
+    qs = ks = (0, 0, 0)
+    qp = kp = None
+    if q is not None:
+        Hq = q.shape[2]
+        qs, qp = _strided("q", q, dev, dt, (B, T, Hq, d)), q.data_ptr()
+    if k is not None:
+        if k.dim() != 4:
+            raise ValueError("q and k are [B, T, H, d]")
+        Hk = k.shape[2]
+        ks, kp = _strided("k", k, dev, dt, (B, T, Hk, d)), k.data_ptr()
     if expand_keys and (Hk == 0 or Hq % Hk):
         raise ValueError(f"expand_keys: {Hk} key heads do not divide {Hq} query heads")
-    _check_on("q_out", q_out, dev, dt, (B, Hq, T, d))
-    _check_on("k_out", k_out, dev, dt, (B, Hq if expand_keys else Hk, T, d))
-    return QkParams(_dtype_code(ref), B, T, Hq, Hk, d, _norm_code(q_norm), _norm_code(k_norm), rot, int(interleaved),
-                    int(expand_keys), eps, _ptr(q), _ptr(k), *qs, *ks, _ptr(positions), position_offset,
-                    _ptr(inv_freq) if rot else None, _ptr(q_weight), _ptr(k_weight), _ptr(q_out), _ptr(k_out))
+    rot, freqs = 0, None
+    if inv_freq is not None and inv_freq.numel():
+        rot = 2 * inv_freq.numel()
+        freqs = _dense("inv_freq", inv_freq, dev, ops.f32, (rot // 2,))
+    try:
+        norms = _NORMS[q_norm], _NORMS[k_norm]
+    except KeyError as e:
+        raise ValueError(f"unknown norm {e.args[0]!r}: 'none', 'rms' or 'l2'") from None
+    return QkParams(ops.dtype_code(ref), B, T, Hq, Hk, d, *norms, rot, 1 if interleaved else 0, 1 if expand_keys else 0,
+                    eps, qp, kp, *qs, *ks, _dense("positions", positions, dev, ops.i64, (B, T)), position_offset, freqs,
+                    _dense("q_weight", q_weight, dev, ops.f32, (d,)), _dense("k_weight", k_weight, dev, ops.f32, (d,)),
+                    _dense("q_out", q_out, dev, dt, (B, Hq, T, d)),
+                    _dense("k_out", k_out, dev, dt, (B, Hq if expand_keys else Hk, T, d)))
 
 
 def ccq_qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=None, q_norm="rms", k_norm="l2",
@@ -733,21 +757,22 @@ def ccq_qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weigh
     None; positions [B, T] int64, or token t stands at position_offset + t; inv_freq [rot / 2] fp32, or
     None for no rotation.  Returns (q_out [B, H_q, T, d], k_out [B, H_k, T, d], or [B, H_q, T, d] with
     expand_keys), None in the place of an absent side."""
-    import torch
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q or k must be given")
-    dev = ref.device
-    with _place(dev, stream):
+    if ref.dim() != 4:
+        raise ValueError("q and k are [B, T, H, d]")
+    ops, dev = _ops(), ref.device
+    with ops.place(dev, stream):
         B, T, _, d = ref.shape
-        if q is not None and q_out is None:
-            q_out = torch.empty((B, q.shape[2], T, d), dtype=q.dtype, device=dev)
-        if k is not None and k_out is None:
+        if q_out is None and q is not None:
+            q_out = ops.empty((B, q.shape[2], T, d), dtype=q.dtype, device=dev)
+        if k_out is None and k is not None:
             heads = q.shape[2] if expand_keys and q is not None else k.shape[2]
-            k_out = torch.empty((B, heads, T, d), dtype=k.dtype, device=dev)
-        p = _qk_params(q, k, positions, inv_freq, q_weight, k_weight, q_norm, k_norm, eps, interleaved, expand_keys,
-                       position_offset, q_out, k_out)
-        _call("ccq_qk_norm_rope", p, dev)
+            k_out = ops.empty((B, heads, T, d), dtype=k.dtype, device=dev)
+        p = _qk_params(ops, q, k, dev, positions, inv_freq, q_weight, k_weight, q_norm, k_norm, eps, interleaved,
+                       expand_keys, position_offset, q_out, k_out)
+        _launch(ops, "qk_norm_rope", ops.qk_norm_rope, p, dev)
     return q_out, k_out
 
 
@@ -758,39 +783,37 @@ def ccq_qk_norm_rope_backward(q, k, dq_out, dk_out, positions=None, inv_freq=Non
     fp32 gradients of its outputs, dense; dk_out has H_q heads if the keys were expanded.  Returns a
     dict: dq, dk (dtype and shape of q, k, into the given views if any), dq_weight, dk_weight (fp32
     [d], None without that weight)."""
-    import torch
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q or k must be given")
-    dev, dt = ref.device, ref.dtype
-    lib = load_library()
-    with _place(dev, stream):
+    if ref.dim() != 4:
+        raise ValueError("q and k are [B, T, H, d]")
+    ops, dev, dt = _ops(), ref.device, ref.dtype
+    with ops.place(dev, stream):
         B, T, _, d = ref.shape
         Hq = 0 if q is None else q.shape[2]
         Hk = 0 if k is None else k.shape[2]
         expand = k is not None and dk_out is not None and dk_out.shape[1] != Hk
-        f = _qk_params(q, k, positions, inv_freq, q_weight, k_weight, q_norm, k_norm, eps, interleaved, expand,
+        f = _qk_params(ops, q, k, dev, positions, inv_freq, q_weight, k_weight, q_norm, k_norm, eps, interleaved, expand,
                        position_offset, None, None)
-        out = dict(dq=None, dk=None, dq_weight=None, dk_weight=None)
-        if q is not None:
-            out["dq"] = torch.empty((B, T, Hq, d), dtype=dt, device=dev) if dq is None else dq
-        if k is not None:
-            out["dk"] = torch.empty((B, T, Hk, d), dtype=dt, device=dev) if dk is None else dk
-        for name, t, heads in (("dq_out", dq_out, Hq), ("dk_out", dk_out, Hq if expand else Hk)):
+        for name, t, heads in (("dq_out", dq_out, Hq), ("dk_out", dk_out, Hk)):
             if (t is None) != (heads == 0):
                 raise ValueError(f"{name} is given with its input and only with it")
-            _check_on(name, t, dev, torch.float32, (B, heads, T, d))
-        qs = [0, 0, 0] if q is None else _check_strided("dq", out["dq"], dev, dt, (B, T, Hq, d))
-        ks = [0, 0, 0] if k is None else _check_strided("dk", out["dk"], dev, dt, (B, T, Hk, d))
-        if q_weight is not None:
-            out["dq_weight"] = torch.empty(d, dtype=torch.float32, device=dev)
-        if k_weight is not None:
-            out["dk_weight"] = torch.empty(d, dtype=torch.float32, device=dev)
-        p = QkBwdParams(f, _ptr(dq_out), _ptr(dk_out), _ptr(out["dq"]), _ptr(out["dk"]), *qs, *ks,
-                        _ptr(out["dq_weight"]), _ptr(out["dk_weight"]), None, 0)
-        keep = _workspace(p, lib.ccq_qk_backward_workspace_bytes, workspace, dev)  # noqa: F841
-        _call("ccq_qk_norm_rope_backward", p, dev)
-    return out
+        qs = ks = (0, 0, 0)
+        if q is not None:
+            dq = ops.empty((B, T, Hq, d), dtype=dt, device=dev) if dq is None else dq
+            qs = _strided("dq", dq, dev, dt, (B, T, Hq, d))
+        if k is not None:
+            dk = ops.empty((B, T, Hk, d), dtype=dt, device=dev) if dk is None else dk
+            ks = _strided("dk", dk, dev, dt, (B, T, Hk, d))
+        dwq = None if q_weight is None else ops.empty(d, dtype=ops.f32, device=dev)
+        dwk = None if k_weight is None else ops.empty(d, dtype=ops.f32, device=dev)
+        p = QkBwdParams(f, _dense("dq_out", dq_out, dev, ops.f32, (B, Hq, T, d)),
+                        _dense("dk_out", dk_out, dev, ops.f32, (B, Hq if expand else Hk, T, d)),
+                        None if q is None else dq.data_ptr(), None if k is None else dk.data_ptr(), *qs, *ks, _ptr(dwq),
+                        _ptr(dwk), None, 0)
+        _launch(ops, "qk_norm_rope_backward", ops.qk_norm_rope_backward, p, dev, ops.qk_backward_workspace_bytes, workspace)
+    return dict(dq=dq if q is not None else None, dk=dk if k is not None else None, dq_weight=dwq, dk_weight=dwk)
 
 
 def scan_carry_shape(x):
@@ -806,26 +829,19 @@ def ccq_scan(x, log_alpha, h0=None, h_out=None, y=None, lengths=None, complement
     views; h0, h_out [B, D] fp32 (h_out may be h0: the serving step); lengths [B] int32; chunk_carry:
     fp32 tensor of ``scan_carry_shape(x)`` that receives the state before every 64-token chunk, for
     ``ccq_scan_backward``.  Returns y [B, T, D] (rows at t >= length are left as they were)."""
-    import torch
     if x.dim() != 3:
         raise ValueError("x is [B, T, D]")
-    dev, dt = x.device, x.dtype
-    shape = B, T, D = tuple(x.shape)
-    lib = load_library()
-    with _place(dev, stream):
+    ops, dev, dt = _ops(), x.device, x.dtype
+    shape = B, T, D = x.shape
+    with ops.place(dev, stream):
         if y is None:
-            y = torch.empty(shape, dtype=dt, device=dev)
-        xs = _check_strided("x", x, dev, dt, shape)
-        gs = _check_strided("log_alpha", log_alpha, dev, dt, shape)
-        _check_on("y", y, dev, dt, shape)
-        _check_on("h0", h0, dev, torch.float32, (B, D))
-        _check_on("h_out", h_out, dev, torch.float32, (B, D))
-        _check_on("lengths", lengths, dev, torch.int32, (B,))
-        _check_on("chunk_carry", chunk_carry, dev, torch.float32, (B, (T + 63) // 64, D))
-        p = ScanParams(_dtype_code(x), B, T, D, int(complement), _ptr(x), _ptr(log_alpha), *xs, *gs, _ptr(lengths),
-                       _ptr(h0), _ptr(y), _ptr(h_out), _ptr(chunk_carry), None, 0)
-        keep = _workspace(p, lib.ccq_scan_workspace_bytes, workspace, dev)  # noqa: F841
-        _call("ccq_scan", p, dev)
+            y = ops.empty(shape, dtype=dt, device=dev)
+        p = ScanParams(ops.dtype_code(x), B, T, D, 1 if complement else 0, x.data_ptr(), log_alpha.data_ptr(),
+                       *_strided("x", x, dev, dt, shape), *_strided("log_alpha", log_alpha, dev, dt, shape),
+                       _dense("lengths", lengths, dev, ops.i32, (B,)), _dense("h0", h0, dev, ops.f32, (B, D)),
+                       _dense("y", y, dev, dt, shape), _dense("h_out", h_out, dev, ops.f32, (B, D)),
+                       _dense("chunk_carry", chunk_carry, dev, ops.f32, (B, (T + 63) // 64, D)), None, 0)
+        _launch(ops, "scan", ops.scan, p, dev, ops.scan_workspace_bytes, workspace)
     return y
 
 
@@ -835,31 +851,24 @@ def ccq_scan_backward(x, log_alpha, dy, h0=None, dh_out=None, lengths=None, comp
     strided view is fine); dh_out [B, D] fp32: gradient of h_out, or None; chunk_carry: what the
     forward kept, or None to form it again.  Returns a dict: dx, dlog_alpha (dtype of x; zeros at
     t >= length) and, with want_dh0, dh0 fp32."""
-    import torch
     if x.dim() != 3:
         raise ValueError("x is [B, T, D]")
-    dev, dt = x.device, x.dtype
-    shape = B, T, D = tuple(x.shape)
-    lib = load_library()
-    with _place(dev, stream):
-        out = dict(dx=torch.empty(shape, dtype=dt, device=dev) if dx is None else dx,
-                   dlog_alpha=torch.empty(shape, dtype=dt, device=dev) if dlog_alpha is None else dlog_alpha)
-        xs = _check_strided("x", x, dev, dt, shape)
-        gs = _check_strided("log_alpha", log_alpha, dev, dt, shape)
-        ys = _check_strided("dy", dy, dev, dt, shape)
-        _check_on("dx", out["dx"], dev, dt, shape)
-        _check_on("dlog_alpha", out["dlog_alpha"], dev, dt, shape)
-        _check_on("h0", h0, dev, torch.float32, (B, D))
-        _check_on("dh_out", dh_out, dev, torch.float32, (B, D))
-        _check_on("lengths", lengths, dev, torch.int32, (B,))
-        _check_on("chunk_carry", chunk_carry, dev, torch.float32, (B, (T + 63) // 64, D))
+    ops, dev, dt = _ops(), x.device, x.dtype
+    shape = B, T, D = x.shape
+    with ops.place(dev, stream):
+        out = dict(dx=ops.empty(shape, dtype=dt, device=dev) if dx is None else dx,
+                   dlog_alpha=ops.empty(shape, dtype=dt, device=dev) if dlog_alpha is None else dlog_alpha)
         if want_dh0:
-            out["dh0"] = torch.empty((B, D), dtype=torch.float32, device=dev)
-        p = ScanBwdParams(_dtype_code(x), B, T, D, int(complement), _ptr(x), _ptr(log_alpha), _ptr(dy), *xs, *gs, *ys,
-                          _ptr(lengths), _ptr(h0), _ptr(dh_out), _ptr(chunk_carry), _ptr(out["dx"]),
-                          _ptr(out["dlog_alpha"]), _ptr(out.get("dh0")), None, 0)
-        keep = _workspace(p, lib.ccq_scan_backward_workspace_bytes, workspace, dev)  # noqa: F841
-        _call("ccq_scan_backward", p, dev)
+            out["dh0"] = ops.empty((B, D), dtype=ops.f32, device=dev)
+        p = ScanBwdParams(ops.dtype_code(x), B, T, D, 1 if complement else 0, x.data_ptr(), log_alpha.data_ptr(),
+                          dy.data_ptr(), *_strided("x", x, dev, dt, shape),
+                          *_strided("log_alpha", log_alpha, dev, dt, shape), *_strided("dy", dy, dev, dt, shape),
+                          _dense("lengths", lengths, dev, ops.i32, (B,)), _dense("h0", h0, dev, ops.f32, (B, D)),
+                          _dense("dh_out", dh_out, dev, ops.f32, (B, D)),
+                          _dense("chunk_carry", chunk_carry, dev, ops.f32, (B, (T + 63) // 64, D)),
+                          _dense("dx", out["dx"], dev, dt, shape), _dense("dlog_alpha", out["dlog_alpha"], dev, dt, shape),
+                          _ptr(out.get("dh0")), None, 0)
+        _launch(ops, "scan_backward", ops.scan_backward, p, dev, ops.scan_backward_workspace_bytes, workspace)
     return out
 
 
@@ -867,57 +876,48 @@ def ccq_beam_select(logits, scores, m: int, finished=None, pad_token: int = 0, w
     """One selection step of beam search (see ``ccq_beam_select`` in ccq.h).  logits [N, K, V] (rows may
     be padded: logits[..., :V] of a wider tensor), scores [N, K] fp32, finished [N, K] bool / uint8 or
     None.  Returns a dict: token, parent (int32 [N, m]) and score (fp32 [N, m]), best first."""
-    import torch
     if logits.dim() != 3:
         raise ValueError("logits is [N, K, V]")
-    dev = logits.device
-    N, K, V = logits.shape
-    lib = load_library()
-    with _place(dev, stream):
-        st = _check_strided("logits", logits, dev, logits.dtype, (N, K, V))
+    if m <= 0:
+        raise ValueError("m must be positive")
+    ops, dev = _ops(), logits.device
+    shape = N, K, V = logits.shape
+    with ops.place(dev, stream):
+        st = _strided("logits", logits, dev, logits.dtype, shape)
         stride = st[1] if K > 1 else st[0] if N > 1 else V
         if N > 1 and K > 1 and st[0] != K * st[1]:
             raise ValueError("the rows of logits must be evenly spaced")
-        _check_on("scores", scores, dev, torch.float32, (N, K))
-        if finished is not None and finished.dtype == torch.bool:
-            finished = finished.view(torch.uint8)
-        _check_on("finished", finished, dev, torch.uint8, (N, K))
-        if m <= 0:
-            raise ValueError("m must be positive")
-        out = dict(token=torch.empty((N, m), dtype=torch.int32, device=dev),
-                   parent=torch.empty((N, m), dtype=torch.int32, device=dev),
-                   score=torch.empty((N, m), dtype=torch.float32, device=dev))
-        p = BeamParams(_dtype_code(logits), N, K, V, m, _ptr(logits), stride, _ptr(scores), _ptr(finished), pad_token,
-                       _ptr(out["token"]), _ptr(out["parent"]), _ptr(out["score"]), None, 0)
-        keep = _workspace(p, lib.ccq_beam_select_workspace_bytes, workspace, dev)  # noqa: F841
-        _call("ccq_beam_select", p, dev)
-    return out
+        if finished is not None and finished.dtype == ops.torch.bool:
+            finished = finished.view(ops.u8)
+        token = ops.empty((N, m), dtype=ops.i32, device=dev)
+        parent = ops.empty((N, m), dtype=ops.i32, device=dev)
+        score = ops.empty((N, m), dtype=ops.f32, device=dev)
+        p = BeamParams(ops.dtype_code(logits), N, K, V, m, logits.data_ptr(), stride,
+                       _dense("scores", scores, dev, ops.f32, (N, K)), _dense("finished", finished, dev, ops.u8, (N, K)),
+                       pad_token, token.data_ptr(), parent.data_ptr(), score.data_ptr(), None, 0)
+        _launch(ops, "beam_select", ops.beam_select, p, dev, ops.beam_select_workspace_bytes, workspace)
+    return dict(token=token, parent=parent, score=score)
 
 
 def ccq_beam_reorder(states, parent, stream=None):
     """Moves every state's rows to the beams that continue them, in place (see ``ccq_beam_reorder`` in
     ccq.h).  states: up to 16 dense tensors [N K, ...] of any dtype whose rows are a multiple of 4
     bytes; parent [N, K] int32, as ``ccq_beam_select`` returns it for m = K."""
-    import torch
-    lib = load_library()
-    if not states or len(states) > MAX_REORDER_STATES:
-        raise ValueError(f"1 to {MAX_REORDER_STATES} states, got {len(states)}")
+    count = len(states)
+    if not 0 < count <= MAX_REORDER_STATES:
+        raise ValueError(f"1 to {MAX_REORDER_STATES} states, got {count}")
     if parent.dim() != 2:
         raise ValueError("parent is [N, K]")
-    dev = parent.device
+    ops, dev = _ops(), parent.device
     N, K = parent.shape
-    with _place(dev, stream):
-        _check_on("parent", parent, dev, torch.int32, (N, K))
-        count = len(states)
-        ptrs, rows = (ctypes.c_void_p * count)(), (ctypes.c_size_t * count)()
+    with ops.place(dev, stream):
+        at = _dense("parent", parent, dev, ops.i32, (N, K))
+        rows = N * K
         for i, t in enumerate(states):
-            if t.device != dev:
-                raise ValueError(f"states[{i}] must be on {dev}, is on {t.device}")
-            if not t.is_contiguous() or t.dim() < 1 or t.shape[0] != N * K:
-                raise ValueError(f"states[{i}] must be contiguous with {N * K} rows")
-            ptrs[i] = t.data_ptr()
-            rows[i] = t.numel() // (N * K) * t.element_size() if N * K else 0
-        st = lib.ccq_beam_reorder(count, ptrs, rows, N, K, parent.data_ptr(),
-                                  torch._C._cuda_getCurrentRawStream(dev.index))
+            if t.device != dev or not t.is_contiguous() or t.dim() < 1 or t.shape[0] != rows:
+                raise ValueError(f"states[{i}] must be a contiguous tensor on {dev} with {rows} rows")
+        ptrs = (ctypes.c_void_p * count)(*[t.data_ptr() for t in states])
+        sizes = (ctypes.c_size_t * count)(*[t.nbytes // rows if rows else 0 for t in states])
+        st = ops.beam_reorder(count, ptrs, sizes, N, K, at, ops.raw_stream(dev.index))
         if st != 0:
             raise CcqError(st, "ccq_beam_reorder")
