@@ -244,6 +244,11 @@ __device__ __forceinline__ int count_greater(const uint64_t* keys, int n, uint64
   return r;
 }
 
+// How many of the lanes in `mask` stand before this one.
+__device__ __forceinline__ int lanes_below(uint64_t mask) {
+  return __builtin_amdgcn_mbcnt_hi((unsigned)(mask >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)mask, 0));
+}
+
 // A wave's candidates in LDS, in the order they were found.  Before a group of eight logits a lane is looked
 // at, there is room for all of them.
 constexpr int kGroup = 8;
@@ -358,13 +363,13 @@ __global__ __launch_bounds__(kThreads) void beam_rows_kernel(ccq_beam_params p, 
       float most = x[0];
 #pragma unroll
       for (int i = 1; i < G; ++i) most = fmaxf(most, x[i]);
-      if (__any(most > bound)) {
+      if (__builtin_amdgcn_ballot_w64(most > bound)) {
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-          const uint64_t all = __ballot(x[i] > bound);
+          const uint64_t all = __builtin_amdgcn_ballot_w64(x[i] > bound);
           if (all == 0) continue;
           if (x[i] > bound) {
-            const int to = n + __popcll(all & ((1ull << lane) - 1));
+            const int to = n + lanes_below(all);
             held[wave].key[to] = to_key(x[i], first + (g + i) / VE * (kThreads * VE) + (g + i) % VE);
             x[i] = -INFINITY;  // not in the fp32 sum
           }
@@ -465,14 +470,18 @@ __device__ __forceinline__ double key_order(uint64_t key) {
   return __longlong_as_double((long long)((int64_t)key < 0 ? key & 0x7fffffffffffffffull : ~key));
 }
 
-// Picks M of a request's lists: eight bits at a time of the total and then of the place, the continuations
-// that agree with the M-th best so far are counted by their next digit, until few enough are left with those
-// above them to be ranked by counting.
+// Picks M of a request's lists.  With more lists than picks, M of the lists' heads give a bound that few
+// others reach.  Where many do, or there are few lists: eight bits at a time of the total and then of the
+// place, the continuations that agree with the M-th best so far are counted by their next digit, until few
+// enough are left with those above them to be ranked by counting.
 constexpr int kRanked = 128;
+constexpr int kHeads = 256;
 __global__ __launch_bounds__(kThreads) void beam_join_kernel(ccq_beam_params p, int stretches, BeamWork work) {
   __shared__ BeamBase base[kBeamMaxBeams];
   __shared__ int bins[256];
   __shared__ int digit, above, inside, found;
+  __shared__ unsigned long long least;
+  __shared__ __align__(16) uint64_t heads[kHeads + 8];
   __shared__ uint64_t keys[kRanked + 4];
   __shared__ unsigned places[kRanked + 4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = blockIdx.x, K = p.K, M = p.M;
@@ -502,7 +511,10 @@ __global__ __launch_bounds__(kThreads) void beam_join_kernel(ccq_beam_params p, 
     }
     if (lane == 0) base[k] = b;
   }
-  if (tid == 0) found = 0;
+  if (tid == 0) {
+    found = 0;
+    least = ~0ull;
+  }
   __syncthreads();
 
   auto entry = [&](int i, double& total, unsigned& place) {
@@ -512,10 +524,37 @@ __global__ __launch_bounds__(kThreads) void beam_join_kernel(ccq_beam_params p, 
     place = (unsigned)k * (unsigned)p.V + (unsigned)q.token;
     return q.token >= 0;
   };
+  bool few = false;  // those that reach the heads' bound
+  if (lists > M && lists <= kHeads) {
+    double total;
+    unsigned place;
+    const uint64_t head = tid < lists && entry(tid * M, total, place) ? order_key(total) : 0;
+    heads[tid] = head;
+    if (tid < 8) heads[kHeads + tid] = 0;
+    __syncthreads();
+    if (head != 0 && count_greater(heads, lists, head) < M) atomicMin(&least, (unsigned long long)head);
+    __syncthreads();
+    const uint64_t bound = least;
+    for (int i = tid; i < entries; i += kThreads) {
+      if (!entry(i, total, place)) continue;
+      const uint64_t key = order_key(total);
+      if (key >= bound) {
+        const int at = atomicAdd(&found, 1);
+        if (at < kRanked) {
+          keys[at] = key;
+          places[at] = place;
+        }
+      }
+    }
+    __syncthreads();
+    few = found >= M && found <= kRanked;
+    __syncthreads();
+    if (!few && tid == 0) found = 0;
+  }
   uint64_t high = 0;  // the digits of the M-th best known so far: of the total, and of the place's complement
   unsigned low = 0;
   int step = 0, more = 0, left = entries;  // digits known, continuations above them, those that agree
-  while (more + left > kRanked) {
+  while (!few && more + left > kRanked) {
     bins[tid] = 0;
     __syncthreads();
     for (int i = tid; i < entries; i += kThreads) {
@@ -561,23 +600,24 @@ __global__ __launch_bounds__(kThreads) void beam_join_kernel(ccq_beam_params p, 
     __syncthreads();
   }
 
-  for (int i = tid; i < entries; i += kThreads) {
-    double total;
-    unsigned place;
-    if (!entry(i, total, place)) continue;
-    const uint64_t key = order_key(total);
-    bool in = true;
-    if (step > 0) {
-      const int bits = step < 8 ? 64 - 8 * step : 0;
-      in = (key >> bits) >= (high >> bits);
-      if (step > 8 && key == high) in = (~place >> (96 - 8 * step)) >= (low >> (96 - 8 * step));
+  if (!few)
+    for (int i = tid; i < entries; i += kThreads) {
+      double total;
+      unsigned place;
+      if (!entry(i, total, place)) continue;
+      const uint64_t key = order_key(total);
+      bool in = true;
+      if (step > 0) {
+        const int bits = step < 8 ? 64 - 8 * step : 0;
+        in = (key >> bits) >= (high >> bits);
+        if (step > 8 && key == high) in = (~place >> (96 - 8 * step)) >= (low >> (96 - 8 * step));
+      }
+      if (in) {
+        const int at = atomicAdd(&found, 1);
+        keys[at] = key;
+        places[at] = place;
+      }
     }
-    if (in) {
-      const int at = atomicAdd(&found, 1);
-      keys[at] = key;
-      places[at] = place;
-    }
-  }
   __syncthreads();
   const int c = found;
   if (tid < 4) keys[c + tid] = 0;  // the least there is

@@ -243,7 +243,13 @@ __device__ __forceinline__ Pair unpack(uint64_t word) {
   return Pair{__uint_as_float((unsigned)word), __uint_as_float((unsigned)(word >> 32))};
 }
 
-// The fold of n published pairs, `stride` words apart.  The wave waits as one.
+__device__ __forceinline__ uint64_t peek(const uint64_t* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ bool is_empty(uint64_t word) { return (unsigned)word == 0xffffffffu; }
+
+// The fold of n published pairs, `stride` words apart.  The wave waits as one: where a pair is missing, one
+// lane for each pair watches its first word, so that waiting costs the memory little.
 template <int BATCH>
 __device__ __forceinline__ Pair fold_published(const uint64_t* from, int lane, int n, size_t stride) {
   Pair acc{1.f, 0.f};
@@ -253,13 +259,14 @@ __device__ __forceinline__ Pair fold_published(const uint64_t* from, int lane, i
     for (;;) {
       bool empty = false;
 #pragma unroll
-      for (int j = 0; j < BATCH; ++j)
-        w[j] = __hip_atomic_load(from + (size_t)min(i + j, n - 1) * stride + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      for (int j = 0; j < BATCH; ++j) w[j] = peek(from + (size_t)min(i + j, n - 1) * stride + lane);
 #pragma unroll
-      for (int j = 0; j < BATCH; ++j) empty |= (unsigned)w[j] == 0xffffffffu;
+      for (int j = 0; j < BATCH; ++j) empty |= is_empty(w[j]);
       if (!__any(empty)) break;
-      if (++polls > (1 << 19)) return Pair{-0.f, __int_as_float(0x7fc00000)};
-      __builtin_amdgcn_s_sleep(1);
+      do {
+        if (++polls > (1 << 19)) return Pair{-0.f, __int_as_float(0x7fc00000)};
+        __builtin_amdgcn_s_sleep(4);
+      } while (__any(lane < BATCH && is_empty(peek(from + (size_t)min(i + lane, n - 1) * stride))));
     }
 #pragma unroll
     for (int j = 0; j < BATCH; ++j)
@@ -379,10 +386,10 @@ __device__ __forceinline__ Place next_tile(const Tiles& t, unsigned* shared) {
 template <typename T, bool COMPLEMENT>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : COMPLEMENT ? 4 : 6) void scan_tile_kernel(ccq_scan_params p, Tiles tiles) {
   constexpr int RUN = Run<T, false>::n, TILE = Run<T, false>::tile;
-  __shared__ unsigned ticket;
+  // 40 KB: four workgroups fit a CU
   __shared__ __align__(16) Pair runs[kRuns][kCols];  // every run's pair, and then the state before it
   __shared__ Parts own, parts;
-  const Place place = next_tile(tiles, &ticket);
+  const Place place = next_tile(tiles, reinterpret_cast<unsigned*>(&parts));
   const int s = place.order, column = place.column;
   const int b = column / tiles.per_row, c_tile = (column - b * tiles.per_row) * kCols;
   const int n = sequence_length(p.lengths, b, p.T);
@@ -533,11 +540,10 @@ template <typename T, bool COMPLEMENT>
 __global__ __launch_bounds__(kThreads, 4) void scan_backward_tile_kernel(ccq_scan_bwd_params p, const float* carry,
                                                                          Tiles tiles) {
   constexpr int RUN = Run<T, true>::n, TILE = Run<T, true>::tile;
-  __shared__ unsigned ticket;
   __shared__ __align__(16) Pair runs[kRuns][kCols];   // every run's pair; then state before it, adjoint behind it
   __shared__ __align__(16) float back[kRuns][kCols];  // q of every run for the adjoint
   __shared__ Parts ahead, own, parts;                 // own: for the adjoint, the tile's last part first
-  const Place place = next_tile(tiles, &ticket);
+  const Place place = next_tile(tiles, reinterpret_cast<unsigned*>(&parts));
   const int order = place.order, column = place.column, s = tiles.segments - 1 - order;
   const int b = column / tiles.per_row, c_tile = (column - b * tiles.per_row) * kCols;
   const int n = sequence_length(p.lengths, b, p.T);
