@@ -7,12 +7,15 @@
 // best continuations out of the stretches' lists.
 //
 // Picking M of many needs no sort.  A workgroup goes through its stretch in pieces held in registers (32
-// logits a thread).  In the first, the (M / 4 + 1)-th best of each wave's thread maxima is found; at least
-// M logits reach the least of the four, the bound, and few lie above it.  Those, and in the later pieces
-// whatever lies above the bound, go into a list of their wave's own, in no order, without a word between
-// the waves; a list that fills up (a row that rises, a mask over the first tokens) is thinned to its M best,
-// which raise the wave's bound.  Should fewer than M logits lie above the bound, as in a row of few values
-// or under a mask that leaves few tokens, the lowest tokens at the bound itself are looked up at the end.
+// logits a thread).  In the first, the (M / 4 + 1)-th best of each wave's thread maxima is found (of a stretch
+// shorter than a piece, for the waves that it fills); at least M logits reach the least of them, the bound,
+// and few lie above it.  Those, and in the later pieces whatever lies above the bound, go into a list of their
+// wave's own, in no order, without a word between the waves; a list that fills up (a row that rises, a mask
+// over the first tokens) is thinned to its M best, which raise the wave's bound.  Should fewer than M logits
+// lie above the bound, as in a row of few values or under a mask that leaves few tokens, the lowest tokens at
+// the bound itself are looked up at the end.  The lists are put in order by counting, for each candidate, the
+// greater ones; that is quadratic, so longer lists are thinned first (72 bf16 rows of 1,532, M = 24: 64 us
+// with a bound from all four waves, one of them empty, and no thinning; 8 us).
 //
 // Scores of different beams meet in the comparison, so the normaliser has to be good to more than
 // fp32: the candidates, which carry most of a peaked distribution, are left out of the fp32 sum and added
@@ -254,35 +257,67 @@ __device__ __forceinline__ int lanes_below(uint64_t mask) {
 constexpr int kGroup = 8;
 constexpr int kHeld = 64 * kGroup + 128;
 struct Held {
-  uint64_t key[kHeld + 8];
-};
-struct Best {
-  uint64_t key[64];
+  uint64_t key[(kHeld + 8 + 255) / 256 * 256];
 };
 __device__ __forceinline__ void wave_fence() {
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_wave_barrier();
 }
 
-// Thins a wave's n candidates to the M best, in order.  The others are added to gone, which counts from ref.
-__device__ __forceinline__ void thin(Held& held, Best& best, int n, int M, double& gone, float& ref) {
-  const int lane = threadIdx.x & 63;
-  if (lane < 8) held.key[n + lane] = 0;
+// Thins a wave's n >= M candidates to the M best, in the order they stand; returns the least of their logits.
+// The others are added to gone, which counts from ref.  All keys differ, so some number is reached by M of
+// them alone: its bits are found from the highest down.
+// The keys are read again for every bit: held in registers they would cost the kernel a workgroup a CU.
+__device__ __forceinline__ float thin(Held& held, int n, int M, double& gone, float& ref) {
+  const int lane = threadIdx.x & 63, padded = (n + 255) & ~255;
+  for (int i = n + lane; i < padded; i += 64) held.key[i] = 0;
   wave_fence();
-  float highest = -INFINITY;
-  for (int i = lane; i < n; i += 64) highest = fmaxf(highest, key_logit(held.key[i]));
+  float highest = -INFINITY, lowest = INFINITY;
+  for (int i = lane; i < n; i += 64) {
+    const float logit = key_logit(held.key[i]);
+    highest = fmaxf(highest, logit);
+    lowest = fminf(lowest, logit);
+  }
   highest = wave_max(highest);
+  lowest = -wave_max(-lowest);
   if (ref > -INFINITY) gone *= exp((double)ref - (double)highest);
   ref = highest;
-  for (int i = lane; i < n; i += 64) {
-    const uint64_t key = held.key[i];
-    const int r = count_greater(held.key, n, key);
-    if (r < M) best.key[r] = key;
-    else gone += exp((double)key_logit(key) - (double)highest);
+  // the highest bits are those that all logits share
+  const uint64_t ends = to_key(highest, -1) ^ to_key(lowest, 0);
+  int bit = 63 - __clzll((long long)ends);
+  uint64_t reached = to_key(lowest, 0) >> bit >> 1 << bit << 1;
+  for (; bit >= 0; --bit) {
+    const uint64_t higher = reached | 1ull << bit;
+    int count = 0;
+    for (int i = lane; i < padded; i += 256) {
+      uint64_t key[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) key[j] = held.key[i + 64 * j];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) count += __popcll(__builtin_amdgcn_ballot_w64(key[j] >= higher));
+    }
+    if (count >= M) reached = higher;
+    if (count == M) break;
+  }
+  int to = 0;
+  float least = INFINITY;
+  for (int i = 0; i < n; i += 64) {
+    const bool is = i + lane < n;
+    const uint64_t key = held.key[min(i + lane, n - 1)];
+    const float logit = key_logit(key);
+    const bool stays = is && key >= reached;
+    const uint64_t all = __builtin_amdgcn_ballot_w64(stays);
+    wave_fence();  // read before it is written: places behind these 64 stay
+    if (stays) {
+      held.key[to + lanes_below(all)] = key;
+      least = fminf(least, logit);
+    } else if (is) {
+      gone += exp((double)logit - (double)highest);
+    }
+    to += __popcll(all);
   }
   wave_fence();
-  if (lane < M) held.key[lane] = best.key[lane];
-  wave_fence();
+  return -wave_max(-least);
 }
 
 // Tokens of a piece: 256 threads hold E each, in vectors of VE, vector j from token (j 256 + tid) VE of the
@@ -293,7 +328,6 @@ __global__ __launch_bounds__(kThreads) void beam_rows_kernel(ccq_beam_params p, 
   constexpr int VE = 16 / sizeof(T), NV = E / VE, G = kGroup;  // a group of logits has a maximum of its own
   constexpr int PIECE = kThreads * E;
   __shared__ __align__(16) Held held[kWaves];
-  __shared__ Best best[kWaves];
   __shared__ __align__(16) float few[8];
   __shared__ float bounds[kWaves], tops[kWaves], mosts[kWaves], refs[kWaves];
   __shared__ int counts[kWaves];
@@ -338,6 +372,8 @@ __global__ __launch_bounds__(kThreads) void beam_rows_kernel(ccq_beam_params p, 
     const Raw<T, NV> raw = ahead;
     if (at + PIECE < end) ahead.load(src, first + PIECE, at + PIECE, p.V);
     if (at == begin) {
+      // of a short stretch, only the waves whose every thread holds logits speak for the bound
+      const int full = max(1, min(kWaves, (end - begin) / (64 * VE)));
       float mine = -INFINITY;
 #pragma unroll
       for (int g = 0; g < E; g += G) {
@@ -348,9 +384,10 @@ __global__ __launch_bounds__(kThreads) void beam_rows_kernel(ccq_beam_params p, 
       }
       const float sorted = sort_lanes(mine, lane);
       if (lane == 0) tops[wave] = sorted;
-      if (lane == (M + kWaves - 1) / kWaves) bounds[wave] = sorted;
+      if (lane == min((M + full - 1) / full, 63)) bounds[wave] = sorted;
       __syncthreads();
-      bound = fminf(fminf(bounds[0], bounds[1]), fminf(bounds[2], bounds[3]));
+      bound = bounds[0];
+      for (int w = 1; w < full; ++w) bound = fminf(bound, bounds[w]);
       top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
     }
     float higher = bound;  // for the pieces to come: this one's later groups hold tokens on either side of a tie
@@ -376,9 +413,8 @@ __global__ __launch_bounds__(kThreads) void beam_rows_kernel(ccq_beam_params p, 
           n += __popcll(all);
         }
         if (n > kHeld - 64 * G) {
-          thin(held[wave], best[wave], n, M, gone, ref);
+          higher = thin(held[wave], n, M, gone, ref);
           n = M;
-          higher = key_logit(held[wave].key[M - 1]);
         }
       }
       if (fabsf(top) < 1e30f) {
@@ -397,6 +433,10 @@ __global__ __launch_bounds__(kThreads) void beam_rows_kernel(ccq_beam_params p, 
     bound = higher;
   }
   bool careful = part != part || top == INFINITY;
+  if (n > 128) {
+    thin(held[wave], n, M, gone, ref);
+    n = M;
+  }
   if (lane < 8) held[wave].key[n + lane] = 0;
   wave_fence();
   float most = -INFINITY;  // of the wave's candidates
@@ -423,14 +463,16 @@ __global__ __launch_bounds__(kThreads) void beam_rows_kernel(ccq_beam_params p, 
     careful_stretch(src, begin, end, M, picks, work.parts + list, few);
     return;
   }
-  // all waves' candidates in order: a lane's against every other
-  for (int i = lane; i < n; i += 64) {
-    const uint64_t key = held[wave].key[i];
+  // all waves' candidates in order: a thread's against every other
+  const int m = counts[0] + counts[1] + counts[2] + counts[3];
+  for (int i = tid; i < m; i += kThreads) {
+    int w = 0, at = i;
+    while (at >= counts[w]) at -= counts[w++];
+    const uint64_t key = held[w].key[at];
     int r = 0;
-    for (int w = 0; w < kWaves; ++w) r += count_greater(held[w].key, counts[w], key);
+    for (int o = 0; o < kWaves; ++o) r += count_greater(held[o].key, counts[o], key);
     if (r < M) picks[r] = Pick{key_logit(key), key_token(key)};
   }
-  const int m = counts[0] + counts[1] + counts[2] + counts[3];
   if (tid == 0) {
     const float highest = fmaxf(fmaxf(fmaxf(mosts[0], mosts[1]), fmaxf(mosts[2], mosts[3])), top);
     double s = 0.0;
@@ -489,27 +531,30 @@ __global__ __launch_bounds__(kThreads) void beam_join_kernel(ccq_beam_params p, 
   const Part* parts = work.parts + (size_t)n * lists;
   const Pick* picks = work.picks + (size_t)n * lists * M;
 
-  for (int k = wave; k < K; k += kWaves) {
-    const int kind = beam_kind(p, n * K + k);
-    const float score = p.scores[n * K + k];
+  // as many lanes a beam as it has stretches: the exponentials and logarithms in 64 bits, 2 us a time, are then
+  // formed for many beams at once (12 beams of one stretch: 10.8 us with a wave a beam, 7.6)
+  int width = 1;
+  while (width < stretches && width < 64) width *= 2;
+  for (int k = tid / width; k < (K + kThreads / width - 1) / (kThreads / width) * (kThreads / width); k += kThreads / width) {
+    const int kind = k < K ? beam_kind(p, n * K + k) : 2, mine = tid & (width - 1);
+    const float score = k < K ? p.scores[n * K + k] : -INFINITY;
     BeamBase b{score > -INFINITY ? score : -INFINITY, 0.0, kind};  // NaN counts as -inf
-    if (kind == 0) {
-      float top = -INFINITY;
-      for (int c = lane; c < stretches; c += 64) top = fmaxf(top, parts[k * stretches + c].top);
-      top = wave_max(top);
-      double s = 0.0;
-      if (top > -INFINITY)
-        for (int c = lane; c < stretches; c += 64) {
-          const Part q = parts[k * stretches + c];
-          if (q.top > -INFINITY) s += q.sum * exp((double)q.top - (double)top);
-        }
-      s = wave_sum(s);
-      if (top > -INFINITY) {
-        b.rest -= log(s);
-        b.top = top;
+    float top = -INFINITY;
+    if (kind == 0)
+      for (int c = mine; c < stretches; c += width) top = fmaxf(top, parts[k * stretches + c].top);
+    for (int off = width / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+    double s = 0.0;
+    if (top > -INFINITY)
+      for (int c = mine; c < stretches; c += width) {
+        const Part q = parts[k * stretches + c];
+        if (q.top > -INFINITY) s += q.sum * exp((double)q.top - (double)top);
       }
+    for (int off = width / 2; off > 0; off >>= 1) s += __shfl_xor(s, off, 64);
+    if (top > -INFINITY) {
+      b.rest -= log(s);
+      b.top = top;
     }
-    if (lane == 0) base[k] = b;
+    if (mine == 0 && k < K) base[k] = b;
   }
   if (tid == 0) {
     found = 0;

@@ -45,6 +45,11 @@ def _logits(N, K, V, dtype, seed, stride=None):
     return x.cuda(), g
 
 
+def _uniform(N, K, g):
+    import torch
+    return torch.rand(N, K, generator=g)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("N,K,V,m,stride", [
     (1, 1, 1, 1, None), (1, 4, 3, 12, None), (2, 3, 17, 5, None), (3, 2, 255, 4, 256), (1, 4, 2048, 4, None),
@@ -119,6 +124,25 @@ def test_peaked_rows_where_few_terms_carry_the_sum(gpu_lib):
     logits[1, :, 8 : 8 + 4] += 25.0
     logits[2, :, 2048 * torch.arange(19)] += 20.0
     _run(logits, (-torch.rand(4, 4, generator=g)).cuda(), 32, tag="peaked")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,m", [(250, 64), (513, 1), (900, 64), (1532, 24), (2049, 64), (20857, 10)])
+def test_rows_that_end_in_the_first_waves_of_a_piece(gpu_lib, dtype, V, m):
+    logits, g = _logits(6, 12, V, dtype, V)
+    _run(logits, (-_uniform(6, 12, g)).cuda(), m, tag="short")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m", [1, 16, 64])
+def test_long_rows_that_rise(gpu_lib, dtype, m):
+    """Every later token is better, so that the wave's list fills again and again; equal values among them."""
+    import torch
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    N, K, V = 64, 16, 12001
+    g = torch.Generator().manual_seed(m)
+    x = (torch.arange(V, dtype=torch.float32) / V * 12 + 0.05 * torch.rand(V, generator=g)).to(dt).expand(N, K, V).contiguous().cuda()
+    _run(x, (-_uniform(N, K, g)).cuda(), m, tag="rising")
 
 
 @pytest.mark.parametrize("K", [1, 2, 3, 4, 5, 8, 13, 16, 17, 40, 64])
