@@ -17,6 +17,10 @@
 // greater ones; that is quadratic, so longer lists are thinned first (72 bf16 rows of 1,532, M = 24: 64 us
 // with a bound from all four waves, one of them empty, and no thinning; 8 us).
 //
+// Measured, 32 requests of 8 beams over 131,071 tokens, M = 16, bf16: 28 us for the rows (67 MB, 2.4 TB/s: four
+// pieces a workgroup, one batch of workgroups, so its first loads, the first piece's bound and the last
+// ranking stand alone) and 10 for the join.  Four rows of 32,000 in fp32: 7.5 and 5 us, latencies throughout.
+//
 // Scores of different beams meet in the comparison, so the normaliser has to be good to more than
 // fp32: the candidates, which carry most of a peaked distribution, are left out of the fp32 sum and added
 // in 64 bits, and the threads' sums of the rest, 2^(x log2(e) - c), are joined in 64 bits.
@@ -735,6 +739,7 @@ struct ReorderArgs {
 // One thread owns the same W bytes of all K beams of a request, reads what moves and then writes it:
 // no other thread touches those bytes, so the move is in place, whatever the parents are, and only
 // rows that move are touched.
+// Measured: 64 requests of 4 beams, the carries of 16 heads of 128 (718 MB moved): 130 us, 5.5 TB/s past the caches.
 template <typename W, int KMAX>
 __device__ __forceinline__ void move_columns(unsigned char* base, size_t row, size_t off, const int (&par)[KMAX], int K) {
   W v[KMAX];

@@ -11,6 +11,11 @@
 // they were about 5 of 56 us of the prefill).  Consecutive tokens of a workgroup are consecutive rows of
 // the head-major side, consecutive heads are consecutive rows of the projection, so both sides move
 // whole cache lines.
+//
+// Measured: B4 T4096 16 + 16 heads of 128, bf16: 51 us for the 268 MB it reads and writes, 5.3 TB/s, against
+// 6.0 of a plain stream past the caches; the gradient (16 + 4 heads, expanded; 436 MB with the fp32 gradients
+// it reads) 86 us and the sum of the weights' parts 4.5, 4.8 TB/s over both.  A decode step's 64 tokens take
+// 4.2 us, the launch's and one load's latency.
 #include "ccq_device.hpp"
 #include "ccq_internal.hpp"
 
@@ -23,8 +28,8 @@ constexpr int kBackAhead = 4;  // and of the gradient, whose rows are three time
 constexpr float kL2Floor = 1e-12f;
 
 // Rows are read past the caches, being read once.  The gradient, whose rows leave as they came, is also
-// written past them (101 against 108 us at the prefill's size, before the workgroups were halved); the forward, whose rows part by head, is
-// not: its caches gather the rows of a head (53 against 59 us).
+// written past them (101 against 108 us at B4 T4096, with twice the workgroups it has now); the forward, whose
+// rows part by head, is not: its caches gather the rows of a head (53 against 59 us).
 // Eight entries as they are stored, so that several rows' loads are under way at a time.
 template <typename T>
 struct Raw8;

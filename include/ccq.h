@@ -370,11 +370,13 @@ typedef struct {
 /*
  * Queries and keys of a projection, made ready for the read step in one pass: every head's row is
  * normalised, weighted, rotated by its position (rotary embedding; the angle position * inv_freq
- * is formed in 64 bits, so it holds at any position below 2^53) and stored head-major as
+ * is formed and reduced in 64 bits, to within 2^-51 of itself, then turned in 32: positions of
+ * 10^8 lose nothing that fp32 holds) and stored head-major as
  * ccq_fwd_chunked ([B, H, T, d]) and ccq_decode_step (T = 1: [N, H, d]) read it.  A rotation keeps
  * lengths, so keys under CCQ_NORM_L2 without a weight are unit keys.  The arithmetic is fp32; the
  * result is rounded once.  Either side may be absent (H_q == 0 or H_k == 0).  A value row is
- * laid out the same way by CCQ_NORM_NONE and rot == 0.  Returns a ccq_status.
+ * laid out the same way by CCQ_NORM_NONE and rot == 0.  B T <= 2^30 and at most 4,096 heads a side
+ * (CCQ_ERR_UNSUPPORTED beyond, and for other d or rot).  Returns a ccq_status.
  */
 int ccq_qk_norm_rope(const ccq_qk_params *p, void *hip_stream);
 
@@ -425,9 +427,11 @@ typedef struct {
  * The state is fp32 throughout and a call continues where h0 left off, so T = 1 with h_out == h0
  * is the serving step.  Where alpha_t is 0 the old state is dropped, whatever it holds (an
  * infinity or NaN before it does not pass); alpha_t is 0 for log_alpha_t below about -87.  (With
- * the complement scale an infinite input may give NaN instead of itself.)  Rows behind a sequence's length are neither read
- * into a result nor written.  Long sequences are cut along T and the pieces joined in a fixed
- * order: two calls give the same bits.  Returns a ccq_status.
+ * the complement scale an infinite input may give NaN instead of itself.)  Rows behind a sequence's
+ * length are neither read into a result nor written.  Long sequences are cut along T and the pieces
+ * joined in a fixed order: two calls give the same bits.  D <= 2^24, B T <= 2^30, B D < 2^31 and
+ * fewer than 2^31 tiles of 64 tokens by 128 channels (CCQ_ERR_UNSUPPORTED beyond).  Returns a
+ * ccq_status.
  */
 int ccq_scan(const ccq_scan_params *p, void *hip_stream);
 /* Bytes of device workspace ccq_scan needs (0 if none and for invalid p): depends on dtype, B, T, D. */
@@ -463,7 +467,7 @@ size_t ccq_scan_backward_workspace_bytes(const ccq_scan_bwd_params *p);
 typedef struct {
   int32_t dtype;             /* ccq_dtype of logits                                                 */
   int32_t N, K, V, M;        /* requests, beams of each, vocabulary, picks: K <= 64, M <= min(64, K V),
-                                K V < 2^31 and K ceil(V / 16384) <= 4096                            */
+                                K V < 2^31, K ceil(V / 16384) <= 4096 and N K <= 2^24               */
   const void *logits;        /* [N, K, V], a row every logits_stride elements                        */
   int64_t logits_stride;     /* >= V                                                                 */
   const float *scores;       /* [N, K] log-probability of every beam so far                          */
@@ -496,8 +500,9 @@ size_t ccq_beam_select_workspace_bytes(const ccq_beam_params *p);
  * and beam j, row (i K + j) of states[s] becomes what row (i K + parent[i][j]) was.  A row is
  * row_bytes[s] bytes, a multiple of 4: S, C, ksum and n of a decode step with N K sequences, h of
  * ccq_scan, or anything else kept per beam.  parent is [N, K]; a parent outside 0 .. K - 1 leaves
- * its beam as it is.  1 <= K <= 64, 1 <= n_states <= CCQ_MAX_REORDER_STATES; states and row_bytes
- * are host arrays, read before the call returns.  Rows that stay are neither read nor written.
+ * its beam as it is.  1 <= K <= 64, N K <= 2^24, rows of at most 2^36 bytes,
+ * 1 <= n_states <= CCQ_MAX_REORDER_STATES; states and row_bytes are host arrays, read before the
+ * call returns.  Rows that stay are neither read nor written.
  * Returns a ccq_status.
  */
 int ccq_beam_reorder(int32_t n_states, void *const *states, const size_t *row_bytes, int32_t N, int32_t K,

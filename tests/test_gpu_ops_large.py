@@ -1,0 +1,95 @@
+"""The operators around the read step on tensors of more than 2^32 elements.
+
+A token, channel, row or request is worked on alike wherever it stands, so the ends of a large call are
+compared with a small call on the same values: equal bits, but for selection's scores, whose sums are cut
+differently (each within 2^-24 |score| + 64 2^-24 of the score in 64 bits, so twice that apart).
+"""
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+@pytest.fixture(autouse=True)
+def _memory(gpu_lib):
+    import torch
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GiB of device memory")
+    yield
+    torch.cuda.empty_cache()
+
+
+def test_scan_and_gradient(gpu_lib):
+    import torch
+    from curvature_conditioned_query_amd import ccq_scan, ccq_scan_backward
+    T, D = 260, 1 << 24
+    g = torch.Generator(device="cuda").manual_seed(1)
+    row = lambda: torch.randn(1, 1, D, device="cuda", generator=g).to(torch.bfloat16)
+    x, la, dy = row().expand(1, T, D), (-row().abs()).expand(1, T, D), row().expand(1, T, D)
+    y = ccq_scan(x, la)
+    assert y.numel() > 1 << 32
+    y2 = ccq_scan(y, la)  # reads past 2^32 elements too
+    out = ccq_scan_backward(y, la, dy)
+    for part in (slice(0, 136), slice(D // 2, D // 2 + 8), slice(D - 264, D)):
+        cut = [t[..., part] for t in (x, la, dy)]
+        small = ccq_scan(*cut[:2])
+        assert torch.equal(y[..., part], small)
+        assert torch.equal(y2[..., part], ccq_scan(small, cut[1]))
+        back = ccq_scan_backward(small, cut[1], cut[2])
+        assert torch.equal(out["dx"][..., part], back["dx"]) and torch.equal(out["dlog_alpha"][..., part], back["dlog_alpha"])
+
+
+def test_qk_norm_rope_and_gradient(gpu_lib):
+    import torch
+    from curvature_conditioned_query_amd import ccq_qk_norm_rope, ccq_qk_norm_rope_backward
+    T, H, d = (1 << 20) + 3, 32, 128
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q = torch.randn(1, 1, H, d, device="cuda", generator=g).to(torch.bfloat16).expand(1, T, H, d)
+    freq = torch.rand(32, device="cuda", generator=g)
+    kw = dict(inv_freq=freq, q_norm="l2")
+    out, _ = ccq_qk_norm_rope(q, None, **kw)
+    assert out.numel() > 1 << 32
+    grad = torch.zeros(1, H, T, d, device="cuda")
+    for part in (slice(0, 7), slice(T - 9, T)):
+        grad[:, :, part] = torch.randn(grad[:, :, part].shape, device="cuda", generator=g)
+    dq = ccq_qk_norm_rope_backward(q, None, grad, None, **kw)["dq"]
+    for part in (slice(0, 7), slice(T - 9, T)):
+        here = dict(kw, position_offset=part.start)
+        assert torch.equal(out[:, :, part], ccq_qk_norm_rope(q[:, part], None, **here)[0])
+        small = ccq_qk_norm_rope_backward(q[:, part], None, grad[:, :, part].contiguous(), None, **here)["dq"]
+        assert torch.equal(dq[:, part], small)
+    assert not any(dq[0, at : at + 65536].any() for at in range(7, T - 9 - 65536, 65536))
+    turned, _ = ccq_qk_norm_rope(out.transpose(1, 2), None, q_norm="none")  # reads past 2^32 elements too
+    assert all(torch.equal(turned[0, h], out[0, h]) for h in range(H))
+
+
+def test_beam_select(gpu_lib):
+    import torch
+    from curvature_conditioned_query_amd import ccq_beam_select
+    N, K, V = 65, 8, 1 << 23
+    g = torch.Generator(device="cuda").manual_seed(3)
+    logits = torch.empty(N, K, V, device="cuda", dtype=torch.bfloat16).normal_(generator=g)
+    scores = -torch.rand(N, K, device="cuda", generator=g)
+    out = ccq_beam_select(logits, scores, 16)
+    for n in (0, N - 1):
+        small = ccq_beam_select(logits[n : n + 1], scores[n : n + 1], 16)
+        assert torch.equal(out["token"][n], small["token"][0]) and torch.equal(out["parent"][n], small["parent"][0])
+        assert ((out["score"][n] - small["score"][0]).abs() <= 2 * (U * small["score"][0].abs() + 64 * U)).all()
+
+
+def test_beam_reorder(gpu_lib):
+    import torch
+    from curvature_conditioned_query_amd import ccq_beam_reorder
+    for cols in ((1 << 30) + 4, (1 << 30) + 1):
+        count = torch.arange(cols, device="cuda", dtype=torch.int32)
+        state = torch.empty(4, cols, device="cuda", dtype=torch.int32)
+        for j in range(4):
+            state[j] = count + 11 * j
+        assert state.numel() > 1 << 32
+        ccq_beam_reorder([state], torch.tensor([[3, 0, 0, 2]], dtype=torch.int32, device="cuda"))
+        for j, was in enumerate((3, 0, 0, 2)):
+            assert torch.equal(state[j] - 11 * was, count)
+        del state
