@@ -53,7 +53,7 @@ def library_sha256() -> str:
 
 
 def _short(name: str) -> str:
-    name = name.replace("void ", "")
+    name = name.replace("void ", "").replace("(anonymous namespace)::", "")
     return name.split("(")[0][:96]
 
 
