@@ -7,19 +7,21 @@
 // best continuations out of the stretches' lists.
 //
 // Picking M of many needs no sort.  A workgroup goes through its stretch in pieces held in registers (32
-// logits a thread).  In the first, the (M / 4 + 1)-th best of each wave's thread maxima is found (of a stretch
-// shorter than a piece, for the waves that it fills); at least M logits reach the least of them, the bound,
-// and few lie above it.  Those, and in the later pieces whatever lies above the bound, go into a list of their
-// wave's own, in no order, without a word between the waves; a list that fills up (a row that rises, a mask
-// over the first tokens) is thinned to its M best, which raise the wave's bound.  Should fewer than M logits
-// lie above the bound, as in a row of few values or under a mask that leaves few tokens, the lowest tokens at
-// the bound itself are looked up at the end.  The lists are put in order by counting, for each candidate, the
-// greater ones; that is quadratic, so longer lists are thinned first (72 bf16 rows of 1,532, M = 24: 64 us
-// with a bound from all four waves, one of them empty, and no thinning; 8 us).
+// logits a thread, 8 where there are few rows).  In the first, the (M + 1)-th best of the threads' maxima, the
+// bound, is found bit by bit; at least M logits reach it, and few lie above it.  Those, and in the later pieces
+// whatever lies above the bound, go into a list of their wave's own, in no order, without a word between the
+// waves; a list that fills up (a row that rises, a mask over the first tokens) is thinned to its M best, which
+// raise the wave's bound.  Should fewer than M logits lie above the bound, as in a row of few values or under
+// a mask that leaves few tokens, the lowest tokens at the bound itself are looked up at the end.  The lists are
+// put in order by counting, for each candidate, the greater ones; that is quadratic, so longer lists are
+// thinned first.  A stretch of one piece takes its bound from the waves' own maxima, sorted and joined more
+// loosely: 7.9 against 8.8 us for four rows of 32,000, where for 256 rows of 131,071, in stretches of four
+// pieces, it is 28.5 against 26.3.
 //
-// Measured, 32 requests of 8 beams over 131,071 tokens, M = 16, bf16: 28 us for the rows (67 MB, 2.4 TB/s: four
-// pieces a workgroup, one batch of workgroups, so its first loads, the first piece's bound and the last
-// ranking stand alone) and 10 for the join.  Four rows of 32,000 in fp32: 7.5 and 5 us, latencies throughout.
+// Measured, 32 requests of 8 beams over 131,071 tokens, M = 16, bf16: 26 us for the rows (67 MB, 2.6 TB/s: the
+// vector units are busy for half of it, 15 cycles a logit and SIMD lane, and with one batch of workgroups of four
+// pieces each the first loads, the bound and the last ranking stand alone) and 6.5 for the join.  Four rows of
+// 32,000 in fp32: 7.9 and 5 us, latencies throughout.
 //
 // Scores of different beams meet in the comparison, so the normaliser has to be good to more than
 // fp32: the candidates, which carry most of a peaked distribution, are left out of the fp32 sum and added
@@ -227,15 +229,14 @@ __device__ __attribute__((noinline)) void fill_picks(const T* src, int begin, in
   for (int i = n + (int)threadIdx.x; i < M; i += kThreads) picks[i] = Pick{-INFINITY, -1};
 }
 
-// A logit and its token as one number: the greater comes first.
-__device__ __forceinline__ uint64_t to_key(float x, int token) {
+// A logit as a number of the same order, and back; with its token as one number, the greater comes first.
+__device__ __forceinline__ unsigned to_word(float x) {
   const unsigned b = __float_as_uint(x + 0.f);  // -0 ties with 0
-  return (uint64_t)((int)b < 0 ? ~b : b | 0x80000000u) << 32 | (unsigned)~token;
+  return (int)b < 0 ? ~b : b | 0x80000000u;
 }
-__device__ __forceinline__ float key_logit(uint64_t key) {
-  const unsigned b = (unsigned)(key >> 32);
-  return __uint_as_float((int)b < 0 ? b & 0x7fffffffu : ~b);
-}
+__device__ __forceinline__ float word_logit(unsigned b) { return __uint_as_float((int)b < 0 ? b & 0x7fffffffu : ~b); }
+__device__ __forceinline__ uint64_t to_key(float x, int token) { return (uint64_t)to_word(x) << 32 | (unsigned)~token; }
+__device__ __forceinline__ float key_logit(uint64_t key) { return word_logit((unsigned)(key >> 32)); }
 __device__ __forceinline__ int key_token(uint64_t key) { return (int)~(unsigned)key; }
 
 // How many of n keys are greater; behind them stand seven that are 0, the least there is.
@@ -249,6 +250,26 @@ __device__ __forceinline__ int count_greater(const uint64_t* keys, int n, uint64
     for (int i = 0; i < 8; ++i) r += k[i] > mine ? 1 : 0;
   }
   return r;
+}
+
+// A number that `count` of the threads' words reach and, unless words are equal, no more do; words that differ
+// in their BITS highest bits at most.
+template <int BITS>
+__device__ __forceinline__ unsigned reached_by(const unsigned (&words)[kThreads], int count) {
+  unsigned w[kWaves], reached = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) w[i] = words[(threadIdx.x & 63) + 64 * i];
+  for (int bit = 30; bit >= 32 - BITS; bit -= 2) {
+    int n[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i)
+#pragma unroll
+      for (unsigned d = 1; d < 4; ++d) n[d] += __popcll(__builtin_amdgcn_ballot_w64(w[i] >= (reached | d << bit)));
+    const int digit = n[3] >= count ? 3 : n[2] >= count ? 2 : n[1] >= count ? 1 : 0;
+    reached |= (unsigned)digit << bit;
+    if (digit && (digit == 3 ? n[3] : digit == 2 ? n[2] : n[1]) == count) break;
+  }
+  return reached;
 }
 
 // How many of the lanes in `mask` stand before this one.
@@ -327,12 +348,14 @@ __device__ __forceinline__ float thin(Held& held, int n, int M, double& gone, fl
 // Tokens of a piece: 256 threads hold E each, in vectors of VE, vector j from token (j 256 + tid) VE of the
 // piece on.  The logits are taken as they come: a NaN shows in the sum and +inf among the candidates, and a
 // stretch that has one is left to careful_stretch.
-template <typename T, int E>
-__global__ __launch_bounds__(kThreads) void beam_rows_kernel(ccq_beam_params p, int stretches, int pieces, BeamWork work) {
+// ONE: a stretch is one piece.
+template <typename T, int E, bool ONE>
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 1) void beam_rows_kernel(ccq_beam_params p, int stretches, int pieces, BeamWork work) {
   constexpr int VE = 16 / sizeof(T), NV = E / VE, G = kGroup;  // a group of logits has a maximum of its own
   constexpr int PIECE = kThreads * E;
   __shared__ __align__(16) Held held[kWaves];
   __shared__ __align__(16) float few[8];
+  __shared__ unsigned words[kThreads];
   __shared__ float bounds[kWaves], tops[kWaves], mosts[kWaves], refs[kWaves];
   __shared__ int counts[kWaves];
   __shared__ double sums[kWaves], gones[kWaves], helds[kWaves];
@@ -376,8 +399,6 @@ __global__ __launch_bounds__(kThreads) void beam_rows_kernel(ccq_beam_params p, 
     const Raw<T, NV> raw = ahead;
     if (at + PIECE < end) ahead.load(src, first + PIECE, at + PIECE, p.V);
     if (at == begin) {
-      // of a short stretch, only the waves whose every thread holds logits speak for the bound
-      const int full = max(1, min(kWaves, (end - begin) / (64 * VE)));
       float mine = -INFINITY;
 #pragma unroll
       for (int g = 0; g < E; g += G) {
@@ -386,12 +407,23 @@ __global__ __launch_bounds__(kThreads) void beam_rows_kernel(ccq_beam_params p, 
 #pragma unroll
         for (int i = 0; i < G; ++i) mine = fmaxf(mine, x[i]);
       }
-      const float sorted = sort_lanes(mine, lane);
-      if (lane == 0) tops[wave] = sorted;
-      if (lane == min((M + full - 1) / full, 63)) bounds[wave] = sorted;
-      __syncthreads();
-      bound = bounds[0];
-      for (int w = 1; w < full; ++w) bound = fminf(bound, bounds[w]);
+      if constexpr (ONE) {
+        // no later piece that a tighter bound would spare candidates: the least of the waves' own (M / 4 + 1)-th best, of a short stretch of those
+        // whose every thread holds logits
+        const int full = max(1, min(kWaves, (end - begin) / (64 * VE)));
+        const float sorted = sort_lanes(mine, lane);
+        if (lane == 0) tops[wave] = sorted;
+        if (lane == min((M + full - 1) / full, 63)) bounds[wave] = sorted;
+        __syncthreads();
+        bound = bounds[0];
+        for (int w = 1; w < full; ++w) bound = fminf(bound, bounds[w]);
+      } else {
+        words[tid] = to_word(mine);
+        mine = wave_max(mine);
+        if (lane == 0) tops[wave] = mine;
+        __syncthreads();
+        bound = word_logit(max(reached_by<sizeof(T) * 8>(words, M + 1), to_word(-INFINITY)));
+      }
       top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
     }
     float higher = bound;  // for the pieces to come: this one's later groups hold tokens on either side of a tie
@@ -725,15 +757,17 @@ BeamShape beam_shape(const ccq_beam_params& p) {
   return s;
 }
 
-template <typename T, int E>
+template <typename T, int E, bool ONE>
 void launch_rows(const ccq_beam_params& p, const BeamShape& s, BeamWork w, hipStream_t stream) {
-  beam_rows_kernel<T, E><<<(unsigned)(p.N * p.K * s.stretches), kThreads, 0, stream>>>(p, s.stretches, s.pieces, w);
+  beam_rows_kernel<T, E, ONE><<<(unsigned)(p.N * p.K * s.stretches), kThreads, 0, stream>>>(p, s.stretches, s.pieces, w);
 }
 
+// At 8 logits a thread there are fewer than 1024 pieces in all, so a stretch is one of them.
 template <typename T>
 void launch_rows_of(const ccq_beam_params& p, const BeamShape& s, BeamWork w, hipStream_t stream) {
-  if (s.per_thread == 32) launch_rows<T, 32>(p, s, w, stream);
-  else launch_rows<T, 8>(p, s, w, stream);
+  if (s.per_thread == 8) launch_rows<T, 8, true>(p, s, w, stream);
+  else if (s.pieces == 1) launch_rows<T, 32, true>(p, s, w, stream);
+  else launch_rows<T, 32, false>(p, s, w, stream);
 }
 
 // ---------------------------------------------------------------- reordering

@@ -145,6 +145,33 @@ def test_long_rows_that_rise(gpu_lib, dtype, m):
     _run(x, (-_uniform(N, K, g)).cuda(), m, tag="rising")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m", [1, 7, 64])
+def test_rows_of_several_pieces(gpu_lib, dtype, m):
+    """1024 rows, so that a workgroup goes through a whole row of 8192 tokens and 900 more: ties, masks, NaN and
+    infinities that begin in the second part or end with the first."""
+    import torch
+    N, K, V, cut = 64, 16, 9092, 8192
+    inf, nan = float("inf"), float("nan")
+    x, g = _logits(N, K, V, dtype, m)
+    rows = x.view(N * K, V)
+    few = torch.randperm(cut, generator=g)[:5].cuda()
+    late = cut + torch.randperm(V - cut, generator=g)[:5].cuda()
+    rows[0::12] = 0.5
+    rows[1::12] = torch.randint(0, 3, (V,), generator=g).cuda().to(x.dtype)
+    for start, keep in ((2, few), (3, late), (4, few[:0])):
+        kept = rows[start::12][:, keep].clone()
+        rows[start::12] = -inf
+        rows[start::12, keep] = kept
+    rows[5::12, cut + 3] = nan
+    rows[6::12, cut + 7] = inf
+    rows[7::12, :cut] = torch.finfo(x.dtype).min
+    rows[8::12, :cut] = -inf
+    rows[9::12, cut:] = -inf
+    rows[10::12] = torch.linspace(5, -5, V).cuda().to(x.dtype)
+    _run(x, (-_uniform(N, K, g)).cuda(), m, tag="pieces")
+
+
 @pytest.mark.parametrize("K", [1, 2, 3, 4, 5, 8, 13, 16, 17, 40, 64])
 def test_reorder(gpu_lib, K):
     """States of many row sizes and types, moved in place by every kind of parents."""
