@@ -14,12 +14,13 @@
 // 128 bytes reach 4.8; past the caches (non-temporal), which a single use has no use for, 6.0 and 5.4.
 //
 // Measured.  B4 T4096 D2048 bf16: 49 us for 201 MB, 4.1 TB/s (43 without the waiting, and 2 for the clearing of
-// the pairs); its gradient with the complement 79 us for 287 MB, 3.6 TB/s (70 without the waiting): two
-// workgroups fit a CU and the vector units are busy for 37 us, so loads and arithmetic overlap in part only.
-// B1 T20480 D1024 fp32: 70 us for 251 MB, 3.6 TB/s (54 to 60 without the waiting): eight columns of 160 tiles one
-// behind the other.
-// Not kept: workgroups that stay and load their next tile ahead (98 us against 59: fewer share a CU, and the
-// waiting shows); 64-token tiles (56; of 256 threads 53, with the fp32 sequence at 68 and the gradient at 80); seven or eight waves a SIMD (53 and 63: spills); groups of 8 or 32 tiles.
+// the pairs); the gradient of a padded batch of that size with the complement, lengths 1/2 to 1, 70 us for 287 MB,
+// 4.1 TB/s (63 without the waiting; 79 with the rows behind the sequences read, too): two workgroups fit a CU
+// and the vector units are busy for half of it, so loads and arithmetic overlap in part only.  B1 T20480 D1024
+// fp32: 70 us for 251 MB, 3.6 TB/s (54 to 60 without the waiting): eight columns of 160 tiles one behind the
+// other.  Not kept: workgroups that stay and load their next tile ahead (98 us against 59: fewer share a CU, and
+// the waiting shows); 64-token tiles (56; of 256 threads 53, with the fp32 sequence at 68 and the gradient at
+// 80 against 79); seven or eight waves a SIMD (53 and 63: spills); groups of 8 or 32 tiles.
 //
 // Waiting.  A tile's pair depends on its own inputs alone and is published before its workgroup waits
 // for any other, and each column's tiles are handed out by a counter in the order of the recurrence, so
@@ -213,13 +214,13 @@ __device__ __forceinline__ void in_turn(R (&raw)[N], int i, float done) {
 }
 
 // A thread's run of one input: token t0 on, eight channels from c0 on.  Every load is made, at a row and
-// column inside the tensor; what lies outside the sequence is cleared later.
+// column inside the tensor (behind the sequence: its last, read once for all); what lies outside is cleared later.
 template <typename T, int RUN>
 __device__ __forceinline__ void load_run(Raw8<T> (&raw)[RUN], const void* base, int64_t stride_b, int64_t stride_t, int b,
-                                         int t0, int c0, int T_max, int D) {
+                                         int t0, int c0, int n, int D) {
   const T* p = static_cast<const T*>(base) + b * stride_b + min(c0, D - 8);
 #pragma unroll
-  for (int r = 0; r < RUN; ++r) raw[r].load(p + (int64_t)min(t0 + r, T_max - 1) * stride_t);
+  for (int r = 0; r < RUN; ++r) raw[r].load(p + (int64_t)max(min(t0 + r, n - 1), 0) * stride_t);
 }
 
 // ---------------------------------------------------------------- tiles
@@ -317,6 +318,14 @@ __device__ __forceinline__ float state_before(const Tiles& t, int s, int column,
   return through(fold_parts(parts, ch).q, here);
 }
 
+// A tile behind the sequence, the order-th of its column, lets the state pass.  It need not wait for it, and
+// there is nothing else to do, unless it is the column's first or last or ends a group.
+__device__ __forceinline__ bool passes_on(const Tiles& t, int order, int column, int part, int ch) {
+  if (order == 0 || order == t.segments - 1 || order % kGroup == kGroup - 1) return false;
+  if (part == 0) publish(t.pairs + ((size_t)order * t.columns + column) * kCols + ch, Pair{1.f, 0.f});
+  return true;
+}
+
 __global__ __launch_bounds__(kStepThreads) void scan_clear_kernel(Tiles t, size_t words) {
   if (blockIdx.x == 0 && threadIdx.x < kCounters) t.counters[threadIdx.x * kCounterStride] = 0;
   // words come 128 at a time
@@ -408,9 +417,10 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : COMPLEMENT ? 4 : 6) 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int part = wave / (kCols / 64), half = wave % (kCols / 64), ch = 64 * half + lane, c = c_tile + ch;
 
+  if (s * TILE >= n && passes_on(tiles, s, column, part, ch)) return;
   Raw8<T> g_raw[RUN], x_raw[RUN];
-  load_run(g_raw, p.log_alpha, p.la_stride_b, p.la_stride_t, b, t0, c0, p.T, p.D);
-  load_run(x_raw, p.x, p.x_stride_b, p.x_stride_t, b, t0, c0, p.T, p.D);
+  load_run(g_raw, p.log_alpha, p.la_stride_b, p.la_stride_t, b, t0, c0, n, p.D);
+  load_run(x_raw, p.x, p.x_stride_b, p.x_stride_t, b, t0, c0, n, p.D);
   if ((s + 1) * TILE > n) {
     clear_from(g_raw, n - t0);
     clear_from(x_raw, n - t0);
@@ -541,6 +551,21 @@ __device__ __forceinline__ void walk_run_back(Raw8<T> (&g_raw)[RUN], Raw8<T> (&x
   }
 }
 
+template <typename T, int RUN>
+__device__ __forceinline__ void store_runs(const ccq_scan_bwd_params& p, const Raw8<T> (&x_raw)[RUN], const Raw8<T> (&g_raw)[RUN],
+                                           int b, int t0, int c0) {
+  if (c0 >= p.D) return;
+  const size_t at = ((size_t)b * p.T + t0) * p.D + c0;
+  T *dx = static_cast<T*>(p.dx) + at, *dg = static_cast<T*>(p.dlog_alpha) + at;
+#pragma unroll
+  for (int r = 0; r < RUN; ++r) {
+    if (t0 + r < p.T) {
+      x_raw[r].store(dx + (size_t)r * p.D);
+      g_raw[r].store(dg + (size_t)r * p.D);
+    }
+  }
+}
+
 // The gradient: the same tiles from the end.  The adjoint that reaches a token from behind, d, becomes
 // alpha (d + dy) in front of it, so a run acts on it as d -> P d + q with the run's own product of gates.
 // The states are walked forward again, from the state kept before the tile.
@@ -561,9 +586,15 @@ __global__ __launch_bounds__(kThreads, 4) void scan_backward_tile_kernel(ccq_sca
   const int part = wave / (kCols / 64), half = wave % (kCols / 64), ch = 64 * half + lane, c = c_tile + ch;
 
   Raw8<T> g_raw[RUN], x_raw[RUN], d_raw[RUN];
-  load_run(g_raw, p.log_alpha, p.la_stride_b, p.la_stride_t, b, t0, c0, p.T, p.D);
-  load_run(x_raw, p.x, p.x_stride_b, p.x_stride_t, b, t0, c0, p.T, p.D);
-  load_run(d_raw, p.dy, p.dy_stride_b, p.dy_stride_t, b, t0, c0, p.T, p.D);
+  if (s * TILE >= n && passes_on(tiles, order, column, part, ch)) {
+    clear_from(g_raw, 0);
+    clear_from(x_raw, 0);
+    store_runs(p, x_raw, g_raw, b, t0, c0);
+    return;
+  }
+  load_run(g_raw, p.log_alpha, p.la_stride_b, p.la_stride_t, b, t0, c0, n, p.D);
+  load_run(x_raw, p.x, p.x_stride_b, p.x_stride_t, b, t0, c0, n, p.D);
+  load_run(d_raw, p.dy, p.dy_stride_b, p.dy_stride_t, b, t0, c0, n, p.D);
   float h = 0.f;  // state before the tile
   if (s * TILE < n && c < p.D)
     h = carry[((size_t)b * ((p.T + kChunk - 1) / kChunk) + s * (TILE / kChunk)) * p.D + c];
@@ -619,7 +650,6 @@ __global__ __launch_bounds__(kThreads, 4) void scan_backward_tile_kernel(ccq_sca
     h = through(h, pair);
   }
   __syncthreads();
-  if (c0 >= p.D) return;
   const Pair* ends = &runs[run][8 * oct];
   if (resets) walk_run_back<true, COMPLEMENT>(g_raw, x_raw, d_raw, ends);
   else walk_run_back<false, COMPLEMENT>(g_raw, x_raw, d_raw, ends);
@@ -627,15 +657,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_backward_tile_kernel(ccq_sca
     clear_from(g_raw, n - t0);
     clear_from(x_raw, n - t0);
   }
-  const size_t at = ((size_t)b * p.T + t0) * p.D + c0;
-  T *dx = static_cast<T*>(p.dx) + at, *dg = static_cast<T*>(p.dlog_alpha) + at;
-#pragma unroll
-  for (int r = 0; r < RUN; ++r) {
-    if (t0 + r < p.T) {
-      x_raw[r].store(dx + (size_t)r * p.D);
-      g_raw[r].store(dg + (size_t)r * p.D);
-    }
-  }
+  store_runs(p, x_raw, g_raw, b, t0, c0);
 }
 
 // A few tokens: eight channels a thread, one token behind the other.

@@ -96,6 +96,18 @@ def test_lengths(gpu_lib, dtype, T, lengths):
     _both(dtype, x, la, h0, n, True)
 
 
+@pytest.mark.parametrize("dtype,complement", [("bf16", True), ("bf16", False), ("f32", True), ("f32", False)])
+def test_short_sequences_among_long_ones(gpu_lib, dtype, complement):
+    """Many tiles behind a sequence's end, beginning or ending a group of them, and not a multiple of a group."""
+    T, lengths = 4700, [0, 1, 4700, 2048, 2049, 130, 4601]
+    print(f"scan lengths {dtype} T{T} {lengths}", flush=True)
+    x, la, h0, n = _make(dtype, len(lengths), T, 136, 6, lengths=lengths)
+    for b, k in enumerate(lengths):
+        x[b, k:] = float("nan")
+        la[b, k:] = float("inf")
+    _both(dtype, x, la, h0, n, complement)
+
+
 @pytest.mark.parametrize("decay", [1e-5, 20.0])
 def test_slow_and_fast_gates(gpu_lib, decay):
     """Gates next to 1 (nothing is lost over the whole length) and gates that forget within a token."""
