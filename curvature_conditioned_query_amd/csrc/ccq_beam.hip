@@ -18,10 +18,10 @@
 // loosely: 7.9 against 8.8 us for four rows of 32,000, where for 256 rows of 131,071, in stretches of four
 // pieces, it is 28.5 against 26.3.
 //
-// Measured, 32 requests of 8 beams over 131,071 tokens, M = 16, bf16: 26 us for the rows (67 MB, 2.6 TB/s: the
+// Measured, 32 requests of 8 beams over 131,071 tokens, M = 16, bf16: 25 us for the rows (67 MB, 2.7 TB/s: the
 // vector units are busy for half of it, 15 cycles a logit and SIMD lane, and with one batch of workgroups of four
-// pieces each the first loads, the bound and the last ranking stand alone) and 6.5 for the join.  Four rows of
-// 32,000 in fp32: 7.9 and 5 us, latencies throughout.
+// pieces each the first loads, the bound and the last ranking stand alone) and 6 for the join.  Four rows of
+// 32,000 in fp32: 7 and 5 us, latencies throughout.
 //
 // Scores of different beams meet in the comparison, so the normaliser has to be good to more than
 // fp32: the candidates, which carry most of a peaked distribution, are left out of the fp32 sum and added
@@ -71,11 +71,12 @@ __device__ __forceinline__ float as_counted(float x) { return fminf(fmaxf(x, -IN
 
 constexpr float kLog2e = 1.44269502162933349609f;
 
-// A row's beam: 0 goes on, 1 finished, 2 dead (its score is -inf or NaN).
-__device__ __forceinline__ int beam_kind(const ccq_beam_params& p, int row) {
-  if (p.finished && p.finished[row]) return 1;
-  const float s = p.scores[row];
-  return s > -INFINITY ? 0 : 2;
+// A row's beam: 0 goes on, 1 finished, 2 dead (its score is -inf or NaN).  Both loads are made, so that neither
+// waits for the other.
+__device__ __forceinline__ int beam_kind(const ccq_beam_params& p, int row, float& score) {
+  score = p.scores[row];
+  const bool finished = p.finished && p.finished[row];
+  return finished ? 1 : score > -INFINITY ? 0 : 2;
 }
 
 // 16 bytes from any element on: a row starts where the one before ends, at an odd address for an odd
@@ -356,16 +357,21 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 1) void beam_rows_ke
   __shared__ __align__(16) Held held[kWaves];
   __shared__ __align__(16) float few[8];
   __shared__ unsigned words[kThreads];
-  __shared__ float bounds[kWaves], tops[kWaves], mosts[kWaves], refs[kWaves];
+  __shared__ float bounds[kWaves], tops[kWaves], froms[kWaves];
   __shared__ int counts[kWaves];
-  __shared__ double sums[kWaves], gones[kWaves], helds[kWaves];
+  __shared__ double sums[kWaves];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), M = p.M;
   const int row = blockIdx.x / stretches, stretch = blockIdx.x - row * stretches;
   const size_t list = blockIdx.x;
   Pick* picks = work.picks + list * M;
 
-  const int kind = beam_kind(p, row);
+  const T* src = static_cast<const T*>(p.logits) + (int64_t)row * p.logits_stride;
+  const int begin = stretch * pieces * PIECE, end = min(p.V, begin + pieces * PIECE);
+  Raw<T, NV> ahead;
+  ahead.load(src, begin + tid * VE, begin, p.V);  // under way while the beam's kind is found
+  float score;
+  const int kind = beam_kind(p, row, score);
   if (kind != 0) {
     // a finished beam's one continuation and then, as a dead beam's, tokens in order at -inf
     for (int i = tid; i < M; i += kThreads) {
@@ -382,10 +388,6 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 1) void beam_rows_ke
     return;
   }
 
-  const T* src = static_cast<const T*>(p.logits) + (int64_t)row * p.logits_stride;
-  const int begin = stretch * pieces * PIECE, end = min(p.V, begin + pieces * PIECE);
-  Raw<T, NV> ahead;
-  ahead.load(src, begin + tid * VE, begin, p.V);
   float bound = -INFINITY;  // candidates lie above it
   float top = -INFINITY;    // the sum of the others counts from here
   float part = 0.f;
@@ -479,21 +481,21 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 1) void beam_rows_ke
   for (int i = lane; i < n; i += 64) most = fmaxf(most, key_logit(held[wave].key[i]));
   most = wave_max(most);
   careful |= most == INFINITY;
-  double own = 0.0;  // the candidates' part of the sum, counted from most
-  for (int i = lane; i < n; i += 64) own += exp((double)key_logit(held[wave].key[i]) - (double)most);
-  own = wave_sum(own);
-  // c is the rounded top log2(e): its rounding is a factor of all terms
-  double total = top > -INFINITY ? (double)part : 0.0;
-  if (fabsf(top) < 1e30f) total *= exp((double)(top * kLog2e) * 0.69314718055994530942 - (double)top);
-  total = wave_sum(total);
-  gone = wave_sum(gone);
+  // the wave's part of the normaliser, from the greater of the two on; c, the rounded top log2(e), is what the
+  // fp32 sum counts from
+  const float from = fmaxf(top, most);
+  double sum = 0.0;
+  if (from > -INFINITY) {
+    if (top > -INFINITY)
+      sum = (double)part * exp((fabsf(top) < 1e30f ? (double)(top * kLog2e) * 0.69314718055994530942 : (double)top) - (double)from);
+    for (int i = lane; i < n; i += 64) sum += exp((double)key_logit(held[wave].key[i]) - (double)from);
+    if (ref > -INFINITY) sum += gone * exp((double)ref - (double)from);
+  }
+  sum = wave_sum(sum);
   if (lane == 0) {
-    sums[wave] = total;
-    gones[wave] = gone;
-    refs[wave] = ref;
+    sums[wave] = sum;
+    froms[wave] = from;
     counts[wave] = n;
-    helds[wave] = own;
-    mosts[wave] = most;
   }
   if (__syncthreads_or(careful)) {
     careful_stretch(src, begin, end, M, picks, work.parts + list, few);
@@ -509,17 +511,12 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 1) void beam_rows_ke
     for (int o = 0; o < kWaves; ++o) r += count_greater(held[o].key, counts[o], key);
     if (r < M) picks[r] = Pick{key_logit(key), key_token(key)};
   }
-  if (tid == 0) {
-    const float highest = fmaxf(fmaxf(fmaxf(mosts[0], mosts[1]), fmaxf(mosts[2], mosts[3])), top);
-    double s = 0.0;
-    if (highest > -INFINITY) {
-      if (top > -INFINITY) s = ((sums[0] + sums[1]) + (sums[2] + sums[3])) * exp((double)top - (double)highest);
-      for (int w = 0; w < kWaves; ++w) {
-        if (counts[w]) s += helds[w] * exp((double)mosts[w] - (double)highest);
-        if (refs[w] > -INFINITY) s += gones[w] * exp((double)refs[w] - (double)highest);
-      }
-    }
-    work.parts[list] = Part{s, highest, 0};
+  if (tid < kWaves) {
+    const float highest = fmaxf(fmaxf(froms[0], froms[1]), fmaxf(froms[2], froms[3]));
+    double s = froms[tid] > -INFINITY ? sums[tid] * exp((double)froms[tid] - (double)highest) : 0.0;
+    s += __shfl_xor(s, 1, 64);
+    s += __shfl_xor(s, 2, 64);
+    if (tid == 0) work.parts[list] = Part{s, highest, 0};
   }
   if (m < M) {
     __syncthreads();
@@ -575,19 +572,27 @@ __global__ __launch_bounds__(kThreads) void beam_join_kernel(ccq_beam_params p, 
   int width = 1;
   while (width < stretches && width < 64) width *= 2;
   for (int k = tid / width; k < (K + kThreads / width - 1) / (kThreads / width) * (kThreads / width); k += kThreads / width) {
-    const int kind = k < K ? beam_kind(p, n * K + k) : 2, mine = tid & (width - 1);
-    const float score = k < K ? p.scores[n * K + k] : -INFINITY;
+    const int mine = tid & (width - 1), row = n * K + min(k, K - 1);
+    const Part* at = parts + min(k, K - 1) * stretches;
+    const Part first = at[min(mine, stretches - 1)];
+    float score;
+    int kind = beam_kind(p, row, score);
+    if (k >= K) kind = 2;
     BeamBase b{score > -INFINITY ? score : -INFINITY, 0.0, kind};  // NaN counts as -inf
     float top = -INFINITY;
-    if (kind == 0)
-      for (int c = mine; c < stretches; c += width) top = fmaxf(top, parts[k * stretches + c].top);
+    if (kind == 0) {
+      if (mine < stretches) top = first.top;
+      for (int c = mine + width; c < stretches; c += width) top = fmaxf(top, at[c].top);
+    }
     for (int off = width / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
     double s = 0.0;
-    if (top > -INFINITY)
-      for (int c = mine; c < stretches; c += width) {
-        const Part q = parts[k * stretches + c];
+    if (top > -INFINITY) {
+      if (mine < stretches && first.top > -INFINITY) s = first.sum * exp((double)first.top - (double)top);
+      for (int c = mine + width; c < stretches; c += width) {
+        const Part q = at[c];
         if (q.top > -INFINITY) s += q.sum * exp((double)q.top - (double)top);
       }
+    }
     for (int off = width / 2; off > 0; off >>= 1) s += __shfl_xor(s, off, 64);
     if (top > -INFINITY) {
       b.rest -= log(s);
