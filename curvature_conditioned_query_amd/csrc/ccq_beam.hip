@@ -19,7 +19,7 @@
 // pieces, it is 28.5 against 26.3.
 //
 // Measured, 32 requests of 8 beams over 131,071 tokens, M = 16, bf16: 25 us for the rows (67 MB, 2.7 TB/s: the
-// vector units are busy for half of it, 15 cycles a logit and SIMD lane, and with one batch of workgroups of four
+// vector units are busy for half of it, the time of 15 instructions a logit, and with one batch of workgroups of four
 // pieces each the first loads, the bound and the last ranking stand alone) and 6 for the join.  Four rows of
 // 32,000 in fp32: 7 and 5 us, latencies throughout.
 //
