@@ -93,3 +93,21 @@ def test_beam_reorder(gpu_lib):
         for j, was in enumerate((3, 0, 0, 2)):
             assert torch.equal(state[j] - 11 * was, count)
         del state
+
+
+@pytest.mark.parametrize("K", [1, 2, 3, 8, 11, 16, 33, 64])
+@pytest.mark.parametrize("odd", [0, 1])
+def test_beam_reorder_past_the_caches(gpu_lib, K, odd):
+    """States of more than 128 MB, which are moved past the caches: rows of whole and of broken 16 bytes."""
+    import torch
+    from curvature_conditioned_query_amd import ccq_beam_reorder
+    N = 3
+    cols = (150 << 20) // 4 // (N * K) // 4 * 4 + odd
+    g = torch.Generator(device="cuda").manual_seed(K)
+    state = torch.randint(-(1 << 31), 1 << 31, (N * K, cols), device="cuda", dtype=torch.int32, generator=g)
+    small = torch.rand(N * K, 5, device="cuda", generator=g)
+    parent = torch.randint(0, K, (N, K), device="cuda", dtype=torch.int32, generator=g)
+    rows = (torch.arange(N, device="cuda")[:, None] * K + parent).view(-1)
+    want, want_small = state[rows], small[rows]
+    ccq_beam_reorder([small, state], parent)
+    assert torch.equal(state, want) and torch.equal(small, want_small)
