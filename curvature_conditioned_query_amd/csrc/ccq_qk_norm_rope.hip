@@ -5,7 +5,8 @@
 // Everything is a few operations an element, so both directions are bound by memory: a row is read
 // once and written once.  A row lies on d / 8 lanes, eight entries (16 bytes of bf16) a lane; 256
 // threads hold 256 / (d / 8) tokens, each thread the same eight entries of one token, and walk over
-// that token's heads, queries and then keys, a few rows' loads ahead.  The angles depend on token and
+// that token's heads, queries and then keys, several rows' loads under way: as many as there are heads left,
+// not more (loading the last head again in their place: 50 against 40 us for fp32 rows of 4 + 2 heads).  The angles depend on token and
 // entry alone: a workgroup forms each cosine and sine once, in LDS, and a thread takes its eight into
 // registers for all heads it visits (formed by every thread for itself and for queries and keys apart
 // they were about 5 of 56 us of the prefill).  Consecutive tokens of a workgroup are consecutive rows of
@@ -16,6 +17,8 @@
 // 6.0 of a plain stream past the caches; the gradient (16 + 4 heads, expanded; 436 MB with the fp32 gradients
 // it reads) 86 us and the sum of the weights' parts 4.5, 4.8 TB/s over both.  A decode step's 64 tokens take
 // 4.2 us, the launch's and one load's latency.
+#include <type_traits>
+
 #include "ccq_device.hpp"
 #include "ccq_internal.hpp"
 
@@ -23,7 +26,9 @@ namespace ccq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 8;      // rows a thread loads at a time
+// Rows a thread loads at a time: 128 bytes (fp32, 4 + 2 heads of 128, 23,361 tokens: 37.5 us; eight rows 40).
+template <typename T>
+constexpr int kAhead = 16 / (int)sizeof(T);
 constexpr int kBackAhead = 4;  // and of the gradient, whose rows are three times as wide
 constexpr float kL2Floor = 1e-12f;
 
@@ -222,14 +227,15 @@ __global__ __launch_bounds__(kThreads) void qk_forward_kernel(ccq_qk_params p, i
     const int64_t out_step = (int64_t)p.T * D;
     float wt[8];
     load_weight(s.w, rl, wt);
-    for (int h0 = begin; h0 < end; h0 += kAhead) {
-      Raw8<T> raw[kAhead];
+    // rows h0 .. h0 + n - 1, all loads under way
+    auto rows = [&](auto n, int h0) {
+      constexpr int N = decltype(n)::value;
+      Raw8<T> raw[N];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) raw[i].load(in + min(h0 + i, end - 1) * s.sh);
+      for (int i = 0; i < N; ++i) raw[i].load(in + (h0 + i) * s.sh);
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
+      for (int i = 0; i < N; ++i) {
         const int h = h0 + i;
-        if (h >= end) break;
         float x[8];
         raw[i].get(x);
         if (s.norm != CCQ_NORM_NONE) {
@@ -247,7 +253,13 @@ __global__ __launch_bounds__(kThreads) void qk_forward_kernel(ccq_qk_params p, i
           for (int c = 0; c < s.copies; ++c) store8<false>(out + (h * s.copies + c) * out_step, x);
         }
       }
-    }
+      return h0 + N;
+    };
+    int h = begin;
+    while (h + kAhead<T> <= end) h = rows(std::integral_constant<int, kAhead<T>>{}, h);
+    if (sizeof(T) == 2 && h + 4 <= end) h = rows(std::integral_constant<int, 4>{}, h);
+    if (h + 2 <= end) h = rows(std::integral_constant<int, 2>{}, h);
+    if (h < end) rows(std::integral_constant<int, 1>{}, h);
   }
 }
 
@@ -319,23 +331,27 @@ __global__ __launch_bounds__(kThreads) void qk_backward_kernel(ccq_qk_bwd_params
         }
       };
       if (s.copies == 1) {
-        for (int h0 = begin; h0 < end; h0 += kBackAhead) {
-          Raw8<T> x_raw[kBackAhead];
-          Raw8<float> z_raw[kBackAhead];
+        auto rows = [&](auto n, int h0) {
+          constexpr int N = decltype(n)::value;
+          Raw8<T> x_raw[N];
+          Raw8<float> z_raw[N];
 #pragma unroll
-          for (int i = 0; i < kBackAhead; ++i) {
-            const int h = min(h0 + i, end - 1);
-            x_raw[i].load(in + h * s.sh);
-            z_raw[i].load(grad + h * grad_step);
+          for (int i = 0; i < N; ++i) {
+            x_raw[i].load(in + (h0 + i) * s.sh);
+            z_raw[i].load(grad + (h0 + i) * grad_step);
           }
 #pragma unroll
-          for (int i = 0; i < kBackAhead; ++i) {
-            if (h0 + i >= end) break;
+          for (int i = 0; i < N; ++i) {
             float z[8];
             z_raw[i].get(z);
             gradient(x_raw[i], z, h0 + i);
           }
-        }
+          return h0 + N;
+        };
+        int h = begin;
+        while (h + kBackAhead <= end) h = rows(std::integral_constant<int, kBackAhead>{}, h);
+        if (h + 2 <= end) h = rows(std::integral_constant<int, 2>{}, h);
+        if (h < end) rows(std::integral_constant<int, 1>{}, h);
       } else {
         for (int h = begin; h < end; ++h) {
           Raw8<T> x_raw;
