@@ -6,16 +6,16 @@
 // once and written once.  A row lies on d / 8 lanes, eight entries (16 bytes of bf16) a lane; 256
 // threads hold 256 / (d / 8) tokens, each thread the same eight entries of one token, and walk over
 // that token's heads, queries and then keys, several rows' loads under way: as many as there are heads left,
-// not more (loading the last head again in their place: 50 against 40 us for fp32 rows of 4 + 2 heads).  The angles depend on token and
-// entry alone: a workgroup forms each cosine and sine once, in LDS, and a thread takes its eight into
-// registers for all heads it visits (formed by every thread for itself and for queries and keys apart
-// they were about 5 of 56 us of the prefill).  Consecutive tokens of a workgroup are consecutive rows of
+// not more (loading the last head again in their place: 50 against 40 us for fp32 rows of 4 + 2 heads).  The
+// angles depend on token and entry alone: a workgroup forms each cosine and sine once, in LDS, and a thread
+// takes its eight into registers for all heads it visits (formed by every thread for itself and for queries
+// and keys apart they were about 5 of 56 us of the prefill).  Consecutive tokens of a workgroup are consecutive rows of
 // the head-major side, consecutive heads are consecutive rows of the projection, so both sides move
 // whole cache lines.
 //
 // Measured: B4 T4096 16 + 16 heads of 128, bf16: 51 us for the 268 MB it reads and writes, 5.3 TB/s, against
 // 6.0 of a plain stream past the caches; the gradient (16 + 4 heads, expanded; 436 MB with the fp32 gradients
-// it reads) 86 us and the sum of the weights' parts 4.5, 4.8 TB/s over both.  A decode step's 64 tokens take
+// it reads) 87 us and the sum of the weights' parts 4.6, 4.8 TB/s over both.  A decode step's 64 tokens take
 // 4.2 us, the launch's and one load's latency.
 #include <type_traits>
 
