@@ -626,7 +626,7 @@ class _Ops:
     def __init__(self):
         import torch
         lib = load_library()
-        self.torch, self.empty = torch, torch.empty
+        self.torch, self.empty, self.empty_strided = torch, torch.empty, torch.empty_strided
         self.f32, self.i32, self.i64, self.u8 = torch.float32, torch.int32, torch.int64, torch.uint8
         self.codes = {torch.float32: CCQ_DTYPE_F32, torch.bfloat16: CCQ_DTYPE_BF16}
         self.current_device, self.raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
@@ -690,7 +690,23 @@ def _strided(name, t, dev, dtype, shape):
     st = t.stride()
     if t.shape != shape or t.dtype != dtype or t.device != dev or (st[-1] != 1 and shape[-1] != 1):
         _refuse(name, t, dev, dtype, shape, "dense in its last dimension")
-    return [s if n > 1 else 0 for s, n in zip(st[:-1], shape)]
+    if len(st) == 4:
+        return st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0, st[2] if shape[2] > 1 else 0
+    return st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0
+
+
+def _into(ops, name, t, dev, dtype, shape):
+    """An output and its address: the given tensor, checked as by _dense, or a new one."""
+    if t is not None:
+        return t, _dense(name, t, dev, dtype, shape)
+    if len(shape) == 4:
+        _, a, b, c = shape
+        strides = (a * b * c, b * c, c, 1)
+    else:
+        _, b, c = shape
+        strides = (b * c, c, 1)
+    t = ops.empty_strided(shape, strides, dtype=dtype, device=dev)
+    return t, t.data_ptr()
 
 
 def _launch(ops, name, fn, params, dev, size_fn=None, workspace=None):
@@ -717,6 +733,7 @@ def _launch(ops, name, fn, params, dev, size_fn=None, workspace=None):
 
 def _qk_params(ops, q, k, dev, positions, inv_freq, q_weight, k_weight, q_norm, k_norm, eps, interleaved, expand_keys,
                position_offset, q_out, k_out):
+    """q_out, k_out: addresses."""
     ref = q if q is not None else k
     dt = ref.dtype
     B, T, _, d = ref.shape
@@ -744,8 +761,7 @@ def _qk_params(ops, q, k, dev, positions, inv_freq, q_weight, k_weight, q_norm, 
     return QkParams(ops.dtype_code(ref), B, T, Hq, Hk, d, *norms, rot, 1 if interleaved else 0, 1 if expand_keys else 0,
                     eps, qp, kp, *qs, *ks, _dense("positions", positions, dev, ops.i64, (B, T)), position_offset, freqs,
                     _dense("q_weight", q_weight, dev, ops.f32, (d,)), _dense("k_weight", k_weight, dev, ops.f32, (d,)),
-                    _dense("q_out", q_out, dev, dt, (B, Hq, T, d)),
-                    _dense("k_out", k_out, dev, dt, (B, Hq if expand_keys else Hk, T, d)))
+                    q_out, k_out)
 
 
 def ccq_qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=None, q_norm="rms", k_norm="l2",
@@ -764,14 +780,18 @@ def ccq_qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weigh
         raise ValueError("q and k are [B, T, H, d]")
     ops, dev = _ops(), ref.device
     with ops.place(dev, stream):
-        B, T, _, d = ref.shape
-        if q_out is None and q is not None:
-            q_out = ops.empty((B, q.shape[2], T, d), dtype=q.dtype, device=dev)
-        if k_out is None and k is not None:
-            heads = q.shape[2] if expand_keys and q is not None else k.shape[2]
-            k_out = ops.empty((B, heads, T, d), dtype=k.dtype, device=dev)
+        B, T, heads, d = ref.shape
+        qp = kp = None
+        if q is not None:
+            q_out, qp = _into(ops, "q_out", q_out, dev, ref.dtype, (B, heads, T, d))
+        elif q_out is not None:
+            raise ValueError("q_out is given without q")
+        if k is not None:
+            k_out, kp = _into(ops, "k_out", k_out, dev, ref.dtype, (B, heads if expand_keys else k.shape[2], T, d))
+        elif k_out is not None:
+            raise ValueError("k_out is given without k")
         p = _qk_params(ops, q, k, dev, positions, inv_freq, q_weight, k_weight, q_norm, k_norm, eps, interleaved,
-                       expand_keys, position_offset, q_out, k_out)
+                       expand_keys, position_offset, qp, kp)
         _launch(ops, "qk_norm_rope", ops.qk_norm_rope, p, dev)
     return q_out, k_out
 
@@ -834,12 +854,11 @@ def ccq_scan(x, log_alpha, h0=None, h_out=None, y=None, lengths=None, complement
     ops, dev, dt = _ops(), x.device, x.dtype
     shape = B, T, D = x.shape
     with ops.place(dev, stream):
-        if y is None:
-            y = ops.empty(shape, dtype=dt, device=dev)
+        y, yp = _into(ops, "y", y, dev, dt, shape)
         p = ScanParams(ops.dtype_code(x), B, T, D, 1 if complement else 0, x.data_ptr(), log_alpha.data_ptr(),
                        *_strided("x", x, dev, dt, shape), *_strided("log_alpha", log_alpha, dev, dt, shape),
                        _dense("lengths", lengths, dev, ops.i32, (B,)), _dense("h0", h0, dev, ops.f32, (B, D)),
-                       _dense("y", y, dev, dt, shape), _dense("h_out", h_out, dev, ops.f32, (B, D)),
+                       yp, _dense("h_out", h_out, dev, ops.f32, (B, D)),
                        _dense("chunk_carry", chunk_carry, dev, ops.f32, (B, (T + 63) // 64, D)), None, 0)
         _launch(ops, "scan", ops.scan, p, dev, ops.scan_workspace_bytes, workspace)
     return y
@@ -856,8 +875,9 @@ def ccq_scan_backward(x, log_alpha, dy, h0=None, dh_out=None, lengths=None, comp
     ops, dev, dt = _ops(), x.device, x.dtype
     shape = B, T, D = x.shape
     with ops.place(dev, stream):
-        out = dict(dx=ops.empty(shape, dtype=dt, device=dev) if dx is None else dx,
-                   dlog_alpha=ops.empty(shape, dtype=dt, device=dev) if dlog_alpha is None else dlog_alpha)
+        dx, dxp = _into(ops, "dx", dx, dev, dt, shape)
+        dlog_alpha, dgp = _into(ops, "dlog_alpha", dlog_alpha, dev, dt, shape)
+        out = dict(dx=dx, dlog_alpha=dlog_alpha)
         if want_dh0:
             out["dh0"] = ops.empty((B, D), dtype=ops.f32, device=dev)
         p = ScanBwdParams(ops.dtype_code(x), B, T, D, 1 if complement else 0, x.data_ptr(), log_alpha.data_ptr(),
@@ -866,8 +886,7 @@ def ccq_scan_backward(x, log_alpha, dy, h0=None, dh_out=None, lengths=None, comp
                           _dense("lengths", lengths, dev, ops.i32, (B,)), _dense("h0", h0, dev, ops.f32, (B, D)),
                           _dense("dh_out", dh_out, dev, ops.f32, (B, D)),
                           _dense("chunk_carry", chunk_carry, dev, ops.f32, (B, (T + 63) // 64, D)),
-                          _dense("dx", out["dx"], dev, dt, shape), _dense("dlog_alpha", out["dlog_alpha"], dev, dt, shape),
-                          _ptr(out.get("dh0")), None, 0)
+                          dxp, dgp, _ptr(out.get("dh0")), None, 0)
         _launch(ops, "scan_backward", ops.scan_backward, p, dev, ops.scan_backward_workspace_bytes, workspace)
     return out
 
@@ -889,9 +908,10 @@ def ccq_beam_select(logits, scores, m: int, finished=None, pad_token: int = 0, w
             raise ValueError("the rows of logits must be evenly spaced")
         if finished is not None and finished.dtype == ops.torch.bool:
             finished = finished.view(ops.u8)
-        token = ops.empty((N, m), dtype=ops.i32, device=dev)
-        parent = ops.empty((N, m), dtype=ops.i32, device=dev)
-        score = ops.empty((N, m), dtype=ops.f32, device=dev)
+        size, strides = (N, m), (m, 1)
+        token = ops.empty_strided(size, strides, dtype=ops.i32, device=dev)
+        parent = ops.empty_strided(size, strides, dtype=ops.i32, device=dev)
+        score = ops.empty_strided(size, strides, dtype=ops.f32, device=dev)
         p = BeamParams(ops.dtype_code(logits), N, K, V, m, logits.data_ptr(), stride,
                        _dense("scores", scores, dev, ops.f32, (N, K)), _dense("finished", finished, dev, ops.u8, (N, K)),
                        pad_token, token.data_ptr(), parent.data_ptr(), score.data_ptr(), None, 0)
