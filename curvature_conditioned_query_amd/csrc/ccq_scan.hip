@@ -596,7 +596,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_backward_tile_kernel(ccq_sca
   load_run(x_raw, p.x, p.x_stride_b, p.x_stride_t, b, t0, c0, n, p.D);
   load_run(d_raw, p.dy, p.dy_stride_b, p.dy_stride_t, b, t0, c0, n, p.D);
   float h = 0.f;  // state before the tile
-  if (s * TILE < n && c < p.D)
+  if (carry && s * TILE < n && c < p.D)
     h = carry[((size_t)b * ((p.T + kChunk - 1) / kChunk) + s * (TILE / kChunk)) * p.D + c];
   if ((s + 1) * TILE > n) {
     clear_from(g_raw, n - t0);
@@ -735,10 +735,13 @@ hipError_t launch_tiles(const ccq_scan_params& p, void* workspace, hipStream_t s
   return hipGetLastError();
 }
 
+// Whether the gradient forms the states again: not if they were kept, or where h0 is the only one.
+bool forms_states(const ccq_scan_bwd_params& p) { return p.chunk_carry == nullptr && p.T > kChunk; }
+
 // The gradient's tiles and, where the states are formed again, the forward's before them.
 size_t tile_space(const ccq_scan_bwd_params& p) {
   const size_t back = tile_bytes(p.dtype, true, p.B, p.T, p.D);
-  const size_t ahead = p.chunk_carry ? 0 : tile_bytes(p.dtype, false, p.B, p.T, p.D);
+  const size_t ahead = forms_states(p) ? tile_bytes(p.dtype, false, p.B, p.T, p.D) : 0;
   return back > ahead ? back : ahead;
 }
 size_t carry_bytes(int B, int T, int D) {
@@ -763,12 +766,12 @@ hipError_t launch_scan(const ccq_scan_params& p, hipStream_t stream) {
 }
 
 size_t scan_backward_workspace_bytes(const ccq_scan_bwd_params& p) {
-  return tile_space(p) + (p.chunk_carry ? 0 : carry_bytes(p.B, p.T, p.D));
+  return tile_space(p) + (forms_states(p) ? carry_bytes(p.B, p.T, p.D) : 0);
 }
 
 hipError_t launch_scan_backward(const ccq_scan_bwd_params& p, hipStream_t stream) {
-  const float* carry = p.chunk_carry;
-    if (carry == nullptr) {
+  const float* carry = p.chunk_carry ? p.chunk_carry : p.h0;
+  if (forms_states(p)) {
     // the forward once more, for its kept states alone
     float* kept = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + tile_space(p));
     ccq_scan_params f{};

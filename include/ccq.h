@@ -448,7 +448,7 @@ typedef struct {
   const int32_t *lengths;    /* the forward's                                                       */
   const float *h0;           /* the forward's                                                       */
   const float *dh_out;       /* [B, D] gradient of h_out, or NULL: zeros                            */
-  const float *chunk_carry;  /* the forward's, or NULL: recomputed                                  */
+  const float *chunk_carry;  /* the forward's, or NULL: recomputed (T <= 64: h0 is all there is)    */
   void *dx, *dlog_alpha;     /* [B, T, D] dtype, written; zeros at t >= length                      */
   float *dh0;                /* [B, D], written, or NULL; may be dh_out itself                      */
   void *workspace;           /* ccq_scan_backward_workspace_bytes(p) bytes, or NULL when that is 0   */

@@ -108,6 +108,16 @@ def test_short_sequences_among_long_ones(gpu_lib, dtype, complement):
     _both(dtype, x, la, h0, n, complement)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 9, 64, 65])
+@pytest.mark.parametrize("state", [True, False])
+def test_gradient_of_one_chunk(gpu_lib, dtype, T, state):
+    """Up to 64 tokens the gradient needs no state but h0, which may be absent; beyond, it forms them."""
+    print(f"scan one chunk {dtype} T{T} h0={state}", flush=True)
+    x, la, h0, n = _make(dtype, 3, T, 136, 7, h0=state, lengths=[T, T // 2, 0])
+    _both(dtype, x, la, h0, n, True)
+
+
 @pytest.mark.parametrize("decay", [1e-5, 20.0])
 def test_slow_and_fast_gates(gpu_lib, decay):
     """Gates next to 1 (nothing is lost over the whole length) and gates that forget within a token."""
