@@ -660,6 +660,126 @@ __global__ __launch_bounds__(kThreads, 4) void scan_backward_tile_kernel(ccq_sca
   store_runs(p, x_raw, g_raw, b, t0, c0);
 }
 
+// ---------------------------------------------------------------- short sequences
+
+// Up to kChunk tokens: the runs of a workgroup are dealt out to several sequences, `each` (a power of two) a
+// sequence, on the same channels.  A thread folds its sequence's other runs for itself, and nothing is waited
+// for.  (131 sequences of up to 11 tokens, 2992 channels, bf16: 49 us in tiles, whose runs stood empty.)
+struct Seat {
+  int b, n, t0, c0;      // sequence, its length, the run's first token, the first of eight channels
+  int first, run, last;  // runs of the sequence
+  bool live;             // inside the tensor; else b is the last sequence
+};
+template <int RUN>
+__device__ __forceinline__ Seat take_seat(const int32_t* lengths, int B, int T, int D, int per_row, int each) {
+  Seat a;
+  const int group = blockIdx.x / per_row;
+  a.run = threadIdx.x / kOct;
+  a.first = a.run & ~(each - 1);
+  a.last = a.first + each - 1;
+  a.c0 = (blockIdx.x - group * per_row) * kCols + 8 * (threadIdx.x % kOct);
+  a.t0 = (a.run - a.first) * RUN;
+  const int b = group * (kRuns / each) + a.run / each;
+  a.live = b < B && a.c0 < D;
+  a.b = min(b, B - 1);
+  a.n = sequence_length(lengths, a.b, T);
+  return a;
+}
+
+template <typename T, bool COMPLEMENT>
+__global__ __launch_bounds__(kThreads, 4) void scan_short_kernel(ccq_scan_params p, int per_row, int each) {
+  constexpr int RUN = Run<T, false>::n;
+  __shared__ __align__(16) Pair runs[kRuns][kCols];
+  const Seat a = take_seat<RUN>(p.lengths, p.B, p.T, p.D, per_row, each);
+  const int ch = 8 * (threadIdx.x % kOct);
+  const size_t at = (size_t)a.b * p.D + min(a.c0, p.D - 8);
+  Raw8<T> g_raw[RUN], x_raw[RUN];
+  load_run(g_raw, p.log_alpha, p.la_stride_b, p.la_stride_t, a.b, a.t0, a.c0, a.n, p.D);
+  load_run(x_raw, p.x, p.x_stride_b, p.x_stride_t, a.b, a.t0, a.c0, a.n, p.D);
+  float h[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (p.h0) load8(p.h0 + at, h);  // before anyone writes h_out, which may be h0
+  clear_from(g_raw, a.n - a.t0);
+  clear_from(x_raw, a.n - a.t0);
+  Pair mine[8];
+  const bool resets = __any(fold_run<false, COMPLEMENT>(g_raw, x_raw, mine));
+  if (resets) fold_run<true, COMPLEMENT>(g_raw, x_raw, mine);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) runs[a.run][ch + e] = mine[e];
+  __syncthreads();
+  if (!a.live) return;
+  if (p.chunk_carry && a.run == a.first && a.n > 0) store8(p.chunk_carry + at, h);
+  for (int r = a.first; r < a.run; ++r) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = through(h[e], runs[r][ch + e]);
+  }
+  if (p.h_out && a.run == a.last) {
+    float end[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) end[e] = through(h[e], mine[e]);
+    store8(p.h_out + at, end);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) mine[e].P = h[e];
+  if (resets) walk_run<true, COMPLEMENT>(g_raw, x_raw, mine);
+  else walk_run<false, COMPLEMENT>(g_raw, x_raw, mine);
+  T* y = static_cast<T*>(p.y) + ((size_t)a.b * p.T + a.t0) * p.D + a.c0;
+#pragma unroll
+  for (int r = 0; r < RUN; ++r)
+    if (a.t0 + r < a.n) x_raw[r].store(y + (size_t)r * p.D);
+}
+
+// states: before the only chunk, [B, D], or null.
+template <typename T, bool COMPLEMENT>
+__global__ __launch_bounds__(kThreads, 4) void scan_short_backward_kernel(ccq_scan_bwd_params p, const float* states,
+                                                                          int per_row, int each) {
+  constexpr int RUN = Run<T, true>::n;
+  __shared__ __align__(16) Pair runs[kRuns][kCols];
+  __shared__ __align__(16) float back[kRuns][kCols];
+  const Seat a = take_seat<RUN>(p.lengths, p.B, p.T, p.D, per_row, each);
+  const int ch = 8 * (threadIdx.x % kOct);
+  const size_t at = (size_t)a.b * p.D + min(a.c0, p.D - 8);
+  Raw8<T> g_raw[RUN], x_raw[RUN], d_raw[RUN];
+  load_run(g_raw, p.log_alpha, p.la_stride_b, p.la_stride_t, a.b, a.t0, a.c0, a.n, p.D);
+  load_run(x_raw, p.x, p.x_stride_b, p.x_stride_t, a.b, a.t0, a.c0, a.n, p.D);
+  load_run(d_raw, p.dy, p.dy_stride_b, p.dy_stride_t, a.b, a.t0, a.c0, a.n, p.D);
+  float h[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, d[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (states && a.n > 0) load8(states + at, h);
+  if (p.dh_out) load8(p.dh_out + at, d);  // before anyone writes dh0, which may be dh_out
+  clear_from(g_raw, a.n - a.t0);
+  clear_from(x_raw, a.n - a.t0);
+  clear_from(d_raw, a.n - a.t0);
+  Pair mine[8];
+  float q[8];
+  const bool resets = __any(fold_run_back<false, COMPLEMENT>(g_raw, x_raw, d_raw, mine, q));
+  if (resets) fold_run_back<true, COMPLEMENT>(g_raw, x_raw, d_raw, mine, q);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) runs[a.run][ch + e] = mine[e];
+  store8(&back[a.run][ch], q);
+  __syncthreads();
+  if (!a.live) return;
+  for (int r = a.first; r < a.run; ++r) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = through(h[e], runs[r][ch + e]);
+  }
+  for (int r = a.last; r > a.run; --r) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) d[e] = through(d[e], Pair{runs[r][ch + e].P, back[r][ch + e]});
+  }
+  if (p.dh0 && a.run == a.first) {
+    float front[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) front[e] = through(d[e], Pair{mine[e].P, q[e]});
+    store8(p.dh0 + at, front);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) mine[e] = Pair{h[e], d[e]};
+  if (resets) walk_run_back<true, COMPLEMENT>(g_raw, x_raw, d_raw, mine);
+  else walk_run_back<false, COMPLEMENT>(g_raw, x_raw, d_raw, mine);
+  clear_from(g_raw, a.n - a.t0);
+  clear_from(x_raw, a.n - a.t0);
+  store_runs(p, x_raw, g_raw, a.b, a.t0, a.c0);
+}
+
 // A few tokens: eight channels a thread, one token behind the other.
 template <typename T>
 __global__ __launch_bounds__(kStepThreads) void scan_step_kernel(ccq_scan_params p) {
@@ -720,6 +840,20 @@ hipError_t clear_tiles(const Tiles& t, size_t words, hipStream_t stream) {
 // Up to this many tokens go one behind the other in a thread.
 constexpr int kMostSteps = 8;
 
+// Runs of a short sequence, which every thread of it goes through, and the workgroups that hold all sequences.
+// With 32 a sequence (the fp32 gradient of 64 tokens) the tiles' own way is faster, 35 against 58 us at B64
+// D2048; with 16 it is not (30 tokens 23.6 against 22.9; the bf16 forward of 64 14.8 against 13.5).
+constexpr int kMostRuns = 16;
+int runs_each(int T, int run) {
+  int each = 1;
+  while (each <= kMostRuns && each * run < T) each *= 2;
+  return each;
+}
+unsigned short_grid(int B, int D, int each) {
+  const int sequences = kRuns / each;
+  return (unsigned)(((int64_t)B + sequences - 1) / sequences * ((D + kCols - 1) / kCols));
+}
+
 hipError_t launch_tiles(const ccq_scan_params& p, void* workspace, hipStream_t stream) {
   const Tiles t = tiles_of(p.dtype, false, p.B, p.T, p.D, workspace);
   const hipError_t e = clear_tiles(t, tile_words(p.dtype, false, p.B, p.T, p.D), stream);
@@ -758,6 +892,20 @@ bool scan_grid_fits(int B, int T, int D) {
 size_t scan_workspace_bytes(const ccq_scan_params& p) { return p.T <= kMostSteps ? 0 : tile_bytes(p.dtype, false, p.B, p.T, p.D); }
 
 hipError_t launch_scan(const ccq_scan_params& p, hipStream_t stream) {
+  if (p.T > kMostSteps && p.T <= kChunk) {
+    static_assert(kChunk <= kMostRuns * Run<__bf16, false>::n && kChunk <= kMostRuns * Run<float, false>::n, "short");
+    const int per_row = (p.D + kCols - 1) / kCols;
+    const int each = runs_each(p.T, p.dtype == CCQ_DTYPE_BF16 ? Run<__bf16, false>::n : Run<float, false>::n);
+    const unsigned grid = short_grid(p.B, p.D, each);
+    if (p.dtype == CCQ_DTYPE_BF16) {
+      if (p.complement) scan_short_kernel<__bf16, true><<<grid, kThreads, 0, stream>>>(p, per_row, each);
+      else scan_short_kernel<__bf16, false><<<grid, kThreads, 0, stream>>>(p, per_row, each);
+    } else {
+      if (p.complement) scan_short_kernel<float, true><<<grid, kThreads, 0, stream>>>(p, per_row, each);
+      else scan_short_kernel<float, false><<<grid, kThreads, 0, stream>>>(p, per_row, each);
+    }
+    return hipGetLastError();
+  }
   if (p.T > kMostSteps) return launch_tiles(p, p.workspace, stream);
   const unsigned grid = (unsigned)(((int64_t)p.B * (p.D / 8) + kStepThreads - 1) / kStepThreads);
   if (p.dtype == CCQ_DTYPE_BF16) scan_step_kernel<__bf16><<<grid, kStepThreads, 0, stream>>>(p);
@@ -771,6 +919,19 @@ size_t scan_backward_workspace_bytes(const ccq_scan_bwd_params& p) {
 
 hipError_t launch_scan_backward(const ccq_scan_bwd_params& p, hipStream_t stream) {
   const float* carry = p.chunk_carry ? p.chunk_carry : p.h0;
+  const int each = runs_each(p.T, p.dtype == CCQ_DTYPE_BF16 ? Run<__bf16, true>::n : Run<float, true>::n);
+  if (p.T <= kChunk && each <= kMostRuns) {
+    const int per_row = (p.D + kCols - 1) / kCols;
+    const unsigned grid = short_grid(p.B, p.D, each);
+    if (p.dtype == CCQ_DTYPE_BF16) {
+      if (p.complement) scan_short_backward_kernel<__bf16, true><<<grid, kThreads, 0, stream>>>(p, carry, per_row, each);
+      else scan_short_backward_kernel<__bf16, false><<<grid, kThreads, 0, stream>>>(p, carry, per_row, each);
+    } else {
+      if (p.complement) scan_short_backward_kernel<float, true><<<grid, kThreads, 0, stream>>>(p, carry, per_row, each);
+      else scan_short_backward_kernel<float, false><<<grid, kThreads, 0, stream>>>(p, carry, per_row, each);
+    }
+    return hipGetLastError();
+  }
   if (forms_states(p)) {
     // the forward once more, for its kept states alone
     float* kept = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + tile_space(p));

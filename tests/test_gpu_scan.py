@@ -118,6 +118,32 @@ def test_gradient_of_one_chunk(gpu_lib, dtype, T, state):
     _both(dtype, x, la, h0, n, True)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("complement", [False, True])
+@pytest.mark.parametrize("B,T,D", [(70, 9, 136), (33, 17, 8), (9, 33, 264), (40, 4, 128), (130, 1, 72), (5, 48, 640)])
+def test_many_short_sequences(gpu_lib, dtype, complement, B, T, D):
+    """Several sequences a workgroup: lengths from 0 to T beside each other, resets in some of them."""
+    print(f"scan short {dtype} B{B} T{T} D{D}", flush=True)
+    lengths = [(7 * b) % (T + 1) for b in range(B)]
+    x, la, h0, n = _make(dtype, B, T, D, 8, lengths=lengths)
+    la[1::3, T // 2, ::5] = -float("inf")
+    for b, k in enumerate(lengths):
+        x[b, k:] = float("nan")
+        la[b, k:] = float("inf")
+    _both(dtype, x, la, h0, n, complement)
+
+
+@pytest.mark.parametrize("T", [1, 7, 20, 64])
+def test_short_sequences_in_place(gpu_lib, T):
+    """h_out over h0, which other threads of the sequence read."""
+    import torch
+    from curvature_conditioned_query_amd import ccq_scan
+    x, la, h0, _ = _make("bf16", 50, T, 256, 9)
+    h, apart = h0.clone(), torch.empty_like(h0)
+    y = ccq_scan(x, la, h0=h0, h_out=apart)
+    assert torch.equal(ccq_scan(x, la, h0=h, h_out=h), y) and torch.equal(h, apart)
+
+
 @pytest.mark.parametrize("decay", [1e-5, 20.0])
 def test_slow_and_fast_gates(gpu_lib, decay):
     """Gates next to 1 (nothing is lost over the whole length) and gates that forget within a token."""
