@@ -548,12 +548,11 @@ __device__ __forceinline__ double key_order(uint64_t key) {
 // Picks M of a request's lists.  Of the lists' entries at one depth, the best M / depth give a bound that M
 // continuations reach and few others do; the depth is such that one list in eight speaks for it, beams being
 // unlike (8 beams of 4 lists, M = 16: 20 to 70 reach it, 6.5 us; with half of the lists, their heads, 70 to 140,
-// 10 us).  Where many reach it all the same, as at M = 64 of 32 lists (24 us, 21 without the attempt), or
-// there are more lists than threads: eight bits at a time of the total and then of the place, the continuations
-// that agree with the M-th best so far are counted by their next digit, until few enough are left with those
-// above them to be ranked by counting.
+// 10 us).  Where many reach it all the same, as at M = 64 of 32 lists (24 us, 21 without the attempt):
+// eight bits at a time of the total and then of the place, the continuations that agree with the M-th best so
+// far are counted by their next digit, until few enough are left with those above them to be ranked by counting.
 constexpr int kRanked = 128;
-constexpr int kHeads = 256;
+constexpr int kHeads = 256;  // most lists of a request
 __global__ __launch_bounds__(kThreads) void beam_join_kernel(ccq_beam_params p, int stretches, BeamWork work) {
   __shared__ BeamBase base[kBeamMaxBeams];
   __shared__ int bins[256];
@@ -614,7 +613,7 @@ __global__ __launch_bounds__(kThreads) void beam_join_kernel(ccq_beam_params p, 
   };
   auto entry = [&](int i, double& total, unsigned& place) { return value(i, picks[i], total, place); };
   bool few = false;  // those that reach the bound
-  if (lists <= kHeads && (M <= 32 || lists > M)) {
+  if (M <= 32 || lists > M) {
     const int deep = min(M, (8 * M + lists - 1) / lists), enough = (M + deep - 1) / deep;
     double total;
     unsigned place;
@@ -747,7 +746,9 @@ struct BeamShape {
 };
 
 // 32 logits a thread and as many stretches a row as make 1024 workgroups, four for each CU; with few rows,
-// where the time is the latency of one workgroup, 8 logits a thread.
+// where the time is the latency of one workgroup, 8 logits a thread.  A request has no more lists than the
+// join has threads (one of 16 beams, 41,115 tokens, bf16: 19 us; with 336 lists
+// 43; one of 64, 131,072 tokens, fp32, M = 64: 108 and 400).
 BeamShape beam_shape(const ccq_beam_params& p) {
   const long long rows = (long long)p.N * p.K;
   BeamShape s;
@@ -756,7 +757,7 @@ BeamShape beam_shape(const ccq_beam_params& p) {
   const long long whole = (p.V + (long long)kThreads * s.per_thread - 1) / (kThreads * s.per_thread);  // pieces of a row
   long long want = (1024 + rows - 1) / rows;
   if (want > whole) want = whole;
-  if (want * p.K > kBeamMaxLists) want = kBeamMaxLists / p.K;
+  if (want * p.K > kHeads) want = kHeads / p.K;
   s.pieces = (int)((whole + want - 1) / want);
   s.stretches = (int)((whole + s.pieces - 1) / s.pieces);
   return s;
@@ -767,10 +768,10 @@ void launch_rows(const ccq_beam_params& p, const BeamShape& s, BeamWork w, hipSt
   beam_rows_kernel<T, E, ONE><<<(unsigned)(p.N * p.K * s.stretches), kThreads, 0, stream>>>(p, s.stretches, s.pieces, w);
 }
 
-// At 8 logits a thread there are fewer than 1024 pieces in all, so a stretch is one of them.
 template <typename T>
 void launch_rows_of(const ccq_beam_params& p, const BeamShape& s, BeamWork w, hipStream_t stream) {
-  if (s.per_thread == 8) launch_rows<T, 8, true>(p, s, w, stream);
+  if (s.per_thread == 8 && s.pieces == 1) launch_rows<T, 8, true>(p, s, w, stream);
+  else if (s.per_thread == 8) launch_rows<T, 8, false>(p, s, w, stream);
   else if (s.pieces == 1) launch_rows<T, 32, true>(p, s, w, stream);
   else launch_rows<T, 32, false>(p, s, w, stream);
 }

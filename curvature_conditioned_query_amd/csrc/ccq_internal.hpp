@@ -165,8 +165,8 @@ size_t scan_backward_workspace_bytes(const ccq_scan_bwd_params& p);
 hipError_t launch_scan_backward(const ccq_scan_bwd_params& p, hipStream_t stream);
 constexpr int kBeamMaxBeams = 64;
 constexpr int kBeamMaxPicks = 64;
-constexpr int kBeamMaxChunk = 16384;  // a row counts as this many logits a list in the limit below
-constexpr int kBeamMaxLists = 4096;   // lists of a request, joined by one workgroup
+constexpr int kBeamMaxChunk = 16384;  // logits of a beam are counted by as many in the limit below,
+constexpr int kBeamMaxLists = 4096;   // which keeps a request's within 2^26
 size_t beam_workspace_bytes(const ccq_beam_params& p);
 hipError_t launch_beam_select(const ccq_beam_params& p, hipStream_t stream);
 hipError_t launch_beam_reorder(int n_states, void* const* states, const size_t* row_bytes, int N, int K,

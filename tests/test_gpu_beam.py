@@ -172,6 +172,26 @@ def test_rows_of_several_pieces(gpu_lib, dtype, m):
     _run(x, (-_uniform(N, K, g)).cuda(), m, tag="pieces")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K,V,m", [(64, 9001, 64), (40, 14337, 7), (16, 41115, 16), (64, 40000, 64), (3, 250001, 8)])
+def test_one_request_of_many_beams(gpu_lib, dtype, K, V, m):
+    """Its lists are kept to a workgroup's threads, so that stretches get longer: ties and masks at their ends."""
+    import torch
+    x, g = _logits(1, K, V, dtype, K)
+    rows = x[0]
+    rows[0] = 0.5
+    rows[1] = torch.randint(0, 3, (V,), generator=g).cuda().to(x.dtype)
+    rows[2, : V - 3] = -float("inf")
+    if K > 8:
+        rows[3, 2048] = float("nan")
+        rows[4, 2047] = float("inf")
+        rows[5, 2048:] = -float("inf")
+        rows[6] = torch.linspace(-5, 5, V).cuda().to(x.dtype)
+        rows[7] = rows[6]
+    _run(x, (-_uniform(1, K, g)).cuda(), m, tag="one request")
+    _run(x, torch.zeros(1, K).cuda(), m, tag="one request, equal scores")
+
+
 @pytest.mark.parametrize("K", [1, 2, 3, 4, 5, 8, 13, 16, 17, 40, 64])
 def test_reorder(gpu_lib, K):
     """States of many row sizes and types, moved in place by every kind of parents."""
