@@ -790,7 +790,7 @@ struct ReorderArgs {
 // no other thread touches those bytes, so the move is in place, whatever the parents are, and only
 // rows that move are touched.  STREAM: past the caches.
 // Measured: 64 requests of 4 beams, the carries of 16 heads of 128 (718 MB moved): 130 us, 5.5 TB/s past the
-// caches, 141 through them; 20 of 8 beams and 2 heads (42 MB of states): 22 and 17.6.
+// caches, 141 through them; 8 requests' (67 MB of states): 17.2 and 14.9.
 template <typename W, int KMAX, bool STREAM>
 __device__ __forceinline__ void move_columns(unsigned char* base, size_t row, size_t off, const int (&par)[KMAX], int K) {
   W v[KMAX];
@@ -858,10 +858,11 @@ hipError_t launch_beam_select(const ccq_beam_params& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Room for 4, 16 or 64 beams.  (Room for 8 takes 222 registers, two waves a SIMD, where 16 takes 66: 223 requests
+// of 8 beams, 468 MB of states, 214 us against 135.)
 template <bool STREAM>
 static void launch_reorder(const ReorderArgs& a, unsigned grid, unsigned blocks, hipStream_t stream) {
   if (a.K <= 4) beam_reorder_kernel<4, STREAM><<<grid, kThreads, 0, stream>>>(a, blocks);
-  else if (a.K <= 8) beam_reorder_kernel<8, STREAM><<<grid, kThreads, 0, stream>>>(a, blocks);
   else if (a.K <= 16) beam_reorder_kernel<16, STREAM><<<grid, kThreads, 0, stream>>>(a, blocks);
   else beam_reorder_kernel<64, STREAM><<<grid, kThreads, 0, stream>>>(a, blocks);
 }
