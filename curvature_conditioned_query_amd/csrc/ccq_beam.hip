@@ -645,6 +645,7 @@ __global__ __launch_bounds__(kThreads) void beam_join_kernel(ccq_beam_params p, 
     few = found >= M && found <= kRanked;
     __syncthreads();
     if (!few && tid == 0) found = 0;
+    __syncthreads();  // what is counted below may follow at once
   }
   uint64_t high = 0;  // the digits of the M-th best known so far: of the total, and of the place's complement
   unsigned low = 0;

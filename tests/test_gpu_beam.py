@@ -249,3 +249,13 @@ def test_other_stream_and_replayed_capture(gpu_lib):
         assert all(torch.equal(want[n], out[n]) for n in want)
         rows = (torch.arange(3, device="cuda")[:, None] * 4 + want["parent"]).flatten().long()
         assert torch.equal(state, fresh[rows])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K,V,m", [(8, 5, 16), (16, 3, 8), (4, 20, 32), (2, 40, 64), (32, 2, 4), (13, 3, 9)])
+def test_lists_shorter_than_the_picks(gpu_lib, dtype, K, V, m):
+    """No list has an entry at the depth that the join looks at first, and 65 to 128 entries in all, held by
+    two waves: none of them may be lost."""
+    logits, g = _logits(40, K, V, dtype, V + m)
+    for i in range(3):
+        _run(logits, (-_uniform(40, K, g)).cuda(), m, tag=f"short lists {i}")
