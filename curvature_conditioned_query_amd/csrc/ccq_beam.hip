@@ -71,12 +71,12 @@ __device__ __forceinline__ float as_counted(float x) { return fminf(fmaxf(x, -IN
 
 constexpr float kLog2e = 1.44269502162933349609f;
 
-// A row's beam: 0 goes on, 1 finished, 2 dead (its score is -inf or NaN).  Both loads are made, so that neither
-// waits for the other.
+// A row's beam: 0 goes on, 1 finished, 2 dead (its score is -inf or NaN, finished or not: all its continuations are
+// at -inf, the pad token's too).  Both loads are made, so that neither waits for the other.
 __device__ __forceinline__ int beam_kind(const ccq_beam_params& p, int row, float& score) {
   score = p.scores[row];
   const bool finished = p.finished && p.finished[row];
-  return finished ? 1 : score > -INFINITY ? 0 : 2;
+  return score > -INFINITY ? (finished ? 1 : 0) : 2;
 }
 
 // 16 bytes from any element on: a row starts where the one before ends, at an odd address for an odd
@@ -577,7 +577,7 @@ __global__ __launch_bounds__(kThreads) void beam_join_kernel(ccq_beam_params p, 
     float score;
     int kind = beam_kind(p, row, score);
     if (k >= K) kind = 2;
-    BeamBase b{score > -INFINITY ? score : -INFINITY, 0.0, kind};  // NaN counts as -inf
+    BeamBase b{score, 0.0, kind};
     float top = -INFINITY;
     if (kind == 0) {
       if (mine < stretches) top = first.top;

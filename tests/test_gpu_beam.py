@@ -259,3 +259,16 @@ def test_lists_shorter_than_the_picks(gpu_lib, dtype, K, V, m):
     logits, g = _logits(40, K, V, dtype, V + m)
     for i in range(3):
         _run(logits, (-_uniform(40, K, g)).cuda(), m, tag=f"short lists {i}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,pad,m", [(50, 49, 8), (5000, 4999, 16), (5000, 3000, 64), (3, 2, 2)])
+def test_finished_beams_without_a_score(gpu_lib, dtype, V, pad, m):
+    """A finished beam at -inf or NaN has nothing but continuations at -inf, its pad token among them: they go
+    in order of token, wherever that token stands."""
+    import torch
+    inf, nan = float("inf"), float("nan")
+    logits, _ = _logits(4, 2, V, dtype, V)
+    scores = torch.tensor([[-inf, -inf], [nan, -1.0], [-inf, nan], [-2.0, -inf]]).cuda()
+    fin = torch.tensor([[1, 0], [1, 1], [1, 1], [1, 1]], dtype=torch.uint8).cuda()
+    _run(logits, scores, m, finished=fin, pad=pad, tag="finished without a score")
