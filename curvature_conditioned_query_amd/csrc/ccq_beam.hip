@@ -25,7 +25,10 @@
 //
 // Scores of different beams meet in the comparison, so the normaliser has to be good to more than
 // fp32: the candidates, which carry most of a peaked distribution, are left out of the fp32 sum and added
-// in 64 bits, and the threads' sums of the rest, 2^(x log2(e) - c), are joined in 64 bits.
+// in 64 bits, and the threads' sums of the rest, 2^((x - top) log2(e)), are joined in 64 bits.  The difference
+// comes first, so that a term's error goes by its distance from the top and not by the logits' size, and what lies
+// far below is 0 (x log2(e) - top log2(e) as one fused operation saves an instruction a logit, and is wrong by the
+// product's rounding: 0.01 % for logits at 10^4, everything from 10^9 on).
 #include <float.h>
 
 #include "ccq_device.hpp"
@@ -429,7 +432,6 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 1) void beam_rows_ke
       top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
     }
     float higher = bound;  // for the pieces to come: this one's later groups hold tokens on either side of a tie
-    const float c = top * kLog2e;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int g = 0; g < E; g += G) {
@@ -455,10 +457,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 1) void beam_rows_ke
           n = M;
         }
       }
-      if (fabsf(top) < 1e30f) {
-#pragma unroll
-        for (int i = 0; i < G; ++i) sum[i & 3] += __builtin_amdgcn_exp2f(fmaf(x[i], kLog2e, -c));
-      } else if (top > -INFINITY) {
+      if (top > -INFINITY) {
 #pragma unroll
         for (int i = 0; i < G; ++i) sum[i & 3] += __builtin_amdgcn_exp2f((x[i] - top) * kLog2e);
       } else {
@@ -481,13 +480,11 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 1) void beam_rows_ke
   for (int i = lane; i < n; i += 64) most = fmaxf(most, key_logit(held[wave].key[i]));
   most = wave_max(most);
   careful |= most == INFINITY;
-  // the wave's part of the normaliser, from the greater of the two on; c, the rounded top log2(e), is what the
-  // fp32 sum counts from
+  // the wave's part of the normaliser, from the greater of the two on
   const float from = fmaxf(top, most);
   double sum = 0.0;
   if (from > -INFINITY) {
-    if (top > -INFINITY)
-      sum = (double)part * exp((fabsf(top) < 1e30f ? (double)(top * kLog2e) * 0.69314718055994530942 : (double)top) - (double)from);
+    if (top > -INFINITY) sum = (double)part * exp((double)top - (double)from);
     for (int i = lane; i < n; i += 64) sum += exp((double)key_logit(held[wave].key[i]) - (double)from);
     if (ref > -INFINITY) sum += gone * exp((double)ref - (double)from);
   }

@@ -272,3 +272,29 @@ def test_finished_beams_without_a_score(gpu_lib, dtype, V, pad, m):
     scores = torch.tensor([[-inf, -inf], [nan, -1.0], [-inf, nan], [-2.0, -inf]]).cuda()
     fin = torch.tensor([[1, 0], [1, 1], [1, 1], [1, 1]], dtype=torch.uint8).cuda()
     _run(logits, scores, m, finished=fin, pad=pad, tag="finished without a score")
+
+
+MASKS = [-1e3, -1e4, -1e6, -1e7, -1e9, -1e10, -1e11, -1e12, -1e18, -1e20, -1e30, -1e38, 1e4]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,K,V,m", [(1, 15, 32000, 8), (2, 15, 70001, 16), (70, 15, 9000, 16)])
+def test_finite_masks_of_every_size(gpu_lib, dtype, N, K, V, m):
+    """Rows, stretches and a row's first or last 8192 tokens at one far value: it counts as what it is, and what stands
+    beside it as if it stood alone."""
+    import torch
+    for where in ("row", "first", "last", "all but a few"):
+        logits, g = _logits(N, K, V, dtype, V)
+        for i, value in enumerate(MASKS):
+            part = {"row": slice(0, V), "first": slice(0, 8192), "last": slice(V - 8192, V), "all but a few": slice(3, V - 2)}[where]
+            logits[:, i, part] = value
+        _run(logits.view(N * K, 1, V), -torch.ones(N * K, 1).cuda(), m, tag=f"{where}, one beam a request")
+        _run(logits, (-_uniform(N, K, g)).cuda(), m, tag=where)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("offset", [60.0, 1e3, -1e3, 1e4, -1e4, 1e6])
+def test_scores_do_not_depend_on_an_offset(gpu_lib, dtype, offset):
+    logits, g = _logits(2, 4, 32001, dtype, 5)
+    moved = (logits.float() + offset).to(logits.dtype)
+    _run(moved, (-_uniform(2, 4, g)).cuda(), 8, tag=f"offset {offset}")
