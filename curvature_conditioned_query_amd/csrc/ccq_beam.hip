@@ -392,9 +392,9 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 1) void beam_rows_ke
   }
 
   float bound = -INFINITY;  // candidates lie above it
-  float top = -INFINITY;    // the sum of the others counts from here
+  float top = -INFINITY;    // the sum of the others counts from here: no logit of theirs lies above it
   float part = 0.f;
-  double gone = 0.0;        // of candidates that were thinned out, counted from ref
+  double gone = 0.0;        // of candidates that were thinned out, counted from ref; and of part before top moved
   float ref = -INFINITY;
   int n = 0;                // candidates of the wave
 
@@ -455,6 +455,13 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 1) void beam_rows_ke
         if (n > kHeld - 64 * G) {
           higher = thin(held[wave], n, M, gone, ref);
           n = M;
+          if (!ONE && higher > top) {
+            // logits up to here are no candidates from now on, and may lie far above the first piece's top: what
+            // was summed goes to the thinned ones' sum, and the fp32 sum begins anew
+            gone += (double)(part + ((sum[0] + sum[1]) + (sum[2] + sum[3]))) * exp((double)top - (double)ref);
+            part = sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
+            top = higher;
+          }
         }
       }
       if (top > -INFINITY) {
@@ -469,7 +476,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 1) void beam_rows_ke
     part += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     bound = higher;
   }
-  bool careful = part != part || top == INFINITY;
+  bool careful = part != part || gone != gone || top == INFINITY;
   if (n > 128) {
     thin(held[wave], n, M, gone, ref);
     n = M;

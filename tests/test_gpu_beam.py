@@ -298,3 +298,24 @@ def test_scores_do_not_depend_on_an_offset(gpu_lib, dtype, offset):
     logits, g = _logits(2, 4, 32001, dtype, 5)
     moved = (logits.float() + offset).to(logits.dtype)
     _run(moved, (-_uniform(2, 4, g)).cuda(), 8, tag=f"offset {offset}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,K,V,m", [(64, 16, 32003, 16), (64, 16, 24577, 1), (64, 16, 26000, 64), (1, 64, 100000, 16), (1, 8, 253000, 8)])
+def test_pieces_far_above_the_first(gpu_lib, dtype, N, K, V, m):
+    """A workgroup goes through three and more pieces, and the first tells nothing of the rest: at -inf, at a mask,
+    or of a row that rises by several hundred.  Every later token is in the normaliser."""
+    import torch
+    x, g = _logits(N, K, V, dtype, V)
+    rows = x.view(N * K, V)
+    lowest = torch.finfo(x.dtype).min
+    rows[0::8, :8192] = -float("inf")
+    rows[1::8, :8192] = -1e4
+    rows[2::8, :8192] = lowest
+    rows[3::8] = rows[3::8] * 0.1 + torch.linspace(-300, 400, V).cuda().to(x.dtype)
+    rows[4::8, : V // 2] = -float("inf")
+    rows[5::8, 8192:16384] -= 200
+    rows[6::8, :8192] -= 100
+    rows[7::8] = torch.linspace(400, -300, V).cuda().to(x.dtype)
+    _run(x, (-_uniform(N, K, g)).cuda(), m, tag="rising pieces")
+    _run(x.view(N * K, 1, V), -torch.ones(N * K, 1).cuda(), m, tag="rising pieces, one beam a request")
