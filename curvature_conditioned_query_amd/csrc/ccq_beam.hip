@@ -273,6 +273,9 @@ __device__ __forceinline__ unsigned reached_by(const unsigned (&words)[kThreads]
     reached |= (unsigned)digit << bit;
     if (digit && (digit == 3 ? n[3] : digit == 2 ? n[2] : n[1]) == count) break;
   }
+  // the bits that none differs in are ones in the word of a negative number: without them the number would lie
+  // just below the one it stands for, and a row of one negative value would be all candidates
+  if (BITS < 32 && reached < 0x80000000u) reached |= (1u << (32 - BITS)) - 1;
   return reached;
 }
 

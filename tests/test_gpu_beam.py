@@ -319,3 +319,14 @@ def test_pieces_far_above_the_first(gpu_lib, dtype, N, K, V, m):
     rows[7::8] = torch.linspace(400, -300, V).cuda().to(x.dtype)
     _run(x, (-_uniform(N, K, g)).cuda(), m, tag="rising pieces")
     _run(x.view(N * K, 1, V), -torch.ones(N * K, 1).cuda(), m, tag="rising pieces, one beam a request")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("value", [-3.0, -0.0, -1e4, 2.0])
+def test_rows_of_one_value_in_several_pieces(gpu_lib, dtype, value):
+    """The bound is the row's one value, positive or negative: no token lies above it, and the lowest are looked up."""
+    import torch
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    x = torch.full((64, 16, 20000), value, dtype=dt).cuda()
+    x[5:, :, 17000] += 1
+    _run(x, torch.zeros(64, 16).cuda(), 16, tag=f"all {value}")
