@@ -92,6 +92,16 @@ __device__ __forceinline__ float one_minus(float g, float alpha) {
   return fabsf(g) < 0.25f ? -g * s : 1.f - alpha;
 }
 
+// The same within 2^-19 of itself, for what is stored in bf16 a few tokens on (all of the series there: 56 against 55 us
+// at B4 T4096 D2048, 84 against 82 for the gradient).
+__device__ __forceinline__ float one_minus_short(float g, float alpha) {
+  return fabsf(g) < 1.f / 32.f ? -g * fmaf(fmaf(1.f / 6.f, g, 0.5f), g, 1.f) : 1.f - alpha;
+}
+template <bool SHORT>
+__device__ __forceinline__ float complement_of(float g, float alpha) {
+  return SHORT ? one_minus_short(g, alpha) : one_minus(g, alpha);
+}
+
 // alpha h, and alpha h + u; with RESETS 0 h = 0 for every h.  Where no gate of a wave is 0, as is the
 // rule, its walks go without that test, a third of their operations.
 template <bool RESETS>
@@ -102,14 +112,12 @@ template <bool RESETS>
 __device__ __forceinline__ float step(float alpha, float h, float u) {
   return RESETS && alpha == 0.f ? u : fmaf(alpha, h, u);
 }
-// The state behind a token.  With the complement scale, alpha h + (1 - alpha) x: EXACT from 1 - alpha formed
-// to its last place, as an fp32 result needs; else as x + alpha (h - x), which rounds at the size of x, for
-// the few tokens between a state so formed and results stored in bf16.
-template <bool RESETS, bool COMPLEMENT, bool EXACT>
+// The state behind a token.  With the complement scale, alpha h + (1 - alpha) x, from 1 - alpha formed for itself:
+// x + alpha (h - x), which spares some operations, rounds at the size of x, and behind gates next to 1 the state is
+// far smaller.
+template <bool RESETS, bool COMPLEMENT, bool SHORT>
 __device__ __forceinline__ float advance(float alpha, float g, float h, float x) {
-  if constexpr (!COMPLEMENT) return step<RESETS>(alpha, h, x);
-  if constexpr (EXACT) return step<RESETS>(alpha, h, x * one_minus(g, alpha));
-  return step<RESETS>(alpha, h - x, x);
+  return step<RESETS>(alpha, h, COMPLEMENT ? x * complement_of<SHORT>(g, alpha) : x);
 }
 
 // The product of a run's gates, one more of them.
@@ -351,7 +359,7 @@ __device__ __forceinline__ bool fold_run(Raw8<T> (&g_raw)[RUN], Raw8<T> (&x_raw)
 #pragma unroll
       for (int t = 0; t < RUN; ++t) {
         const float g = g_raw[t].get(i, e), x = x_raw[t].get(i, e), a = gate<T>(g);
-        r.q = advance<RESETS, COMPLEMENT, true>(a, g, r.q, x);
+        r.q = advance<RESETS, COMPLEMENT, false>(a, g, r.q, x);
         r.P = t == 0 && !RESETS ? a : gates_product<RESETS>(r.P, a);
       }
       zero |= r.P == 0.f;
@@ -376,7 +384,7 @@ __device__ __forceinline__ void walk_run(Raw8<T> (&g_raw)[RUN], Raw8<T> (&x_raw)
 #pragma unroll
       for (int t = 0; t < RUN; ++t) {
         const float g = g_raw[t].get(i, e), x = x_raw[t].get(i, e), a = gate<T>(g);
-        h[t][e] = state = advance<RESETS, COMPLEMENT, sizeof(T) == 4>(a, g, state, x);
+        h[t][e] = state = advance<RESETS, COMPLEMENT, sizeof(T) == 2>(a, g, state, x);
       }
       done = state;
     }
@@ -486,9 +494,12 @@ __device__ __forceinline__ bool fold_run_back(Raw8<T> (&g_raw)[RUN], Raw8<T> (&x
       for (int t = 0; t < RUN; ++t) {
         const float g = g_raw[t].get(i, e), x = x_raw[t].get(i, e);
         a[t] = gate<T>(g);
-        r.q = advance<RESETS, COMPLEMENT, sizeof(T) == 4>(a[t], g, r.q, x);
+        r.q = advance<RESETS, COMPLEMENT, sizeof(T) == 2>(a[t], g, r.q, x);
         r.P = t == 0 && !RESETS ? a[t] : gates_product<RESETS>(r.P, a[t]);
       }
+      // the scaled inputs first: the adjoint's gradients taken up among them, registers spill (94 against 82 us at
+      // B4 T4096 D2048)
+      if constexpr (COMPLEMENT && sizeof(T) == 2) in_turn(d_raw, i, r.q);
 #pragma unroll
       for (int t = RUN - 1; t >= 0; --t) adj = gated<RESETS>(a[t], adj + d_raw[t].get(i, e));
       zero |= r.P == 0.f;
@@ -497,11 +508,6 @@ __device__ __forceinline__ bool fold_run_back(Raw8<T> (&g_raw)[RUN], Raw8<T> (&x
     }
   }
   return zero;
-}
-// (1 - alpha) full for a bf16 result, from alpha full: their difference, or for gates next to 1, where it
-// would be all rounding, -(g + g^2 / 2) full (each within 2^-16 of the result).
-__device__ __forceinline__ float less(float g, float full, float scaled) {
-  return fabsf(g) < 1.f / 256.f ? -g * fmaf(0.5f, g, 1.f) * full : full - scaled;
 }
 // From the states before the run and the adjoints behind it (P, q of `ends`) to the stored gradients: the
 // input's in the place of x_raw, log_alpha's in the place of g_raw.
@@ -525,20 +531,14 @@ __device__ __forceinline__ void walk_run_back(Raw8<T> (&g_raw)[RUN], Raw8<T> (&x
         const float g = g_raw[t].get(i, e), x = x_raw[t].get(i, e);
         a[t] = gate<T>(g);
         of[t] = COMPLEMENT ? h - x : h;
-        if constexpr (COMPLEMENT && sizeof(T) == 4) {
-          s[t] = one_minus(g, a[t]);
-          h = step<RESETS>(a[t], h, s[t] * x);
-        } else {
-          h = advance<RESETS, COMPLEMENT, false>(a[t], g, h, x);
-        }
+        s[t] = COMPLEMENT ? complement_of<sizeof(T) == 2>(g, a[t]) : 1.f;
+        h = step<RESETS>(a[t], h, COMPLEMENT ? s[t] * x : x);
       }
 #pragma unroll
       for (int t = RUN - 1; t >= 0; --t) {
         const float full = adj + d_raw[t].get(i, e);
         adj = gated<RESETS>(a[t], full);
-        if constexpr (!COMPLEMENT) ox[t][e] = full;
-        else if constexpr (sizeof(T) == 4) ox[t][e] = s[t] * full;
-        else ox[t][e] = less(g_raw[t].get(i, e), full, a[t] * full);
+        ox[t][e] = COMPLEMENT ? s[t] * full : full;
         og[t][e] = RESETS ? gated<RESETS>(a[t], full * of[t]) : adj * of[t];
       }
       done = adj;
@@ -743,8 +743,13 @@ __global__ __launch_bounds__(kThreads, 4) void scan_short_backward_kernel(ccq_sc
   load_run(x_raw, p.x, p.x_stride_b, p.x_stride_t, a.b, a.t0, a.c0, a.n, p.D);
   load_run(d_raw, p.dy, p.dy_stride_b, p.dy_stride_t, a.b, a.t0, a.c0, a.n, p.D);
   float h[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, d[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (states && a.n > 0) load8(states + at, h);
-  if (p.dh_out) load8(p.dh_out + at, d);  // before anyone writes dh0, which may be dh_out
+  auto load_ends = [&] {  // before anyone writes dh0, which may be dh_out
+    if (states && a.n > 0) load8(states + at, h);
+    if (p.dh_out) load8(p.dh_out + at, d);
+  };
+  // with bf16 and the complement the fold needs their registers (18.2 against 17 us for 131 sequences of up to 11 tokens)
+  constexpr bool LATE = COMPLEMENT && sizeof(T) == 2;
+  if constexpr (!LATE) load_ends();
   clear_from(g_raw, a.n - a.t0);
   clear_from(x_raw, a.n - a.t0);
   clear_from(d_raw, a.n - a.t0);
@@ -752,6 +757,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_short_backward_kernel(ccq_sc
   float q[8];
   const bool resets = __any(fold_run_back<false, COMPLEMENT>(g_raw, x_raw, d_raw, mine, q));
   if (resets) fold_run_back<true, COMPLEMENT>(g_raw, x_raw, d_raw, mine, q);
+  if constexpr (LATE) load_ends();
 #pragma unroll
   for (int e = 0; e < 8; ++e) runs[a.run][ch + e] = mine[e];
   store8(&back[a.run][ch], q);

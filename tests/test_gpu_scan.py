@@ -280,3 +280,17 @@ def test_two_streams_at_once(gpu_lib):
         got = [ccq_scan(x, la, h0=h0, stream=s) for s, (x, la, h0, _) in zip(streams, sets)]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("decay", [1e-8, 1e-7, 1e-5, 1e-3, 0.05])
+@pytest.mark.parametrize("T", [8, 9, 64, 65, 700])
+def test_complement_of_gates_next_to_one(gpu_lib, dtype, decay, T):
+    """From no state, a channel holds (1 - alpha) x, which keeps its own relative rounding however small 1 - alpha is;
+    also where one token's input is far above the others',
+    and the gradient at tokens without an input, which see that state alone."""
+    x, la, _, _ = _make(dtype, 2, T, 64, 12, decay=decay, h0=False)
+    x[0, 1::2] = 0
+    x[1, T // 2] *= 512
+    x[1, T // 2 + 1 :: 3] = 0
+    _both(dtype, x, la, None, None, True, tag=f"decay {decay} ")
