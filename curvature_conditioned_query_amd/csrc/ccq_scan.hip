@@ -120,18 +120,22 @@ __device__ __forceinline__ float advance(float alpha, float g, float h, float x)
   return step<RESETS>(alpha, h, COMPLEMENT ? x * complement_of<SHORT>(g, alpha) : x);
 }
 
-// The product of a run's gates, one more of them.
+__device__ __forceinline__ bool drops(float P) { return __float_as_int(P) < 0; }
+
+// The product of a run's gates, one more of them.  Once it drops the state it stays so, whatever gates follow.
 template <bool RESETS>
 __device__ __forceinline__ float gates_product(float P, float alpha) {
-  return RESETS && alpha == 0.f ? -0.f : P * alpha;
+  return RESETS && (alpha == 0.f || drops(P)) ? -0.f : P * alpha;
 }
+
+// Whether a run's product of gates leaves open that one of them is 0: NaN, too, is 0 times an infinity or NaN.
+__device__ __forceinline__ bool may_drop(float P) { return !(P > 0.f); }
 
 // ---------------------------------------------------------------- runs
 
 struct Pair {
   float P, q;
 };
-__device__ __forceinline__ bool drops(float P) { return __float_as_int(P) < 0; }
 
 // The state behind a run that found `h`.
 __device__ __forceinline__ float through(float h, const Pair& r) {
@@ -362,7 +366,7 @@ __device__ __forceinline__ bool fold_run(Raw8<T> (&g_raw)[RUN], Raw8<T> (&x_raw)
         r.q = advance<RESETS, COMPLEMENT, false>(a, g, r.q, x);
         r.P = t == 0 && !RESETS ? a : gates_product<RESETS>(r.P, a);
       }
-      zero |= r.P == 0.f;
+      zero |= may_drop(r.P);
       out[i * PER + e] = r;
     }
   }
@@ -502,7 +506,7 @@ __device__ __forceinline__ bool fold_run_back(Raw8<T> (&g_raw)[RUN], Raw8<T> (&x
       if constexpr (COMPLEMENT && sizeof(T) == 2) in_turn(d_raw, i, r.q);
 #pragma unroll
       for (int t = RUN - 1; t >= 0; --t) adj = gated<RESETS>(a[t], adj + d_raw[t].get(i, e));
-      zero |= r.P == 0.f;
+      zero |= may_drop(r.P);
       out[i * PER + e] = r;
       q[i * PER + e] = adj;
     }

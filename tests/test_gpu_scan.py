@@ -294,3 +294,42 @@ def test_complement_of_gates_next_to_one(gpu_lib, dtype, decay, T):
     x[1, T // 2] *= 512
     x[1, T // 2 + 1 :: 3] = 0
     _both(dtype, x, la, None, None, True, tag=f"decay {decay} ")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [8, 30, 64, 300])
+@pytest.mark.parametrize("bad", [float("nan"), -float("nan"), float("inf"), 200.0])
+def test_reset_beside_a_gate_that_is_no_number(gpu_lib, dtype, T, bad):
+    """A NaN or infinite gate just before a reset, or just behind it, at every place of a thread's run: the states
+    behind the reset do not see the first, the adjoints before it do not see the second."""
+    import torch
+    from curvature_conditioned_query_amd import ccq_scan, ccq_scan_backward
+
+    def gradient(part, tag):
+        out = ccq_scan_backward(x, la, dy, h0=h0, dh_out=dh, complement=complement, want_dh0=True)
+        want = layer.scan_backward(_np(x), _np(la), _np(dy), _np(h0), _np(dh), None, complement)
+        for i, name in enumerate(("dx", "dlog_alpha")):
+            got = out[name][:, part]
+            assert torch.isfinite(got).all() and np.isfinite(want[i][:, part]).all(), (tag, name)
+            _check(got, want[i][:, part], want[3 + i][:, part], dtype, 20, f"{tag} {name} ")
+        return out["dh0"], want[2], want[5]
+
+    for where in range(max(1, T // 2 - 3), T // 2 + 2):
+        for complement in (False, True):
+            tag = f"reset at {where} complement={complement}"
+            x, clean, h0, _ = _make(dtype, 1, T, 24, where)
+            clean[:, where, ::2] = -float("inf")
+            dy = torch.randn(x.shape, generator=torch.Generator().manual_seed(2)).to(x.dtype).cuda()
+            dh = torch.randn(1, 24, generator=torch.Generator().manual_seed(3)).cuda()
+            want_y = ccq_scan(x, clean, h0=h0, complement=complement)
+            la = clean.clone()
+            la[:, where - 1, ::2] = bad
+            y = ccq_scan(x, la, h0=h0, complement=complement)
+            assert torch.equal(y[:, where:], want_y[:, where:]), tag
+            gradient(slice(where, T), tag + ", before it")
+            if where + 1 < T:
+                la = clean.clone()
+                la[:, where + 1, ::2] = bad
+                got, want, size = gradient(slice(0, where), tag + ", behind it")
+                assert torch.isfinite(got).all(), tag
+                _check(got, want, size, "f32", 20, tag + " dh0")
