@@ -137,9 +137,10 @@ struct Pair {
   float P, q;
 };
 
-// The state behind a run that found `h`.
+// The state behind a run that found `h`.  A product of gates that has left the range of fp32 counts as its least or
+// its largest number: an infinity or NaN passes the one, and no state, 0, is left alone by the other.
 __device__ __forceinline__ float through(float h, const Pair& r) {
-  return drops(r.P) ? r.q : fmaf(fmaxf(r.P, FLT_MIN), h, r.q);
+  return drops(r.P) ? r.q : fmaf(__builtin_amdgcn_fmed3f(r.P, FLT_MIN, FLT_MAX), h, r.q);
 }
 __device__ __forceinline__ Pair then(const Pair& a, const Pair& b) {
   Pair c;

@@ -427,7 +427,10 @@ typedef struct {
  * The state is fp32 throughout and a call continues where h0 left off, so T = 1 with h_out == h0
  * is the serving step.  Where alpha_t is 0 the old state is dropped, whatever it holds (an
  * infinity or NaN before it does not pass); alpha_t is 0 for log_alpha_t below about -87.  (With
- * the complement scale an infinite input may give NaN instead of itself.)  Rows behind a sequence's
+ * the complement scale an infinite input may give NaN instead of itself.)  Gates above 1 are taken
+ * as they are, and a state of 0 stays 0 behind any number of them; growth of another state, and of
+ * the gradient that reaches a token from behind, is told as long as the product of consecutive
+ * gates stays below 2^128.  Rows behind a sequence's
  * length are neither read into a result nor written.  Long sequences are cut along T and the pieces
  * joined in a fixed order: two calls give the same bits.  D <= 2^24, B T <= 2^30, B D < 2^31 and
  * fewer than 2^31 tiles of 64 tokens by 128 channels (CCQ_ERR_UNSUPPORTED beyond).  Returns a

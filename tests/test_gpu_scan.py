@@ -333,3 +333,27 @@ def test_reset_beside_a_gate_that_is_no_number(gpu_lib, dtype, T, bad):
                 got, want, size = gradient(slice(0, where), tag + ", behind it")
                 assert torch.isfinite(got).all(), tag
                 _check(got, want, size, "f32", 20, tag + " dh0")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("complement", [False, True])
+@pytest.mark.parametrize("T", [8, 60, 64, 300, 2500])
+def test_gates_above_one_leave_a_zero_state_alone(gpu_lib, dtype, complement, T):
+    """The gates' product passes every number, but there is no state to grow: inputs and gradients only at a few tokens."""
+    import torch
+    from curvature_conditioned_query_amd import ccq_scan, ccq_scan_backward
+    x, la, _, _ = _make(dtype, 2, T, 72, 13, h0=False)
+    la[:] = 1.5
+    x[:, : T - 5] = 0
+    y = ccq_scan(x, la, complement=complement)
+    hs, _, es, _ = layer.scan(_np(x), _np(la), None, None, complement)
+    _check(y, hs, es, dtype, 10, "y")
+    assert (y[:, : T - 5] == 0).all()
+    dy = torch.randn(x.shape, generator=torch.Generator().manual_seed(2)).to(x.dtype).cuda()
+    dy[:, 5:] = 0
+    out = ccq_scan_backward(x, la, dy, complement=complement, want_dh0=True)
+    want = layer.scan_backward(_np(x), _np(la), _np(dy), None, None, None, complement)
+    for i, name in enumerate(("dx", "dlog_alpha", "dh0")):
+        assert torch.isfinite(out[name]).all(), name
+        _check(out[name], want[i], want[3 + i], "f32" if name == "dh0" else dtype, 20, name)
+    assert (out["dx"][:, 5:] == 0).all()
