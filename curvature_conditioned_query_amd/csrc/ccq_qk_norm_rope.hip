@@ -86,6 +86,7 @@ __device__ __forceinline__ void store8(__bf16* p, const float (&x)[8]) {
 struct Turn {
   float c[8], s[8];
   int partner;  // lane that holds the partners (split halves)
+  bool on;      // whether the entries are rotated at all
 };
 
 // The angle is formed in 64 bits and in turns, reduced to [-1/2, 1/2] there, so a far position loses
@@ -125,7 +126,8 @@ struct Angles {
       u.s[e] = 0.f;
     }
     const int i0 = 8 * row_lane, half = p.rot / 2;
-    if (i0 < p.rot) {
+    u.on = i0 < p.rot;
+    if (u.on) {
       if (p.interleaved) {
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
@@ -161,8 +163,11 @@ __device__ __forceinline__ void turn(float (&x)[8], const Turn& u, const ccq_qk_
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = __shfl(x[e], u.partner, 64);
   }
+  // an entry behind the rotated part is not multiplied by 1 and its neighbour by 0: infinities would make NaN
+  if (u.on) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = BACK ? x[e] * u.c[e] - y[e] * u.s[e] : x[e] * u.c[e] + y[e] * u.s[e];
+    for (int e = 0; e < 8; ++e) x[e] = BACK ? x[e] * u.c[e] - y[e] * u.s[e] : x[e] * u.c[e] + y[e] * u.s[e];
+  }
 }
 
 // 1 / norm of a row from its sum of squares.

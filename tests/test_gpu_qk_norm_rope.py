@@ -179,3 +179,29 @@ def test_other_stream_and_replayed_capture(gpu_lib):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, got))
         assert all(torch.equal(back[n], gback[n]) for n in back)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_entries_that_are_not_rotated_pass_as_they_are(gpu_lib, dtype, interleaved):
+    """Behind the rotated part an infinity stays one, and neither it nor a NaN reaches the entry beside it;
+    inside, only the two of a pair."""
+    from curvature_conditioned_query_amd import ccq_qk_norm_rope, ccq_qk_norm_rope_backward
+    torch, dts = _torch()
+    inf, nan = float("inf"), float("nan")
+    q = torch.randn(1, 9, 2, 128, generator=torch.Generator().manual_seed(4)).to(dts[dtype]).cuda()
+    f = torch.linspace(1.0, 0.1, 16).cuda()
+    how = dict(inv_freq=f, q_norm="none", position_offset=3, interleaved=interleaved)
+    clean, _ = ccq_qk_norm_rope(q, None, **how)
+    assert torch.equal(clean[..., 32:], q.transpose(1, 2)[..., 32:])
+    q[0, 4, 1, 40], q[0, 5, 0, 101], q[0, 6, 1, 2] = inf, nan, nan
+    out, _ = ccq_qk_norm_rope(q, None, **how)
+    touched = torch.zeros_like(out, dtype=torch.bool)
+    touched[0, 1, 4, 40] = touched[0, 0, 5, 101] = touched[0, 1, 6, 2] = touched[0, 1, 6, 3 if interleaved else 18] = True
+    assert out[0, 1, 4, 40] == inf and out[0, 0, 5, 101].isnan() and torch.equal(out[~touched], clean[~touched])
+    grad = torch.zeros(1, 2, 9, 128, device="cuda")
+    grad[0, 1, 4, 40], grad[0, 0, 5, 101] = -inf, nan
+    dq = ccq_qk_norm_rope_backward(torch.ones_like(q), None, grad, None, **how)["dq"]
+    assert dq[0, 4, 1, 40] == -inf and dq[0, 5, 0, 101].isnan()
+    dq[0, 4, 1, 40], dq[0, 5, 0, 101] = 0, 0
+    assert (dq == 0).all()
