@@ -173,7 +173,10 @@ __device__ __forceinline__ void turn(float (&x)[8], const Turn& u, const ccq_qk_
 // 1 / norm of a row from its sum of squares.
 __device__ __forceinline__ float row_scale(float sumsq, int kind, float inv_d, float eps) {
   if (kind == CCQ_NORM_RMS) return 1.f / sqrtf(sumsq * inv_d + eps);
-  if (kind == CCQ_NORM_L2) return 1.f / fmaxf(sqrtf(sumsq), kL2Floor);
+  if (kind == CCQ_NORM_L2) {
+    const float n = sqrtf(sumsq);
+    return 1.f / (n < kL2Floor ? kL2Floor : n);  // NaN stays
+  }
   return 1.f;
 }
 

@@ -205,3 +205,19 @@ def test_entries_that_are_not_rotated_pass_as_they_are(gpu_lib, dtype, interleav
     assert dq[0, 4, 1, 40] == -inf and dq[0, 5, 0, 101].isnan()
     dq[0, 4, 1, 40], dq[0, 5, 0, 101] = 0, 0
     assert (dq == 0).all()
+
+
+def test_a_nan_fills_its_row_under_both_norms(gpu_lib):
+    """A row's norm is NaN with one of its entries, and so are the row and its gradient; its neighbours' are not."""
+    from curvature_conditioned_query_amd import ccq_qk_norm_rope, ccq_qk_norm_rope_backward
+    torch, dts = _torch()
+    for dt in dts.values():
+        for norm in ("rms", "l2"):
+            q = torch.randn(1, 9, 2, 64, generator=torch.Generator().manual_seed(6)).to(dt).cuda()
+            grad = torch.randn(1, 2, 9, 64, generator=torch.Generator().manual_seed(7)).cuda()
+            clean = ccq_qk_norm_rope(q, None, q_norm=norm)[0], ccq_qk_norm_rope_backward(q, None, grad, None, q_norm=norm)["dq"]
+            q[0, 4, 1, 7] = float("nan")
+            out = ccq_qk_norm_rope(q, None, q_norm=norm)[0], ccq_qk_norm_rope_backward(q, None, grad, None, q_norm=norm)["dq"]
+            assert out[0][0, 1, 4].isnan().all() and out[1][0, 4, 1].isnan().all(), norm
+            out[0][0, 1, 4], out[1][0, 4, 1] = clean[0][0, 1, 4], clean[1][0, 4, 1]
+            assert torch.equal(out[0], clean[0]) and torch.equal(out[1], clean[1]), norm
