@@ -334,7 +334,7 @@ __global__ __launch_bounds__(kThreads) void qk_backward_kernel(ccq_qk_bwd_params
 #pragma unroll
           for (int e = 0; e < 8; ++e) dw[side][e] += z[e] * x[e] * r;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = wt[e] * z[e] * r - x[e] * pull;
+          for (int e = 0; e < 8; ++e) x[e] = wt[e] * z[e] * r - (s.norm != CCQ_NORM_NONE ? x[e] * pull : 0.f);
           store8<true>(out + h * oh, x);
         }
       };

@@ -221,3 +221,16 @@ def test_a_nan_fills_its_row_under_both_norms(gpu_lib):
             assert out[0][0, 1, 4].isnan().all() and out[1][0, 4, 1].isnan().all(), norm
             out[0][0, 1, 4], out[1][0, 4, 1] = clean[0][0, 1, 4], clean[1][0, 4, 1]
             assert torch.equal(out[0], clean[0]) and torch.equal(out[1], clean[1]), norm
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_without_a_norm_the_gradient_does_not_see_the_row(gpu_lib, dtype):
+    """Rows of infinities and NaN, as in a padded batch: dq is the gradient turned back, whatever the row holds."""
+    from curvature_conditioned_query_amd import ccq_qk_norm_rope_backward
+    torch, dts = _torch()
+    f = torch.linspace(1.0, 0.1, 16).cuda()
+    grad = torch.randn(1, 2, 9, 64, generator=torch.Generator().manual_seed(8)).cuda()
+    q = torch.randn(1, 9, 2, 64, generator=torch.Generator().manual_seed(9)).to(dts[dtype]).cuda()
+    want = ccq_qk_norm_rope_backward(q, None, grad, None, inv_freq=f, q_norm="none")["dq"]
+    q[0, 3], q[0, 4, 1, 7], q[0, 5] = float("inf"), -float("inf"), float("nan")
+    assert torch.equal(ccq_qk_norm_rope_backward(q, None, grad, None, inv_freq=f, q_norm="none")["dq"], want)
