@@ -848,6 +848,10 @@ __global__ __launch_bounds__(kThreads) void beam_reorder_kernel(ReorderArgs a, u
 
 }  // namespace
 
+bool beam_grid_fits(const ccq_beam_params& p) {
+  return (long long)p.N * p.K < (1LL << 24) && grid_fits((uint64_t)p.N * p.K * beam_shape(p).stretches, kThreads);
+}
+
 size_t beam_workspace_bytes(const ccq_beam_params& p) {
   const size_t lists = (size_t)p.N * p.K * beam_shape(p).stretches;
   return parts_bytes(lists) + lists * p.M * sizeof(Pick);
@@ -879,6 +883,17 @@ static void launch_reorder(const ReorderArgs& a, unsigned grid, unsigned blocks,
 // caches, 27 through them if they were there, 34.6 against 33.4 if not.)
 static constexpr uint64_t kCached = 128 << 20;
 
+// Workgroups that go along a request's rows of one state.
+static uint64_t reorder_blocks(size_t row_bytes, int K) {
+  const size_t width = K <= 16 && row_bytes % 16 == 0 ? 16 : 4;
+  return (row_bytes / width + kThreads - 1) / kThreads;
+}
+bool beam_reorder_grid_fits(int n_states, const size_t* row_bytes, int N, int K) {
+  uint64_t blocks = 0;
+  for (int i = 0; i < n_states; ++i) blocks += reorder_blocks(row_bytes[i], K);
+  return grid_fits(blocks * N, kThreads);
+}
+
 hipError_t launch_beam_reorder(int n_states, void* const* states, const size_t* row_bytes, int N, int K,
                                const int32_t* parent, hipStream_t stream) {
   ReorderArgs a{};
@@ -891,9 +906,7 @@ hipError_t launch_beam_reorder(int n_states, void* const* states, const size_t* 
     a.state[i] = static_cast<unsigned char*>(states[i]);
     a.row_bytes[i] = row_bytes[i];
     a.first_block[i] = (unsigned)blocks;
-    const size_t width = K <= 16 && row_bytes[i] % 16 == 0 ? 16 : 4;
-    blocks += (row_bytes[i] / width + kThreads - 1) / kThreads;
-    if (blocks * N > 0x7fffffffu) return hipErrorInvalidValue;
+    blocks += reorder_blocks(row_bytes[i], K);
   }
   a.first_block[n_states] = (unsigned)blocks;
   const unsigned grid = (unsigned)(blocks * N);

@@ -155,10 +155,16 @@ hipError_t launch_gdn(const FwdArgs& a, hipStream_t stream);
 hipError_t launch_gdn_summary(const FwdArgs& a, hipStream_t stream);
 
 // Operators around the read step (one call each after validation, ccq_ops_api.cpp).
+// Whether a launch can have so many workgroups: its threads along a dimension are counted in 32 bits.
+constexpr bool grid_fits(uint64_t blocks, uint64_t threads) { return blocks <= 0xffffffffull / threads; }
+bool qk_grid_fits(const ccq_qk_params& p);
+bool scan_grid_fits(int dtype, int B, int T, int D);
+bool scan_backward_grid_fits(const ccq_scan_bwd_params& p);
+bool beam_grid_fits(const ccq_beam_params& p);
+bool beam_reorder_grid_fits(int n_states, const size_t* row_bytes, int N, int K);
 hipError_t launch_qk(const ccq_qk_params& p, hipStream_t stream);
 size_t qk_backward_workspace_bytes(const ccq_qk_bwd_params& p);
 hipError_t launch_qk_backward(const ccq_qk_bwd_params& p, hipStream_t stream);
-bool scan_grid_fits(int B, int T, int D);  // whether the sizes' tiles can be one launch
 size_t scan_workspace_bytes(const ccq_scan_params& p);
 hipError_t launch_scan(const ccq_scan_params& p, hipStream_t stream);
 size_t scan_backward_workspace_bytes(const ccq_scan_bwd_params& p);

@@ -86,6 +86,7 @@ int validate_qk(const ccq_qk_params* p) {
   if (!p) return CCQ_ERR_INVALID_ARG;
   const int st = qk_sizes(*p);
   if (st != CCQ_OK) return st;
+  if (!ccq::qk_grid_fits(*p)) return CCQ_ERR_UNSUPPORTED;
   if ((p->H_q > 0) != (p->q_out != nullptr) || (p->H_k > 0) != (p->k_out != nullptr)) return CCQ_ERR_INVALID_ARG;
   const size_t E = esize(p->dtype);
   const Range r[] = {{p->q_out, qk_dense(*p, p->H_q, E)},
@@ -166,7 +167,6 @@ int validate_qk_backward(const ccq_qk_bwd_params* p) {
 int scan_sizes(int dtype, int B, int T, int D, int complement) {
   if (bad_dtype(dtype) || B <= 0 || T <= 0 || D <= 0 || (complement & ~1)) return CCQ_ERR_INVALID_ARG;
   if (D % 8 != 0 || D > (1 << 24) || (long long)B * T > (1LL << 30) || (long long)B * D > 0x7fffffffLL) return CCQ_ERR_UNSUPPORTED;
-  if (!ccq::scan_grid_fits(B, T, D)) return CCQ_ERR_UNSUPPORTED;
   return CCQ_OK;
 }
 size_t scan_carry_bytes(int B, int T, int D) { return (size_t)B * ((T + 63) / 64) * D * 4; }
@@ -175,6 +175,7 @@ int validate_scan(const ccq_scan_params* p) {
   if (!p) return CCQ_ERR_INVALID_ARG;
   const int st = scan_sizes(p->dtype, p->B, p->T, p->D, p->complement);
   if (st != CCQ_OK) return st;
+  if (!ccq::scan_grid_fits(p->dtype, p->B, p->T, p->D)) return CCQ_ERR_UNSUPPORTED;
   if (!p->x || !p->log_alpha || !p->y) return CCQ_ERR_INVALID_ARG;
   if (!strides_in_range(p->B, p->x_stride_b, p->T, p->x_stride_t, 1, 0) ||
       !strides_in_range(p->B, p->la_stride_b, p->T, p->la_stride_t, 1, 0))
@@ -199,6 +200,7 @@ int validate_scan_backward(const ccq_scan_bwd_params* p) {
   if (!p) return CCQ_ERR_INVALID_ARG;
   const int st = scan_sizes(p->dtype, p->B, p->T, p->D, p->complement);
   if (st != CCQ_OK) return st;
+  if (!ccq::scan_backward_grid_fits(*p)) return CCQ_ERR_UNSUPPORTED;
   if (!p->x || !p->log_alpha || !p->dy || !p->dx || !p->dlog_alpha) return CCQ_ERR_INVALID_ARG;
   if (!strides_in_range(p->B, p->x_stride_b, p->T, p->x_stride_t, p->B, p->dy_stride_b) ||
       !strides_in_range(p->B, p->la_stride_b, p->T, p->la_stride_t, p->T, p->dy_stride_t))
@@ -232,7 +234,7 @@ int validate_beam(const ccq_beam_params* p) {
   if (p->pad_token < 0 || p->pad_token >= p->V) return CCQ_ERR_INVALID_ARG;
   const long long chunks = ((long long)p->V + ccq::kBeamMaxChunk - 1) / ccq::kBeamMaxChunk;
   if (p->K > ccq::kBeamMaxBeams || p->M > ccq::kBeamMaxPicks || (long long)p->K * p->V > 0x7fffffffLL ||
-      p->K * chunks > ccq::kBeamMaxLists || (long long)p->N * p->K > (1LL << 24))
+      p->K * chunks > ccq::kBeamMaxLists || !ccq::beam_grid_fits(*p))
     return CCQ_ERR_UNSUPPORTED;
   if (!p->logits || !p->scores || !p->token || !p->parent || !p->score) return CCQ_ERR_INVALID_ARG;
   const size_t E = esize(p->dtype), rows = (size_t)p->N * p->K, picks = (size_t)p->N * p->M * 4;
@@ -318,6 +320,7 @@ int ccq_beam_reorder(int32_t n_states, void* const* states, const size_t* row_by
     if (row_bytes[i] > ((size_t)1 << 36)) return CCQ_ERR_UNSUPPORTED;
     r[i] = {states[i], row_bytes[i] * (size_t)N * K};
   }
+  if (!ccq::beam_reorder_grid_fits(n_states, row_bytes, N, K)) return CCQ_ERR_UNSUPPORTED;
   r[n_states] = {parent, (size_t)N * K * 4};
   for (int i = 0; i <= n_states; ++i)
     if (misaligned(r[i].p)) return CCQ_ERR_MISALIGNED;

@@ -446,6 +446,8 @@ constexpr int kBackGroups = 512;
 
 }  // namespace
 
+bool qk_grid_fits(const ccq_qk_params& p) { return grid_fits(tiles_of(p), kThreads); }
+
 hipError_t launch_qk(const ccq_qk_params& p, hipStream_t stream) {
   const int per = heads_per_group(p, tiles_of(p));
   const dim3 grid = grid_of(p, per, 0x7fffffff);

@@ -860,16 +860,20 @@ int runs_each(int T, int run) {
   while (each <= kMostRuns && each * run < T) each *= 2;
   return each;
 }
-unsigned short_grid(int B, int D, int each) {
+uint64_t short_grid(int B, int D, int each) {
   const int sequences = kRuns / each;
-  return (unsigned)(((int64_t)B + sequences - 1) / sequences * ((D + kCols - 1) / kCols));
+  return ((uint64_t)B + sequences - 1) / sequences * ((D + kCols - 1) / kCols);
 }
+uint64_t tile_grid(int dtype, bool back, int B, int T, int D) {
+  return (uint64_t)B * ((D + kCols - 1) / kCols) * ((T - 1) / tile_tokens(dtype, back) + 1);
+}
+int run_tokens(int dtype, bool back) { return tile_tokens(dtype, back) / kRuns; }
 
 hipError_t launch_tiles(const ccq_scan_params& p, void* workspace, hipStream_t stream) {
   const Tiles t = tiles_of(p.dtype, false, p.B, p.T, p.D, workspace);
   const hipError_t e = clear_tiles(t, tile_words(p.dtype, false, p.B, p.T, p.D), stream);
   if (e != hipSuccess) return e;
-  const unsigned grid = (unsigned)((int64_t)t.columns * t.segments);
+  const unsigned grid = (unsigned)tile_grid(p.dtype, false, p.B, p.T, p.D);
   if (p.dtype == CCQ_DTYPE_BF16) {
     if (p.complement) scan_tile_kernel<__bf16, true><<<grid, kThreads, 0, stream>>>(p, t);
     else scan_tile_kernel<__bf16, false><<<grid, kThreads, 0, stream>>>(p, t);
@@ -895,9 +899,16 @@ size_t carry_bytes(int B, int T, int D) {
 
 }  // namespace
 
-bool scan_grid_fits(int B, int T, int D) {
-  const int64_t columns = (int64_t)B * ((D + kCols - 1) / kCols), segments = (T - 1) / Run<float, true>::tile + 1;  // the smaller tile
-  return columns * segments <= 0x7fffffff;
+bool scan_grid_fits(int dtype, int B, int T, int D) {
+  if (T <= kMostSteps) return true;  // at most 2^28 threads
+  return grid_fits(T <= kChunk ? short_grid(B, D, runs_each(T, run_tokens(dtype, false))) : tile_grid(dtype, false, B, T, D), kThreads);
+}
+
+bool scan_backward_grid_fits(const ccq_scan_bwd_params& p) {
+  const int each = runs_each(p.T, run_tokens(p.dtype, true));
+  if (p.T <= kChunk && each <= kMostRuns) return grid_fits(short_grid(p.B, p.D, each), kThreads);
+  return grid_fits(tile_grid(p.dtype, true, p.B, p.T, p.D), kThreads) &&
+         (!forms_states(p) || grid_fits(tile_grid(p.dtype, false, p.B, p.T, p.D), kThreads));
 }
 
 size_t scan_workspace_bytes(const ccq_scan_params& p) { return p.T <= kMostSteps ? 0 : tile_bytes(p.dtype, false, p.B, p.T, p.D); }
@@ -906,8 +917,8 @@ hipError_t launch_scan(const ccq_scan_params& p, hipStream_t stream) {
   if (p.T > kMostSteps && p.T <= kChunk) {
     static_assert(kChunk <= kMostRuns * Run<__bf16, false>::n && kChunk <= kMostRuns * Run<float, false>::n, "short");
     const int per_row = (p.D + kCols - 1) / kCols;
-    const int each = runs_each(p.T, p.dtype == CCQ_DTYPE_BF16 ? Run<__bf16, false>::n : Run<float, false>::n);
-    const unsigned grid = short_grid(p.B, p.D, each);
+    const int each = runs_each(p.T, run_tokens(p.dtype, false));
+    const unsigned grid = (unsigned)short_grid(p.B, p.D, each);
     if (p.dtype == CCQ_DTYPE_BF16) {
       if (p.complement) scan_short_kernel<__bf16, true><<<grid, kThreads, 0, stream>>>(p, per_row, each);
       else scan_short_kernel<__bf16, false><<<grid, kThreads, 0, stream>>>(p, per_row, each);
@@ -930,10 +941,10 @@ size_t scan_backward_workspace_bytes(const ccq_scan_bwd_params& p) {
 
 hipError_t launch_scan_backward(const ccq_scan_bwd_params& p, hipStream_t stream) {
   const float* carry = p.chunk_carry ? p.chunk_carry : p.h0;
-  const int each = runs_each(p.T, p.dtype == CCQ_DTYPE_BF16 ? Run<__bf16, true>::n : Run<float, true>::n);
+  const int each = runs_each(p.T, run_tokens(p.dtype, true));
   if (p.T <= kChunk && each <= kMostRuns) {
     const int per_row = (p.D + kCols - 1) / kCols;
-    const unsigned grid = short_grid(p.B, p.D, each);
+    const unsigned grid = (unsigned)short_grid(p.B, p.D, each);
     if (p.dtype == CCQ_DTYPE_BF16) {
       if (p.complement) scan_short_backward_kernel<__bf16, true><<<grid, kThreads, 0, stream>>>(p, carry, per_row, each);
       else scan_short_backward_kernel<__bf16, false><<<grid, kThreads, 0, stream>>>(p, carry, per_row, each);
@@ -968,7 +979,7 @@ hipError_t launch_scan_backward(const ccq_scan_bwd_params& p, hipStream_t stream
   const Tiles t = tiles_of(p.dtype, true, p.B, p.T, p.D, p.workspace);
   const hipError_t e = clear_tiles(t, tile_words(p.dtype, true, p.B, p.T, p.D), stream);
   if (e != hipSuccess) return e;
-  const unsigned grid = (unsigned)((int64_t)t.columns * t.segments);
+  const unsigned grid = (unsigned)tile_grid(p.dtype, true, p.B, p.T, p.D);
   if (p.dtype == CCQ_DTYPE_BF16) {
     if (p.complement) scan_backward_tile_kernel<__bf16, true><<<grid, kThreads, 0, stream>>>(p, carry, t);
     else scan_backward_tile_kernel<__bf16, false><<<grid, kThreads, 0, stream>>>(p, carry, t);

@@ -375,8 +375,9 @@ typedef struct {
  * ccq_fwd_chunked ([B, H, T, d]) and ccq_decode_step (T = 1: [N, H, d]) read it.  A rotation keeps
  * lengths, so keys under CCQ_NORM_L2 without a weight are unit keys.  The arithmetic is fp32; the
  * result is rounded once.  Either side may be absent (H_q == 0 or H_k == 0).  A value row is
- * laid out the same way by CCQ_NORM_NONE and rot == 0.  B T <= 2^30 and at most 4,096 heads a side
- * (CCQ_ERR_UNSUPPORTED beyond, and for other d or rot).  Returns a ccq_status.
+ * laid out the same way by CCQ_NORM_NONE and rot == 0.  At most 4,096 heads a side and fewer than
+ * 2^28 tokens B T at d = 128, 2^29 at d = 64; 2^30 in the gradient (CCQ_ERR_UNSUPPORTED beyond, and
+ * for other d or rot).  Returns a ccq_status.
  */
 int ccq_qk_norm_rope(const ccq_qk_params *p, void *hip_stream);
 
@@ -430,11 +431,11 @@ typedef struct {
  * the complement scale an infinite input may give NaN instead of itself.)  Gates above 1 are taken
  * as they are, and a state of 0 stays 0 behind any number of them; growth of another state, and of
  * the gradient that reaches a token from behind, is told as long as the product of consecutive
- * gates stays below 2^128.  Rows behind a sequence's
- * length are neither read into a result nor written.  Long sequences are cut along T and the pieces
- * joined in a fixed order: two calls give the same bits.  D <= 2^24, B T <= 2^30, B D < 2^31 and
- * fewer than 2^31 tiles of 64 tokens by 128 channels (CCQ_ERR_UNSUPPORTED beyond).  Returns a
- * ccq_status.
+ * gates stays below 2^128.  Rows behind a sequence's length are neither read into a result nor
+ * written.  Long sequences are cut along T and the pieces joined in a fixed order: two calls give
+ * the same bits.  D <= 2^24, B T <= 2^30, B D < 2^31, and
+ * for T > 8 fewer than 2^23 workgroups, which B ceil(T / 64) ceil(D / 128) < 2^23 always keeps to
+ * (CCQ_ERR_UNSUPPORTED beyond; the gradient alike).  Returns a ccq_status.
  */
 int ccq_scan(const ccq_scan_params *p, void *hip_stream);
 /* Bytes of device workspace ccq_scan needs (0 if none and for invalid p): depends on dtype, B, T, D. */
@@ -470,7 +471,7 @@ size_t ccq_scan_backward_workspace_bytes(const ccq_scan_bwd_params *p);
 typedef struct {
   int32_t dtype;             /* ccq_dtype of logits                                                 */
   int32_t N, K, V, M;        /* requests, beams of each, vocabulary, picks: K <= 64, M <= min(64, K V),
-                                K V < 2^31, K ceil(V / 16384) <= 4096 and N K <= 2^24               */
+                                K V < 2^31, K ceil(V / 16384) <= 4096 and N K < 2^24                */
   const void *logits;        /* [N, K, V], a row every logits_stride elements                        */
   int64_t logits_stride;     /* >= V                                                                 */
   const float *scores;       /* [N, K] log-probability of every beam so far                          */
@@ -503,10 +504,11 @@ size_t ccq_beam_select_workspace_bytes(const ccq_beam_params *p);
  * and beam j, row (i K + j) of states[s] becomes what row (i K + parent[i][j]) was.  A row is
  * row_bytes[s] bytes, a multiple of 4: S, C, ksum and n of a decode step with N K sequences, h of
  * ccq_scan, or anything else kept per beam.  parent is [N, K]; a parent outside 0 .. K - 1 leaves
- * its beam as it is.  1 <= K <= 64, N K <= 2^24, rows of at most 2^36 bytes,
- * 1 <= n_states <= CCQ_MAX_REORDER_STATES; states and row_bytes are host arrays, read before the
- * call returns.  Rows that stay are neither read nor written.
- * Returns a ccq_status.
+ * its beam as it is.  1 <= K <= 64, N K <= 2^24, rows of at most 2^36 bytes, and N times the pieces
+ * of 4,096 bytes that the states' rows make (1,024 bytes where K > 16 or a row is no multiple of 16)
+ * below 2^24 (CCQ_ERR_UNSUPPORTED beyond).  1 <= n_states <= CCQ_MAX_REORDER_STATES; states and
+ * row_bytes are host arrays, read before the call returns.  Rows that stay are neither read nor
+ * written.  Returns a ccq_status.
  */
 int ccq_beam_reorder(int32_t n_states, void *const *states, const size_t *row_bytes, int32_t N, int32_t K,
                      const int32_t *parent, void *hip_stream);

@@ -111,3 +111,55 @@ def test_beam_reorder_past_the_caches(gpu_lib, K, odd):
     want, want_small = state[rows], small[rows]
     ccq_beam_reorder([small, state], parent)
     assert torch.equal(state, want) and torch.equal(small, want_small)
+
+
+def test_launches_of_the_most_workgroups(gpu_lib):
+    """The last sizes before the refusals: sequences, rows and requests by the million, alike or short, their ends
+    compared with small calls."""
+    import torch
+    from curvature_conditioned_query_amd import ccq_beam_reorder, ccq_beam_select, ccq_scan, ccq_scan_backward
+    g = torch.Generator(device="cuda").manual_seed(4)
+    for dt, T, B in ((torch.bfloat16, 9, (1 << 26) - 8), (torch.bfloat16, 65, (1 << 23) - 1)):
+        print(f"scan T{T} B{B}", flush=True)
+        x, la = torch.randn(2, 1, T, 8, device="cuda", generator=g).to(dt)
+        la = -la.abs()
+        y = ccq_scan(x.expand(B, T, 8), la.expand(B, T, 8))
+        small = ccq_scan(x, la)
+        assert all(torch.equal(y[b : b + 1], small) for b in (0, 1, B // 2, B - 2, B - 1))
+        del y
+    T, B = 65, (1 << 22) - 1
+    print(f"scan backward T{T} B{B}", flush=True)
+    x, la, dy = torch.randn(3, 1, T, 8, device="cuda", generator=g)
+    la = -la.abs()
+    out, small = ccq_scan_backward(x.expand(B, T, 8), la.expand(B, T, 8), dy.expand(B, T, 8)), ccq_scan_backward(x, la, dy)
+    assert all(torch.equal(out[n][b : b + 1], small[n]) for n in ("dx", "dlog_alpha") for b in (0, 1, B // 2, B - 1))
+    del out
+    torch.cuda.empty_cache()
+    N = (1 << 24) - 1
+    print(f"select and reorder N{N}", flush=True)
+    logits = torch.randn(N, 1, 8, device="cuda", generator=g)
+    scores = -torch.rand(N, 1, device="cuda", generator=g)
+    out = ccq_beam_select(logits, scores, 2)
+    for part in (slice(0, 500), slice(N // 2, N // 2 + 500), slice(N - 500, N)):
+        small = ccq_beam_select(logits[part].clone(), scores[part].clone(), 2)
+        assert torch.equal(out["token"][part], small["token"]) and torch.equal(out["parent"][part], small["parent"])
+        assert ((out["score"][part] - small["score"]).abs() <= 2 * (U * small["score"].abs() + 64 * U)).all()
+    N = 1 << 23
+    state = torch.randn(2 * N, 1, device="cuda", generator=g)
+    want = state.view(N, 2).flip(1).reshape(2 * N, 1)
+    ccq_beam_reorder([state], torch.tensor([[1, 0]], dtype=torch.int32, device="cuda").expand(N, 2).contiguous())
+    assert torch.equal(state, want)
+
+
+def test_qk_norm_rope_of_the_most_tokens(gpu_lib):
+    import torch
+    from curvature_conditioned_query_amd import ccq_qk_norm_rope
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GiB of device memory")
+    T = (1 << 28) - 16
+    print(f"qk T{T}", flush=True)
+    q = torch.randn(1, 1, 1, 128, device="cuda").to(torch.bfloat16).expand(1, T, 1, 128)
+    freq = torch.linspace(1, 0.1, 64, device="cuda")
+    out, _ = ccq_qk_norm_rope(q, None, inv_freq=freq)
+    for part in (slice(0, 50), slice(T // 2, T // 2 + 50), slice(T - 50, T)):
+        assert torch.equal(out[:, :, part], ccq_qk_norm_rope(q[:, part], None, inv_freq=freq, position_offset=part.start)[0])

@@ -220,3 +220,61 @@ def test_param_structs_match_the_header(tmp_path):
         assert got[(cname, "size")] == ctypes.sizeof(cls)
         for f in cls._fields_:
             assert got[(cname, f[0])] == getattr(cls, f[0]).offset, (cname, f[0])
+
+
+# A launch counts its threads in 32 bits: what would pass that is refused, and what is just inside is not (the
+# outputs overlap an input there, so no call goes on to a launch).
+QK_DENSE = dict(q_stride_b=0, q_stride_t=0, q_stride_h=0, k_stride_b=0, k_stride_t=0, k_stride_h=0)
+
+
+@pytest.mark.parametrize("d,most", [(128, (1 << 28) - 16), (64, (1 << 29) - 32)])
+def test_qk_launch_limit(lib, d, most):
+    for B, T in ((1, most), (most // 16, 16), (2, most // 2)):
+        assert lib.ccq_qk_norm_rope(_qk(B=B, T=T, d=d, q_out=BASE, **QK_DENSE), None) == INVALID
+    assert lib.ccq_qk_norm_rope(_qk(B=1, T=most + 1, d=d, **QK_DENSE), None) == UNSUPPORTED
+    assert lib.ccq_qk_norm_rope(_qk(B=4, T=most // 4 + 4, d=d, **QK_DENSE), None) == UNSUPPORTED
+    assert lib.ccq_qk_norm_rope_backward(_qkb(**{"fwd.B": 1, "fwd.T": 1 << 30, "fwd.d": d, "dq": BASE}), None) != UNSUPPORTED
+
+
+SCAN_DENSE = dict(x_stride_b=0, x_stride_t=0, la_stride_b=0, la_stride_t=0)
+N23 = 1 << 23
+
+
+@pytest.mark.parametrize("dtype,T,D,inside,beyond", [
+    (1, 65, 8, N23 - 1, N23), (1, 129, 8, N23 // 2 - 1, N23 // 2), (0, 65, 8, N23 - 1, N23), (1, 65, 264, N23 // 3, N23 // 3 + 1),
+    (1, 9, 8, 8 * N23 - 8, 8 * N23 - 7), (0, 64, 8, 2 * N23 - 2, 2 * N23 - 1), (1, 33, 8, 2 * N23 - 2, 2 * N23 - 1)])
+def test_scan_launch_limit(lib, dtype, T, D, inside, beyond):
+    assert lib.ccq_scan(_scan(dtype=dtype, B=inside, T=T, D=D, y=BASE, **SCAN_DENSE), None) == INVALID
+    assert lib.ccq_scan(_scan(dtype=dtype, B=beyond, T=T, D=D, y=BASE, **SCAN_DENSE), None) == UNSUPPORTED
+    assert lib.ccq_scan_workspace_bytes(_scan(dtype=dtype, B=beyond, T=T, D=D, **SCAN_DENSE)) == 0
+
+
+@pytest.mark.parametrize("dtype,T,D,inside,beyond", [
+    (1, 65, 8, N23 - 1, N23), (1, 129, 8, N23 // 2 - 1, N23 // 2), (0, 65, 8, N23 // 2 - 1, N23 // 2), (0, 64, 8, N23 - 1, N23),
+    (1, 64, 8, 2 * N23 - 2, 2 * N23 - 1), (0, 32, 8, 2 * N23 - 2, 2 * N23 - 1)])
+def test_scan_backward_launch_limit(lib, dtype, T, D, inside, beyond):
+    dense = dict(SCAN_DENSE, dy_stride_b=0, dy_stride_t=0)
+    for carry in (BASE, None):
+        assert lib.ccq_scan_backward(_scanb(dtype=dtype, B=inside, T=T, D=D, dx=BASE, chunk_carry=carry, **dense), None) == INVALID
+        assert lib.ccq_scan_backward(_scanb(dtype=dtype, B=beyond, T=T, D=D, dx=BASE, chunk_carry=carry, **dense), None) == UNSUPPORTED
+
+
+def test_beam_launch_limits(lib):
+    few = dict(V=8, logits_stride=8, token=BASE)
+    for N, K in (((1 << 24) - 1, 1), ((1 << 23) - 1, 2), ((1 << 18) - 1, 64)):
+        assert lib.ccq_beam_select(_beam(N=N, K=K, **few), None) == INVALID
+    for N, K in ((1 << 24, 1), (1 << 23, 2), (1 << 18, 64)):
+        assert lib.ccq_beam_select(_beam(N=N, K=K, **few), None) == UNSUPPORTED
+
+    def reorder(rows, N, K):
+        n = len(rows)
+        return lib.ccq_beam_reorder(n, (ctypes.c_void_p * n)(*[BASE] * n), (ctypes.c_size_t * n)(*rows), N, K, BASE, None)
+    assert reorder([(1 << 36) - 4096], 1, 2) == INVALID  # parent inside the state
+    assert reorder([1 << 36], 1, 2) == UNSUPPORTED
+    assert reorder([(1 << 34) - 1028], 1, 2) == INVALID
+    assert reorder([(1 << 34) - 1028, 4], 1, 2) == UNSUPPORTED
+    assert reorder([(1 << 34) - 1024], 1, 17) == INVALID
+    assert reorder([1 << 34], 1, 17) == UNSUPPORTED
+    assert reorder([4], (1 << 24) - 1, 1) == INVALID
+    assert reorder([4], 1 << 24, 1) == UNSUPPORTED
+    assert reorder([16, 16], 1 << 23, 2) == UNSUPPORTED
