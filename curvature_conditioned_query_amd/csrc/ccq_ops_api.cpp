@@ -155,7 +155,9 @@ int validate_qk_backward(const ccq_qk_bwd_params* p) {
                      {f.k_weight, (size_t)f.d * 4}};
   if (any_misaligned(r)) return CCQ_ERR_MISALIGNED;
   // dq and dk are commonly the two parts of one packed gradient: their extents interleave, their
-  // rows do not, which the caller answers for
+  // rows do not.  Where not even their first rows are apart the call is refused; for the others the
+  // caller answers.
+  if (overlap({p->dq, (size_t)f.d * E}, {p->dk, (size_t)f.d * E})) return CCQ_ERR_INVALID_ARG;
   for (int i = 0; i < 5; ++i)
     for (int j = i + 1; j < 13; ++j)
       if (!(i == 2 && j == 4) && overlap(r[i], r[j])) return CCQ_ERR_INVALID_ARG;

@@ -388,7 +388,7 @@ typedef struct {
   const float *dk_out;       /* fp32, the shape of k_out                                            */
   void *dq;                  /* [B, T, H_q, d] dtype, strides below, written                        */
   void *dk;                  /* [B, T, H_k, d] dtype, strides below, written: summed over shared heads */
-  int64_t dq_stride_b, dq_stride_t, dq_stride_h; /* no two rows may overlap                         */
+  int64_t dq_stride_b, dq_stride_t, dq_stride_h; /* no two rows may overlap, of dk's either          */
   int64_t dk_stride_b, dk_stride_t, dk_stride_h;
   float *dq_weight;          /* [d] fp32, written (set if and only if q_weight is)                  */
   float *dk_weight;          /* [d] fp32, written (set if and only if k_weight is)                  */

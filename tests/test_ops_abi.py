@@ -278,3 +278,14 @@ def test_beam_launch_limits(lib):
     assert reorder([4], (1 << 24) - 1, 1) == INVALID
     assert reorder([4], 1 << 24, 1) == UNSUPPORTED
     assert reorder([16, 16], 1 << 23, 2) == UNSUPPORTED
+
+
+def test_qk_backward_gradients_apart(lib):
+    """One tensor for both gradients, or rows that overlap, are refused; the parts of a packed gradient are not (the
+    workspace is too small here, so nothing is launched)."""
+    dq = BASE + (12 << 30)
+    packed = dict(dq_stride_b=3840, dq_stride_t=384, dk_stride_b=3840, dk_stride_t=384, workspace_bytes=0)
+    for dk in (dq, dq + 16, dq + 112, dq - 112):
+        assert lib.ccq_qk_norm_rope_backward(_qkb(dk=dk, **packed), None) == INVALID
+    for dk in (dq + 4 * 128, dq - 2 * 128):
+        assert lib.ccq_qk_norm_rope_backward(_qkb(dk=dk, **packed), None) == WORKSPACE
