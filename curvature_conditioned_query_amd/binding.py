@@ -848,7 +848,8 @@ def ccq_scan(x, log_alpha, h0=None, h_out=None, y=None, lengths=None, complement
     in ccq.h; s_t is 1, or 1 - exp(log_alpha_t) with complement).  x and log_alpha may be strided
     views; h0, h_out [B, D] fp32 (h_out may be h0: the serving step); lengths [B] int32; chunk_carry:
     fp32 tensor of ``scan_carry_shape(x)`` that receives the state before every 64-token chunk, for
-    ``ccq_scan_backward``.  Returns y [B, T, D] (rows at t >= length are left as they were)."""
+    ``ccq_scan_backward``.  Returns y [B, T, D]: rows at t >= length are left as they were, which in a y
+    allocated here (y=None) is whatever the memory held."""
     if x.dim() != 3:
         raise ValueError("x is [B, T, D]")
     ops, dev, dt = _ops(), x.device, x.dtype

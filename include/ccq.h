@@ -251,7 +251,7 @@ int ccq_step_backward(int32_t rule, int32_t dtype, int32_t N, int32_t H, int32_t
 /* Static description of a status code (never NULL). */
 const char *ccq_status_string(int32_t status);
 
-/* ABI version of this header: 10. */
+/* ABI version of this header: 11. */
 int32_t ccq_abi_version(void);
 
 /* Arguments of ccq_bwd_chunked.  Zero-initialise, then fill in. */
@@ -489,9 +489,12 @@ typedef struct {
  * and a finished beam goes on with pad_token alone, at its old score (every other token: -inf).
  * For each request the M best of the K V continuations, best first; equal ones in order of beam,
  * then token.  A NaN logit counts as -inf and +inf as the largest finite number; a beam whose
- * score is -inf or NaN has only continuations at -inf, and so has a row of -inf.  The
- * normaliser is formed so that scores of different beams compare as they would in 64 bits (its
- * terms near the top in 64 bits, the tail in 32 with sums in 64).  Returns a ccq_status.
+ * score is -inf or NaN, finished or not, has only continuations at -inf, and so has a row of -inf.
+ * The normaliser is formed so that scores of different beams compare as they would in 64 bits (its
+ * terms near the top in 64 bits, the tail in 32 with sums in 64, all from their distance to the top:
+ * masks of any finite size and logits far from zero take nothing from it).  Beside a logit, or at a
+ * score, so large that 64 bits no longer tell a beam's other continuations apart, it is not told
+ * which of those are picked.  Returns a ccq_status.
  */
 int ccq_beam_select(const ccq_beam_params *p, void *hip_stream);
 size_t ccq_beam_select_workspace_bytes(const ccq_beam_params *p);
