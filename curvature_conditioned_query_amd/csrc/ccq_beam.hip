@@ -18,10 +18,10 @@
 // loosely: 7.9 against 8.8 us for four rows of 32,000, where for 256 rows of 131,071, in stretches of four
 // pieces, it is 28.5 against 26.3.
 //
-// Measured, 32 requests of 8 beams over 131,071 tokens, M = 16, bf16: 25 us for the rows (67 MB, 2.7 TB/s: the
-// vector units are busy for half of it, the time of 15 instructions a logit, and with one batch of workgroups of four
-// pieces each the first loads, the bound and the last ranking stand alone) and 6 for the join.  Four rows of
-// 32,000 in fp32: 7 and 5 us, latencies throughout.
+// Measured, 32 requests of 8 beams over 131,071 tokens, M = 16, bf16: 26 us for the rows (67 MB, 2.6 TB/s: the
+// vector units are busy for half of it, and with one batch of workgroups of four pieces each the first loads, the
+// bound and the last ranking stand alone) and 6 for the join.  464 rows of 23,341 in fp32, M = 8: 21 us for 43 MB and 5,
+// for the same reasons with stretches of one piece.  Four rows of 32,000 in fp32: 7 and 5 us, latencies throughout.
 //
 // Scores of different beams meet in the comparison, so the normaliser has to be good to more than
 // fp32: the candidates, which carry most of a peaked distribution, are left out of the fp32 sum and added
@@ -798,7 +798,8 @@ struct ReorderArgs {
 // no other thread touches those bytes, so the move is in place, whatever the parents are, and only
 // rows that move are touched.  STREAM: past the caches.
 // Measured: 64 requests of 4 beams, the carries of 16 heads of 128 (718 MB moved): 130 us, 5.5 TB/s past the
-// caches, 141 through them; 8 requests' (67 MB of states): 17.2 and 14.9.
+// caches, 141 through them; 8 requests' (67 MB of states): 17.2 and 14.9.  More than 16 beams, four bytes a thread:
+// 16 requests of 17 (895 MB) 216 us, 8 of 32 (860 MB) 163, 4 of 64 (870 MB) 189: 4.1, 5.3 and 4.6 TB/s.
 template <typename W, int KMAX, bool STREAM>
 __device__ __forceinline__ void move_columns(unsigned char* base, size_t row, size_t off, const int (&par)[KMAX], int K) {
   W v[KMAX];

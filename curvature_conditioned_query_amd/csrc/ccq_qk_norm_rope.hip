@@ -15,7 +15,7 @@
 //
 // Measured: B4 T4096 16 + 16 heads of 128, bf16: 51 us for the 268 MB it reads and writes, 5.3 TB/s, against
 // 6.0 of a plain stream past the caches; the gradient (16 + 4 heads, expanded; 436 MB with the fp32 gradients
-// it reads) 87 us and the sum of the weights' parts 4.6, 4.8 TB/s over both.  A decode step's 64 tokens take
+// it reads) 91 us and the sum of the weights' parts 4.6, 4.6 TB/s over both.  A decode step's 64 tokens take
 // 4.2 us, the launch's and one load's latency.
 #include <type_traits>
 
