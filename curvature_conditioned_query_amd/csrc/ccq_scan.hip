@@ -14,15 +14,17 @@
 // 128 bytes reach 4.8; past the caches (non-temporal), which a single use has no use for, 6.0 and 5.4.
 //
 // Measured.  B4 T4096 D2048 bf16: 49 us for 201 MB, 4.1 TB/s (43 without the waiting, and 2 for the clearing of
-// the pairs), 55 with the complement, whose 1 - alpha is formed for the fold and again for the walk; the gradient of a padded batch of that size with the complement, lengths 1/2 to 1, 70 us for 287 MB,
-// 4.1 TB/s (63 without the waiting; 79 with the rows behind the sequences read, too): two workgroups fit a CU
-// and the vector units are busy for half of it, so loads and arithmetic overlap in part only.  B1 T20480 D1024
-// fp32: 70 us for 251 MB, 3.6 TB/s (54 to 60 without the waiting): eight columns of 160 tiles one behind the
-// other, 1,280 tiles on 512 places, so the third round is half empty.  Farther from their floor: the fp32 gradient, whose
-// runs are two tokens and its tiles 64 (B1 T6798 D1464: 71 us for 200 MB), and lengths a little above a multiple of
-// 128 (the gradient of B93 T262 D1264: 105 us for 312 MB, its third tile holding 6 tokens).  Not kept: workgroups that stay and load their next tile ahead (98 us against 59: fewer share a CU, and
-// the waiting shows); 64-token tiles (56; of 256 threads 53, with the fp32 sequence at 68 and the gradient at
-// 80 against 79); seven or eight waves a SIMD (53 and 63: spills); groups of 8 or 32 tiles.
+// the pairs), 55 with the complement, whose 1 - alpha is formed for the fold and again for the walk; the gradient
+// of a padded batch of that size with the complement, lengths 1/2 to 1, 70 us for 287 MB, 4.1 TB/s (63 without the
+// waiting; 79 with the rows behind the sequences read, too): two workgroups fit a CU and the vector units are busy
+// for half of it, so loads and arithmetic overlap in part only.  B1 T20480 D1024 fp32: 70 us for 251 MB, 3.6 TB/s
+// (54 to 60 without the waiting): eight columns of 160 tiles one behind the other, 1,280 tiles on 512 places, so
+// the third round is half empty.  Farther from their floor: the fp32 gradient, whose runs are two tokens and its
+// tiles 64 (B1 T6798 D1464: 71 us for 200 MB), and lengths a little above a multiple of 128 (the gradient of B93
+// T262 D1264: 105 us for 312 MB, its third tile holding 6 tokens).  Not kept: workgroups that stay and load their
+// next tile ahead (98 us against 59: fewer share a CU, and the waiting shows); 64-token tiles (56; of 256 threads
+// 53, with the fp32 sequence at 68 and the gradient at 80 against 79); seven or eight waves a SIMD (53 and 63:
+// spills); groups of 8 or 32 tiles.
 //
 // Waiting.  A tile's pair depends on its own inputs alone and is published before its workgroup waits
 // for any other, and each column's tiles are handed out by a counter in the order of the recurrence, so
