@@ -330,3 +330,26 @@ def test_rows_of_one_value_in_several_pieces(gpu_lib, dtype, value):
     x = torch.full((64, 16, 20000), value, dtype=dt).cuda()
     x[5:, :, 17000] += 1
     _run(x, torch.zeros(64, 16).cuda(), 16, tag=f"all {value}")
+
+
+def test_selections_in_flight_together(gpu_lib):
+    """Calls on several streams at once, each with its own workspace, and one captured graph replayed among them."""
+    import torch
+    from curvature_conditioned_query_amd import ccq_beam_select
+    sets = []
+    for i, (N, K, V, m) in enumerate(((64, 16, 26000, 16), (1, 8, 32001, 8), (7, 5, 20, 32), (3, 64, 9001, 64))):
+        logits, g = _logits(N, K, V, "bf16" if i % 2 else "f32", 40 + i)
+        logits[..., : V // 2] = -1e10 if i % 2 else -float("inf")
+        sets.append((logits, -_uniform(N, K, g).cuda(), m))
+    want = [ccq_beam_select(*s) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = [ccq_beam_select(*s) for s in sets]
+    for _ in range(4):
+        graph.replay()
+        got = [ccq_beam_select(*s, stream=t) for s, t in zip(sets, streams)]
+        torch.cuda.synchronize()
+        for a, b, c in zip(want, got, kept):
+            assert all(torch.equal(a[n], b[n]) and torch.equal(a[n], c[n]) for n in a)

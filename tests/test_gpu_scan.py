@@ -357,3 +357,29 @@ def test_gates_above_one_leave_a_zero_state_alone(gpu_lib, dtype, complement, T)
         assert torch.isfinite(out[name]).all(), name
         _check(out[name], want[i], want[3 + i], "f32" if name == "dh0" else dtype, 20, name)
     assert (out["dx"][:, 5:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 30, 64, 65, 300, 2500])
+def test_gradient_of_the_state_in_place(gpu_lib, dtype, T):
+    """dh0 over dh_out, through the C interface: the serving step's counterpart in training by pieces."""
+    import ctypes
+    import torch
+    from curvature_conditioned_query_amd import ccq_scan_backward
+    from curvature_conditioned_query_amd.binding import ScanBwdParams
+    for complement in (0, 1):
+        x, la, h0, n = _make(dtype, 3, T, 136, 14, lengths=[T, T // 2, 0])
+        dy, dh = torch.randn_like(x), torch.randn_like(h0)
+        want = ccq_scan_backward(x, la, dy, h0=h0, dh_out=dh, lengths=n, complement=bool(complement), want_dh0=True)
+        dx, dg = torch.empty_like(x), torch.empty_like(x)
+        p = ScanBwdParams(dtype=1 if dtype == "bf16" else 0, B=3, T=T, D=136, complement=complement, x=x.data_ptr(),
+                          log_alpha=la.data_ptr(), dy=dy.data_ptr(), lengths=n.data_ptr(), h0=h0.data_ptr(), dh_out=dh.data_ptr(),
+                          dx=dx.data_ptr(), dlog_alpha=dg.data_ptr(), dh0=dh.data_ptr())
+        for name in ("x", "la", "dy"):
+            setattr(p, name + "_stride_b", T * 136)
+            setattr(p, name + "_stride_t", 136)
+        need = gpu_lib.ccq_scan_backward_workspace_bytes(ctypes.byref(p))
+        work = torch.empty(max(16, need), dtype=torch.uint8, device="cuda")
+        p.workspace, p.workspace_bytes = work.data_ptr(), need
+        assert gpu_lib.ccq_scan_backward(ctypes.byref(p), torch.cuda.current_stream().cuda_stream) == 0
+        assert torch.equal(dx, want["dx"]) and torch.equal(dg, want["dlog_alpha"]) and torch.equal(dh, want["dh0"])
