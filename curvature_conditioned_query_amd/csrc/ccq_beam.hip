@@ -396,7 +396,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 1) void beam_rows_ke
 
   float bound = -INFINITY;  // candidates lie above it
   float top = -INFINITY;    // the sum of the others counts from here: no logit of theirs lies above it
-  float part = 0.f;
+  double part = 0.0;        // a thread's 32 logits of a piece go into it together, summed in fp32
   double gone = 0.0;        // of candidates that were thinned out, counted from ref; and of part before top moved
   float ref = -INFINITY;
   int n = 0;                // candidates of the wave
@@ -461,8 +461,9 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 1) void beam_rows_ke
           if (!ONE && higher > top) {
             // logits up to here are no candidates from now on, and may lie far above the first piece's top: what
             // was summed goes to the thinned ones' sum, and the fp32 sum begins anew
-            gone += (double)(part + ((sum[0] + sum[1]) + (sum[2] + sum[3]))) * exp((double)top - (double)ref);
-            part = sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
+            gone += (part + (double)((sum[0] + sum[1]) + (sum[2] + sum[3]))) * exp((double)top - (double)ref);
+            part = 0.0;
+            sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
             top = higher;
           }
         }
@@ -476,7 +477,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 1) void beam_rows_ke
         for (int i = 0; i < G; ++i) sum[0] = x[i] != x[i] ? x[i] : sum[0];
       }
     }
-    part += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    part += (double)((sum[0] + sum[1]) + (sum[2] + sum[3]));
     bound = higher;
   }
   bool careful = part != part || gone != gone || top == INFINITY;
@@ -494,7 +495,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 1) void beam_rows_ke
   const float from = fmaxf(top, most);
   double sum = 0.0;
   if (from > -INFINITY) {
-    if (top > -INFINITY) sum = (double)part * exp((double)top - (double)from);
+    if (top > -INFINITY) sum = part * exp((double)top - (double)from);
     for (int i = lane; i < n; i += 64) sum += exp((double)key_logit(held[wave].key[i]) - (double)from);
     if (ref > -INFINITY) sum += gone * exp((double)ref - (double)from);
   }

@@ -80,6 +80,24 @@ def test_beam_select(gpu_lib):
         assert ((out["score"][n] - small["score"][0]).abs() <= 2 * (U * small["score"][0].abs() + 64 * U)).all()
 
 
+def test_normaliser_of_very_long_rows(gpu_lib):
+    """67 million tokens a row, 2048 pieces for a workgroup, all but one token at a value whose terms' fp32 sum
+    drifts: the score is the closed form's to the same bound as a short row's."""
+    import math
+    import torch
+    from curvature_conditioned_query_amd import ccq_beam_select
+    N, V = 256, 1 << 26
+    logits = torch.empty(N, 1, V, device="cuda", dtype=torch.bfloat16)
+    for d in (1.5625, 1.75, 1.8125):
+        logits.fill_(-d)
+        logits[..., 77] = 0
+        out = ccq_beam_select(logits, torch.zeros(N, 1, device="cuda"), 2)
+        best = -math.log1p((V - 1) * math.exp(-d))
+        assert (out["token"][:, 0] == 77).all() and (out["token"][:, 1] == 0).all()
+        for i, want in enumerate((best, best - d)):
+            assert ((out["score"][:, i].double() - want).abs() <= U * abs(want) + 64 * U).all(), (d, i)
+
+
 def test_beam_reorder(gpu_lib):
     import torch
     from curvature_conditioned_query_amd import ccq_beam_reorder
