@@ -25,6 +25,11 @@ from .binding import (  # noqa: F401
     ccq_scan_backward,
     ccq_beam_select,
     ccq_beam_reorder,
+    ccq_linear_attn,
+    ccq_linear_attn_backward,
+    ccq_group_norm,
+    ccq_group_norm_backward,
+    ccq_logits_adjust,
     scan_carry_shape,
     new_chunk_carry,
     library_path,

@@ -41,6 +41,14 @@ EXPORTED_SYMBOLS = (
     "ccq_beam_select",
     "ccq_beam_select_workspace_bytes",
     "ccq_beam_reorder",
+    "ccq_linear_attn",
+    "ccq_linear_attn_workspace_bytes",
+    "ccq_linear_attn_backward",
+    "ccq_linear_attn_backward_workspace_bytes",
+    "ccq_group_norm",
+    "ccq_group_norm_backward",
+    "ccq_group_norm_backward_workspace_bytes",
+    "ccq_logits_adjust",
     "ccq_status_string",
     "ccq_abi_version",
 )
@@ -171,6 +179,75 @@ class BeamParams(ctypes.Structure):
     ]
 
 
+def _stride_fields(*names):
+    return [(f"{n}_stride_{axis}", ctypes.c_int64) for n in names for axis in "bth"]
+
+
+class LinearAttnParams(ctypes.Structure):
+    """Mirror of ``ccq_linear_attn_params``."""
+
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("gate_dtype", ctypes.c_int32), ("B", ctypes.c_int32), ("T", ctypes.c_int32),
+        ("H", ctypes.c_int32), ("H_q", ctypes.c_int32), ("H_k", ctypes.c_int32), ("H_v", ctypes.c_int32),
+        ("d_k", ctypes.c_int32), ("d_v", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        *_stride_fields("q", "k", "v"),
+        ("log_alpha", ctypes.c_void_p), *_stride_fields("la"),
+        ("lengths", ctypes.c_void_p), ("offsets", ctypes.c_void_p), ("rows", ctypes.c_int64),
+        ("S0", ctypes.c_void_p), ("o", ctypes.c_void_p), *_stride_fields("o"), ("S_out", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class LinearAttnBwdParams(ctypes.Structure):
+    """Mirror of ``ccq_linear_attn_bwd_params``."""
+
+    _fields_ = [
+        ("fwd", LinearAttnParams), ("grad_dtype", ctypes.c_int32),
+        ("d_o", ctypes.c_void_p), *_stride_fields("do"), ("dS_out", ctypes.c_void_p),
+        ("dq", ctypes.c_void_p), ("dk", ctypes.c_void_p), ("dv", ctypes.c_void_p), *_stride_fields("dq", "dk", "dv"),
+        ("dlog_alpha", ctypes.c_void_p), ("dS0", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class GroupNormParams(ctypes.Structure):
+    """Mirror of ``ccq_group_norm_params``."""
+
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("G", ctypes.c_int32),
+        ("d", ctypes.c_int32), ("center", ctypes.c_int32), ("activation", ctypes.c_int32),
+        ("affine_shared", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("x", ctypes.c_void_p), ("gate", ctypes.c_void_p), *_stride_fields("x", "gate"),
+        ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("y", ctypes.c_void_p), *_stride_fields("y"),
+    ]
+
+
+class GroupNormBwdParams(ctypes.Structure):
+    """Mirror of ``ccq_group_norm_bwd_params``."""
+
+    _fields_ = [
+        ("fwd", GroupNormParams), ("dy", ctypes.c_void_p), *_stride_fields("dy"),
+        ("dx", ctypes.c_void_p), *_stride_fields("dx"), ("dgate", ctypes.c_void_p), *_stride_fields("dgate"),
+        ("dweight", ctypes.c_void_p), ("dbias", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class LogitsAdjustParams(ctypes.Structure):
+    """Mirror of ``ccq_logits_adjust_params``."""
+
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("R", ctypes.c_int32), ("V", ctypes.c_int32), ("L", ctypes.c_int32),
+        ("n_bias", ctypes.c_int32), ("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_int64),
+        ("history", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("prompt_lengths", ctypes.c_void_p),
+        ("repetition", ctypes.c_float), ("presence", ctypes.c_float), ("frequency", ctypes.c_float),
+        ("repetition_rows", ctypes.c_void_p), ("presence_rows", ctypes.c_void_p), ("frequency_rows", ctypes.c_void_p),
+        ("bias_token", ctypes.c_void_p), ("bias_value", ctypes.c_void_p), ("allowed", ctypes.c_void_p),
+        ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64),
+    ]
+
+
 def library_path() -> str:
     return os.environ.get("CCQ_LIBRARY", os.path.join(_HERE, "libccq.so"))
 
@@ -208,12 +285,17 @@ def load_library():
     lib.ccq_chunk_carry_bytes.restype = ctypes.c_size_t
     for name, cls in (("ccq_qk_norm_rope", QkParams), ("ccq_qk_norm_rope_backward", QkBwdParams),
                       ("ccq_scan", ScanParams), ("ccq_scan_backward", ScanBwdParams),
-                      ("ccq_beam_select", BeamParams)):
+                      ("ccq_beam_select", BeamParams), ("ccq_linear_attn", LinearAttnParams),
+                      ("ccq_linear_attn_backward", LinearAttnBwdParams), ("ccq_group_norm", GroupNormParams),
+                      ("ccq_group_norm_backward", GroupNormBwdParams), ("ccq_logits_adjust", LogitsAdjustParams)):
         getattr(lib, name).argtypes = [ctypes.POINTER(cls), vp]
         getattr(lib, name).restype = ctypes.c_int
     for name, cls in (("ccq_qk_backward_workspace_bytes", QkBwdParams), ("ccq_scan_workspace_bytes", ScanParams),
                       ("ccq_scan_backward_workspace_bytes", ScanBwdParams),
-                      ("ccq_beam_select_workspace_bytes", BeamParams)):
+                      ("ccq_beam_select_workspace_bytes", BeamParams),
+                      ("ccq_linear_attn_workspace_bytes", LinearAttnParams),
+                      ("ccq_linear_attn_backward_workspace_bytes", LinearAttnBwdParams),
+                      ("ccq_group_norm_backward_workspace_bytes", GroupNormBwdParams)):
         getattr(lib, name).argtypes = [ctypes.POINTER(cls)]
         getattr(lib, name).restype = ctypes.c_size_t
     lib.ccq_beam_reorder.argtypes = [i32, ctypes.POINTER(vp), ctypes.POINTER(ctypes.c_size_t), i32, i32, vp, vp]
@@ -633,7 +715,9 @@ class _Ops:
         self.nowhere = _NoContext()
         for name in ("qk_norm_rope", "qk_norm_rope_backward", "scan", "scan_backward", "beam_select", "beam_reorder",
                      "qk_backward_workspace_bytes", "scan_workspace_bytes", "scan_backward_workspace_bytes",
-                     "beam_select_workspace_bytes"):
+                     "beam_select_workspace_bytes", "linear_attn", "linear_attn_workspace_bytes",
+                     "linear_attn_backward", "linear_attn_backward_workspace_bytes", "group_norm",
+                     "group_norm_backward", "group_norm_backward_workspace_bytes", "logits_adjust"):
             setattr(self, name, getattr(lib, "ccq_" + name))
 
     def dtype_code(self, t):
@@ -942,3 +1026,221 @@ def ccq_beam_reorder(states, parent, stream=None):
         st = ops.beam_reorder(count, ptrs, sizes, N, K, at, ops.raw_stream(dev.index))
         if st != 0:
             raise CcqError(st, "ccq_beam_reorder")
+
+
+# ---------------------------------------------------------------- operators of a linear-attention layer
+
+
+def _la_params(ops, q, k, v, log_alpha, scale, S0, lengths, offsets, max_length, dev):
+    """The forward's arguments without o, S_out and a workspace; and (rows of the token dimensions, B, T, H)."""
+    dt = q.dtype
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k and v are [B, T, H, d]")
+    n0, n1, Hq, dk = q.shape
+    Hk, Hv, dv = k.shape[2], v.shape[2], v.shape[3]
+    H = max(Hq, Hk, Hv)
+    gate, la, ls = CCQ_DTYPE_F32, None, (0, 0, 0)
+    if log_alpha is not None:
+        if log_alpha.dim() != 3:
+            raise ValueError("log_alpha is [B, T, H]")
+        H = max(H, log_alpha.shape[2])
+        if log_alpha.shape != (n0, n1, H) or log_alpha.device != dev:
+            _refuse("log_alpha", log_alpha, dev, log_alpha.dtype, (n0, n1, H), "given")
+        gate, la, ls = ops.dtype_code(log_alpha), log_alpha.data_ptr(), log_alpha.stride()
+    if H % Hq or H % Hk or H % Hv:
+        raise ValueError(f"{Hq} query, {Hk} key and {Hv} value heads must divide {H} heads")
+    B, T, rows = n0, n1, 0
+    if offsets is not None:
+        if n0 != 1:
+            raise ValueError("packed sequences lie in tensors [1, rows, H, d]")
+        if offsets.dim() != 1 or offsets.shape[0] < 2:
+            raise ValueError("offsets is [B + 1]")
+        B, rows, T = offsets.shape[0] - 1, n1, n1 if max_length is None else max_length
+    elif max_length is not None:
+        raise ValueError("max_length is given with offsets and only with them")
+    return LinearAttnParams(
+        ops.dtype_code(q), gate, B, T, H, Hq, Hk, Hv, dk, dv, scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        *_strided("q", q, dev, dt, (n0, n1, Hq, dk)), *_strided("k", k, dev, dt, (n0, n1, Hk, dk)),
+        *_strided("v", v, dev, dt, (n0, n1, Hv, dv)), la, *ls, _dense("lengths", lengths, dev, ops.i32, (B,)),
+        _dense("offsets", offsets, dev, ops.i32, (B + 1,)), rows, _dense("S0", S0, dev, ops.f32, (B, H, dv, dk))), n0, n1
+
+
+def _view_into(ops, name, t, dev, dtype, shape):
+    """A strided output, the given one or a new one, and its strides."""
+    if t is None:
+        _, a, b, c = shape
+        t = ops.empty_strided(shape, (a * b * c, b * c, c, 1), dtype=dtype, device=dev)
+    return t, _strided(name, t, dev, dtype, shape)
+
+
+def ccq_linear_attn(q, k, v, log_alpha=None, scale: float = 1.0, S0=None, S_out=None, o=None, lengths=None,
+                    offsets=None, max_length=None, workspace=None, stream=None):
+    """Linear attention with one decay for each head, S_t = exp(log_alpha_t) S_{t-1} + v_t k_t^T,
+    o_t = scale S_t q_t (see ``ccq_linear_attn`` in ccq.h).  q [B, T, H_q, d_k], k [B, T, H_k, d_k],
+    v [B, T, H_v, d_v]: strided views are fine (head-major tensors by ``.transpose(1, 2)``), fewer heads are
+    shared; log_alpha [B, T, H] of q's dtype or fp32, expanded if tokens share it, or None; S0, S_out
+    [B, H, d_v, d_k] fp32 (S_out may be S0: the serving step is T = 1); lengths [B] int32.  Packed sequences:
+    tensors [1, rows, ..] with offsets [B + 1] int32, not falling, and max_length, no sequence being longer.
+    Returns o [B, T, H, d_v]: rows of no token are left as they were, which in an o allocated here (o=None) is
+    whatever the memory held."""
+    ops, dev = _ops(), q.device
+    with ops.place(dev, stream):
+        p, n0, n1 = _la_params(ops, q, k, v, log_alpha, scale, S0, lengths, offsets, max_length, dev)
+        o, st = _view_into(ops, "o", o, dev, q.dtype, (n0, n1, p.H, p.d_v))
+        p.o = o.data_ptr()
+        p.o_stride_b, p.o_stride_t, p.o_stride_h = st
+        p.S_out = _dense("S_out", S_out, dev, ops.f32, (p.B, p.H, p.d_v, p.d_k))
+        _launch(ops, "linear_attn", ops.linear_attn, p, dev, ops.linear_attn_workspace_bytes if p.T > 8 else None, workspace)
+    return o
+
+
+def ccq_linear_attn_backward(q, k, v, d_o, log_alpha=None, scale: float = 1.0, S0=None, dS_out=None, lengths=None,
+                             offsets=None, max_length=None, want_dS0: bool = False, grad_dtype=None, dq=None, dk=None,
+                             dv=None, workspace=None, stream=None):
+    """Gradient of ``ccq_linear_attn`` (see ``ccq_linear_attn_backward`` in ccq.h).  d_o [B, T, H, d_v]: gradient
+    of o (a strided view is fine); dS_out [B, H, d_v, d_k] fp32: gradient of S_out, or None.  Returns a dict: dq, dk,
+    dv (the shapes of q, k, v; of grad_dtype, torch.float32 or q's, which None means; into the given views if any),
+    dlog_alpha ([B, T, H], log_alpha's dtype, with log_alpha: one entry a token, also where tokens share a gate) and,
+    with want_dS0, dS0 fp32."""
+    ops, dev = _ops(), q.device
+    with ops.place(dev, stream):
+        f, n0, n1 = _la_params(ops, q, k, v, log_alpha, scale, S0, lengths, offsets, max_length, dev)
+        gt = next((t.dtype for t in (dq, dk, dv) if t is not None), q.dtype) if grad_dtype is None else grad_dtype
+        code = ops.codes.get(gt)
+        if code is None:
+            raise TypeError(f"unsupported gradient dtype {gt}")
+        dq, sq = _view_into(ops, "dq", dq, dev, gt, q.shape)
+        dk, sk = _view_into(ops, "dk", dk, dev, gt, k.shape)
+        dv, sv = _view_into(ops, "dv", dv, dev, gt, v.shape)
+        out = dict(dq=dq, dk=dk, dv=dv)
+        if log_alpha is not None:
+            out["dlog_alpha"] = ops.empty((n0, n1, f.H), dtype=log_alpha.dtype, device=dev)
+        if want_dS0:
+            out["dS0"] = ops.empty((f.B, f.H, f.d_v, f.d_k), dtype=ops.f32, device=dev)
+        p = LinearAttnBwdParams(f, code, d_o.data_ptr(), *_strided("d_o", d_o, dev, q.dtype, (n0, n1, f.H, f.d_v)),
+                                _dense("dS_out", dS_out, dev, ops.f32, (f.B, f.H, f.d_v, f.d_k)), dq.data_ptr(),
+                                dk.data_ptr(), dv.data_ptr(), *sq, *sk, *sv, _ptr(out.get("dlog_alpha")),
+                                _ptr(out.get("dS0")), None, 0)
+        _launch(ops, "linear_attn_backward", ops.linear_attn_backward, p, dev, ops.linear_attn_backward_workspace_bytes,
+                workspace)
+    return out
+
+
+_ACTIVATIONS = {"none": 0, None: 0, "silu": 1, "sigmoid": 2}
+
+
+def _group_norm_params(ops, x, weight, bias, gate, center, eps, activation, dev):
+    """The forward's arguments without y."""
+    if x.dim() != 4:
+        raise ValueError("x is [B, T, G, d]")
+    dt, shape = x.dtype, x.shape
+    B, T, G, d = shape
+    kind = _ACTIVATIONS.get(activation)
+    if kind is None:
+        raise ValueError(f"unknown activation {activation!r}: 'none', 'silu' or 'sigmoid'")
+    ref = weight if weight is not None else bias
+    shared = ref is not None and ref.dim() == 1
+    affine = (d,) if shared else (G, d)
+    gs = (0, 0, 0) if gate is None else _strided("gate", gate, dev, dt, shape)
+    return GroupNormParams(ops.dtype_code(x), B, T, G, d, 1 if center else 0, kind, 1 if shared else 0, eps, x.data_ptr(),
+                           None if gate is None else gate.data_ptr(), *_strided("x", x, dev, dt, shape), *gs,
+                           _dense("weight", weight, dev, ops.f32, affine), _dense("bias", bias, dev, ops.f32, affine))
+
+
+def ccq_group_norm(x, weight=None, bias=None, gate=None, center: bool = False, eps: float = 1e-6,
+                   activation: str = "none", y=None, stream=None):
+    """Group norm of every token, channels last, with an activation (see ``ccq_group_norm`` in ccq.h).  x, gate
+    [B, T, G, d]: G groups of d channels, strided views are fine (head-major tensors by ``.transpose(1, 2)``);
+    weight, bias fp32 [G, d], or [d] for all groups.  y = act(z), or z act(gate), of the normalised z; center: the
+    mean is taken off.  Returns y [B, T, G, d], dense unless given."""
+    ops, dev = _ops(), x.device
+    with ops.place(dev, stream):
+        p = _group_norm_params(ops, x, weight, bias, gate, center, eps, activation, dev)
+        y, st = _view_into(ops, "y", y, dev, x.dtype, x.shape)
+        p.y = y.data_ptr()
+        p.y_stride_b, p.y_stride_t, p.y_stride_h = st
+        _launch(ops, "group_norm", ops.group_norm, p, dev)
+    return y
+
+
+def ccq_group_norm_backward(x, dy, weight=None, bias=None, gate=None, center: bool = False, eps: float = 1e-6,
+                            activation: str = "none", dx=None, dgate=None, workspace=None, stream=None):
+    """Gradient of ``ccq_group_norm`` (see ``ccq_group_norm_backward`` in ccq.h).  dy [B, T, G, d]: gradient of y (a
+    strided view is fine).  Returns a dict: dx, dgate (dtype of x, into the given views if any), dweight, dbias (fp32),
+    None for what was not given."""
+    ops, dev = _ops(), x.device
+    with ops.place(dev, stream):
+        f = _group_norm_params(ops, x, weight, bias, gate, center, eps, activation, dev)
+        dt, shape = x.dtype, x.shape
+        if dgate is not None and gate is None:
+            raise ValueError("dgate is given without gate")
+        dx, sx = _view_into(ops, "dx", dx, dev, dt, shape)
+        sg = (0, 0, 0)
+        if gate is not None:
+            dgate, sg = _view_into(ops, "dgate", dgate, dev, dt, shape)
+        dw = None if weight is None else ops.empty(weight.shape, dtype=ops.f32, device=dev)
+        db = None if bias is None else ops.empty(bias.shape, dtype=ops.f32, device=dev)
+        p = GroupNormBwdParams(f, dy.data_ptr(), *_strided("dy", dy, dev, dt, shape), dx.data_ptr(), *sx, _ptr(dgate), *sg,
+                               _ptr(dw), _ptr(db), None, 0)
+        _launch(ops, "group_norm_backward", ops.group_norm_backward, p, dev,
+                None if dw is None and db is None else ops.group_norm_backward_workspace_bytes, workspace)
+    return dict(dx=dx, dgate=dgate, dweight=dw, dbias=db)
+
+
+def _row_spread(name, t, dev, dtype, shape):
+    """The distance of the rows of t [.., V], which are evenly spaced and dense."""
+    st = t.stride()
+    if t.shape != shape or t.dtype != dtype or t.device != dev or (st[-1] != 1 and shape[-1] != 1):
+        _refuse(name, t, dev, dtype, shape, "dense in its last dimension")
+    if len(shape) == 2:
+        return st[0] if shape[0] > 1 else shape[1]
+    N, K, V = shape
+    if N > 1 and K > 1 and st[0] != K * st[1]:
+        raise ValueError(f"the rows of {name} must be evenly spaced")
+    return st[1] if K > 1 else st[0] if N > 1 else V
+
+
+def ccq_logits_adjust(logits, history=None, lengths=None, prompt_lengths=None, repetition=1.0, presence=0.0, frequency=0.0,
+                      bias_token=None, bias_value=None, allowed=None, out=None, stream=None):
+    """Penalties for tokens seen, biases and a grammar's mask on logits (see ``ccq_logits_adjust`` in ccq.h).  logits
+    [N, K, V] or [R, V] (rows may be padded), R = N K; history [R, L] int32, lengths and prompt_lengths [R] int32;
+    repetition, presence and frequency each one number, or fp32 [R]; bias_token int32 and bias_value fp32 [R, n];
+    allowed [R, ceil(V / 32)] int32, a bit a token.  Returns out, of the shape of logits (out=logits: in place)."""
+    if logits.dim() not in (2, 3):
+        raise ValueError("logits is [N, K, V] or [R, V]")
+    ops, dev, shape, dt = _ops(), logits.device, logits.shape, logits.dtype
+    with ops.place(dev, stream):
+        V = shape[-1]
+        R = shape[0] if len(shape) == 2 else shape[0] * shape[1]
+        if out is None:
+            out = ops.empty(shape, dtype=dt, device=dev)
+        L = n = 0
+        if history is not None:
+            if history.dim() != 2:
+                raise ValueError("history is [R, L]")
+            L = history.shape[1]
+            if L == 0:
+                history = lengths = prompt_lengths = None
+        elif lengths is not None or prompt_lengths is not None:
+            raise ValueError("lengths are given with history and only with it")
+        if bias_token is not None:
+            if bias_token.dim() != 2:
+                raise ValueError("bias_token is [R, n]")
+            n = bias_token.shape[1]
+            if n == 0:
+                bias_token = bias_value = None
+        one, rows = [1.0, 0.0, 0.0], [None, None, None]
+        for i, (name, x) in enumerate((("repetition", repetition), ("presence", presence), ("frequency", frequency))):
+            if isinstance(x, ops.torch.Tensor):
+                rows[i] = _dense(name, x, dev, ops.f32, (R,))
+            else:
+                one[i] = x
+        p = LogitsAdjustParams(ops.dtype_code(logits), R, V, L, n, logits.data_ptr(), _row_spread("logits", logits, dev, dt, shape),
+                               _dense("history", history, dev, ops.i32, (R, L)), _dense("lengths", lengths, dev, ops.i32, (R,)),
+                               _dense("prompt_lengths", prompt_lengths, dev, ops.i32, (R,)), *one, *rows,
+                               _dense("bias_token", bias_token, dev, ops.i32, (R, n)),
+                               _dense("bias_value", bias_value, dev, ops.f32, (R, n)),
+                               _dense("allowed", allowed, dev, ops.i32, (R, (V + 31) // 32)),
+                               out.data_ptr(), _row_spread("out", out, dev, dt, shape))
+        _launch(ops, "logits_adjust", ops.logits_adjust, p, dev)
+    return out

@@ -23,7 +23,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libccq.so")
 SOURCES = ["ccq_api.cpp", "ccq_decode.hip", "ccq_decode_packed.hip", "ccq_prefill.hip", "ccq_prefill_summary.hip", "ccq_prefill_gdn.hip", "ccq_prefill_gdn_summary.hip", "ccq_prefill_pipe.hip", "ccq_subspace.hip",
            "ccq_step_backward.hip", "ccq_backward.hip", "ccq_backward_gdn.hip", "ccq_noalloc.hip",
-           "ccq_ops_api.cpp", "ccq_qk_norm_rope.hip", "ccq_scan.hip", "ccq_beam.hip"]
+           "ccq_ops_api.cpp", "ccq_qk_norm_rope.hip", "ccq_scan.hip", "ccq_beam.hip",
+           "ccq_linear_attn.hip", "ccq_group_norm.hip", "ccq_logits.hip"]
 ARCH = "gfx950"
 # Packed-fp32 VALU forms are disabled for all device code.
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]

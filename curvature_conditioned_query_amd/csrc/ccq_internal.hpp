@@ -178,4 +178,15 @@ hipError_t launch_beam_select(const ccq_beam_params& p, hipStream_t stream);
 hipError_t launch_beam_reorder(int n_states, void* const* states, const size_t* row_bytes, int N, int K,
                                const int32_t* parent, hipStream_t stream);
 
+// Operators of a linear-attention layer.
+size_t linear_attn_workspace_bytes(const ccq_linear_attn_params& p);
+hipError_t launch_linear_attn(const ccq_linear_attn_params& p, hipStream_t stream);
+size_t linear_attn_backward_workspace_bytes(const ccq_linear_attn_bwd_params& p);
+hipError_t launch_linear_attn_backward(const ccq_linear_attn_bwd_params& p, hipStream_t stream);
+hipError_t launch_group_norm(const ccq_group_norm_params& p, hipStream_t stream);
+size_t group_norm_backward_workspace_bytes(const ccq_group_norm_bwd_params& p);
+hipError_t launch_group_norm_backward(const ccq_group_norm_bwd_params& p, hipStream_t stream);
+bool logits_adjust_grid_fits(const ccq_logits_adjust_params& p);
+hipError_t launch_logits_adjust(const ccq_logits_adjust_params& p, hipStream_t stream);
+
 }  // namespace ccq

@@ -516,6 +516,168 @@ size_t ccq_beam_select_workspace_bytes(const ccq_beam_params *p);
 int ccq_beam_reorder(int32_t n_states, void *const *states, const size_t *row_bytes, int32_t N, int32_t K,
                      const int32_t *parent, void *hip_stream);
 
+/* Arguments of ccq_linear_attn.  Zero-initialise, then fill in. */
+typedef struct {
+  int32_t dtype;             /* ccq_dtype of q, k, v and o                                          */
+  int32_t gate_dtype;        /* ccq_dtype of log_alpha                                              */
+  int32_t B, T;              /* sequences, and the most tokens of one                               */
+  int32_t H, H_q, H_k, H_v;  /* heads of o; H_q, H_k and H_v divide H: head h reads query head
+                                h / (H / H_q), and key and value heads alike                        */
+  int32_t d_k, d_v;          /* each 64 or 128                                                      */
+  float scale;               /* of the outputs; finite                                              */
+  const void *q, *k, *v;     /* [B, T, H_q | H_k | H_v, d_k | d_k | d_v], strides below             */
+  int64_t q_stride_b, q_stride_t, q_stride_h; /* >= 0                                               */
+  int64_t k_stride_b, k_stride_t, k_stride_h;
+  int64_t v_stride_b, v_stride_t, v_stride_h;
+  const void *log_alpha;     /* [B, T, H], strides below, any (0: a gate for each head, say); or NULL: no decay */
+  int64_t la_stride_b, la_stride_t, la_stride_h; /* >= 0                                            */
+  const int32_t *lengths;    /* [B] tokens of each sequence (taken into 0 .. T), or NULL            */
+  const int32_t *offsets;    /* [B + 1], or NULL.  Packed sequences: the tensors have one row for each of
+                                `rows` tokens, sequence b those from offsets[b] to offsets[b + 1] - 1 (the
+                                first T of them, if there are more); strides over b are not read.  Not
+                                with lengths                                                        */
+  int64_t rows;              /* with offsets: rows of the packed tensors; else 0                    */
+  const float *S0;           /* [B, H, d_v, d_k] state before the first token, or NULL: zeros       */
+  void *o;                   /* [B, T, H, d_v] dtype, strides below, written; rows of no token are left as they were */
+  int64_t o_stride_b, o_stride_t, o_stride_h; /* no two rows may overlap                            */
+  float *S_out;              /* [B, H, d_v, d_k] state after the last token, or NULL; may be S0 itself */
+  void *workspace;           /* ccq_linear_attn_workspace_bytes(p) bytes, or NULL when that is 0    */
+  size_t workspace_bytes;
+} ccq_linear_attn_params;
+
+/*
+ * Linear attention with one decay for each head (and token):
+ *   S_t = alpha_t S_{t-1} + v_t k_t^T,  alpha_t = exp(log_alpha_t),  o_t = scale S_t q_t,
+ * the write rule of the read step with a scalar in the place of the decay per key channel, and no
+ * cleaning of the query.  A prompt is worked on in chunks of 64 tokens; T = 1 with S_out == S0 is the
+ * serving step.  The state is fp32 throughout (with 16-bit inputs what is added to it is right to 2^-16 of
+ * each term); o is rounded once more for the chunk's scores and for the state, in 16 bits, where the
+ * inputs have 16.  Gates are taken as they are, above 1 too, as long as the product of consecutive gates
+ * stays inside the range of fp32; where alpha_t is 0 (log_alpha_t below about -104) the state before
+ * token t is dropped, whatever it holds.  An input that is infinite or NaN may reach the outputs of all
+ * tokens of its 64-token chunk, earlier ones too; what stands in rows of no token reaches nothing.
+ * Long sequences with few heads are cut along T and the pieces joined in a fixed order: two calls give
+ * the same bits.  B H <= 2^20, B T <= 2^30, rows < 2^31 (CCQ_ERR_UNSUPPORTED beyond, and for other d).
+ * Returns a ccq_status.
+ */
+int ccq_linear_attn(const ccq_linear_attn_params *p, void *hip_stream);
+/* Bytes of device workspace that call needs (0 if none and for invalid p): depends on the sizes alone. */
+size_t ccq_linear_attn_workspace_bytes(const ccq_linear_attn_params *p);
+
+/* Arguments of ccq_linear_attn_backward.  Zero-initialise, then fill in. */
+typedef struct {
+  ccq_linear_attn_params fwd; /* the forward's arguments; o, S_out and its workspace are not used   */
+  int32_t grad_dtype;        /* ccq_dtype of dq, dk and dv: CCQ_DTYPE_F32, or that of q             */
+  const void *d_o;           /* [B, T, H, d_v] dtype: gradient of o, strides below                  */
+  int64_t do_stride_b, do_stride_t, do_stride_h; /* >= 0                                            */
+  const float *dS_out;       /* [B, H, d_v, d_k] gradient of S_out, or NULL: zeros                  */
+  void *dq, *dk, *dv;        /* grad_dtype, the shapes of q, k and v, strides below, written: summed over
+                                the heads that share a row; zeros at t >= length (packed rows of no
+                                sequence are left as they were)                                     */
+  int64_t dq_stride_b, dq_stride_t, dq_stride_h; /* no two rows may overlap                         */
+  int64_t dk_stride_b, dk_stride_t, dk_stride_h;
+  int64_t dv_stride_b, dv_stride_t, dv_stride_h;
+  void *dlog_alpha;          /* [B, T, H] (packed: [rows, H]) gate_dtype, dense, written, or NULL: one entry
+                                for each token whatever the strides of log_alpha: a gate that tokens
+                                share has their sum as its gradient                                 */
+  float *dS0;                /* [B, H, d_v, d_k], written, or NULL                                  */
+  void *workspace;           /* ccq_linear_attn_backward_workspace_bytes(p) bytes                   */
+  size_t workspace_bytes;
+} ccq_linear_attn_bwd_params;
+
+/* Gradient of ccq_linear_attn.  With the adjoint A_t = scale d_o_t q_t^T + alpha_{t+1} A_{t+1} (dS_out
+ * behind the last token): dq_t = scale S_t^T d_o_t, dk_t = A_t^T v_t, dv_t = A_t k_t,
+ * dlog_alpha_t = alpha_t <A_t, S_{t-1}>, which is formed as the sum over i >= t of
+ * q_i . dq_i - k_i . dk_i, plus <dS_out, S_out>; 0 where alpha_t is 0.  Sums over shared heads go in a
+ * fixed order: two calls give the same bits.  Returns a ccq_status. */
+int ccq_linear_attn_backward(const ccq_linear_attn_bwd_params *p, void *hip_stream);
+size_t ccq_linear_attn_backward_workspace_bytes(const ccq_linear_attn_bwd_params *p);
+
+/* Activations of ccq_group_norm: x, x sigmoid(x), sigmoid(x). */
+typedef enum { CCQ_ACT_NONE = 0, CCQ_ACT_SILU = 1, CCQ_ACT_SIGMOID = 2 } ccq_activation;
+
+/* Arguments of ccq_group_norm.  Zero-initialise, then fill in. */
+typedef struct {
+  int32_t dtype;             /* ccq_dtype of x, gate and y                                          */
+  int32_t B, T, G, d;        /* G groups of d channels a token; d a multiple of 8, at most 1024      */
+  int32_t center;            /* 1: the group's mean is taken off first; 0: mean square alone        */
+  int32_t activation;        /* ccq_activation                                                      */
+  int32_t affine_shared;     /* 1: weight and bias are [d], the same for every group; 0: [G, d]     */
+  float eps;                 /* >= 0                                                                */
+  const void *x;             /* [B, T, G, d], strides below                                         */
+  const void *gate;          /* [B, T, G, d], strides below, or NULL                                */
+  int64_t x_stride_b, x_stride_t, x_stride_h;          /* >= 0: over sequences, tokens, groups      */
+  int64_t gate_stride_b, gate_stride_t, gate_stride_h; /* >= 0                                      */
+  const float *weight;       /* or NULL (ones)                                                      */
+  const float *bias;         /* or NULL (zeros)                                                     */
+  void *y;                   /* [B, T, G, d] dtype, strides below, written; may be x or gate itself */
+  int64_t y_stride_b, y_stride_t, y_stride_h;          /* no two rows may overlap                   */
+} ccq_group_norm_params;
+
+/*
+ * Group norm of every token by itself, channels last, with an activation: with the mean mu (center) and
+ * r = 1 / sqrt(mean((x - mu)^2) + eps) of a group's d channels, z = (x - mu) r weight + bias and
+ *   y = act(z)        without a gate,
+ *   y = z act(gate)   with one.
+ * It takes the heads of a linear-attention or read-step output (head-major through its strides) to the
+ * output projection (token-major).  The arithmetic is fp32; the result is rounded once.  Fewer than 2^31
+ * groups B T G, G < 2^16 (CCQ_ERR_UNSUPPORTED beyond, and for other d).  Returns a ccq_status.
+ */
+int ccq_group_norm(const ccq_group_norm_params *p, void *hip_stream);
+
+/* Arguments of ccq_group_norm_backward.  Zero-initialise, then fill in. */
+typedef struct {
+  ccq_group_norm_params fwd; /* the forward's arguments; y is not used                              */
+  const void *dy;            /* [B, T, G, d] dtype: gradient of y, strides below                    */
+  int64_t dy_stride_b, dy_stride_t, dy_stride_h;       /* >= 0                                      */
+  void *dx;                  /* [B, T, G, d] dtype, strides below, written; may be dy itself        */
+  int64_t dx_stride_b, dx_stride_t, dx_stride_h;       /* no two rows may overlap                   */
+  void *dgate;               /* the same for the gate; set if and only if gate is; may be gate itself */
+  int64_t dgate_stride_b, dgate_stride_t, dgate_stride_h;
+  float *dweight, *dbias;    /* the shapes of weight and bias, written; each set if and only if that is */
+  void *workspace;           /* ccq_group_norm_backward_workspace_bytes(p) bytes, or NULL when that is 0 */
+  size_t workspace_bytes;
+} ccq_group_norm_bwd_params;
+
+/* Gradient of ccq_group_norm; weight and bias are summed over tokens (and groups that share them) in a
+ * fixed order: two calls give the same bits.  Returns a ccq_status. */
+int ccq_group_norm_backward(const ccq_group_norm_bwd_params *p, void *hip_stream);
+size_t ccq_group_norm_backward_workspace_bytes(const ccq_group_norm_bwd_params *p);
+
+/* Arguments of ccq_logits_adjust.  Zero-initialise, then fill in. */
+typedef struct {
+  int32_t dtype;             /* ccq_dtype of logits and out                                         */
+  int32_t R, V;              /* rows (beams of all requests), vocabulary                            */
+  int32_t L;                 /* width of history; 0 with history NULL                               */
+  int32_t n_bias;            /* width of the bias lists, 0 .. 1024; 0 with them NULL                */
+  const void *logits;        /* [R, V], a row every logits_stride elements, anywhere                */
+  int64_t logits_stride;     /* >= V                                                                */
+  const int32_t *history;    /* [R, L] tokens seen; one outside 0 .. V - 1 counts for nothing       */
+  const int32_t *lengths;    /* [R] tokens in each row's history (taken into 0 .. L), or NULL: L     */
+  const int32_t *prompt_lengths; /* [R] how many of them, in front, are the prompt's, or NULL: none  */
+  float repetition, presence, frequency; /* the penalties of every row whose list below is NULL      */
+  const float *repetition_rows, *presence_rows, *frequency_rows; /* [R], or NULL                     */
+  const int32_t *bias_token; /* [R, n_bias]; one outside 0 .. V - 1 counts for nothing              */
+  const float *bias_value;   /* [R, n_bias]; a token that stands in the list twice gets both         */
+  const uint32_t *allowed;   /* [R, ceil(V / 32)]: token v may follow if bit v % 32 of word v / 32 is set;
+                                or NULL: all may                                                     */
+  void *out;                 /* [R, V] dtype, a row every out_stride elements, written; may be logits itself,
+                                with the same stride                                                 */
+  int64_t out_stride;        /* >= V                                                                */
+} ccq_logits_adjust_params;
+
+/*
+ * Logits made ready for a selection (ccq_beam_select) or for sampling.  For token v of a row, which stands
+ * c times in the row's history behind the prompt:
+ *   x = logits[v];  if v stands in the history, prompt or not: x = x > 0 ? x / repetition : x repetition;
+ *   x = x - frequency c - presence [c > 0] + the sum of v's biases, in the list's order;
+ *   out[v] = x if v is allowed, else -INFINITY (whatever x is).
+ * The arithmetic is fp32; the result is rounded once; a logit that nothing touches stays as it is, a NaN
+ * or infinity too.  repetition must be above 0 (a row's own is taken as it stands).  V <= 2^24, L <= 2^24,
+ * R (V / 4096 + 1) < 2^24 (CCQ_ERR_UNSUPPORTED beyond).  Returns a ccq_status.
+ */
+int ccq_logits_adjust(const ccq_logits_adjust_params *p, void *hip_stream);
+
 #ifdef __cplusplus
 }
 #endif
