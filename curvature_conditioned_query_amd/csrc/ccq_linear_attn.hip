@@ -16,8 +16,8 @@
 //            the tiles, weighted by e^{B_i - B_j} element by element, are the B operand of
 //   near     out^T += Z^T P^T as they lie in the registers;
 //   far      out^T += a_i St X^T with the state's copy St in LDS, in the inputs' type;
-//   update   S^T = e^{B_L} S^T + Y^T (b z), b z as a pair of bf16 (hi + lo) where the inputs have 16 bits, so that
-//            states are right to 2^-16.
+//   update   S^T = e^{B_L} S^T + Y^T (b z), b z as a sum of three bf16 where the inputs have 16 bits: what enters a
+//            state, which later tokens and calls build on, is right to 2^-24.
 // Weights of pairs, not e^{B_i} e^{-B_j}: nothing leaves fp32's range whatever the decay.  Running sums are
 // formed in 64 bits and kept as two floats, in units of log 2.
 #include "ccq_prefill_common.hpp"
@@ -114,7 +114,7 @@ __device__ __forceinline__ void store_out(void* p, int64_t at, const f32x4& v, i
 template <typename T, int DX, bool SPLIT>
 struct Smem {
   static constexpr int PY = DX + 16 / (int)sizeof(T), PZ = kSlice + 16 / (int)sizeof(T);
-  static constexpr int NH = sizeof(T) == 2 ? 2 : 1;             // parts of b z
+  static constexpr int NH = sizeof(T) == 2 ? 3 : 1;             // parts of b z
   static constexpr int NS = sizeof(T) == 2 && SPLIT ? 2 : 1;    // parts of the state's copy
   T Y[2][kL][PY];
   T Z[2][kL][PZ];
@@ -361,15 +361,18 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
       float z[8];
       if constexpr (sizeof(T) == 2) {
         const bf16x8 v = *reinterpret_cast<const bf16x8*>(&sm.Z[buf][row][col]);
-        bf16x8 hi, lo;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          z[e] = bw == 0.f ? 0.f : (float)v[e] * bw;
-          hi[e] = (__bf16)z[e];
-          lo[e] = (__bf16)(z[e] - (float)hi[e]);
+        for (int e = 0; e < 8; ++e) z[e] = bw == 0.f ? 0.f : (float)v[e] * bw;
+#pragma unroll
+        for (int p = 0; p < SM::NH; ++p) {
+          bf16x8 part;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            part[e] = (__bf16)z[e];
+            z[e] -= (float)part[e];
+          }
+          *reinterpret_cast<bf16x8*>(&sm.Zw[p][row][col]) = part;
         }
-        *reinterpret_cast<bf16x8*>(&sm.Zw[0][row][col]) = hi;
-        *reinterpret_cast<bf16x8*>(&sm.Zw[SM::NH - 1][row][col]) = lo;
       } else {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {

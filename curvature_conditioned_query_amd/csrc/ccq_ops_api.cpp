@@ -294,6 +294,8 @@ int la_inputs(const ccq_linear_attn_params& p) {
     const int st = check_layout(l, n, E, false);
     if (st != CCQ_OK) return st;
   }
+  // gates are read one by one: a slice of another tensor will do
+  if (reinterpret_cast<uintptr_t>(p.log_alpha) % esize(p.gate_dtype) != 0) return CCQ_ERR_MISALIGNED;
   if (p.log_alpha && !strides_in_range(n.nb, n.nb > 1 ? p.la_stride_b : 0, n.nt, p.la_stride_t, p.H, p.la_stride_h))
     return CCQ_ERR_INVALID_ARG;
   return CCQ_OK;
@@ -319,12 +321,13 @@ int validate_la(const ccq_linear_attn_params* p) {
                      {p->q, extent_of(la_q(*p), n, E)},
                      {p->k, extent_of(la_k(*p), n, E)},
                      {p->v, extent_of(la_v(*p), n, E)},
-                     {p->log_alpha, la_gate_extent(*p, n)},
                      {p->lengths, (size_t)p->B * 4},
                      {p->offsets, (size_t)p->B * 4 + 4},
                      {p->S0 == p->S_out ? nullptr : p->S0, la_state(*p)}};
   if (any_misaligned(r)) return CCQ_ERR_MISALIGNED;
-  if (written_overlaps(r, 10, 3)) return CCQ_ERR_INVALID_ARG;
+  if (written_overlaps(r, 9, 3)) return CCQ_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i)
+    if (overlap(r[i], {p->log_alpha, la_gate_extent(*p, n)})) return CCQ_ERR_INVALID_ARG;
   return CCQ_OK;
 }
 
@@ -357,7 +360,6 @@ int validate_la_backward(const ccq_linear_attn_bwd_params* p) {
                      {f.q, extent_of(la_q(f), n, E)},
                      {f.k, extent_of(la_k(f), n, E)},
                      {f.v, extent_of(la_v(f), n, E)},
-                     {f.log_alpha, la_gate_extent(f, n)},
                      {f.lengths, (size_t)f.B * 4},
                      {f.offsets, (size_t)f.B * 4 + 4},
                      {f.S0, la_state(f)},
@@ -368,9 +370,11 @@ int validate_la_backward(const ccq_linear_attn_bwd_params* p) {
   for (int i = 0; i < 3; ++i)
     for (int j = i + 1; j < 3; ++j)
       if (overlap({g[i].p, g[i].d * GE}, {g[j].p, g[j].d * GE})) return CCQ_ERR_INVALID_ARG;
-  for (int i = 0; i < 6; ++i)
-    for (int j = i < 3 ? 3 : i + 1; j < 15; ++j)
+  for (int i = 0; i < 6; ++i) {
+    for (int j = i < 3 ? 3 : i + 1; j < 14; ++j)
       if (overlap(r[i], r[j])) return CCQ_ERR_INVALID_ARG;
+    if (overlap(r[i], {f.log_alpha, la_gate_extent(f, n)})) return CCQ_ERR_INVALID_ARG;
+  }
   return CCQ_OK;
 }
 

@@ -529,7 +529,7 @@ typedef struct {
   int64_t q_stride_b, q_stride_t, q_stride_h; /* >= 0                                               */
   int64_t k_stride_b, k_stride_t, k_stride_h;
   int64_t v_stride_b, v_stride_t, v_stride_h;
-  const void *log_alpha;     /* [B, T, H], strides below, any (0: a gate for each head, say); or NULL: no decay */
+  const void *log_alpha;     /* [B, T, H], strides below, any (0: a gate for each head, say), starting anywhere; or NULL: no decay */
   int64_t la_stride_b, la_stride_t, la_stride_h; /* >= 0                                            */
   const int32_t *lengths;    /* [B] tokens of each sequence (taken into 0 .. T), or NULL            */
   const int32_t *offsets;    /* [B + 1], or NULL.  Packed sequences: the tensors have one row for each of
@@ -550,12 +550,12 @@ typedef struct {
  *   S_t = alpha_t S_{t-1} + v_t k_t^T,  alpha_t = exp(log_alpha_t),  o_t = scale S_t q_t,
  * the write rule of the read step with a scalar in the place of the decay per key channel, and no
  * cleaning of the query.  A prompt is worked on in chunks of 64 tokens; T = 1 with S_out == S0 is the
- * serving step.  The state is fp32 throughout (with 16-bit inputs what is added to it is right to 2^-16 of
- * each term); o is rounded once more for the chunk's scores and for the state, in 16 bits, where the
- * inputs have 16.  Gates are taken as they are, above 1 too, as long as the product of consecutive gates
- * stays inside the range of fp32; where alpha_t is 0 (log_alpha_t below about -104) the state before
- * token t is dropped, whatever it holds.  An input that is infinite or NaN may reach the outputs of all
- * tokens of its 64-token chunk, earlier ones too; what stands in rows of no token reaches nothing.
+ * serving step.  The state is fp32 throughout.  Where the inputs have 16 bits and T > 8, a chunk's scores
+ * and the state are rounded to 16 bits once on the way to o.  Gates are taken as they are, above 1 too, as
+ * long as the product of consecutive gates stays inside the range of fp32; where alpha_t is 0
+ * (log_alpha_t below about -104) the state before token t is dropped, whatever it holds.  An input that is
+ * infinite or NaN may reach the outputs of all tokens of its 64-token chunk, earlier ones too; what stands
+ * in rows of no token reaches nothing.
  * Long sequences with few heads are cut along T and the pieces joined in a fixed order: two calls give
  * the same bits.  B H <= 2^20, B T <= 2^30, rows < 2^31 (CCQ_ERR_UNSUPPORTED beyond, and for other d).
  * Returns a ccq_status.
