@@ -25,7 +25,7 @@
 namespace ccq {
 namespace {
 
-constexpr int kThreads = 256, kWaves = 4;
+constexpr int kThreads = 256;
 constexpr int kSlice = 32;             // columns of z that a workgroup owns
 constexpr double kLog2e = 1.4426950408889634074;
 constexpr float kGateFloor = -1.0e4f;  // log decays below count as this: e^-10000 is 0, sums of 64 stay exact enough
@@ -51,7 +51,7 @@ struct Role {
   int s_i, s_j;
   float* s_out;                   // state behind, [dz][dx] rows, or null
   const float* dot;               // matrix whose product with the state behind is summed (strides s_i, s_j), or null
-  float* dot_out;                 // [chains][slices]
+  float* dot_out;                 // [chains][slices][4]
   float in_scale, out_scale;
   int reverse, slices, dz;
   float* slots;                   // summaries of segments, or null with one segment
@@ -94,13 +94,18 @@ __device__ __forceinline__ T* rows_of(const void* p, const Strides& s, int share
   return const_cast<T*>(static_cast<const T*>(p)) + (a.offsets ? sp.row0 * s.t : b * s.b) + (h / share) * s.h;
 }
 
-// log2 of the decay of one token.
-__device__ __forceinline__ double gate_of(const Args& a, int64_t at) {
-  if (a.la == nullptr) return 0.0;
-  float g = a.gate_bf16 ? (float)static_cast<const __bf16*>(a.la)[at] : static_cast<const float*>(a.la)[at];
+// log2 of the decay of one token, from its bits as stored: a load that is not waited for until its value is needed.
+__device__ __forceinline__ unsigned gate_bits(const Args& a, int64_t at) {
+  if (a.la == nullptr) return 0u;
+  if (a.gate_bf16) return static_cast<const uint16_t*>(a.la)[at];
+  return static_cast<const uint32_t*>(a.la)[at];
+}
+__device__ __forceinline__ double gate_value(const Args& a, unsigned bits) {
+  float g = __builtin_bit_cast(float, a.gate_bf16 ? bits << 16 : bits);
   g = g < kGateFloor ? kGateFloor : g;  // NaN stays
   return (double)g * kLog2e;
 }
+__device__ __forceinline__ double gate_of(const Args& a, int64_t at) { return gate_value(a, gate_bits(a, at)); }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -111,21 +116,7 @@ __device__ __forceinline__ void store_out(void* p, int64_t at, const f32x4& v, i
   else *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(p) + at) = to_bf16x4(v);
 }
 
-template <typename T, int DX, bool SPLIT>
-struct Smem {
-  static constexpr int PY = DX + 16 / (int)sizeof(T), PZ = kSlice + 16 / (int)sizeof(T);
-  static constexpr int NH = sizeof(T) == 2 ? 3 : 1;             // parts of b z
-  static constexpr int NS = sizeof(T) == 2 && SPLIT ? 2 : 1;    // parts of the state's copy
-  T Y[2][kL][PY];
-  T Z[2][kL][PZ];
-  T Zw[NH][kL][PZ];
-  T St[NS][kSlice][PY];
-  float bh[2][kL], bl[2][kL];  // running sums, as two floats
-  float aw[2][kL], bw[2][kL];  // weights of the state for each query, of each key in the state
-  float dec[2];
-  float red[kWaves];
-};
-
+// The wave's rows as MFMA operands: lane (g, l) row l, entries 8 g .. of every 32.
 template <typename T, int DX>
 __device__ __forceinline__ void load_x(Frag<T> (&f)[DX / 32], const T* p) {
 #pragma unroll
@@ -143,291 +134,293 @@ __device__ __forceinline__ void load_x(Frag<T> (&f)[DX / 32], const T* p) {
   }
 }
 
-// Rows 0 .. n - 1 (COLS entries every `step`) of a chunk straight into an LDS tile of pitch P, rows n .. 63 as row 0
-// (their weights are 0).  The caller waits.
-template <typename T, int COLS, int P>
-__device__ __forceinline__ void load_rows(T (*dst)[P], const T* src, int64_t step, int n, int w, int lane) {
-  constexpr int U = P * (int)sizeof(T) / 16, DU = COLS * (int)sizeof(T) / 16, EPU = 16 / (int)sizeof(T);
-  const unsigned base = (unsigned)(uintptr_t)(__attribute__((address_space(3))) T*)&dst[0][0];
-#pragma unroll
-  for (int m = 0; m < (U + kWaves - 1) / kWaves; ++m) {
-    const int j = w + kWaves * m;
-    if (j >= U) break;
-    const int u = 64 * j + lane, row = u / U, slot = u - row * U;
-    const T* p = src + (slot < DU && row < n ? row * step + slot * EPU : 0);
-    const unsigned m0 = __builtin_amdgcn_readfirstlane(base + 1024u * (unsigned)j);
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(m0), "v"(p) : "memory", "m0");
-  }
+template <typename T, int DX, bool SPLIT, bool SUMMARY>
+struct Smem {
+  static constexpr int PY = DX + 16 / (int)sizeof(T), PZ = kSlice + 16 / (int)sizeof(T);
+  static constexpr int AHEAD = sizeof(T) == 2 ? 2 : 1;          // chunks between a load and its use
+  static constexpr int NY = AHEAD + 1, NZ = AHEAD + 2;          // tiles held of y and z
+  static constexpr int NH = sizeof(T) == 2 ? 3 : 1;             // parts of b z
+  static constexpr int NS = sizeof(T) == 2 && SPLIT ? 2 : 1;    // parts of the state's copy
+  T Y[NY][kL][PY];
+  T Z[NZ][kL][PZ];
+  T Zw[2][NH][kL][PZ];
+  T St[SUMMARY ? 1 : 2][NS][SUMMARY ? 1 : kSlice][PY];
+  // Of each token: its running sum as two floats, the weight of the state before the chunk for it, its weight in
+  // the state behind, and e^(its sum to the end of its 16 tokens), or from their beginning.
+  float bh[3][kL], bl[3][kL], aw[3][kL], bw[3][kL], cf[3][kL];
+  float dec[3];
+};
+
+// A wave's running sum of 64-bit values, in registers alone.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const unsigned lo = (unsigned)__builtin_amdgcn_update_dpp(0, (int)(unsigned)u, CTRL, ROWS, 0xf, true);
+  const unsigned hi = (unsigned)__builtin_amdgcn_update_dpp(0, (int)(unsigned)(u >> 32), CTRL, ROWS, 0xf, true);
+  return x + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_running(double x) {
+  x = dpp_add<0x111, 0xf>(x);  // by 1, 2, 4 and 8 within 16 lanes
+  x = dpp_add<0x112, 0xf>(x);
+  x = dpp_add<0x114, 0xf>(x);
+  x = dpp_add<0x118, 0xf>(x);
+  x = dpp_add<0x142, 0xa>(x);  // lane 15 to the next 16, then lane 31 to the upper half
+  return dpp_add<0x143, 0xc>(x);
 }
 
-// The weights of a chunk's 64 tokens into buffer `buf`; one wave, lane t token t, g its log2 decay (0 behind the end).
+// The weights of a chunk's 64 tokens into buffer `buf`; one wave, lane t token t, g its log2 decay (0 behind the
+// end).  Returns the chunk's log2 decay.
 template <bool REV, typename SM>
 __device__ __forceinline__ double form_gates(SM& sm, int buf, double g, bool live, float in_scale, int lane) {
-  double s = g;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const double up = __shfl_up(s, off, 64);
-    if (lane >= off) s += up;
-  }
-  const double all = __shfl(s, 63, 64);
+  const double s = wave_running(g), all = __shfl(s, 63, 64), near = __shfl(s, REV ? lane & 48 : lane | 15, 64);
   const float hi = (float)s;
   sm.bh[buf][lane] = hi;
   sm.bl[buf][lane] = (float)(s - (double)hi);
   const float up = exp2_fast((float)s), down = exp2_fast((float)(all - s));
   sm.aw[buf][lane] = REV ? down : up;
   sm.bw[buf][lane] = live ? (REV ? up : down) * in_scale : 0.f;
+  sm.cf[buf][lane] = live ? exp2_fast((float)(REV ? s - near : near - s)) * in_scale : 0.f;
   if (lane == 0) sm.dec[buf] = exp2_fast((float)all);
   return all;
 }
 
-// One chain, slice and segment.  SUMMARY: the state alone, from zeros, into the segment's slot.
-template <typename T, int DX, bool SPLIT, bool REV, bool SUMMARY>
-__device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, int slice, int seg, Smem<T, DX, SPLIT>& sm) {
-  using SM = Smem<T, DX, SPLIT>;
-  constexpr int NX = DX / 16 / kWaves, NZ = kSlice / 16, NK = DX / 32;
-  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l = lane & 15;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int b = chain / a.H, h = chain - b * a.H;
-  const Span sp = span_of(a, b);
-  const int nc = (sp.len + kL - 1) / kL;
-  const int c_lo = seg * a.chunks_per_segment, c_hi = min(nc, c_lo + a.chunks_per_segment), n = c_hi - c_lo;
-  constexpr int kGateWave = REV ? kWaves - 1 : 0;  // the wave with the fewest score tiles
-  const size_t mat = (size_t)ro.dz * DX;
-
-  const T* xb = rows_of<T>(ro.x, ro.xs, ro.x_share, a, sp, b, h);
-  const T* yb = rows_of<T>(ro.y, ro.ys, ro.y_share, a, sp, b, h);
-  const T* zb = rows_of<T>(ro.z, ro.zs, ro.z_share, a, sp, b, h) + slice * kSlice;
-  const T* wb = ro.r ? rows_of<T>(ro.w, ro.ws, ro.w_share, a, sp, b, h) + slice * kSlice : nullptr;
-  const int64_t la0 = (a.offsets ? sp.row0 * a.ls.t : b * a.ls.b) + h * a.ls.h;
-  const int64_t ob = (a.offsets ? sp.row0 * ro.os.t : b * ro.os.b) + h * ro.os.h + slice * kSlice;
-
-  // a state's place in the accumulators' order: 16 bytes a lane
-  auto slot_of = [&](int s) {
-    return ro.slots + (((size_t)chain * a.segments + s) * ro.slices + slice) * (kSlice * DX) + (size_t)w * NX * NZ * 256 + lane * 4;
-  };
-  f32x4 S[NX][NZ];
-  auto take_in = [&]() {
+// A chunk's rows of COLS entries straight into an LDS tile of pitch P by four waves, rows behind the sequence's end as
+// row 0 (their weights are 0).  Each lane's places are worked out once; unit j of the tile belongs to wave
+// FLIP ? 3 - j % 4 : j % 4, which has COUNT of them.  The loads are not the compiler's: the caller waits.
+template <typename T, int COLS, int P, bool FLIP>
+struct RowLoads {
+  static constexpr int U = P * (int)sizeof(T) / 16, DU = COLS * (int)sizeof(T) / 16, M = (U + 3) / 4;
+  unsigned off[M];
+  static constexpr int count(int w) { return (U - (FLIP ? 3 - w : w) + 3) / 4; }
+  __device__ __forceinline__ RowLoads(int w, int lane, int64_t step) {
 #pragma unroll
-    for (int x = 0; x < NX; ++x)
-#pragma unroll
-      for (int z = 0; z < NZ; ++z) {
-        S[x][z] = zero4();
-        if (ro.s_in) {
-          const float* p = ro.s_in + chain * mat + (size_t)(slice * kSlice + 16 * z + l) * ro.s_i +
-                           (size_t)(16 * (w * NX + x) + 4 * g) * ro.s_j;
-          if (ro.s_j == 1) S[x][z] = *reinterpret_cast<const f32x4*>(p);
-          else
-#pragma unroll
-            for (int r = 0; r < 4; ++r) S[x][z][r] = p[(size_t)r * ro.s_j];
-        }
-      }
-  };
-  auto store_slot = [&](int s) {
-    float* p = slot_of(s);
-#pragma unroll
-    for (int x = 0; x < NX; ++x)
-#pragma unroll
-      for (int z = 0; z < NZ; ++z) *reinterpret_cast<f32x4*>(p + (x * NZ + z) * 256) = S[x][z];
-  };
-  auto decay_by = [&](float d) {
-#pragma unroll
-    for (int x = 0; x < NX; ++x)
-#pragma unroll
-      for (int z = 0; z < NZ; ++z)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) S[x][z][r] = d == 0.f ? 0.f : S[x][z][r] * d;
-  };
-
-  if constexpr (SUMMARY) {
-    if (a.snapshot && seg == 0) {  // the state before, which the last segment may write over
-      take_in();
-      store_slot(a.segments - 1);
+    for (int m = 0; m < M; ++m) {
+      const int u = 64 * (4 * m + (FLIP ? 3 - w : w)) + lane, row = u / U, slot = u - row * U;
+      off[m] = slot < DU ? (unsigned)row * (unsigned)(step * (int)sizeof(T)) + 16u * slot : 0u;
     }
-    if (n <= 0) return;
+  }
+  __device__ __forceinline__ void load(T (*dst)[P], const T* src, int live, int w, int lane) const {
+    const unsigned base = (unsigned)(uintptr_t)(__attribute__((address_space(3))) T*)&dst[0][0];
 #pragma unroll
-    for (int x = 0; x < NX; ++x)
-#pragma unroll
-      for (int z = 0; z < NZ; ++z) S[x][z] = zero4();
+    for (int m = 0; m < M; ++m) {
+      const int j = 4 * m + (FLIP ? 3 - w : w);
+      if (j >= U) break;
+      unsigned o = off[m];
+      if (live < kL) o = (64 * j + lane) / U < live ? o : 0u;
+      const unsigned m0 = __builtin_amdgcn_readfirstlane(base + 1024u * (unsigned)j);
+      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m0), "v"(o), "s"(src) : "memory", "m0");
+    }
+  }
+};
+
+// Columns of a row-major LDS tile as an MFMA operand in the order of an accumulator pair (tr_frag_acc), from the
+// lane's own place in the tile: what is added to it is known at compile time.
+template <typename T>
+__device__ __forceinline__ int tr_place(int pitch, int lane) {
+  const int g = lane >> 4, i = lane & 15;
+  return sizeof(T) == 2 ? (4 * g + (i >> 2)) * pitch + 4 * (i & 3) : 4 * g * pitch + i;
+}
+template <typename T, int PITCH>
+__device__ __forceinline__ Frag<T> tr_at(const T* p) {
+  Frag<T> f;
+  if constexpr (sizeof(T) == 2) {
+    const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(p));
+    const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(p + 16 * PITCH));
+    f.v = bf16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   } else {
-    if (ro.zero_tail && a.offsets == nullptr) {  // rows of no token
-      const int last = seg == a.segments - 1 ? a.T : min(a.T, (c_lo + a.chunks_per_segment) * kL);
-      for (int t = max(sp.len, c_lo * kL) + (tid >> 3); t < last; t += kThreads / 8)
-        store_out<T>(ro.out, ob + (int64_t)t * ro.os.t + 4 * (tid & 7), zero4(), ro.out_f32);
-    }
-    if (n <= 0 && !(nc == 0 && seg == 0)) return;
-    // the state before the segment: the one before the sequence, then the segments between
-    const int nseg = (nc + a.chunks_per_segment - 1) / a.chunks_per_segment;
-    if (a.snapshot) {
-      const float* p = slot_of(a.segments - 1);
 #pragma unroll
-      for (int x = 0; x < NX; ++x)
+    for (int e = 0; e < 8; ++e) f.v[e] = p[(16 * (e >> 2) + (e & 3)) * PITCH];
+  }
+  return f;
+}
+// Rows alike (lds_frag in order): lane (g, l) row l, entries 8 g .. 8 g + 7.
+template <typename T>
+__device__ __forceinline__ int row_place(int pitch, int lane) { return (lane & 15) * pitch + 8 * (lane >> 4); }
+template <typename T>
+__device__ __forceinline__ Frag<T> row_at(const T* p) {
+  Frag<T> f;
+  if constexpr (sizeof(T) == 2) {
+    f.v = *reinterpret_cast<const bf16x8*>(p);
+  } else {
+    const f32x4 lo = *reinterpret_cast<const f32x4*>(p), hi = *reinterpret_cast<const f32x4*>(p + 4);
 #pragma unroll
-        for (int z = 0; z < NZ; ++z) S[x][z] = *reinterpret_cast<const f32x4*>(p + (x * NZ + z) * 256);
-    } else {
-      take_in();
-    }
-    for (int i = REV ? nseg - 1 : 0; REV ? i > seg : i < seg; i += REV ? -1 : 1) {
-      decay_by(exp2_fast((float)ro.slot_log[(size_t)chain * a.segments + i]));
-      const float* p = slot_of(i);
-#pragma unroll
-      for (int x = 0; x < NX; ++x)
-#pragma unroll
-        for (int z = 0; z < NZ; ++z) S[x][z] += *reinterpret_cast<const f32x4*>(p + (x * NZ + z) * 256);
+    for (int e = 0; e < 4; ++e) {
+      f.v[e] = lo[e];
+      f.v[4 + e] = hi[e];
     }
   }
+  return f;
+}
 
-  auto store_copy = [&]() {
+template <int N>
+__device__ __forceinline__ void vm_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+template <typename T>
+struct Raw4 {
+  typedef bf16x4 type;
+};
+template <>
+struct Raw4<float> {
+  typedef f32x4 type;
+};
+
+template <typename T>
+__device__ __forceinline__ T* uniform_ptr(T* p) {
+  const uint64_t u = reinterpret_cast<uint64_t>(p);
+  return reinterpret_cast<T*>((uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((int)(u >> 32)) << 32 |
+                              (unsigned)__builtin_amdgcn_readfirstlane((int)u));
+}
+
+// The gates of a walk's chunks, by one wave: formed two chunks ahead, loaded three.
+template <bool REV, typename SM>
+struct Gates {
+  const Args& a;
+  SM& sm;
+  int64_t la0;
+  int len, c_lo, c_hi, lane;
+  float in_scale;
+  double total;
+  unsigned ahead;
+  __device__ __forceinline__ int token(int it) const { return (REV ? c_hi - 1 - it : c_lo + it) * kL + lane; }
+  __device__ __forceinline__ unsigned load(int it) const {
+    const int t = token(min(it, c_hi - c_lo - 1));
+    return gate_bits(a, la0 + (int64_t)min(t, len - 1) * a.ls.t);
+  }
+  __device__ __forceinline__ void form(int it, unsigned bits) {
+    if (it >= c_hi - c_lo) return;
+    const bool live = token(it) < len;
+    total += form_gates<REV>(sm, it % 3, live ? gate_value(a, bits) : 0.0, live, in_scale, lane);
+  }
+  __device__ __forceinline__ Gates(const Args& a, const Role& ro, SM& sm, const Span& sp, int b, int h, int c_lo, int c_hi, int lane)
+      : a(a), sm(sm), la0((a.offsets ? sp.row0 * a.ls.t : b * a.ls.b) + h * a.ls.h), len(sp.len), c_lo(c_lo), c_hi(c_hi), lane(lane),
+        in_scale(ro.in_scale), total(0.0) {
+    const unsigned g0 = load(0), g1 = load(1);
+    ahead = load(2);
+    form(0, g0);
+    form(1, g1);
+  }
+  __device__ __forceinline__ void next(int it) {
+    const unsigned now = ahead;
+    ahead = load(it + 3);
+    form(it + 2, now);
+  }
+};
+
+// Wave W of a walk's outputs: queries 16 W .. 16 W + 15 of every chunk.
+template <typename T, int DX, bool SPLIT, bool REV, int W>
+__device__ __forceinline__ void walk_outputs(const Args& a, const Role& ro, int chain, int slice, const Span& sp, int c_lo, int c_hi, int lane,
+                                             Smem<T, DX, SPLIT, false>& sm) {
+  using SM = Smem<T, DX, SPLIT, false>;
+  typedef typename Raw4<T>::type R4;
+  constexpr int NZ = kSlice / 16, NK = DX / 32, AH = SM::AHEAD, T0 = REV ? W : 0, T1 = REV ? 3 : W;
+  constexpr bool kGateWave = W == (REV ? 3 : 0);  // the wave with the fewest score tiles
+  const int g = lane >> 4, l = lane & 15, n = c_hi - c_lo;
+  const int b = chain / a.H, h = chain - b * a.H;
+  auto chunk_at = [&](int it) { return REV ? c_hi - 1 - it : c_lo + it; };
+  const T* xb = uniform_ptr(rows_of<T>(ro.x, ro.xs, ro.x_share, a, sp, b, h));
+  const T* wb = ro.r ? uniform_ptr(rows_of<T>(ro.w, ro.ws, ro.w_share, a, sp, b, h) + slice * kSlice) : nullptr;
+  const int64_t ob = (a.offsets ? sp.row0 * ro.os.t : b * ro.os.b) + h * ro.os.h + slice * kSlice;
+  const int oe = sizeof(T) == 4 || ro.out_f32 ? 4 : 2;
+  char* outb = uniform_ptr(static_cast<char*>(ro.out) + ob * oe);
+  constexpr unsigned kElem = sizeof(T);
+  const unsigned own = 16 * W + l;
+  const unsigned x_off = own * (unsigned)(ro.xs.t * (int)sizeof(T)) + 8 * g * kElem;
+  const unsigned w_off = own * (unsigned)(ro.ws.t * (int)sizeof(T)) + 4 * g * kElem;
+  const unsigned o_off = own * (unsigned)(ro.os.t * oe) + 4 * g * oe;
+  Frag<T> X[AH + 1][NK];
+  R4 wr[AH + 1][NZ];
+  f32x4 out[NZ];
+  float r_out = 0.f;
+  // the wave's own rows of a chunk, the chunk's first where the sequence has ended
+  auto load_own = [&](int k, int it) {
+    const int c = chunk_at(min(it, n - 1));
+    const bool on = (int)own < sp.len - c * kL;
+    load_x<T, DX>(X[k], reinterpret_cast<const T*>(reinterpret_cast<const char*>(xb + (int64_t)c * kL * ro.xs.t) + (on ? x_off : 8u * g * kElem)));
+    if (ro.r) {
+      const char* p = reinterpret_cast<const char*>(wb + (int64_t)c * kL * ro.ws.t) + (on ? w_off : 4u * g * kElem);
 #pragma unroll
-    for (int x = 0; x < NX; ++x)
+      for (int z = 0; z < NZ; ++z) wr[k][z] = *reinterpret_cast<const R4*>(p + 16 * z * kElem);
+    }
+  };
+  auto flush = [&](int it) {  // a chunk's outputs, a chunk later: the stores have time
+    const int c = chunk_at(it);
+    if ((int)own < sp.len - c * kL) {
+      char* p = outb + (int64_t)c * kL * ro.os.t * oe;
 #pragma unroll
       for (int z = 0; z < NZ; ++z) {
-        st4<T>(&sm.St[0][16 * z + l][16 * (w * NX + x) + 4 * g], S[x][z]);
-        if constexpr (SM::NS == 2) {
-          f32x4 lo;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) lo[r] = S[x][z][r] - (float)(__bf16)S[x][z][r];
-          st4<T>(&sm.St[SM::NS - 1][16 * z + l][16 * (w * NX + x) + 4 * g], lo);
-        }
+        if (sizeof(T) == 4 || ro.out_f32) *reinterpret_cast<f32x4*>(p + (o_off + 64u * z)) = out[z];
+        else *reinterpret_cast<bf16x4*>(p + (o_off + 32u * z)) = to_bf16x4(out[z]);
       }
+      if (ro.r && g == 0) ro.r[((size_t)slice * a.chains + chain) * a.T + c * kL + own] = r_out;
+    }
   };
-  auto chunk_at = [&](int it) { return REV ? c_hi - 1 - it : c_lo + it; };
-  auto issue = [&](int it) {
-    const int c = chunk_at(it), live = min(kL, sp.len - c * kL);
-    load_rows<T, DX, SM::PY>(sm.Y[it & 1], yb + (int64_t)c * kL * ro.ys.t, ro.ys.t, live, w, lane);
-    load_rows<T, kSlice, SM::PZ>(sm.Z[it & 1], zb + (int64_t)c * kL * ro.zs.t, ro.zs.t, live, w, lane);
-  };
-  // the wave's own row of a chunk, its first where the sequence has ended
-  auto own_row = [&](int it) {
-    const int t = chunk_at(it) * kL + 16 * w + l;
-    return (int64_t)(t < sp.len ? t : chunk_at(it) * kL);
-  };
-  auto gate_at = [&](int it) {
-    const int t = chunk_at(it) * kL + lane;
-    return it < n && t < sp.len ? gate_of(a, la0 + (int64_t)t * a.ls.t) : 0.0;
-  };
-  double total = 0.0, g_next = 0.0;
-  Frag<T> X[NK], Xn[NK];
-  f32x4 wn[NZ], out[NZ];
-  float r_out = 0.f;
-  int out_chunk = -1;
-  auto load_own = [&](int it) {
-    if constexpr (!SUMMARY) {
-      const int64_t t = own_row(it);
-      load_x<T, DX>(Xn, xb + t * ro.xs.t + 8 * g);
-      if (ro.r) {
 #pragma unroll
-        for (int z = 0; z < NZ; ++z) wn[z] = ld4(wb + t * ro.ws.t + 16 * z + 4 * g);
-      }
-    }
-  };
-  auto flush = [&]() {  // the outputs of the chunk before: its stores have a chunk's time
-    const int t = out_chunk * kL + 16 * w + l;
-    if (out_chunk >= 0 && t < sp.len) {
-#pragma unroll
-      for (int z = 0; z < NZ; ++z) store_out<T>(ro.out, ob + (int64_t)t * ro.os.t + 16 * z + 4 * g, out[z], ro.out_f32);
-      if (ro.r && g == 0) ro.r[((size_t)slice * a.chains + chain) * a.T + t] = r_out;
-    }
-  };
-
-  if (n > 0) {
-    issue(0);
-    load_own(0);
-    if (w == kGateWave) {
-      total += form_gates<REV>(sm, 0, gate_at(0), chunk_at(0) * kL + lane < sp.len, ro.in_scale, lane);
-      g_next = gate_at(1);
-    }
-    if constexpr (!SUMMARY) store_copy();
-  }
-  for (int it = 0; it < n; ++it) {
-    const int buf = it & 1;
-    vm_wait_all();
+  for (int i = 0; i < AH; ++i) load_own(i, i);
+  auto body = [&](auto gates) {
     lds_barrier();
-#pragma unroll
-    for (int kk = 0; kk < NK; ++kk) X[kk] = Xn[kk];
-    f32x4 wr[NZ];
-#pragma unroll
-    for (int z = 0; z < NZ; ++z) wr[z] = wn[z];
-    double g_now = g_next;
-    if constexpr (!SUMMARY) flush();
-    if (w == kGateWave) g_next = gate_at(it + 2);
-    if (it + 1 < n) {
-      issue(it + 1);
-      load_own(it + 1);
-    }
-
-    {  // b z, 8 entries a thread
-      const int row = tid / (kSlice / 8), col = 8 * (tid % (kSlice / 8));
-      const float bw = sm.bw[buf][row];
-      float z[8];
-      if constexpr (sizeof(T) == 2) {
-        const bf16x8 v = *reinterpret_cast<const bf16x8*>(&sm.Z[buf][row][col]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] = bw == 0.f ? 0.f : (float)v[e] * bw;
-#pragma unroll
-        for (int p = 0; p < SM::NH; ++p) {
-          bf16x8 part;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            part[e] = (__bf16)z[e];
-            z[e] -= (float)part[e];
-          }
-          *reinterpret_cast<bf16x8*>(&sm.Zw[p][row][col]) = part;
-        }
-      } else {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          f32x4 v = *reinterpret_cast<const f32x4*>(&sm.Z[buf][row][col + 4 * q]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = bw == 0.f ? 0.f : v[e] * bw;
-          *reinterpret_cast<f32x4*>(&sm.Zw[0][row][col + 4 * q]) = v;
-        }
-      }
-    }
-    f32x4 acc[NZ], P[kWaves];
-    if constexpr (!SUMMARY) {
-      // far: the state before the chunk
+    lds_barrier();
+    int yb_at = 0, zb_at = 0, gb = 0;  // it modulo NY, NZ and 3
+    const int place = row_place<T>(SM::PY, lane), z_place = tr_place<T>(SM::PZ, lane);
+    for (int it = 0; it < n; ++it) {
+      load_own(AH, it + AH);
+      const T* st = &sm.St[it & 1][0][0][0] + place;
+      const T* y0 = &sm.Y[yb_at][0][0] + place;
+      const T* z0 = &sm.Z[zb_at][0][0] + z_place;
+      // scores and far (the state before the chunk)
+      f32x4 acc[NZ], P[4];
 #pragma unroll
       for (int z = 0; z < NZ; ++z) acc[z] = zero4();
 #pragma unroll
-      for (int kk = 0; kk < NK; ++kk)
+      for (int t = 0; t < 4; ++t) P[t] = zero4();
+#pragma unroll
+      for (int kk = 0; kk < NK; ++kk) {
+#pragma unroll
+        for (int t = T0; t <= T1; ++t) mma(P[t], row_at<T>(y0 + 16 * t * SM::PY + 32 * kk), X[0][kk]);
 #pragma unroll
         for (int z = 0; z < NZ; ++z)
 #pragma unroll
-          for (int s = 0; s < SM::NS; ++s)
-            mma(acc[z], lds_frag<T, KORD_CONTIG>(&sm.St[s][0][0], SM::PY, 16 * z, 32 * kk, lane), X[kk]);
-      const float aw = sm.aw[buf][16 * w + l];
+          for (int s = 0; s < SM::NS; ++s) mma(acc[z], row_at<T>(st + (s * kSlice + 16 * z) * SM::PY + 32 * kk), X[0][kk]);
+      }
+      if (it > 0) flush(it - 1);
+      const float bh = sm.bh[gb][own], bl = sm.bl[gb][own], aw = sm.aw[gb][own];
 #pragma unroll
-      for (int z = 0; z < NZ; ++z)
+      for (int t = T0; t <= T1; ++t) {
+        if (t == W) {
+          const f32x4 kh = *reinterpret_cast<const f32x4*>(&sm.bh[gb][16 * t + 4 * g]);
+          const f32x4 kl = *reinterpret_cast<const f32x4*>(&sm.bl[gb][16 * t + 4 * g]);
+          const int live = sp.len - chunk_at(it) * kL - 16 * t;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[z][r] = aw == 0.f ? 0.f : acc[z][r] * aw;
-      // scores
-      const float bh = sm.bh[buf][16 * w + l], bl = sm.bl[buf][16 * w + l];
-      const int live = min(kL, sp.len - chunk_at(it) * kL);
+          for (int r = 0; r < 4; ++r) {
+            const int j = 4 * g + r;
+            const float d = REV ? (kh[r] - bh) + (kl[r] - bl) : (bh - kh[r]) + (bl - kl[r]);
+            P[t][r] = (REV ? j >= l && j < live : j <= l) ? P[t][r] * (exp2_fast(d) * ro.in_scale) : 0.f;
+          }
+        } else {
+          // e^(B_i - B_j) in two parts, from the query to the tile's edge and on to the key: both below 1 for decays
+          const int edge = REV ? 16 * t : 16 * t + 15;
+          const float eh = sm.bh[gb][edge], el = sm.bl[gb][edge];
+          const float row = exp2_fast(REV ? (eh - bh) + (el - bl) : (bh - eh) + (bl - el));
+          const f32x4 cf = *reinterpret_cast<const f32x4*>(&sm.cf[gb][16 * t + 4 * g]);
 #pragma unroll
-      for (int t = 0; t < kWaves; ++t) {
-        P[t] = zero4();
-        if (REV ? t < w : t > w) continue;
-        f32x4 s = zero4();
-#pragma unroll
-        for (int kk = 0; kk < NK; ++kk) mma(s, lds_frag<T, KORD_CONTIG>(&sm.Y[buf][0][0], SM::PY, 16 * t, 32 * kk, lane), X[kk]);
-        const f32x4 kh = *reinterpret_cast<const f32x4*>(&sm.bh[buf][16 * t + 4 * g]);
-        const f32x4 kl = *reinterpret_cast<const f32x4*>(&sm.bl[buf][16 * t + 4 * g]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int j = 16 * t + 4 * g + r, i = 16 * w + l;
-          const float d = REV ? (kh[r] - bh) + (kl[r] - bl) : (bh - kh[r]) + (bl - kl[r]);
-          const float e = exp2_fast(d) * ro.in_scale;
-          const bool on = (REV ? j >= i : j <= i) && j < live && e != 0.f;
-          P[t][r] = on ? s[r] * e : 0.f;
+          for (int r = 0; r < 4; ++r) P[t][r] *= row * cf[r];
         }
       }
-    }
-    lds_barrier();
-    if constexpr (!SUMMARY) {
+      if (sm.dec[gb] == 0.f) {  // a gate of 0: the state before counts for nothing, whatever it holds
+#pragma unroll
+        for (int z = 0; z < NZ; ++z)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[z][r] = aw == 0.f ? 0.f : acc[z][r] * aw;
+      } else {
+#pragma unroll
+        for (int z = 0; z < NZ; ++z)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[z][r] *= aw;
+      }
       // near
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        if (REV ? 2 * kk + 1 < w : 2 * kk > w) continue;
+      for (int kk = T0 / 2; kk <= T1 / 2; ++kk) {
         const Frag<T> p = acc_frag<T>(P[2 * kk], P[2 * kk + 1]);
         Frag<T> q;
         if constexpr (SM::NS == 2) {
@@ -440,79 +433,292 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
         }
 #pragma unroll
         for (int z = 0; z < NZ; ++z) {
-          const Frag<T> v = tr_frag_acc<T>(&sm.Z[buf][0][0], SM::PZ, 32 * kk, 16 * z, lane);
+          const Frag<T> v = tr_at<T, SM::PZ>(z0 + 32 * kk * SM::PZ + 16 * z);
           mma(acc[z], v, p);
           if constexpr (SM::NS == 2) mma(acc[z], v, q);
         }
       }
-      float rs = 0.f;
 #pragma unroll
       for (int z = 0; z < NZ; ++z)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          out[z][r] = acc[z][r] * ro.out_scale;
-          rs += out[z][r] * wr[z][r];
-        }
+        for (int r = 0; r < 4; ++r) out[z][r] = acc[z][r] * ro.out_scale;
       if (ro.r) {
+        float rs = 0.f;
+#pragma unroll
+        for (int z = 0; z < NZ; ++z)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) rs += out[z][r] * (float)wr[0][z][r];
         rs += __shfl_xor(rs, 16, 64);
         r_out = rs + __shfl_xor(rs, 32, 64);
       }
-      out_chunk = chunk_at(it);
+      if constexpr (kGateWave) gates.next(it);
+#pragma unroll
+      for (int i = 0; i < AH; ++i) {
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk) X[i][kk] = X[i + 1][kk];
+#pragma unroll
+        for (int z = 0; z < NZ; ++z) wr[i][z] = wr[i + 1][z];
+      }
+      yb_at = yb_at + 1 == SM::NY ? 0 : yb_at + 1;
+      zb_at = zb_at + 1 == SM::NZ ? 0 : zb_at + 1;
+      gb = gb == 2 ? 0 : gb + 1;
+      lds_barrier();
     }
-    // update
-    decay_by(sm.dec[buf]);
+    flush(n - 1);
+  };
+  if constexpr (kGateWave) body(Gates<REV, SM>(a, ro, sm, sp, b, h, c_lo, c_hi, lane));
+  else body(0);
+}
+
+// One chain, slice and segment.  Waves 0 .. 3 form the outputs (SUMMARY: one wave, for the gates alone), the four
+// behind them carry the state, a chunk ahead with b z and two with the loads, so that a chunk has one barrier.
+// SUMMARY: the state alone, from zeros, into the segment's slot.
+template <typename T, int DX, bool SPLIT, bool REV, bool SUMMARY>
+__device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, int slice, int seg, Smem<T, DX, SPLIT, SUMMARY>& sm) {
+  using SM = Smem<T, DX, SPLIT, SUMMARY>;
+  constexpr int NO = SUMMARY ? 1 : 4, NX = DX / 32, AH = SM::AHEAD;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const bool carries = wave >= NO;
+  const int b = chain / a.H, h = chain - b * a.H;
+  Span sp = span_of(a, b);
+  sp.len = __builtin_amdgcn_readfirstlane(sp.len);
+  const int nc = (sp.len + kL - 1) / kL;
+  const int c_lo = seg * a.chunks_per_segment, c_hi = min(nc, c_lo + a.chunks_per_segment), n = c_hi - c_lo;
+  const size_t mat = (size_t)ro.dz * DX;
+  auto chunk_at = [&](int it) { return REV ? c_hi - 1 - it : c_lo + it; };
+  // a state's place in the accumulators' order: 16 bytes a lane
+  const int sw = wave - NO, zt = sw & 1, xt = (sw >> 1) * NX;
+  auto slot_of = [&](int s) {
+    return ro.slots + (((size_t)chain * a.segments + s) * ro.slices + slice) * (kSlice * DX) + (size_t)sw * NX * 256 + lane * 4;
+  };
+
+  if constexpr (!SUMMARY) {
+    if (ro.zero_tail && a.offsets == nullptr) {  // rows of no token
+      const int64_t ob = b * ro.os.b + h * ro.os.h + slice * kSlice;
+      const int last = seg == a.segments - 1 ? a.T : min(a.T, (c_lo + a.chunks_per_segment) * kL);
+      for (int t = max(sp.len, c_lo * kL) + (tid >> 3); t < last; t += 64)
+        store_out<T>(ro.out, ob + (int64_t)t * ro.os.t + 4 * (tid & 7), zero4(), ro.out_f32);
+    }
+  }
+
+  if (carries) {
+    // ---------------------------------------------------------------- the state
+    f32x4 S[NX];  // rows 16 (xt + x) + 4 g + r of x, column 16 zt + l of z
+    auto take_in = [&]() {
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      Frag<T> y[NX];
+      for (int x = 0; x < NX; ++x) {
+        S[x] = zero4();
+        if (ro.s_in) {
+          const float* p = ro.s_in + chain * mat + (size_t)(slice * kSlice + 16 * zt + l) * ro.s_i + (size_t)(16 * (xt + x) + 4 * g) * ro.s_j;
+          if (ro.s_j == 1) S[x] = *reinterpret_cast<const f32x4*>(p);
+          else
 #pragma unroll
-      for (int x = 0; x < NX; ++x) y[x] = tr_frag<T>(&sm.Y[buf][0][0], SM::PY, 32 * kk, 16 * (w * NX + x), lane);
-#pragma unroll
-      for (int z = 0; z < NZ; ++z)
-#pragma unroll
-        for (int p = 0; p < SM::NH; ++p) {
-          const Frag<T> v = tr_frag<T>(&sm.Zw[p][0][0], SM::PZ, 32 * kk, 16 * z, lane);
-#pragma unroll
-          for (int x = 0; x < NX; ++x) mma(S[x][z], y[x], v);
+            for (int r = 0; r < 4; ++r) S[x][r] = p[(size_t)r * ro.s_j];
         }
+      }
+    };
+    auto store_slot = [&](int s) {
+      float* p = slot_of(s);
+#pragma unroll
+      for (int x = 0; x < NX; ++x) *reinterpret_cast<f32x4*>(p + x * 256) = S[x];
+    };
+    auto decay_by = [&](float d) {
+      if (d == 0.f) {  // whatever the state holds
+#pragma unroll
+        for (int x = 0; x < NX; ++x) S[x] = zero4();
+      } else {
+#pragma unroll
+        for (int x = 0; x < NX; ++x)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) S[x][r] *= d;
+      }
+    };
+    if constexpr (SUMMARY) {
+      if (a.snapshot && seg == 0) {  // the state before, which the last segment may write over
+        take_in();
+        store_slot(a.segments - 1);
+      }
+#pragma unroll
+      for (int x = 0; x < NX; ++x) S[x] = zero4();
+    } else {
+      // the state before the segment: the one before the sequence, then the segments between
+      const int nseg = (nc + a.chunks_per_segment - 1) / a.chunks_per_segment;
+      if (a.snapshot) {
+        const float* p = slot_of(a.segments - 1);
+#pragma unroll
+        for (int x = 0; x < NX; ++x) S[x] = *reinterpret_cast<const f32x4*>(p + x * 256);
+      } else {
+        take_in();
+      }
+      for (int i = REV ? nseg - 1 : 0; REV ? i > seg : i < seg; i += REV ? -1 : 1) {
+        decay_by(exp2_fast((float)ro.slot_log[(size_t)chain * a.segments + i]));
+        const float* p = slot_of(i);
+#pragma unroll
+        for (int x = 0; x < NX; ++x) S[x] += *reinterpret_cast<const f32x4*>(p + x * 256);
+      }
     }
-    if constexpr (!SUMMARY) {
-      if (it + 1 < n) store_copy();
+    if (n > 0) {
+      const T* yb = uniform_ptr(rows_of<T>(ro.y, ro.ys, ro.y_share, a, sp, b, h));
+      const T* zb = uniform_ptr(rows_of<T>(ro.z, ro.zs, ro.z_share, a, sp, b, h) + slice * kSlice);
+      const RowLoads<T, DX, SM::PY, false> yl(sw, lane, ro.ys.t);
+      const RowLoads<T, kSlice, SM::PZ, true> zl(sw, lane, ro.zs.t);
+      auto issue_y = [&](int it) {
+        const int c = chunk_at(it);
+        yl.load(sm.Y[it % SM::NY], yb + (int64_t)c * kL * ro.ys.t, sp.len - c * kL, sw, lane);
+      };
+      auto issue_z = [&](int it) {
+        const int c = chunk_at(it);
+        zl.load(sm.Z[it % SM::NZ], zb + (int64_t)c * kL * ro.zs.t, sp.len - c * kL, sw, lane);
+      };
+      // b z of a chunk, 8 entries a thread
+      auto weigh = [&](T (*src)[SM::PZ], T (*dst)[kL][SM::PZ], const float* weights) {
+        const int t = sw * 64 + lane, row = t / (kSlice / 8), col = 8 * (t % (kSlice / 8));
+        const float bw = weights[row];
+        if constexpr (sizeof(T) == 2) {
+          const bf16x8 v = *reinterpret_cast<const bf16x8*>(&src[row][col]);
+          float z[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z[e] = (float)v[e] * bw;
+#pragma unroll
+          for (int p = 0; p < SM::NH; ++p) {
+            bf16x8 part;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              part[e] = (__bf16)z[e];
+              z[e] -= (float)part[e];
+            }
+            *reinterpret_cast<bf16x8*>(&dst[p][row][col]) = part;
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            f32x4 v = *reinterpret_cast<const f32x4*>(&src[row][col + 4 * q]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] *= bw;
+            *reinterpret_cast<f32x4*>(&dst[0][row][col + 4 * q]) = v;
+          }
+        }
+      };
+      auto store_copy = [&](int it) {
+#pragma unroll
+        for (int x = 0; x < NX; ++x) {
+          st4<T>(&sm.St[it & 1][0][16 * zt + l][16 * (xt + x) + 4 * g], S[x]);
+          if constexpr (SM::NS == 2) {
+            f32x4 lo;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) lo[r] = S[x][r] - (float)(__bf16)S[x][r];
+            st4<T>(&sm.St[it & 1][1][16 * zt + l][16 * (xt + x) + 4 * g], lo);
+          }
+        }
+      };
+      issue_z(0);
+      issue_y(0);
+#pragma unroll
+      for (int i = 1; i < AH; ++i)
+        if (i < n) issue_y(i);
+#pragma unroll
+      for (int i = 1; i <= AH; ++i)
+        if (i < n) issue_z(i);
+      if constexpr (!SUMMARY) store_copy(0);
+      vm_wait_all();
+      lds_barrier();
+      weigh(sm.Z[0], sm.Zw[0], sm.bw[0]);
+      lds_barrier();
+      const int y_place = tr_place<T>(SM::PY, lane) + 16 * xt, z_place = tr_place<T>(SM::PZ, lane) + 16 * zt;
+      int yb_at = 0, zb_at = 0, gb = 0;  // it modulo NY, NZ and 3
+      const int64_t y_step = (REV ? -kL : kL) * ro.ys.t, z_step = (REV ? -kL : kL) * ro.zs.t;
+      const T* y_next = yb + (int64_t)chunk_at(0) * kL * ro.ys.t + AH * y_step;
+      const T* z_next = zb + (int64_t)chunk_at(0) * kL * ro.zs.t + (AH + 1) * z_step;
+      for (int it = 0; it < n; ++it) {
+        const bool more = it + AH + 1 < n;
+        const T* y0 = &sm.Y[yb_at][0][0] + y_place;
+        const T* z0 = &sm.Zw[it & 1][0][0][0] + z_place;
+        const float dec = sm.dec[gb];
+        Frag<T> y[2][NX], zf[2][SM::NH];
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+          for (int x = 0; x < NX; ++x) y[kk][x] = tr_at<T, SM::PY>(y0 + 32 * kk * SM::PY + 16 * x);
+#pragma unroll
+          for (int p = 0; p < SM::NH; ++p) zf[kk][p] = tr_at<T, SM::PZ>(z0 + (p * kL + 32 * kk) * SM::PZ);
+        }
+        if (it + AH < n) yl.load(sm.Y[yb_at + AH >= SM::NY ? yb_at + AH - SM::NY : yb_at + AH], y_next, sp.len - chunk_at(it + AH) * kL, sw, lane);
+        if (more) zl.load(sm.Z[zb_at == 0 ? SM::NZ - 1 : zb_at - 1], z_next, sp.len - chunk_at(it + AH + 1) * kL, sw, lane);
+        y_next += y_step;
+        z_next += z_step;
+        decay_by(dec);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+          for (int p = 0; p < SM::NH; ++p)
+#pragma unroll
+            for (int x = 0; x < NX; ++x) mma(S[x], y[kk][x], zf[kk][p]);
+        yb_at = yb_at + 1 == SM::NY ? 0 : yb_at + 1;
+        zb_at = zb_at + 1 == SM::NZ ? 0 : zb_at + 1;
+        gb = gb == 2 ? 0 : gb + 1;
+        if (it + 1 < n) {
+          weigh(sm.Z[zb_at], sm.Zw[(it + 1) & 1], sm.bw[gb]);
+          if constexpr (!SUMMARY) store_copy(it + 1);
+        }
+        // the loads that this chunk has issued may be under way, those before must have landed
+        if (AH == 1 || !more) vm_wait<0>();
+        else if (sw == 0) vm_wait<yl.count(0) + zl.count(0)>();
+        else if (sw == 1) vm_wait<yl.count(1) + zl.count(1)>();
+        else if (sw == 2) vm_wait<yl.count(2) + zl.count(2)>();
+        else vm_wait<yl.count(3) + zl.count(3)>();
+        lds_barrier();
+      }
     }
-    if (w == kGateWave && it + 1 < n)
-      total += form_gates<REV>(sm, buf ^ 1, g_now, chunk_at(it + 1) * kL + lane < sp.len, ro.in_scale, lane);
+    if constexpr (SUMMARY) {
+      if (n > 0) store_slot(seg);
+      return;
+    } else {
+      const bool ends = REV ? seg == 0 : (nc == 0 ? seg == 0 : n > 0 && c_hi == nc);  // the walk's last chunk is here
+      if (!ends) return;
+      float d = 0.f;
+#pragma unroll
+      for (int x = 0; x < NX; ++x) {
+        const int i = slice * kSlice + 16 * zt + l, j = 16 * (xt + x) + 4 * g;
+        if (ro.s_out) *reinterpret_cast<f32x4*>(ro.s_out + chain * mat + (size_t)i * DX + j) = S[x];
+        if (ro.dot)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) d += S[x][r] * ro.dot[chain * mat + (size_t)i * ro.s_i + (size_t)(j + r) * ro.s_j];
+      }
+      if (ro.dot) {
+        d = group_sum<64>(d);
+        if (lane == 0) ro.dot_out[((size_t)chain * ro.slices + slice) * 4 + sw] = d;
+      }
+      return;
+    }
   }
+
+  // ---------------------------------------------------------------- the outputs, and the gates
+  if (n <= 0) return;
   if constexpr (SUMMARY) {
-    store_slot(seg);
-    if (slice == 0 && w == kGateWave && lane == 0) ro.slot_log[(size_t)chain * a.segments + seg] = total;
-    return;
-  }
-  flush();
-  const bool ends = REV ? seg == 0 : (nc == 0 || c_hi == nc);  // this segment has the walk's last chunk
-  if (!ends) return;
-  float d = 0.f;
-#pragma unroll
-  for (int x = 0; x < NX; ++x)
-#pragma unroll
-    for (int z = 0; z < NZ; ++z) {
-      const int i = slice * kSlice + 16 * z + l, j = 16 * (w * NX + x) + 4 * g;
-      if (ro.s_out) *reinterpret_cast<f32x4*>(ro.s_out + chain * mat + (size_t)i * DX + j) = S[x][z];
-      if (ro.dot)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) d += S[x][z][r] * ro.dot[chain * mat + (size_t)i * ro.s_i + (size_t)(j + r) * ro.s_j];
-    }
-  if (ro.dot) {
-    d = group_sum<64>(d);
-    if (lane == 0) sm.red[w] = d;
+    Gates<REV, SM> gates(a, ro, sm, sp, b, h, c_lo, c_hi, lane);
     lds_barrier();
-    if (tid == 0) ro.dot_out[(size_t)chain * ro.slices + slice] = (sm.red[0] + sm.red[1]) + (sm.red[2] + sm.red[3]);
+    lds_barrier();
+    for (int it = 0; it < n; ++it) {
+      gates.next(it);
+      lds_barrier();
+    }
+    if (slice == 0 && lane == 0) ro.slot_log[(size_t)chain * a.segments + seg] = gates.total;
+  } else {
+    if (wave == 0) walk_outputs<T, DX, SPLIT, REV, 0>(a, ro, chain, slice, sp, c_lo, c_hi, lane, sm);
+    else if (wave == 1) walk_outputs<T, DX, SPLIT, REV, 1>(a, ro, chain, slice, sp, c_lo, c_hi, lane, sm);
+    else if (wave == 2) walk_outputs<T, DX, SPLIT, REV, 2>(a, ro, chain, slice, sp, c_lo, c_hi, lane, sm);
+    else walk_outputs<T, DX, SPLIT, REV, 3>(a, ro, chain, slice, sp, c_lo, c_hi, lane, sm);
   }
 }
+
+constexpr int walk_threads(bool summary) { return summary ? 320 : 512; }
 
 // Workgroups of a launch: along x, eight chains at a time, each on an XCD of its own, with the roles and slices of
 // a chain (which share its rows) next to each other; along y the segments.
 template <typename T, int DX, bool SPLIT, bool SUMMARY>
-__global__ __launch_bounds__(kThreads) void la_walk_kernel(Args a) {
-  __shared__ __align__(16) Smem<T, DX, SPLIT> sm;
+__global__ __launch_bounds__(walk_threads(SUMMARY)) void la_walk_kernel(Args a) {
+  __shared__ __align__(16) Smem<T, DX, SPLIT, SUMMARY> sm;
   const int at = blockIdx.x / 8, group = at / a.slots_per_group;
   int k = at - group * a.slots_per_group, role = 0;
   const int chain = 8 * group + (int)(blockIdx.x % 8);
@@ -682,7 +888,7 @@ constexpr int kStepTokens = 8;
 // Segments: enough workgroups for the card, of at least four chunks each.
 void split_of(const ccq_linear_attn_params& p, int groups, int* segments, int* per) {
   const int nc = (p.T - 1) / kL + 1;
-  int want = (512 + groups - 1) / groups;
+  int want = (256 + groups - 1) / groups;
   want = want < 1 ? 1 : (want > 32 ? 32 : want);
   if (want > nc / 4) want = nc / 4 < 1 ? 1 : nc / 4;
   *per = (nc + want - 1) / want;
@@ -752,8 +958,8 @@ char* plan_forward(const ccq_linear_attn_params& p, Args& a, void* workspace) {
 template <typename T, int DX, bool SPLIT>
 hipError_t run_walk(const Args& a, hipStream_t stream) {
   const unsigned groups = (unsigned)((a.chains + 7) / 8 * 8) * a.slots_per_group;
-  if (a.segments > 1) la_walk_kernel<T, DX, false, true><<<dim3(groups, a.segments - 1), kThreads, 0, stream>>>(a);
-  la_walk_kernel<T, DX, SPLIT, false><<<dim3(groups, a.segments), kThreads, 0, stream>>>(a);
+  if (a.segments > 1) la_walk_kernel<T, DX, false, true><<<dim3(groups, a.segments - 1), walk_threads(true), 0, stream>>>(a);
+  la_walk_kernel<T, DX, SPLIT, false><<<dim3(groups, a.segments), walk_threads(false), 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -832,7 +1038,7 @@ BackPlan plan_backward(const ccq_linear_attn_bwd_params& q) {
   }
   if (q.dlog_alpha && q.dS_out) {
     role[0].dot = q.dS_out;
-    role[0].dot_out = sp.take<float>(chains * role[0].slices);
+    role[0].dot_out = sp.take<float>(chains * role[0].slices * 4);
   }
   role[2].s_out = q.dS0;
   const bool one = p.d_k == p.d_v;
@@ -861,7 +1067,7 @@ BackPlan plan_backward(const ccq_linear_attn_bwd_params& q) {
   bp.gate.dot = role[0].dot_out;
   bp.gate.q_slices = role[0].slices;
   bp.gate.k_slices = role[1].slices;
-  bp.gate.dot_slices = role[0].slices;
+  bp.gate.dot_slices = role[0].slices * 4;
   bp.gate.out = q.dlog_alpha;
   bp.end = sp.at;
   return bp;

@@ -271,6 +271,7 @@ int check_layout(const Layout& l, const Tokens& n, size_t E, bool written) {
   const int64_t b = n.nb > 1 ? l.b : 0;
   if (!strides_in_range(n.nb, b, n.nt, l.t, l.heads, l.h)) return CCQ_ERR_INVALID_ARG;
   if (bad_stride(b, E) || bad_stride(l.t, E) || bad_stride(l.h, E)) return CCQ_ERR_MISALIGNED;
+  if (n.nt > 1 && l.t >= (1 << 24)) return CCQ_ERR_UNSUPPORTED;  // a chunk's rows are told apart by 32-bit offsets
   if (written && !rows_apart(n.nb, b, n.nt, l.t, l.heads, l.h, l.d)) return CCQ_ERR_INVALID_ARG;
   return CCQ_OK;
 }

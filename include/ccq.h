@@ -557,8 +557,8 @@ typedef struct {
  * infinite or NaN may reach the outputs of all tokens of its 64-token chunk, earlier ones too; what stands
  * in rows of no token reaches nothing.
  * Long sequences with few heads are cut along T and the pieces joined in a fixed order: two calls give
- * the same bits.  B H <= 2^20, B T <= 2^30, rows < 2^31 (CCQ_ERR_UNSUPPORTED beyond, and for other d).
- * Returns a ccq_status.
+ * the same bits.  B H <= 2^20, B T <= 2^30, rows < 2^31, strides over tokens below 2^24
+ * (CCQ_ERR_UNSUPPORTED beyond, and for other d).  Returns a ccq_status.
  */
 int ccq_linear_attn(const ccq_linear_attn_params *p, void *hip_stream);
 /* Bytes of device workspace that call needs (0 if none and for invalid p): depends on the sizes alone. */
