@@ -20,6 +20,8 @@
 //            state, which later tokens and calls build on, is right to 2^-24.
 // Weights of pairs, not e^{B_i} e^{-B_j}: nothing leaves fp32's range whatever the decay.  Running sums are
 // formed in 64 bits and kept as two floats, in units of log 2.
+#include <type_traits>
+
 #include "ccq_prefill_common.hpp"
 
 namespace ccq {
@@ -27,6 +29,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kSlice = 32;             // columns of z that a workgroup owns
+constexpr int kStepRows = 32;          // rows of a state that a workgroup owns in a step of single tokens
 constexpr double kLog2e = 1.4426950408889634074;
 constexpr float kGateFloor = -1.0e4f;  // log decays below count as this: e^-10000 is 0, sums of 64 stay exact enough
 
@@ -116,39 +119,32 @@ __device__ __forceinline__ void store_out(void* p, int64_t at, const f32x4& v, i
   else *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(p) + at) = to_bf16x4(v);
 }
 
-// The wave's rows as MFMA operands: lane (g, l) row l, entries 8 g .. of every 32.
-template <typename T, int DX>
-__device__ __forceinline__ void load_x(Frag<T> (&f)[DX / 32], const T* p) {
-#pragma unroll
-  for (int kk = 0; kk < DX / 32; ++kk) {
-    if constexpr (sizeof(T) == 2) {
-      f[kk].v = *reinterpret_cast<const bf16x8*>(p + 32 * kk);
-    } else {
-      const f32x4 lo = *reinterpret_cast<const f32x4*>(p + 32 * kk), hi = *reinterpret_cast<const f32x4*>(p + 32 * kk + 4);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        f[kk].v[e] = lo[e];
-        f[kk].v[4 + e] = hi[e];
-      }
-    }
-  }
-}
-
 template <typename T, int DX, bool SPLIT, bool SUMMARY>
 struct Smem {
-  static constexpr int PY = DX + 16 / (int)sizeof(T), PZ = kSlice + 16 / (int)sizeof(T);
+  // Pitches.  Rows of y are read 16 bytes a lane, 16 rows at a time: with 32 bytes behind each row of bf16 that takes
+  // 4.75 clocks a wave, as reads of consecutive addresses do, with 16 bytes 8.  The state's copy is written 8 bytes a lane as
+  // well, which 32 bytes would slow down from 8 clocks to 16.
+  static constexpr int ZS = kSlice;
+  static constexpr int PY = DX + (sizeof(T) == 2 ? 16 : 4), PS = DX + 16 / (int)sizeof(T), PZ = ZS + (sizeof(T) == 2 ? 0 : 4);
   static constexpr int AHEAD = sizeof(T) == 2 ? 2 : 1;          // chunks between a load and its use
-  static constexpr int NY = AHEAD + 1, NZ = AHEAD + 2;          // tiles held of y and z
+  static constexpr int NB = AHEAD + 1;                          // tiles held of y and z
   static constexpr int NH = sizeof(T) == 2 ? 3 : 1;             // parts of b z
   static constexpr int NS = sizeof(T) == 2 && SPLIT ? 2 : 1;    // parts of the state's copy
-  T Y[NY][kL][PY];
-  T Z[NZ][kL][PZ];
-  T Zw[2][NH][kL][PZ];
-  T St[SUMMARY ? 1 : 2][NS][SUMMARY ? 1 : kSlice][PY];
+  T Y[NB][kL][PY];
+  T Z[NB][kL][PZ];
+  T St[SUMMARY ? 1 : 2][NS][SUMMARY ? 1 : ZS][PS];
+  // Rows of x, 16 for each wave, that no other wave reads: when they have become operands, their place holds the
+  // wave's outputs (fp32, pitch PO) and behind these (at OW) what they are multiplied by, until both have left.  fp32 rows
+  // do not fit and are loaded into registers: there only the outputs' place remains.
+  static constexpr bool XL = sizeof(T) == 2;
+  static constexpr int PO = ZS + 4, OW = 16 * PO * 4;
+  static constexpr int XN = XL ? (16 * PY * (int)sizeof(T) > OW + 1024 ? 16 * PY : (OW + 1024) / (int)sizeof(T)) : 16 * PO;
+  T X[SUMMARY ? 1 : XL ? NB : 2][SUMMARY ? 1 : 4][SUMMARY ? 4 : XN];
   // Of each token: its running sum as two floats, the weight of the state before the chunk for it, its weight in
   // the state behind, and e^(its sum to the end of its 16 tokens), or from their beginning.
-  float bh[3][kL], bl[3][kL], aw[3][kL], bw[3][kL], cf[3][kL];
-  float dec[3];
+  float bh[2][kL], bl[2][kL], aw[2][kL], bw[2][kL], cf[2][kL];
+  float dec[2];
+  uint32_t raw[NB][kL];        // gates as stored
 };
 
 // A wave's running sum of 64-bit values, in registers alone.
@@ -184,9 +180,27 @@ __device__ __forceinline__ double form_gates(SM& sm, int buf, double g, bool liv
   return all;
 }
 
+// An address that is the same in all lanes, in scalar registers, and vectors at byte offsets from it.  (Made of an
+// integer, a plain pointer would be a generic one, whose loads count as LDS accesses too.)
+#define CCQ_GLOBAL __attribute__((address_space(1)))
+typedef CCQ_GLOBAL char* UniformPtr;
+__device__ __forceinline__ UniformPtr uniform_ptr(const void* p) {
+  const uint64_t u = reinterpret_cast<uint64_t>(p);
+  return reinterpret_cast<UniformPtr>((uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((int)(u >> 32)) << 32 |
+                                      (unsigned)__builtin_amdgcn_readfirstlane((int)u));
+}
+template <typename V>
+__device__ __forceinline__ V load_at(UniformPtr p, unsigned off) {
+  return *reinterpret_cast<CCQ_GLOBAL const V*>(p + off);
+}
+template <typename V>
+__device__ __forceinline__ void store_at(UniformPtr p, unsigned off, const V& v) {
+  *reinterpret_cast<CCQ_GLOBAL V*>(p + off) = v;
+}
+
 // A chunk's rows of COLS entries straight into an LDS tile of pitch P by four waves, rows behind the sequence's end as
 // row 0 (their weights are 0).  Each lane's places are worked out once; unit j of the tile belongs to wave
-// FLIP ? 3 - j % 4 : j % 4, which has COUNT of them.  The loads are not the compiler's: the caller waits.
+// FLIP ? 3 - j % 4 : j % 4, which has count() of them.  The loads are not the compiler's: the caller waits.
 template <typename T, int COLS, int P, bool FLIP>
 struct RowLoads {
   static constexpr int U = P * (int)sizeof(T) / 16, DU = COLS * (int)sizeof(T) / 16, M = (U + 3) / 4;
@@ -199,7 +213,7 @@ struct RowLoads {
       off[m] = slot < DU ? (unsigned)row * (unsigned)(step * (int)sizeof(T)) + 16u * slot : 0u;
     }
   }
-  __device__ __forceinline__ void load(T (*dst)[P], const T* src, int live, int w, int lane) const {
+  __device__ __forceinline__ void load(T (*dst)[P], UniformPtr src, int live, int w, int lane) const {
     const unsigned base = (unsigned)(uintptr_t)(__attribute__((address_space(3))) T*)&dst[0][0];
 #pragma unroll
     for (int m = 0; m < M; ++m) {
@@ -257,54 +271,81 @@ __device__ __forceinline__ void vm_wait() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-template <typename T>
-struct Raw4 {
-  typedef bf16x4 type;
-};
-template <>
-struct Raw4<float> {
-  typedef f32x4 type;
-};
-
-template <typename T>
-__device__ __forceinline__ T* uniform_ptr(T* p) {
-  const uint64_t u = reinterpret_cast<uint64_t>(p);
-  return reinterpret_cast<T*>((uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((int)(u >> 32)) << 32 |
-                              (unsigned)__builtin_amdgcn_readfirstlane((int)u));
+// A row as MFMA operands: lane (g, l) entries 8 g .. of every 32 of its row, which begins (with 8 g) at `off`.
+template <typename T, int DX>
+__device__ __forceinline__ void load_x(Frag<T> (&f)[DX / 32], UniformPtr p, unsigned off) {
+#pragma unroll
+  for (int kk = 0; kk < DX / 32; ++kk) {
+    if constexpr (sizeof(T) == 2) {
+      f[kk].v = load_at<bf16x8>(p, off + 64 * kk);
+    } else {
+      const f32x4 lo = load_at<f32x4>(p, off + 128 * kk), hi = load_at<f32x4>(p, off + 128 * kk + 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f[kk].v[e] = lo[e];
+        f[kk].v[4 + e] = hi[e];
+      }
+    }
+  }
 }
 
-// The gates of a walk's chunks, by one wave: formed two chunks ahead, loaded three.
+// The gates of a walk's chunks, by one wave: formed a chunk ahead, from what a wave of the state has loaded into the LDS.
 template <bool REV, typename SM>
 struct Gates {
   const Args& a;
   SM& sm;
-  int64_t la0;
-  int len, c_lo, c_hi, lane;
+  int len, c_lo, c_hi, lane, at;
   float in_scale;
   double total;
-  unsigned ahead;
-  __device__ __forceinline__ int token(int it) const { return (REV ? c_hi - 1 - it : c_lo + it) * kL + lane; }
-  __device__ __forceinline__ unsigned load(int it) const {
-    const int t = token(min(it, c_hi - c_lo - 1));
-    return gate_bits(a, la0 + (int64_t)min(t, len - 1) * a.ls.t);
+  __device__ __forceinline__ Gates(const Args& a, const Role& ro, SM& sm, const Span& sp, int c_lo, int c_hi, int lane)
+      : a(a), sm(sm), len(sp.len), c_lo(c_lo), c_hi(c_hi), lane(lane), at(0), in_scale(ro.in_scale), total(0.0) {}
+  // chunk it, into buffer BUF
+  template <int BUF>
+  __device__ __forceinline__ void form(int it) {
+    if (it < c_hi - c_lo) {
+      const bool live = (REV ? c_hi - 1 - it : c_lo + it) * kL + lane < len;
+      total += form_gates<REV>(sm, BUF, live && a.la ? gate_value(a, sm.raw[at][lane]) : 0.0, live, in_scale, lane);
+    }
+    at = at + 1 == SM::NB ? 0 : at + 1;
   }
-  __device__ __forceinline__ void form(int it, unsigned bits) {
-    if (it >= c_hi - c_lo) return;
-    const bool live = token(it) < len;
-    total += form_gates<REV>(sm, it % 3, live ? gate_value(a, bits) : 0.0, live, in_scale, lane);
+};
+// Loads a chunk's gates into the LDS, one a lane, tokens behind the end as the chunk's first.  The caller waits.
+__device__ __forceinline__ void load_gates(const Args& a, uint32_t* dst, int64_t at, int live, int lane) {
+  if (a.la == nullptr) return;
+  const unsigned base = (unsigned)(uintptr_t)(__attribute__((address_space(3))) uint32_t*)dst;
+  const unsigned m0 = __builtin_amdgcn_readfirstlane(base);
+  const int64_t own = at + (lane < live ? lane * a.ls.t : 0);
+  if (a.gate_bf16) {
+    const uint16_t* p = static_cast<const uint16_t*>(a.la) + own;
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_ushort %1, off" ::"s"(m0), "v"(p) : "memory", "m0");
+  } else {
+    const uint32_t* p = static_cast<const uint32_t*>(a.la) + own;
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(m0), "v"(p) : "memory", "m0");
   }
-  __device__ __forceinline__ Gates(const Args& a, const Role& ro, SM& sm, const Span& sp, int b, int h, int c_lo, int c_hi, int lane)
-      : a(a), sm(sm), la0((a.offsets ? sp.row0 * a.ls.t : b * a.ls.b) + h * a.ls.h), len(sp.len), c_lo(c_lo), c_hi(c_hi), lane(lane),
-        in_scale(ro.in_scale), total(0.0) {
-    const unsigned g0 = load(0), g1 = load(1);
-    ahead = load(2);
-    form(0, g0);
-    form(1, g1);
+}
+
+// 16 rows of COLS entries alike, by one wave for itself, the first row `first` of a chunk.
+template <typename T, int COLS, int P>
+struct OwnLoads {
+  static constexpr int U = P * (int)sizeof(T) / 16, DU = COLS * (int)sizeof(T) / 16, COUNT = (16 * U + 63) / 64;
+  unsigned off[COUNT];
+  __device__ __forceinline__ OwnLoads(int first, int lane, int64_t step) {
+#pragma unroll
+    for (int m = 0; m < COUNT; ++m) {
+      const int u = 64 * m + lane, row = u / U, slot = u - row * U;
+      off[m] = slot < DU ? (unsigned)(first + row) * (unsigned)(step * (int)sizeof(T)) + 16u * slot : 0u;
+    }
   }
-  __device__ __forceinline__ void next(int it) {
-    const unsigned now = ahead;
-    ahead = load(it + 3);
-    form(it + 2, now);
+  __device__ __forceinline__ void load(void* dst, UniformPtr src, int first, int live, int lane) const {
+    const unsigned base = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char*)dst;
+#pragma unroll
+    for (int m = 0; m < COUNT; ++m) {
+      unsigned o = off[m];
+      if (live < kL) o = first + (64 * m + lane) / U < live ? o : 0u;
+      const unsigned m0 = __builtin_amdgcn_readfirstlane(base + 1024u * (unsigned)m);
+      if (64 * m + 64 <= 16 * U || 64 * m + lane < 16 * U)
+        asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m0), "v"(o), "s"(src) : "memory", "m0");
+    }
   }
 };
 
@@ -313,101 +354,168 @@ template <typename T, int DX, bool SPLIT, bool REV, int W>
 __device__ __forceinline__ void walk_outputs(const Args& a, const Role& ro, int chain, int slice, const Span& sp, int c_lo, int c_hi, int lane,
                                              Smem<T, DX, SPLIT, false>& sm) {
   using SM = Smem<T, DX, SPLIT, false>;
-  typedef typename Raw4<T>::type R4;
-  constexpr int NZ = kSlice / 16, NK = DX / 32, AH = SM::AHEAD, T0 = REV ? W : 0, T1 = REV ? 3 : W;
+  constexpr int ZS = SM::ZS, NZ = ZS / 16, NK = DX / 32, T0 = REV ? W : 0, T1 = REV ? 3 : W;
   constexpr bool kGateWave = W == (REV ? 3 : 0);  // the wave with the fewest score tiles
   const int g = lane >> 4, l = lane & 15, n = c_hi - c_lo;
   const int b = chain / a.H, h = chain - b * a.H;
   auto chunk_at = [&](int it) { return REV ? c_hi - 1 - it : c_lo + it; };
-  const T* xb = uniform_ptr(rows_of<T>(ro.x, ro.xs, ro.x_share, a, sp, b, h));
-  const T* wb = ro.r ? uniform_ptr(rows_of<T>(ro.w, ro.ws, ro.w_share, a, sp, b, h) + slice * kSlice) : nullptr;
-  const int64_t ob = (a.offsets ? sp.row0 * ro.os.t : b * ro.os.b) + h * ro.os.h + slice * kSlice;
+  const UniformPtr xb = uniform_ptr(rows_of<T>(ro.x, ro.xs, ro.x_share, a, sp, b, h));
+  const UniformPtr wb = uniform_ptr(ro.r ? rows_of<T>(ro.w, ro.ws, ro.w_share, a, sp, b, h) + slice * ZS : nullptr);
+  const int64_t ob = (a.offsets ? sp.row0 * ro.os.t : b * ro.os.b) + h * ro.os.h + slice * ZS;
   const int oe = sizeof(T) == 4 || ro.out_f32 ? 4 : 2;
-  char* outb = uniform_ptr(static_cast<char*>(ro.out) + ob * oe);
+  const UniformPtr outb = uniform_ptr(static_cast<char*>(ro.out) + ob * oe);
   constexpr unsigned kElem = sizeof(T);
   const unsigned own = 16 * W + l;
   const unsigned x_off = own * (unsigned)(ro.xs.t * (int)sizeof(T)) + 8 * g * kElem;
-  const unsigned w_off = own * (unsigned)(ro.ws.t * (int)sizeof(T)) + 4 * g * kElem;
-  const unsigned o_off = own * (unsigned)(ro.os.t * oe) + 4 * g * oe;
-  Frag<T> X[AH + 1][NK];
-  R4 wr[AH + 1][NZ];
-  f32x4 out[NZ];
-  float r_out = 0.f;
-  // the wave's own rows of a chunk, the chunk's first where the sequence has ended
-  auto load_own = [&](int k, int it) {
-    const int c = chunk_at(min(it, n - 1));
-    const bool on = (int)own < sp.len - c * kL;
-    load_x<T, DX>(X[k], reinterpret_cast<const T*>(reinterpret_cast<const char*>(xb + (int64_t)c * kL * ro.xs.t) + (on ? x_off : 8u * g * kElem)));
-    if (ro.r) {
-      const char* p = reinterpret_cast<const char*>(wb + (int64_t)c * kL * ro.ws.t) + (on ? w_off : 4u * g * kElem);
-#pragma unroll
-      for (int z = 0; z < NZ; ++z) wr[k][z] = *reinterpret_cast<const R4*>(p + 16 * z * kElem);
-    }
-  };
-  auto flush = [&](int it) {  // a chunk's outputs, a chunk later: the stores have time
+  // outputs leave, and what they are multiplied by comes, eight columns a lane: neighbouring lanes on neighbouring columns
+  // (of the accumulators' rows each lane's 8 bytes were a request of their own: a fifth of the kernel's time)
+  constexpr int LPO = ZS / 8;
+  const int o_row = lane / LPO, o_col = 8 * (lane % LPO);
+  const unsigned o_own = 16 * W + o_row;
+  const unsigned w_off = o_own * (unsigned)(ro.ws.t * (int)sizeof(T)) + o_col * kElem;
+  const unsigned o_off = o_own * (unsigned)(ro.os.t * oe) + o_col * oe;
+  constexpr int AX = SM::XL ? 2 : 1;  // chunks that the rows are loaded ahead
+  constexpr int kPlaces = SM::XL ? SM::NB : 2;
+  const OwnLoads<T, DX, SM::PY> xl(16 * W, lane, ro.xs.t);
+  const OwnLoads<T, ZS, ZS> wl(16 * W, lane, ro.ws.t);
+  Frag<T> X[NK], weights;
+  auto issue_x = [&](int it, int to) {
     const int c = chunk_at(it);
-    if ((int)own < sp.len - c * kL) {
-      char* p = outb + (int64_t)c * kL * ro.os.t * oe;
+    xl.load(&sm.X[to][W][0], xb + (int64_t)c * kL * ro.xs.t * kElem, 16 * W, sp.len - c * kL, lane);
+  };
+  auto issue_w = [&](int it, int to) {
+    const int c = chunk_at(it);
+    wl.load(reinterpret_cast<char*>(&sm.X[to][W][0]) + SM::OW, wb + (int64_t)c * kL * ro.ws.t * kElem, 16 * W, sp.len - c * kL, lane);
+  };
+  // fp32: the wave's own rows of a chunk, the chunk's first where the sequence has ended
+  auto load_own = [&](int it) {
+    const int c = chunk_at(it);
+    load_x<T, DX>(X, xb + (int64_t)c * kL * ro.xs.t * kElem, (int)own < sp.len - c * kL ? x_off : 8u * g * kElem);
+  };
+  auto load_w = [&](int it) {
+    const int c = chunk_at(it);
+    const UniformPtr p = wb + (int64_t)c * kL * ro.ws.t * kElem;
+    const unsigned off = (int)o_own < sp.len - c * kL ? w_off : (unsigned)o_col * kElem;
+    if constexpr (!SM::XL) {
+      const f32x4 lo = load_at<f32x4>(p, off), hi = load_at<f32x4>(p, off + 16);
 #pragma unroll
-      for (int z = 0; z < NZ; ++z) {
-        if (sizeof(T) == 4 || ro.out_f32) *reinterpret_cast<f32x4*>(p + (o_off + 64u * z)) = out[z];
-        else *reinterpret_cast<bf16x4*>(p + (o_off + 32u * z)) = to_bf16x4(out[z]);
+      for (int e = 0; e < 4; ++e) {
+        weights.v[e] = lo[e];
+        weights.v[4 + e] = hi[e];
       }
-      if (ro.r && g == 0) ro.r[((size_t)slice * a.chains + chain) * a.T + c * kL + own] = r_out;
     }
   };
+  // a chunk's outputs to memory, a chunk later: the stores have time
+  auto flush = [&](int it, int from) {
+    const int c = chunk_at(it);
+    const float* src = reinterpret_cast<const float*>(&sm.X[from][W][0]) + o_row * SM::PO + o_col;
+    const f32x4 lo = *reinterpret_cast<const f32x4*>(src), hi = *reinterpret_cast<const f32x4*>(src + 4);
+    if constexpr (SM::XL) {
+      if (ro.r) weights.v = *reinterpret_cast<const bf16x8*>(reinterpret_cast<const char*>(&sm.X[from][W][0]) + SM::OW + 16 * lane);
+    }
+    const bool on = (int)o_own < sp.len - c * kL;
+    const UniformPtr p = outb + (int64_t)c * kL * ro.os.t * oe;
+    if (on) {
+      if (sizeof(T) == 4 || ro.out_f32) {
+        store_at<f32x4>(p, o_off, lo);
+        store_at<f32x4>(p, o_off + 16, hi);
+      } else {
+        store_at<bf16x8>(p, o_off, bf16x8{(__bf16)lo[0], (__bf16)lo[1], (__bf16)lo[2], (__bf16)lo[3], (__bf16)hi[0], (__bf16)hi[1],
+                                          (__bf16)hi[2], (__bf16)hi[3]});
+      }
+    }
+    if (ro.r) {
+      float r = 0.f;
 #pragma unroll
-  for (int i = 0; i < AH; ++i) load_own(i, i);
+      for (int e = 0; e < 4; ++e) r += lo[e] * (float)weights.v[e];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r += hi[e] * (float)weights.v[4 + e];
+      r = group_sum<LPO>(r);
+      if (on && o_col == 0) ro.r[((size_t)slice * a.chains + chain) * a.T + c * kL + o_own] = r;
+    }
+  };
+  const int place = row_place<T>(SM::PY, lane), s_place = row_place<T>(SM::PS, lane), z_place = tr_place<T>(SM::PZ, lane);
+  // a chunk's scores, weighted: chunk it, gates in buffer gb
+  auto scores = [&](f32x4 (&P)[4], const Frag<T> (&x)[NK], int it, int at, int gb) {
+    const T* y0 = &sm.Y[at][0][0] + place;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) P[t] = zero4();
+#pragma unroll
+    for (int kk = 0; kk < NK; ++kk)
+#pragma unroll
+      for (int t = T0; t <= T1; ++t) mma(P[t], row_at<T>(y0 + 16 * t * SM::PY + 32 * kk), x[kk]);
+    const float bh = sm.bh[gb][own], bl = sm.bl[gb][own];
+#pragma unroll
+    for (int t = T0; t <= T1; ++t) {
+      if (t == W) {
+        const f32x4 kh = *reinterpret_cast<const f32x4*>(&sm.bh[gb][16 * t + 4 * g]);
+        const f32x4 kl = *reinterpret_cast<const f32x4*>(&sm.bl[gb][16 * t + 4 * g]);
+        const int live = sp.len - chunk_at(it) * kL - 16 * t;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int j = 4 * g + r;
+          const float d = REV ? (kh[r] - bh) + (kl[r] - bl) : (bh - kh[r]) + (bl - kl[r]);
+          P[t][r] = (REV ? j >= l && j < live : j <= l) ? P[t][r] * (exp2_fast(d) * ro.in_scale) : 0.f;
+        }
+      } else {
+        // e^(B_i - B_j) in two parts, from the query to the tile's edge and on to the key: both below 1 for decays
+        const int edge = REV ? 16 * t : 16 * t + 15;
+        const float eh = sm.bh[gb][edge], el = sm.bl[gb][edge];
+        const float row = exp2_fast(REV ? (eh - bh) + (el - bl) : (bh - eh) + (bl - el));
+        const f32x4 cf = *reinterpret_cast<const f32x4*>(&sm.cf[gb][16 * t + 4 * g]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) P[t][r] *= row * cf[r];
+      }
+    }
+  };
+  if constexpr (SM::XL) {
+    issue_x(0, 0);
+    if (n > 1) issue_x(1, 1);
+  } else {
+    load_own(0);
+  }
   auto body = [&](auto gates) {
     lds_barrier();
+    if constexpr (kGateWave) gates.template form<0>(0);
     lds_barrier();
-    int yb_at = 0, zb_at = 0, gb = 0;  // it modulo NY, NZ and 3
-    const int place = row_place<T>(SM::PY, lane), z_place = tr_place<T>(SM::PZ, lane);
-    for (int it = 0; it < n; ++it) {
-      load_own(AH, it + AH);
-      const T* st = &sm.St[it & 1][0][0][0] + place;
-      const T* y0 = &sm.Y[yb_at][0][0] + place;
-      const T* z0 = &sm.Z[zb_at][0][0] + z_place;
-      // scores and far (the state before the chunk)
+    int at = 0, xat = 0, xbefore = 0;  // it modulo NB, and modulo the places of x; the one before
+    // one chunk, whose parity GB is
+    auto step = [&](auto parity, int it) {
+      constexpr int GB = decltype(parity)::value;
+      if constexpr (SM::XL) {
+        // this chunk's rows have landed, and the stores and weights of the chunk before: all but the next chunk's rows
+        if (it + 1 < n) vm_wait<OwnLoads<T, DX, SM::PY>::COUNT>();
+        else vm_wait<0>();
+        const T* x = &sm.X[xat][W][0] + place;
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk) X[kk] = row_at<T>(x + 32 * kk);
+      }
+      if (it > 0) flush(it - 1, xbefore);
+      if constexpr (SM::XL) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the places that the loads go to have been read
+        if (ro.r) issue_w(it, xat);
+        if (it + AX < n) issue_x(it + AX, xat == 0 ? kPlaces - 1 : xat - 1);
+      } else {
+        if (ro.r) load_w(it);
+      }
+      const T* st = &sm.St[GB][0][0][0] + s_place;
+      const T* z0 = &sm.Z[at][0][0] + z_place;
+      const float aw = sm.aw[GB][own], dec = sm.dec[GB];
+      // far: the state before the chunk
       f32x4 acc[NZ], P[4];
 #pragma unroll
       for (int z = 0; z < NZ; ++z) acc[z] = zero4();
 #pragma unroll
-      for (int t = 0; t < 4; ++t) P[t] = zero4();
-#pragma unroll
-      for (int kk = 0; kk < NK; ++kk) {
-#pragma unroll
-        for (int t = T0; t <= T1; ++t) mma(P[t], row_at<T>(y0 + 16 * t * SM::PY + 32 * kk), X[0][kk]);
+      for (int kk = 0; kk < NK; ++kk)
 #pragma unroll
         for (int z = 0; z < NZ; ++z)
 #pragma unroll
-          for (int s = 0; s < SM::NS; ++s) mma(acc[z], row_at<T>(st + (s * kSlice + 16 * z) * SM::PY + 32 * kk), X[0][kk]);
+          for (int s = 0; s < SM::NS; ++s) mma(acc[z], row_at<T>(st + (s * ZS + 16 * z) * SM::PS + 32 * kk), X[kk]);
+      scores(P, X, it, at, GB);
+      if constexpr (!SM::XL) {
+        if (it + 1 < n) load_own(it + 1);
       }
-      if (it > 0) flush(it - 1);
-      const float bh = sm.bh[gb][own], bl = sm.bl[gb][own], aw = sm.aw[gb][own];
-#pragma unroll
-      for (int t = T0; t <= T1; ++t) {
-        if (t == W) {
-          const f32x4 kh = *reinterpret_cast<const f32x4*>(&sm.bh[gb][16 * t + 4 * g]);
-          const f32x4 kl = *reinterpret_cast<const f32x4*>(&sm.bl[gb][16 * t + 4 * g]);
-          const int live = sp.len - chunk_at(it) * kL - 16 * t;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int j = 4 * g + r;
-            const float d = REV ? (kh[r] - bh) + (kl[r] - bl) : (bh - kh[r]) + (bl - kl[r]);
-            P[t][r] = (REV ? j >= l && j < live : j <= l) ? P[t][r] * (exp2_fast(d) * ro.in_scale) : 0.f;
-          }
-        } else {
-          // e^(B_i - B_j) in two parts, from the query to the tile's edge and on to the key: both below 1 for decays
-          const int edge = REV ? 16 * t : 16 * t + 15;
-          const float eh = sm.bh[gb][edge], el = sm.bl[gb][edge];
-          const float row = exp2_fast(REV ? (eh - bh) + (el - bl) : (bh - eh) + (bl - el));
-          const f32x4 cf = *reinterpret_cast<const f32x4*>(&sm.cf[gb][16 * t + 4 * g]);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) P[t][r] *= row * cf[r];
-        }
-      }
-      if (sm.dec[gb] == 0.f) {  // a gate of 0: the state before counts for nothing, whatever it holds
+      if (dec == 0.f) {  // a gate of 0: the state before counts for nothing, whatever it holds
 #pragma unroll
         for (int z = 0; z < NZ; ++z)
 #pragma unroll
@@ -439,34 +547,25 @@ __device__ __forceinline__ void walk_outputs(const Args& a, const Role& ro, int 
         }
       }
 #pragma unroll
-      for (int z = 0; z < NZ; ++z)
+      for (int z = 0; z < NZ; ++z) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) out[z][r] = acc[z][r] * ro.out_scale;
-      if (ro.r) {
-        float rs = 0.f;
-#pragma unroll
-        for (int z = 0; z < NZ; ++z)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) rs += out[z][r] * (float)wr[0][z][r];
-        rs += __shfl_xor(rs, 16, 64);
-        r_out = rs + __shfl_xor(rs, 32, 64);
+        for (int r = 0; r < 4; ++r) acc[z][r] *= ro.out_scale;
+        *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(&sm.X[xat][W][0]) + l * SM::PO + 16 * z + 4 * g) = acc[z];
       }
-      if constexpr (kGateWave) gates.next(it);
-#pragma unroll
-      for (int i = 0; i < AH; ++i) {
-#pragma unroll
-        for (int kk = 0; kk < NK; ++kk) X[i][kk] = X[i + 1][kk];
-#pragma unroll
-        for (int z = 0; z < NZ; ++z) wr[i][z] = wr[i + 1][z];
-      }
-      yb_at = yb_at + 1 == SM::NY ? 0 : yb_at + 1;
-      zb_at = zb_at + 1 == SM::NZ ? 0 : zb_at + 1;
-      gb = gb == 2 ? 0 : gb + 1;
+      if constexpr (kGateWave) gates.template form<1 - GB>(it + 1);
+      at = at + 1 == SM::NB ? 0 : at + 1;
+      xbefore = xat;
+      xat = xat + 1 == kPlaces ? 0 : xat + 1;
       lds_barrier();
+    };
+    for (int it = 0; it < n; it += 2) {
+      step(std::integral_constant<int, 0>{}, it);
+      if (it + 1 < n) step(std::integral_constant<int, 1>{}, it + 1);
     }
-    flush(n - 1);
+    if constexpr (SM::XL) vm_wait<0>();
+    flush(n - 1, xbefore);
   };
-  if constexpr (kGateWave) body(Gates<REV, SM>(a, ro, sm, sp, b, h, c_lo, c_hi, lane));
+  if constexpr (kGateWave) body(Gates<REV, SM>(a, ro, sm, sp, c_lo, c_hi, lane));
   else body(0);
 }
 
@@ -476,7 +575,7 @@ __device__ __forceinline__ void walk_outputs(const Args& a, const Role& ro, int 
 template <typename T, int DX, bool SPLIT, bool REV, bool SUMMARY>
 __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, int slice, int seg, Smem<T, DX, SPLIT, SUMMARY>& sm) {
   using SM = Smem<T, DX, SPLIT, SUMMARY>;
-  constexpr int NO = SUMMARY ? 1 : 4, NX = DX / 32, AH = SM::AHEAD;
+  constexpr int NO = SUMMARY ? 1 : 4, ZS = SM::ZS, NZ = ZS / 16, NX = DX / 16 * NZ / 4, AH = SM::AHEAD;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const bool carries = wave >= NO;
@@ -488,17 +587,17 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
   const size_t mat = (size_t)ro.dz * DX;
   auto chunk_at = [&](int it) { return REV ? c_hi - 1 - it : c_lo + it; };
   // a state's place in the accumulators' order: 16 bytes a lane
-  const int sw = wave - NO, zt = sw & 1, xt = (sw >> 1) * NX;
+  const int sw = wave - NO, zt = sw % NZ, xt = sw / NZ * NX;
   auto slot_of = [&](int s) {
-    return ro.slots + (((size_t)chain * a.segments + s) * ro.slices + slice) * (kSlice * DX) + (size_t)sw * NX * 256 + lane * 4;
+    return ro.slots + (((size_t)chain * a.segments + s) * ro.slices + slice) * (ZS * DX) + (size_t)sw * NX * 256 + lane * 4;
   };
 
   if constexpr (!SUMMARY) {
     if (ro.zero_tail && a.offsets == nullptr) {  // rows of no token
-      const int64_t ob = b * ro.os.b + h * ro.os.h + slice * kSlice;
+      const int64_t ob = b * ro.os.b + h * ro.os.h + slice * ZS;
       const int last = seg == a.segments - 1 ? a.T : min(a.T, (c_lo + a.chunks_per_segment) * kL);
-      for (int t = max(sp.len, c_lo * kL) + (tid >> 3); t < last; t += 64)
-        store_out<T>(ro.out, ob + (int64_t)t * ro.os.t + 4 * (tid & 7), zero4(), ro.out_f32);
+      for (int t = max(sp.len, c_lo * kL) + tid / (ZS / 4); t < last; t += 512 / (ZS / 4))
+        store_out<T>(ro.out, ob + (int64_t)t * ro.os.t + 4 * (tid % (ZS / 4)), zero4(), ro.out_f32);
     }
   }
 
@@ -510,7 +609,7 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
       for (int x = 0; x < NX; ++x) {
         S[x] = zero4();
         if (ro.s_in) {
-          const float* p = ro.s_in + chain * mat + (size_t)(slice * kSlice + 16 * zt + l) * ro.s_i + (size_t)(16 * (xt + x) + 4 * g) * ro.s_j;
+          const float* p = ro.s_in + chain * mat + (size_t)(slice * ZS + 16 * zt + l) * ro.s_i + (size_t)(16 * (xt + x) + 4 * g) * ro.s_j;
           if (ro.s_j == 1) S[x] = *reinterpret_cast<const f32x4*>(p);
           else
 #pragma unroll
@@ -559,46 +658,18 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
       }
     }
     if (n > 0) {
-      const T* yb = uniform_ptr(rows_of<T>(ro.y, ro.ys, ro.y_share, a, sp, b, h));
-      const T* zb = uniform_ptr(rows_of<T>(ro.z, ro.zs, ro.z_share, a, sp, b, h) + slice * kSlice);
+      const UniformPtr yb = uniform_ptr(rows_of<T>(ro.y, ro.ys, ro.y_share, a, sp, b, h));
+      const UniformPtr zb = uniform_ptr(rows_of<T>(ro.z, ro.zs, ro.z_share, a, sp, b, h) + slice * ZS);
       const RowLoads<T, DX, SM::PY, false> yl(sw, lane, ro.ys.t);
-      const RowLoads<T, kSlice, SM::PZ, true> zl(sw, lane, ro.zs.t);
+      const RowLoads<T, ZS, SM::PZ, true> zl(sw, lane, ro.zs.t);
+      const int64_t y_chunk = kL * ro.ys.t * (int)sizeof(T), z_chunk = kL * ro.zs.t * (int)sizeof(T);  // bytes
       auto issue_y = [&](int it) {
         const int c = chunk_at(it);
-        yl.load(sm.Y[it % SM::NY], yb + (int64_t)c * kL * ro.ys.t, sp.len - c * kL, sw, lane);
+        yl.load(sm.Y[it % SM::NB], yb + (int64_t)c * y_chunk, sp.len - c * kL, sw, lane);
       };
       auto issue_z = [&](int it) {
         const int c = chunk_at(it);
-        zl.load(sm.Z[it % SM::NZ], zb + (int64_t)c * kL * ro.zs.t, sp.len - c * kL, sw, lane);
-      };
-      // b z of a chunk, 8 entries a thread
-      auto weigh = [&](T (*src)[SM::PZ], T (*dst)[kL][SM::PZ], const float* weights) {
-        const int t = sw * 64 + lane, row = t / (kSlice / 8), col = 8 * (t % (kSlice / 8));
-        const float bw = weights[row];
-        if constexpr (sizeof(T) == 2) {
-          const bf16x8 v = *reinterpret_cast<const bf16x8*>(&src[row][col]);
-          float z[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) z[e] = (float)v[e] * bw;
-#pragma unroll
-          for (int p = 0; p < SM::NH; ++p) {
-            bf16x8 part;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              part[e] = (__bf16)z[e];
-              z[e] -= (float)part[e];
-            }
-            *reinterpret_cast<bf16x8*>(&dst[p][row][col]) = part;
-          }
-        } else {
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            f32x4 v = *reinterpret_cast<const f32x4*>(&src[row][col + 4 * q]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] *= bw;
-            *reinterpret_cast<f32x4*>(&dst[0][row][col + 4 * q]) = v;
-          }
-        }
+        zl.load(sm.Z[it % SM::NB], zb + (int64_t)c * z_chunk, sp.len - c * kL, sw, lane);
       };
       auto store_copy = [&](int it) {
 #pragma unroll
@@ -612,41 +683,73 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
           }
         }
       };
-      issue_z(0);
-      issue_y(0);
+      const int64_t la0 = (a.offsets ? sp.row0 * a.ls.t : b * a.ls.b) + h * a.ls.h;
+      const bool gater = sw == 2;  // of the waves with the fewest loads
+      auto issue_gates = [&](int it, int to) {
+        const int c = chunk_at(it);
+        load_gates(a, sm.raw[to], la0 + (int64_t)c * kL * a.ls.t, sp.len - c * kL, lane);
+      };
+      if (gater) {
+        issue_gates(0, 0);
+        vm_wait<0>();
+      }
+      lds_barrier();
 #pragma unroll
-      for (int i = 1; i < AH; ++i)
-        if (i < n) issue_y(i);
-#pragma unroll
-      for (int i = 1; i <= AH; ++i)
-        if (i < n) issue_z(i);
+      for (int i = 0; i < AH; ++i)
+        if (i < n) {
+          if (gater && i > 0) issue_gates(i, i);
+          issue_y(i);
+          issue_z(i);
+        }
+      if (gater && AH < n) issue_gates(AH, AH);
       if constexpr (!SUMMARY) store_copy(0);
       vm_wait_all();
       lds_barrier();
-      weigh(sm.Z[0], sm.Zw[0], sm.bw[0]);
-      lds_barrier();
       const int y_place = tr_place<T>(SM::PY, lane) + 16 * xt, z_place = tr_place<T>(SM::PZ, lane) + 16 * zt;
-      int yb_at = 0, zb_at = 0, gb = 0;  // it modulo NY, NZ and 3
-      const int64_t y_step = (REV ? -kL : kL) * ro.ys.t, z_step = (REV ? -kL : kL) * ro.zs.t;
-      const T* y_next = yb + (int64_t)chunk_at(0) * kL * ro.ys.t + AH * y_step;
-      const T* z_next = zb + (int64_t)chunk_at(0) * kL * ro.zs.t + (AH + 1) * z_step;
+      int at = 0;  // it modulo NB
+      const int64_t y_step = REV ? -y_chunk : y_chunk, z_step = REV ? -z_chunk : z_chunk;
+      UniformPtr y_next = yb + (int64_t)chunk_at(0) * y_chunk + AH * y_step;
+      UniformPtr z_next = zb + (int64_t)chunk_at(0) * z_chunk + AH * z_step;
       for (int it = 0; it < n; ++it) {
-        const bool more = it + AH + 1 < n;
-        const T* y0 = &sm.Y[yb_at][0][0] + y_place;
-        const T* z0 = &sm.Zw[it & 1][0][0][0] + z_place;
-        const float dec = sm.dec[gb];
+        const T* y0 = &sm.Y[at][0][0] + y_place;
+        const T* z0 = &sm.Z[at][0][0] + z_place;
+        const float dec = sm.dec[it & 1];
+        // b z: the lane's eight tokens of every 32, as tr_at has them
         Frag<T> y[2][NX], zf[2][SM::NH];
+        Frag<T> z[2];
+        f32x4 bw[2][2];
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
+          z[kk] = tr_at<T, SM::PZ>(z0 + 32 * kk * SM::PZ);
+          bw[kk][0] = *reinterpret_cast<const f32x4*>(&sm.bw[it & 1][32 * kk + 4 * g]);
+          bw[kk][1] = *reinterpret_cast<const f32x4*>(&sm.bw[it & 1][32 * kk + 16 + 4 * g]);
+        }
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
           for (int x = 0; x < NX; ++x) y[kk][x] = tr_at<T, SM::PY>(y0 + 32 * kk * SM::PY + 16 * x);
-#pragma unroll
-          for (int p = 0; p < SM::NH; ++p) zf[kk][p] = tr_at<T, SM::PZ>(z0 + (p * kL + 32 * kk) * SM::PZ);
+        if (it + AH < n) {
+          const int to = at == 0 ? SM::NB - 1 : at - 1, live = sp.len - chunk_at(it + AH) * kL;
+          yl.load(sm.Y[to], y_next, live, sw, lane);
+          zl.load(sm.Z[to], z_next, live, sw, lane);
         }
-        if (it + AH < n) yl.load(sm.Y[yb_at + AH >= SM::NY ? yb_at + AH - SM::NY : yb_at + AH], y_next, sp.len - chunk_at(it + AH) * kL, sw, lane);
-        if (more) zl.load(sm.Z[zb_at == 0 ? SM::NZ - 1 : zb_at - 1], z_next, sp.len - chunk_at(it + AH + 1) * kL, sw, lane);
+        if (gater && it + AH + 1 < n) issue_gates(it + AH + 1, at);
+        at = at + 1 == SM::NB ? 0 : at + 1;
         y_next += y_step;
         z_next += z_step;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = (float)z[kk].v[e] * bw[kk][e >> 2][e & 3];
+#pragma unroll
+          for (int p = 0; p < SM::NH; ++p)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              zf[kk][p].v[e] = (T)v[e];
+              if (p + 1 < SM::NH) v[e] -= (float)zf[kk][p].v[e];
+            }
+        }
         decay_by(dec);
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
@@ -654,17 +757,12 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
           for (int p = 0; p < SM::NH; ++p)
 #pragma unroll
             for (int x = 0; x < NX; ++x) mma(S[x], y[kk][x], zf[kk][p]);
-        yb_at = yb_at + 1 == SM::NY ? 0 : yb_at + 1;
-        zb_at = zb_at + 1 == SM::NZ ? 0 : zb_at + 1;
-        gb = gb == 2 ? 0 : gb + 1;
-        if (it + 1 < n) {
-          weigh(sm.Z[zb_at], sm.Zw[(it + 1) & 1], sm.bw[gb]);
-          if constexpr (!SUMMARY) store_copy(it + 1);
-        }
+        if constexpr (!SUMMARY) store_copy(it + 1);
         // the loads that this chunk has issued may be under way, those before must have landed
-        if (AH == 1 || !more) vm_wait<0>();
+        if (AH == 1 || it + AH + 1 >= n) vm_wait<0>();
         else if (sw == 0) vm_wait<yl.count(0) + zl.count(0)>();
         else if (sw == 1) vm_wait<yl.count(1) + zl.count(1)>();
+        else if (sw == 2 && a.la) vm_wait<yl.count(2) + zl.count(2) + 1>();
         else if (sw == 2) vm_wait<yl.count(2) + zl.count(2)>();
         else vm_wait<yl.count(3) + zl.count(3)>();
         lds_barrier();
@@ -679,7 +777,7 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
       float d = 0.f;
 #pragma unroll
       for (int x = 0; x < NX; ++x) {
-        const int i = slice * kSlice + 16 * zt + l, j = 16 * (xt + x) + 4 * g;
+        const int i = slice * ZS + 16 * zt + l, j = 16 * (xt + x) + 4 * g;
         if (ro.s_out) *reinterpret_cast<f32x4*>(ro.s_out + chain * mat + (size_t)i * DX + j) = S[x];
         if (ro.dot)
 #pragma unroll
@@ -696,12 +794,17 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
   // ---------------------------------------------------------------- the outputs, and the gates
   if (n <= 0) return;
   if constexpr (SUMMARY) {
-    Gates<REV, SM> gates(a, ro, sm, sp, b, h, c_lo, c_hi, lane);
+    Gates<REV, SM> gates(a, ro, sm, sp, c_lo, c_hi, lane);
     lds_barrier();
+    gates.template form<0>(0);
     lds_barrier();
-    for (int it = 0; it < n; ++it) {
-      gates.next(it);
+    for (int it = 0; it < n; it += 2) {
+      gates.template form<1>(it + 1);
       lds_barrier();
+      if (it + 1 < n) {
+        gates.template form<0>(it + 2);
+        lds_barrier();
+      }
     }
     if (slice == 0 && lane == 0) ro.slot_log[(size_t)chain * a.segments + seg] = gates.total;
   } else {
@@ -714,14 +817,16 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
 
 constexpr int walk_threads(bool summary) { return summary ? 320 : 512; }
 
-// Workgroups of a launch: along x, eight chains at a time, each on an XCD of its own, with the roles and slices of
-// a chain (which share its rows) next to each other; along y the segments.
+// Workgroups of a launch: along x, eight chains at a time, one on each XCD, with the roles and slices of a chain (which
+// share its rows) next to each other; along y the segments.  An XCD takes an eighth of the chains in order: heads that
+// lie side by side in a token's row, and with them on the channels of its L2.  (Every eighth chain, two heads of sixteen on
+// an XCD, whose rows 12 KB apart all fell on two channels: 109 against XX us at B4 T4096.)
 template <typename T, int DX, bool SPLIT, bool SUMMARY>
 __global__ __launch_bounds__(walk_threads(SUMMARY)) void la_walk_kernel(Args a) {
   __shared__ __align__(16) Smem<T, DX, SPLIT, SUMMARY> sm;
   const int at = blockIdx.x / 8, group = at / a.slots_per_group;
   int k = at - group * a.slots_per_group, role = 0;
-  const int chain = 8 * group + (int)(blockIdx.x % 8);
+  const int chain = (int)(blockIdx.x % 8) * ((a.chains + 7) / 8) + group;
   if (chain >= a.chains) return;
   while (role + 1 < a.roles && k >= a.role[role].slices) k -= a.role[role++].slices;
   const Role& ro = a.role[role];
@@ -738,19 +843,19 @@ __global__ __launch_bounds__(walk_threads(SUMMARY)) void la_walk_kernel(Args a) 
 // written once.
 template <typename T, int DX>
 __global__ __launch_bounds__(kThreads) void la_step_kernel(Args a) {
-  constexpr int LPR = DX / 4, RPP = kThreads / LPR, NP = kSlice / RPP;
+  constexpr int LPR = DX / 4, RPP = kThreads / LPR, NP = kStepRows / RPP;
   const Role& ro = a.role[0];
-  const int chain = blockIdx.x / ro.slices, slice = blockIdx.x - chain * ro.slices;
+  const int slices = ro.dz / kStepRows, chain = blockIdx.x / slices, slice = blockIdx.x - chain * slices;
   const int b = chain / a.H, h = chain - b * a.H;
   const int col = 4 * (threadIdx.x % LPR), row = threadIdx.x / LPR;
   const Span sp = span_of(a, b);
   const size_t mat = (size_t)ro.dz * DX;
   const T* xb = rows_of<T>(ro.x, ro.xs, ro.x_share, a, sp, b, h) + col;
   const T* yb = rows_of<T>(ro.y, ro.ys, ro.y_share, a, sp, b, h) + col;
-  const T* zb = rows_of<T>(ro.z, ro.zs, ro.z_share, a, sp, b, h) + slice * kSlice + row;
-  T* ob = rows_of<T>(ro.out, ro.os, 1, a, sp, b, h) + slice * kSlice + row;
+  const T* zb = rows_of<T>(ro.z, ro.zs, ro.z_share, a, sp, b, h) + slice * kStepRows + row;
+  T* ob = rows_of<T>(ro.out, ro.os, 1, a, sp, b, h) + slice * kStepRows + row;
   const int64_t la0 = (a.offsets ? sp.row0 * a.ls.t : b * a.ls.b) + h * a.ls.h;
-  const size_t s0 = chain * mat + (size_t)(slice * kSlice + row) * DX + col;
+  const size_t s0 = chain * mat + (size_t)(slice * kStepRows + row) * DX + col;
   f32x4 S[NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
@@ -915,7 +1020,7 @@ void space_for_segments(Args& a, int dx, Space& sp) {
   if (a.segments <= 1) return;
   for (int i = 0; i < a.roles; ++i) {
     Role& r = a.role[i];
-    r.slots = sp.take<float>((size_t)a.chains * a.segments * r.slices * kSlice * dx);
+    r.slots = sp.take<float>((size_t)a.chains * a.segments * r.dz * dx);
     r.slot_log = sp.take<double>((size_t)a.chains * a.segments);
   }
 }
@@ -1090,7 +1195,7 @@ hipError_t launch_linear_attn(const ccq_linear_attn_params& p, hipStream_t strea
   Args a;
   plan_forward(p, a, p.workspace);
   if (p.T <= kStepTokens) {
-    const unsigned grid = (unsigned)a.chains * a.role[0].slices;
+    const unsigned grid = (unsigned)a.chains * (a.role[0].dz / kStepRows);
     if (p.dtype == CCQ_DTYPE_BF16) {
       if (p.d_k == 128) la_step_kernel<__bf16, 128><<<grid, kThreads, 0, stream>>>(a);
       else la_step_kernel<__bf16, 64><<<grid, kThreads, 0, stream>>>(a);
