@@ -133,18 +133,17 @@ struct Smem {
   T Y[NB][kL][PY];
   T Z[NB][kL][PZ];
   T St[SUMMARY ? 1 : 2][NS][SUMMARY ? 1 : ZS][PS];
-  // Rows of x, 16 for each wave, that no other wave reads: when they have become operands, their place holds the
-  // wave's outputs (fp32, pitch PO) and behind these (at OW) what they are multiplied by, until both have left.  fp32 rows
-  // do not fit and are loaded into registers: there only the outputs' place remains.
+  // Rows of x, 16 for each wave of the outputs, which no other wave reads: when they have become operands, the wave's
+  // outputs pass through their place (fp32, pitch PO).  fp32 rows do not fit and are loaded into registers: there only the
+  // outputs' place remains.
   static constexpr bool XL = sizeof(T) == 2;
-  static constexpr int PO = ZS + 4, OW = 16 * PO * 4;
-  static constexpr int XN = XL ? (16 * PY * (int)sizeof(T) > OW + 1024 ? 16 * PY : (OW + 1024) / (int)sizeof(T)) : 16 * PO;
-  T X[SUMMARY ? 1 : XL ? NB : 2][SUMMARY ? 1 : 4][SUMMARY ? 4 : XN];
+  static constexpr int PO = ZS + 4, XN = XL ? (16 * PY * 2 > 16 * PO * 4 ? 16 * PY : 16 * PO * 2) : 16 * PO;
+  T X[SUMMARY ? 1 : XL ? NB : 1][SUMMARY ? 1 : 4][SUMMARY ? 4 : XN];
   // Of each token: its running sum as two floats, the weight of the state before the chunk for it, its weight in
   // the state behind, and e^(its sum to the end of its 16 tokens), or from their beginning.
   float bh[2][kL], bl[2][kL], aw[2][kL], bw[2][kL], cf[2][kL];
   float dec[2];
-  uint32_t raw[NB][kL];        // gates as stored
+  uint32_t raw[NB + 1][kL];    // gates as stored
 };
 
 // A wave's running sum of 64-bit values, in registers alone.
@@ -198,34 +197,37 @@ __device__ __forceinline__ void store_at(UniformPtr p, unsigned off, const V& v)
   *reinterpret_cast<CCQ_GLOBAL V*>(p + off) = v;
 }
 
-// A chunk's rows of COLS entries straight into an LDS tile of pitch P by four waves, rows behind the sequence's end as
-// row 0 (their weights are 0).  Each lane's places are worked out once; unit j of the tile belongs to wave
-// FLIP ? 3 - j % 4 : j % 4, which has count() of them.  The loads are not the compiler's: the caller waits.
-template <typename T, int COLS, int P, bool FLIP>
+// A chunk's rows of COLS entries straight into an LDS tile of pitch P by one wave, rows behind the sequence's end as
+// row 0 (their weights are 0).  Each lane's places are worked out once.  The U loads are not the compiler's: the caller
+// waits.
+template <typename T, int COLS, int P>
 struct RowLoads {
-  static constexpr int U = P * (int)sizeof(T) / 16, DU = COLS * (int)sizeof(T) / 16, M = (U + 3) / 4;
-  unsigned off[M];
-  static constexpr int count(int w) { return (U - (FLIP ? 3 - w : w) + 3) / 4; }
-  __device__ __forceinline__ RowLoads(int w, int lane, int64_t step) {
+  static constexpr int U = P * (int)sizeof(T) / 16, DU = COLS * (int)sizeof(T) / 16;
+  unsigned off[U];
+  __device__ __forceinline__ RowLoads(int lane, int64_t step) {
 #pragma unroll
-    for (int m = 0; m < M; ++m) {
-      const int u = 64 * (4 * m + (FLIP ? 3 - w : w)) + lane, row = u / U, slot = u - row * U;
-      off[m] = slot < DU ? (unsigned)row * (unsigned)(step * (int)sizeof(T)) + 16u * slot : 0u;
+    for (int j = 0; j < U; ++j) {
+      const int u = 64 * j + lane, row = u / U, slot = u - row * U;
+      off[j] = slot < DU ? (unsigned)row * (unsigned)(step * (int)sizeof(T)) + 16u * slot : 0u;
     }
   }
-  __device__ __forceinline__ void load(T (*dst)[P], UniformPtr src, int live, int w, int lane) const {
-    const unsigned base = (unsigned)(uintptr_t)(__attribute__((address_space(3))) T*)&dst[0][0];
+  __device__ __forceinline__ void load(void* dst, UniformPtr src, int live, int lane) const {
+    const unsigned base = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char*)dst;
 #pragma unroll
-    for (int m = 0; m < M; ++m) {
-      const int j = 4 * m + (FLIP ? 3 - w : w);
-      if (j >= U) break;
-      unsigned o = off[m];
+    for (int j = 0; j < U; ++j) {
+      unsigned o = off[j];
       if (live < kL) o = (64 * j + lane) / U < live ? o : 0u;
       const unsigned m0 = __builtin_amdgcn_readfirstlane(base + 1024u * (unsigned)j);
       asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m0), "v"(o), "s"(src) : "memory", "m0");
     }
   }
 };
+
+template <int N>
+__device__ __forceinline__ void vm_wait() {
+  static_assert(N < 64, "the counter of loads under way has six bits");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 
 // Columns of a row-major LDS tile as an MFMA operand in the order of an accumulator pair (tr_frag_acc), from the
 // lane's own place in the tile: what is added to it is known at compile time.
@@ -266,11 +268,6 @@ __device__ __forceinline__ Frag<T> row_at(const T* p) {
   return f;
 }
 
-template <int N>
-__device__ __forceinline__ void vm_wait() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
 // A row as MFMA operands: lane (g, l) entries 8 g .. of every 32 of its row, which begins (with 8 g) at `off`.
 template <typename T, int DX>
 __device__ __forceinline__ void load_x(Frag<T> (&f)[DX / 32], UniformPtr p, unsigned off) {
@@ -306,7 +303,7 @@ struct Gates {
       const bool live = (REV ? c_hi - 1 - it : c_lo + it) * kL + lane < len;
       total += form_gates<REV>(sm, BUF, live && a.la ? gate_value(a, sm.raw[at][lane]) : 0.0, live, in_scale, lane);
     }
-    at = at + 1 == SM::NB ? 0 : at + 1;
+    at = at == SM::NB ? 0 : at + 1;
   }
 };
 // Loads a chunk's gates into the LDS, one a lane, tokens behind the end as the chunk's first.  The caller waits.
@@ -323,31 +320,6 @@ __device__ __forceinline__ void load_gates(const Args& a, uint32_t* dst, int64_t
     asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(m0), "v"(p) : "memory", "m0");
   }
 }
-
-// 16 rows of COLS entries alike, by one wave for itself, the first row `first` of a chunk.
-template <typename T, int COLS, int P>
-struct OwnLoads {
-  static constexpr int U = P * (int)sizeof(T) / 16, DU = COLS * (int)sizeof(T) / 16, COUNT = (16 * U + 63) / 64;
-  unsigned off[COUNT];
-  __device__ __forceinline__ OwnLoads(int first, int lane, int64_t step) {
-#pragma unroll
-    for (int m = 0; m < COUNT; ++m) {
-      const int u = 64 * m + lane, row = u / U, slot = u - row * U;
-      off[m] = slot < DU ? (unsigned)(first + row) * (unsigned)(step * (int)sizeof(T)) + 16u * slot : 0u;
-    }
-  }
-  __device__ __forceinline__ void load(void* dst, UniformPtr src, int first, int live, int lane) const {
-    const unsigned base = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char*)dst;
-#pragma unroll
-    for (int m = 0; m < COUNT; ++m) {
-      unsigned o = off[m];
-      if (live < kL) o = first + (64 * m + lane) / U < live ? o : 0u;
-      const unsigned m0 = __builtin_amdgcn_readfirstlane(base + 1024u * (unsigned)m);
-      if (64 * m + 64 <= 16 * U || 64 * m + lane < 16 * U)
-        asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m0), "v"(o), "s"(src) : "memory", "m0");
-    }
-  }
-};
 
 // Wave W of a walk's outputs: queries 16 W .. 16 W + 15 of every chunk.
 template <typename T, int DX, bool SPLIT, bool REV, int W>
@@ -374,45 +346,37 @@ __device__ __forceinline__ void walk_outputs(const Args& a, const Role& ro, int 
   const unsigned o_own = 16 * W + o_row;
   const unsigned w_off = o_own * (unsigned)(ro.ws.t * (int)sizeof(T)) + o_col * kElem;
   const unsigned o_off = o_own * (unsigned)(ro.os.t * oe) + o_col * oe;
-  constexpr int AX = SM::XL ? 2 : 1;  // chunks that the rows are loaded ahead
-  constexpr int kPlaces = SM::XL ? SM::NB : 2;
-  const OwnLoads<T, DX, SM::PY> xl(16 * W, lane, ro.xs.t);
-  const OwnLoads<T, ZS, ZS> wl(16 * W, lane, ro.ws.t);
-  Frag<T> X[NK], weights;
-  auto issue_x = [&](int it, int to) {
-    const int c = chunk_at(it);
-    xl.load(&sm.X[to][W][0], xb + (int64_t)c * kL * ro.xs.t * kElem, 16 * W, sp.len - c * kL, lane);
-  };
-  auto issue_w = [&](int it, int to) {
-    const int c = chunk_at(it);
-    wl.load(reinterpret_cast<char*>(&sm.X[to][W][0]) + SM::OW, wb + (int64_t)c * kL * ro.ws.t * kElem, 16 * W, sp.len - c * kL, lane);
-  };
+  Frag<T> X[NK], weights[2];
   // fp32: the wave's own rows of a chunk, the chunk's first where the sequence has ended
   auto load_own = [&](int it) {
     const int c = chunk_at(it);
     load_x<T, DX>(X, xb + (int64_t)c * kL * ro.xs.t * kElem, (int)own < sp.len - c * kL ? x_off : 8u * g * kElem);
   };
-  auto load_w = [&](int it) {
-    const int c = chunk_at(it);
+  // what a chunk's outputs are multiplied by, as they leave
+  auto load_w = [&](Frag<T>& f, int it) {
+    const int c = chunk_at(min(it, n - 1));
     const UniformPtr p = wb + (int64_t)c * kL * ro.ws.t * kElem;
     const unsigned off = (int)o_own < sp.len - c * kL ? w_off : (unsigned)o_col * kElem;
-    if constexpr (!SM::XL) {
+    if constexpr (SM::XL) {
+      f.v = load_at<bf16x8>(p, off);
+    } else {
       const f32x4 lo = load_at<f32x4>(p, off), hi = load_at<f32x4>(p, off + 16);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        weights.v[e] = lo[e];
-        weights.v[4 + e] = hi[e];
+        f.v[e] = lo[e];
+        f.v[4 + e] = hi[e];
       }
     }
   };
-  // a chunk's outputs to memory, a chunk later: the stores have time
-  auto flush = [&](int it, int from) {
+  // a chunk's outputs from the accumulators' order to rows, and to memory
+  auto store_rows = [&](const f32x4 (&acc)[NZ], const Frag<T>& w, int it, int xat) {
     const int c = chunk_at(it);
-    const float* src = reinterpret_cast<const float*>(&sm.X[from][W][0]) + o_row * SM::PO + o_col;
+    float* place = reinterpret_cast<float*>(&sm.X[xat][W][0]);
+#pragma unroll
+    for (int z = 0; z < NZ; ++z) *reinterpret_cast<f32x4*>(place + l * SM::PO + 16 * z + 4 * g) = acc[z];
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the wave's own: no barrier
+    const float* src = place + o_row * SM::PO + o_col;
     const f32x4 lo = *reinterpret_cast<const f32x4*>(src), hi = *reinterpret_cast<const f32x4*>(src + 4);
-    if constexpr (SM::XL) {
-      if (ro.r) weights.v = *reinterpret_cast<const bf16x8*>(reinterpret_cast<const char*>(&sm.X[from][W][0]) + SM::OW + 16 * lane);
-    }
     const bool on = (int)o_own < sp.len - c * kL;
     const UniformPtr p = outb + (int64_t)c * kL * ro.os.t * oe;
     if (on) {
@@ -427,9 +391,9 @@ __device__ __forceinline__ void walk_outputs(const Args& a, const Role& ro, int 
     if (ro.r) {
       float r = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) r += lo[e] * (float)weights.v[e];
+      for (int e = 0; e < 4; ++e) r += lo[e] * (float)w.v[e];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) r += hi[e] * (float)weights.v[4 + e];
+      for (int e = 0; e < 4; ++e) r += hi[e] * (float)w.v[4 + e];
       r = group_sum<LPO>(r);
       if (on && o_col == 0) ro.r[((size_t)slice * a.chains + chain) * a.T + c * kL + o_own] = r;
     }
@@ -468,36 +432,23 @@ __device__ __forceinline__ void walk_outputs(const Args& a, const Role& ro, int 
       }
     }
   };
-  if constexpr (SM::XL) {
-    issue_x(0, 0);
-    if (n > 1) issue_x(1, 1);
-  } else {
-    load_own(0);
-  }
+  if constexpr (!SM::XL) load_own(0);
+  if (ro.r) load_w(weights[0], 0);
   auto body = [&](auto gates) {
     lds_barrier();
     if constexpr (kGateWave) gates.template form<0>(0);
     lds_barrier();
-    int at = 0, xat = 0, xbefore = 0;  // it modulo NB, and modulo the places of x; the one before
+    int at = 0;  // it modulo NB
     // one chunk, whose parity GB is
     auto step = [&](auto parity, int it) {
       constexpr int GB = decltype(parity)::value;
+      const int xat = SM::XL ? at : 0;
       if constexpr (SM::XL) {
-        // this chunk's rows have landed, and the stores and weights of the chunk before: all but the next chunk's rows
-        if (it + 1 < n) vm_wait<OwnLoads<T, DX, SM::PY>::COUNT>();
-        else vm_wait<0>();
-        const T* x = &sm.X[xat][W][0] + place;
+        const T* x = &sm.X[xat][0][0] + 16 * W * SM::PY + place;
 #pragma unroll
         for (int kk = 0; kk < NK; ++kk) X[kk] = row_at<T>(x + 32 * kk);
       }
-      if (it > 0) flush(it - 1, xbefore);
-      if constexpr (SM::XL) {
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the places that the loads go to have been read
-        if (ro.r) issue_w(it, xat);
-        if (it + AX < n) issue_x(it + AX, xat == 0 ? kPlaces - 1 : xat - 1);
-      } else {
-        if (ro.r) load_w(it);
-      }
+      if (ro.r) load_w(weights[1 - GB], it + 1);
       const T* st = &sm.St[GB][0][0][0] + s_place;
       const T* z0 = &sm.Z[at][0][0] + z_place;
       const float aw = sm.aw[GB][own], dec = sm.dec[GB];
@@ -547,38 +498,34 @@ __device__ __forceinline__ void walk_outputs(const Args& a, const Role& ro, int 
         }
       }
 #pragma unroll
-      for (int z = 0; z < NZ; ++z) {
+      for (int z = 0; z < NZ; ++z)
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[z][r] *= ro.out_scale;
-        *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(&sm.X[xat][W][0]) + l * SM::PO + 16 * z + 4 * g) = acc[z];
-      }
+      store_rows(acc, weights[GB], it, xat);
       if constexpr (kGateWave) gates.template form<1 - GB>(it + 1);
       at = at + 1 == SM::NB ? 0 : at + 1;
-      xbefore = xat;
-      xat = xat + 1 == kPlaces ? 0 : xat + 1;
       lds_barrier();
     };
     for (int it = 0; it < n; it += 2) {
       step(std::integral_constant<int, 0>{}, it);
       if (it + 1 < n) step(std::integral_constant<int, 1>{}, it + 1);
     }
-    if constexpr (SM::XL) vm_wait<0>();
-    flush(n - 1, xbefore);
   };
   if constexpr (kGateWave) body(Gates<REV, SM>(a, ro, sm, sp, c_lo, c_hi, lane));
   else body(0);
 }
 
 // One chain, slice and segment.  Waves 0 .. 3 form the outputs (SUMMARY: one wave, for the gates alone), the four
-// behind them carry the state, a chunk ahead with b z and two with the loads, so that a chunk has one barrier.
-// SUMMARY: the state alone, from zeros, into the segment's slot.
+// behind them carry the state, two more load (where the other waves issued the loads, 44 KB a chunk at 64 bytes a clock,
+// they stood still for a third of their time), and a chunk has one barrier.  SUMMARY: the state alone, from zeros, into
+// the segment's slot.
 template <typename T, int DX, bool SPLIT, bool REV, bool SUMMARY>
 __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, int slice, int seg, Smem<T, DX, SPLIT, SUMMARY>& sm) {
   using SM = Smem<T, DX, SPLIT, SUMMARY>;
   constexpr int NO = SUMMARY ? 1 : 4, ZS = SM::ZS, NZ = ZS / 16, NX = DX / 16 * NZ / 4, AH = SM::AHEAD;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const bool carries = wave >= NO;
+  const bool carries = wave >= NO && wave < NO + 4;
   const int b = chain / a.H, h = chain - b * a.H;
   Span sp = span_of(a, b);
   sp.len = __builtin_amdgcn_readfirstlane(sp.len);
@@ -596,7 +543,7 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
     if (ro.zero_tail && a.offsets == nullptr) {  // rows of no token
       const int64_t ob = b * ro.os.b + h * ro.os.h + slice * ZS;
       const int last = seg == a.segments - 1 ? a.T : min(a.T, (c_lo + a.chunks_per_segment) * kL);
-      for (int t = max(sp.len, c_lo * kL) + tid / (ZS / 4); t < last; t += 512 / (ZS / 4))
+      for (int t = max(sp.len, c_lo * kL) + tid / (ZS / 4); t < last; t += 640 / (ZS / 4))
         store_out<T>(ro.out, ob + (int64_t)t * ro.os.t + 4 * (tid % (ZS / 4)), zero4(), ro.out_f32);
     }
   }
@@ -658,19 +605,6 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
       }
     }
     if (n > 0) {
-      const UniformPtr yb = uniform_ptr(rows_of<T>(ro.y, ro.ys, ro.y_share, a, sp, b, h));
-      const UniformPtr zb = uniform_ptr(rows_of<T>(ro.z, ro.zs, ro.z_share, a, sp, b, h) + slice * ZS);
-      const RowLoads<T, DX, SM::PY, false> yl(sw, lane, ro.ys.t);
-      const RowLoads<T, ZS, SM::PZ, true> zl(sw, lane, ro.zs.t);
-      const int64_t y_chunk = kL * ro.ys.t * (int)sizeof(T), z_chunk = kL * ro.zs.t * (int)sizeof(T);  // bytes
-      auto issue_y = [&](int it) {
-        const int c = chunk_at(it);
-        yl.load(sm.Y[it % SM::NB], yb + (int64_t)c * y_chunk, sp.len - c * kL, sw, lane);
-      };
-      auto issue_z = [&](int it) {
-        const int c = chunk_at(it);
-        zl.load(sm.Z[it % SM::NB], zb + (int64_t)c * z_chunk, sp.len - c * kL, sw, lane);
-      };
       auto store_copy = [&](int it) {
 #pragma unroll
         for (int x = 0; x < NX; ++x) {
@@ -683,33 +617,11 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
           }
         }
       };
-      const int64_t la0 = (a.offsets ? sp.row0 * a.ls.t : b * a.ls.b) + h * a.ls.h;
-      const bool gater = sw == 2;  // of the waves with the fewest loads
-      auto issue_gates = [&](int it, int to) {
-        const int c = chunk_at(it);
-        load_gates(a, sm.raw[to], la0 + (int64_t)c * kL * a.ls.t, sp.len - c * kL, lane);
-      };
-      if (gater) {
-        issue_gates(0, 0);
-        vm_wait<0>();
-      }
       lds_barrier();
-#pragma unroll
-      for (int i = 0; i < AH; ++i)
-        if (i < n) {
-          if (gater && i > 0) issue_gates(i, i);
-          issue_y(i);
-          issue_z(i);
-        }
-      if (gater && AH < n) issue_gates(AH, AH);
       if constexpr (!SUMMARY) store_copy(0);
-      vm_wait_all();
       lds_barrier();
       const int y_place = tr_place<T>(SM::PY, lane) + 16 * xt, z_place = tr_place<T>(SM::PZ, lane) + 16 * zt;
       int at = 0;  // it modulo NB
-      const int64_t y_step = REV ? -y_chunk : y_chunk, z_step = REV ? -z_chunk : z_chunk;
-      UniformPtr y_next = yb + (int64_t)chunk_at(0) * y_chunk + AH * y_step;
-      UniformPtr z_next = zb + (int64_t)chunk_at(0) * z_chunk + AH * z_step;
       for (int it = 0; it < n; ++it) {
         const T* y0 = &sm.Y[at][0][0] + y_place;
         const T* z0 = &sm.Z[at][0][0] + z_place;
@@ -728,15 +640,7 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
         for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
           for (int x = 0; x < NX; ++x) y[kk][x] = tr_at<T, SM::PY>(y0 + 32 * kk * SM::PY + 16 * x);
-        if (it + AH < n) {
-          const int to = at == 0 ? SM::NB - 1 : at - 1, live = sp.len - chunk_at(it + AH) * kL;
-          yl.load(sm.Y[to], y_next, live, sw, lane);
-          zl.load(sm.Z[to], z_next, live, sw, lane);
-        }
-        if (gater && it + AH + 1 < n) issue_gates(it + AH + 1, at);
         at = at + 1 == SM::NB ? 0 : at + 1;
-        y_next += y_step;
-        z_next += z_step;
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
           float v[8];
@@ -758,13 +662,6 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
 #pragma unroll
             for (int x = 0; x < NX; ++x) mma(S[x], y[kk][x], zf[kk][p]);
         if constexpr (!SUMMARY) store_copy(it + 1);
-        // the loads that this chunk has issued may be under way, those before must have landed
-        if (AH == 1 || it + AH + 1 >= n) vm_wait<0>();
-        else if (sw == 0) vm_wait<yl.count(0) + zl.count(0)>();
-        else if (sw == 1) vm_wait<yl.count(1) + zl.count(1)>();
-        else if (sw == 2 && a.la) vm_wait<yl.count(2) + zl.count(2) + 1>();
-        else if (sw == 2) vm_wait<yl.count(2) + zl.count(2)>();
-        else vm_wait<yl.count(3) + zl.count(3)>();
         lds_barrier();
       }
     }
@@ -791,8 +688,71 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
     }
   }
 
-  // ---------------------------------------------------------------- the outputs, and the gates
   if (n <= 0) return;
+  if (wave >= NO + 4) {
+    // ---------------------------------------------------------------- the loads
+    // the first wave y and the gates, the second z and x
+    auto load_chunks = [&](auto issue, auto count) {
+      for (int i = 0; i < AH && i < n; ++i) issue(i);
+      vm_wait<0>();
+      lds_barrier();
+      for (int it = 0; it < n; ++it) {
+        if (it + AH < n) {
+          issue(it + AH);
+          // what has been issued just now may be under way, what was before must have landed
+          if (AH == 1) vm_wait<0>();
+          else vm_wait<decltype(count)::value>();
+        } else {
+          vm_wait<0>();
+        }
+        lds_barrier();
+      }
+    };
+    if (wave == NO + 4) {
+      const UniformPtr yb = uniform_ptr(rows_of<T>(ro.y, ro.ys, ro.y_share, a, sp, b, h));
+      const RowLoads<T, DX, SM::PY> yl(lane, ro.ys.t);
+      const int64_t la0 = (a.offsets ? sp.row0 * a.ls.t : b * a.ls.b) + h * a.ls.h;
+      auto gates = [&](int it) {
+        const int c = chunk_at(it);
+        load_gates(a, sm.raw[it % (SM::NB + 1)], la0 + (int64_t)c * kL * a.ls.t, sp.len - c * kL, lane);
+      };
+      gates(0);
+      vm_wait<0>();
+      lds_barrier();
+      // a chunk's gates come a chunk before its rows
+      load_chunks(
+          [&](int it) {
+            const int c = chunk_at(it);
+            gates(min(it + 1, n - 1));
+            yl.load(sm.Y[it % SM::NB], yb + (int64_t)c * kL * ro.ys.t * (int)sizeof(T), sp.len - c * kL, lane);
+          },
+          std::integral_constant<int, RowLoads<T, DX, SM::PY>::U>{});
+    } else {
+      const UniformPtr zb = uniform_ptr(rows_of<T>(ro.z, ro.zs, ro.z_share, a, sp, b, h) + slice * ZS);
+      const RowLoads<T, ZS, SM::PZ> zl(lane, ro.zs.t);
+      lds_barrier();
+      if constexpr (!SUMMARY && SM::XL) {
+        const UniformPtr xb = uniform_ptr(rows_of<T>(ro.x, ro.xs, ro.x_share, a, sp, b, h));
+        const RowLoads<T, DX, SM::PY> xl(lane, ro.xs.t);
+        load_chunks(
+            [&](int it) {
+              const int c = chunk_at(it);
+              zl.load(sm.Z[it % SM::NB], zb + (int64_t)c * kL * ro.zs.t * (int)sizeof(T), sp.len - c * kL, lane);
+              xl.load(sm.X[it % SM::NB], xb + (int64_t)c * kL * ro.xs.t * (int)sizeof(T), sp.len - c * kL, lane);
+            },
+            std::integral_constant<int, RowLoads<T, ZS, SM::PZ>::U + RowLoads<T, DX, SM::PY>::U>{});
+      } else {
+        load_chunks(
+            [&](int it) {
+              const int c = chunk_at(it);
+              zl.load(sm.Z[it % SM::NB], zb + (int64_t)c * kL * ro.zs.t * (int)sizeof(T), sp.len - c * kL, lane);
+            },
+            std::integral_constant<int, RowLoads<T, ZS, SM::PZ>::U>{});
+      }
+    }
+    return;
+  }
+  // ---------------------------------------------------------------- the outputs, and the gates
   if constexpr (SUMMARY) {
     Gates<REV, SM> gates(a, ro, sm, sp, c_lo, c_hi, lane);
     lds_barrier();
@@ -815,7 +775,7 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
   }
 }
 
-constexpr int walk_threads(bool summary) { return summary ? 320 : 512; }
+constexpr int walk_threads(bool summary) { return summary ? 448 : 640; }
 
 // Workgroups of a launch: along x, eight chains at a time, one on each XCD, with the roles and slices of a chain (which
 // share its rows) next to each other; along y the segments.  An XCD takes an eighth of the chains in order: heads that
