@@ -10,14 +10,21 @@
 //        adjoint of S (transposed for dk);
 // so one kernel, the walk, computes a "role" (x, y, z, direction), and the gradient is three roles in one launch.
 //
-// The walk.  A workgroup of four waves owns one chain (sequence and head) and a slice of 32 columns of z, keeps
-// its 32 x d_x part of the state in MFMA accumulators, and goes over the chain's 64-token chunks:
-//   scores   K X^T by 16 x 16 tiles, wave w the queries 16 w .. 16 w + 15, against the keys its direction allows;
-//            the tiles, weighted by e^{B_i - B_j} element by element, are the B operand of
-//   near     out^T += Z^T P^T as they lie in the registers;
-//   far      out^T += a_i St X^T with the state's copy St in LDS, in the inputs' type;
-//   update   S^T = e^{B_L} S^T + Y^T (b z), b z as a sum of three bf16 where the inputs have 16 bits: what enters a
-//            state, which later tokens and calls build on, is right to 2^-24.
+// The walk.  A workgroup owns one chain (sequence and head) and a slice of 32 columns of z, keeps its 32 x d_x part of
+// the state in MFMA accumulators, and goes over the chain's 64-token chunks, one barrier a chunk:
+//   two waves issue the rows' loads, straight into LDS, two chunks ahead;
+//   one forms the next chunk's decays;
+//   four form outputs, wave w the tokens 16 w .. 16 w + 15:
+//     scores   Y X^T by 16 x 16 tiles, against the tokens its direction allows; weighted by e^{B_i - B_j} they are the
+//              B operand of
+//     near     out^T += Z^T P^T as they lie in the registers;
+//     far      out^T += a_i St X^T with the state's copy St in LDS, in the inputs' type;
+//   four hold the state, wave w a quarter of d_x:
+//     update   S^T = e^{B_L} S^T + Y^T (b z), b z as a sum of three bf16 where the inputs have 16 bits: what enters a
+//              state, which later tokens and calls build on, is right to 2^-24; and the copy St for the next chunk.
+// What bounds it: the slices of a chain read the same rows, and four workgroups that do so take at most 13.6 TB/s from
+// their L2, 3.4 TB/s of rows; with that alone B4 T4096, 16 heads of 128 takes 87 us, the arithmetic alone 80, both 92.
+// A slice of 64 columns would halve the reading, but its tiles need 174 KB of LDS.
 // Weights of pairs, not e^{B_i} e^{-B_j}: nothing leaves fp32's range whatever the decay.  Running sums are
 // formed in 64 bits and kept as two floats, in units of log 2.
 #include <type_traits>
@@ -121,11 +128,12 @@ __device__ __forceinline__ void store_out(void* p, int64_t at, const f32x4& v, i
 
 template <typename T, int DX, bool SPLIT, bool SUMMARY>
 struct Smem {
-  // Pitches.  Rows of y are read 16 bytes a lane, 16 rows at a time: with 32 bytes behind each row of bf16 that takes
-  // 4.75 clocks a wave, as reads of consecutive addresses do, with 16 bytes 8.  The state's copy is written 8 bytes a lane as
-  // well, which 32 bytes would slow down from 8 clocks to 16.
+  // bf16 rows of x, y and the state's copy lie without padding, 16-byte slot s of row r at slot s ^ swizzle(r): rows and
+  // columns are read at the rate of consecutive addresses (4.75 to 5.25 clocks a wave; with padding 8), and four neighbouring lanes
+  // of a load still take 64 bytes that belong together (with padded rows a load took 44 clocks for 16).  fp32 rows are padded.
   static constexpr int ZS = kSlice;
-  static constexpr int PY = DX + (sizeof(T) == 2 ? 16 : 4), PS = DX + 16 / (int)sizeof(T), PZ = ZS + (sizeof(T) == 2 ? 0 : 4);
+  static constexpr bool SW = sizeof(T) == 2;
+  static constexpr int PY = DX + (SW ? 0 : 4), PS = PY, PZ = ZS + (SW ? 0 : 4);
   static constexpr int AHEAD = sizeof(T) == 2 ? 2 : 1;          // chunks between a load and its use
   static constexpr int NB = AHEAD + 1;                          // tiles held of y and z
   static constexpr int NH = sizeof(T) == 2 ? 3 : 1;             // parts of b z
@@ -133,12 +141,10 @@ struct Smem {
   T Y[NB][kL][PY];
   T Z[NB][kL][PZ];
   T St[SUMMARY ? 1 : 2][NS][SUMMARY ? 1 : ZS][PS];
-  // Rows of x, 16 for each wave of the outputs, which no other wave reads: when they have become operands, the wave's
-  // outputs pass through their place (fp32, pitch PO).  fp32 rows do not fit and are loaded into registers: there only the
-  // outputs' place remains.
-  static constexpr bool XL = sizeof(T) == 2;
-  static constexpr int PO = ZS + 4, XN = XL ? (16 * PY * 2 > 16 * PO * 4 ? 16 * PY : 16 * PO * 2) : 16 * PO;
-  T X[SUMMARY ? 1 : XL ? NB : 1][SUMMARY ? 1 : 4][SUMMARY ? 4 : XN];
+  static constexpr bool XL = sizeof(T) == 2;  // fp32 rows of x do not fit: they are loaded into registers
+  static constexpr int PO = ZS + 4;
+  T X[SUMMARY || !XL ? 1 : NB][SUMMARY || !XL ? 1 : kL][PY];
+  float out[SUMMARY ? 1 : 4][16][PO];  // each wave's outputs of a chunk on their way to memory
   // Of each token: its running sum as two floats, the weight of the state before the chunk for it, its weight in
   // the state behind, and e^(its sum to the end of its 16 tokens), or from their beginning.
   float bh[2][kL], bl[2][kL], aw[2][kL], bw[2][kL], cf[2][kL];
@@ -197,10 +203,14 @@ __device__ __forceinline__ void store_at(UniformPtr p, unsigned off, const V& v)
   *reinterpret_cast<CCQ_GLOBAL V*>(p + off) = v;
 }
 
+// Which slot of 16 bytes of row r of D bf16 the row's first is.
+template <int D>
+__device__ __forceinline__ int swizzle(int r) { return D == 128 ? r & 15 : (r >> 1) & 7; }
+
 // A chunk's rows of COLS entries straight into an LDS tile of pitch P by one wave, rows behind the sequence's end as
 // row 0 (their weights are 0).  Each lane's places are worked out once.  The U loads are not the compiler's: the caller
 // waits.
-template <typename T, int COLS, int P>
+template <typename T, int COLS, int P, bool SWIZZLED>
 struct RowLoads {
   static constexpr int U = P * (int)sizeof(T) / 16, DU = COLS * (int)sizeof(T) / 16;
   unsigned off[U];
@@ -208,7 +218,7 @@ struct RowLoads {
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const int u = 64 * j + lane, row = u / U, slot = u - row * U;
-      off[j] = slot < DU ? (unsigned)row * (unsigned)(step * (int)sizeof(T)) + 16u * slot : 0u;
+      off[j] = slot < DU ? (unsigned)row * (unsigned)(step * (int)sizeof(T)) + 16u * (SWIZZLED ? slot ^ swizzle<COLS>(row) : slot) : 0u;
     }
   }
   __device__ __forceinline__ void load(void* dst, UniformPtr src, int live, int lane) const {
@@ -236,6 +246,13 @@ __device__ __forceinline__ int tr_place(int pitch, int lane) {
   const int g = lane >> 4, i = lane & 15;
   return sizeof(T) == 2 ? (4 * g + (i >> 2)) * pitch + 4 * (i & 3) : 4 * g * pitch + i;
 }
+// As tr_place for columns 16 x .. 16 x + 15 of swizzled rows of D.
+template <typename T, int D, int PITCH>
+__device__ __forceinline__ int tr_place_swizzled(int x, int lane) {
+  if (sizeof(T) == 4) return tr_place<T>(PITCH, lane) + 16 * x;
+  const int g = lane >> 4, i = lane & 15, row = 4 * g + (i >> 2);
+  return row * PITCH + 8 * ((2 * x + ((i & 3) >> 1)) ^ swizzle<D>(row)) + 4 * (i & 1);
+}
 template <typename T, int PITCH>
 __device__ __forceinline__ Frag<T> tr_at(const T* p) {
   Frag<T> f;
@@ -249,9 +266,12 @@ __device__ __forceinline__ Frag<T> tr_at(const T* p) {
   }
   return f;
 }
-// Rows alike (lds_frag in order): lane (g, l) row l, entries 8 g .. 8 g + 7.
-template <typename T>
-__device__ __forceinline__ int row_place(int pitch, int lane) { return (lane & 15) * pitch + 8 * (lane >> 4); }
+// Rows alike (lds_frag in order): lane (g, l) row l, entries 8 g .. 8 g + 7 of every 32: the lane's place for the kk-th of them.
+template <typename T, int D, int PITCH>
+__device__ __forceinline__ int row_place(int kk, int lane) {
+  const int l = lane & 15, slot = 4 * kk + (lane >> 4);
+  return sizeof(T) == 2 ? l * PITCH + 8 * (slot ^ swizzle<D>(l)) : l * PITCH + 8 * slot;
+}
 template <typename T>
 __device__ __forceinline__ Frag<T> row_at(const T* p) {
   Frag<T> f;
@@ -327,7 +347,6 @@ __device__ __forceinline__ void walk_outputs(const Args& a, const Role& ro, int 
                                              Smem<T, DX, SPLIT, false>& sm) {
   using SM = Smem<T, DX, SPLIT, false>;
   constexpr int ZS = SM::ZS, NZ = ZS / 16, NK = DX / 32, T0 = REV ? W : 0, T1 = REV ? 3 : W;
-  constexpr bool kGateWave = W == (REV ? 3 : 0);  // the wave with the fewest score tiles
   const int g = lane >> 4, l = lane & 15, n = c_hi - c_lo;
   const int b = chain / a.H, h = chain - b * a.H;
   auto chunk_at = [&](int it) { return REV ? c_hi - 1 - it : c_lo + it; };
@@ -368,15 +387,11 @@ __device__ __forceinline__ void walk_outputs(const Args& a, const Role& ro, int 
       }
     }
   };
-  // a chunk's outputs from the accumulators' order to rows, and to memory
-  auto store_rows = [&](const f32x4 (&acc)[NZ], const Frag<T>& w, int it, int xat) {
+  // A chunk's outputs, in the accumulators' order when they were put down, as rows to memory: a chunk later, so that neither
+  // the LDS nor the stores are waited for.
+  auto store_rows = [&](const Frag<T>& w, int it) {
     const int c = chunk_at(it);
-    float* place = reinterpret_cast<float*>(&sm.X[xat][W][0]);
-#pragma unroll
-    for (int z = 0; z < NZ; ++z) *reinterpret_cast<f32x4*>(place + l * SM::PO + 16 * z + 4 * g) = acc[z];
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the wave's own: no barrier
-    const float* src = place + o_row * SM::PO + o_col;
-    const f32x4 lo = *reinterpret_cast<const f32x4*>(src), hi = *reinterpret_cast<const f32x4*>(src + 4);
+    const f32x4 lo = *reinterpret_cast<const f32x4*>(&sm.out[W][o_row][o_col]), hi = *reinterpret_cast<const f32x4*>(&sm.out[W][o_row][o_col + 4]);
     const bool on = (int)o_own < sp.len - c * kL;
     const UniformPtr p = outb + (int64_t)c * kL * ro.os.t * oe;
     if (on) {
@@ -398,16 +413,19 @@ __device__ __forceinline__ void walk_outputs(const Args& a, const Role& ro, int 
       if (on && o_col == 0) ro.r[((size_t)slice * a.chains + chain) * a.T + c * kL + o_own] = r;
     }
   };
-  const int place = row_place<T>(SM::PY, lane), s_place = row_place<T>(SM::PS, lane), z_place = tr_place<T>(SM::PZ, lane);
+  int place[NK];  // of rows of x, y and the state's copy alike
+#pragma unroll
+  for (int kk = 0; kk < NK; ++kk) place[kk] = row_place<T, DX, SM::PY>(kk, lane);
+  const int z_place = tr_place<T>(SM::PZ, lane);
   // a chunk's scores, weighted: chunk it, gates in buffer gb
   auto scores = [&](f32x4 (&P)[4], const Frag<T> (&x)[NK], int it, int at, int gb) {
-    const T* y0 = &sm.Y[at][0][0] + place;
+    const T* y0 = &sm.Y[at][0][0];
 #pragma unroll
     for (int t = 0; t < 4; ++t) P[t] = zero4();
 #pragma unroll
     for (int kk = 0; kk < NK; ++kk)
 #pragma unroll
-      for (int t = T0; t <= T1; ++t) mma(P[t], row_at<T>(y0 + 16 * t * SM::PY + 32 * kk), x[kk]);
+      for (int t = T0; t <= T1; ++t) mma(P[t], row_at<T>(y0 + place[kk] + 16 * t * SM::PY), x[kk]);
     const float bh = sm.bh[gb][own], bl = sm.bl[gb][own];
 #pragma unroll
     for (int t = T0; t <= T1; ++t) {
@@ -434,22 +452,21 @@ __device__ __forceinline__ void walk_outputs(const Args& a, const Role& ro, int 
   };
   if constexpr (!SM::XL) load_own(0);
   if (ro.r) load_w(weights[0], 0);
-  auto body = [&](auto gates) {
-    lds_barrier();
-    if constexpr (kGateWave) gates.template form<0>(0);
-    lds_barrier();
+  lds_barrier();
+  lds_barrier();
+  {
     int at = 0;  // it modulo NB
     // one chunk, whose parity GB is
     auto step = [&](auto parity, int it) {
       constexpr int GB = decltype(parity)::value;
-      const int xat = SM::XL ? at : 0;
       if constexpr (SM::XL) {
-        const T* x = &sm.X[xat][0][0] + 16 * W * SM::PY + place;
+        const T* x = &sm.X[at][16 * W][0];
 #pragma unroll
-        for (int kk = 0; kk < NK; ++kk) X[kk] = row_at<T>(x + 32 * kk);
+        for (int kk = 0; kk < NK; ++kk) X[kk] = row_at<T>(x + place[kk]);
       }
+      if (it > 0) store_rows(weights[1 - GB], it - 1);
       if (ro.r) load_w(weights[1 - GB], it + 1);
-      const T* st = &sm.St[GB][0][0][0] + s_place;
+      const T* st = &sm.St[GB][0][0][0];
       const T* z0 = &sm.Z[at][0][0] + z_place;
       const float aw = sm.aw[GB][own], dec = sm.dec[GB];
       // far: the state before the chunk
@@ -461,7 +478,7 @@ __device__ __forceinline__ void walk_outputs(const Args& a, const Role& ro, int 
 #pragma unroll
         for (int z = 0; z < NZ; ++z)
 #pragma unroll
-          for (int s = 0; s < SM::NS; ++s) mma(acc[z], row_at<T>(st + (s * ZS + 16 * z) * SM::PS + 32 * kk), X[kk]);
+          for (int s = 0; s < SM::NS; ++s) mma(acc[z], row_at<T>(st + place[kk] + (s * ZS + 16 * z) * SM::PS), X[kk]);
       scores(P, X, it, at, GB);
       if constexpr (!SM::XL) {
         if (it + 1 < n) load_own(it + 1);
@@ -501,8 +518,8 @@ __device__ __forceinline__ void walk_outputs(const Args& a, const Role& ro, int 
       for (int z = 0; z < NZ; ++z)
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[z][r] *= ro.out_scale;
-      store_rows(acc, weights[GB], it, xat);
-      if constexpr (kGateWave) gates.template form<1 - GB>(it + 1);
+#pragma unroll
+      for (int z = 0; z < NZ; ++z) *reinterpret_cast<f32x4*>(&sm.out[W][l][16 * z + 4 * g]) = acc[z];
       at = at + 1 == SM::NB ? 0 : at + 1;
       lds_barrier();
     };
@@ -510,13 +527,13 @@ __device__ __forceinline__ void walk_outputs(const Args& a, const Role& ro, int 
       step(std::integral_constant<int, 0>{}, it);
       if (it + 1 < n) step(std::integral_constant<int, 1>{}, it + 1);
     }
-  };
-  if constexpr (kGateWave) body(Gates<REV, SM>(a, ro, sm, sp, c_lo, c_hi, lane));
-  else body(0);
+  }
+  if (n & 1) store_rows(weights[0], n - 1);
+  else store_rows(weights[1], n - 1);
 }
 
 // One chain, slice and segment.  Waves 0 .. 3 form the outputs (SUMMARY: one wave, for the gates alone), the four
-// behind them carry the state, two more load (where the other waves issued the loads, 44 KB a chunk at 64 bytes a clock,
+// behind them carry the state, one forms the gates, two load (where the other waves issued the loads, 44 KB a chunk at 64 bytes a clock,
 // they stood still for a third of their time), and a chunk has one barrier.  SUMMARY: the state alone, from zeros, into
 // the segment's slot.
 template <typename T, int DX, bool SPLIT, bool REV, bool SUMMARY>
@@ -543,7 +560,7 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
     if (ro.zero_tail && a.offsets == nullptr) {  // rows of no token
       const int64_t ob = b * ro.os.b + h * ro.os.h + slice * ZS;
       const int last = seg == a.segments - 1 ? a.T : min(a.T, (c_lo + a.chunks_per_segment) * kL);
-      for (int t = max(sp.len, c_lo * kL) + tid / (ZS / 4); t < last; t += 640 / (ZS / 4))
+      for (int t = max(sp.len, c_lo * kL) + tid / (ZS / 4); t < last; t += 704 / (ZS / 4))
         store_out<T>(ro.out, ob + (int64_t)t * ro.os.t + 4 * (tid % (ZS / 4)), zero4(), ro.out_f32);
     }
   }
@@ -608,22 +625,26 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
       auto store_copy = [&](int it) {
 #pragma unroll
         for (int x = 0; x < NX; ++x) {
-          st4<T>(&sm.St[it & 1][0][16 * zt + l][16 * (xt + x) + 4 * g], S[x]);
+          const int slot = 2 * (xt + x) + (g >> 1), at = SM::SW ? 8 * (slot ^ swizzle<DX>(l)) + 4 * (g & 1) : 16 * (xt + x) + 4 * g;
+          st4<T>(&sm.St[it & 1][0][16 * zt + l][at], S[x]);
           if constexpr (SM::NS == 2) {
             f32x4 lo;
 #pragma unroll
             for (int r = 0; r < 4; ++r) lo[r] = S[x][r] - (float)(__bf16)S[x][r];
-            st4<T>(&sm.St[it & 1][1][16 * zt + l][16 * (xt + x) + 4 * g], lo);
+            st4<T>(&sm.St[it & 1][1][16 * zt + l][at], lo);
           }
         }
       };
       lds_barrier();
       if constexpr (!SUMMARY) store_copy(0);
       lds_barrier();
-      const int y_place = tr_place<T>(SM::PY, lane) + 16 * xt, z_place = tr_place<T>(SM::PZ, lane) + 16 * zt;
+      int y_place[NX];
+#pragma unroll
+      for (int x = 0; x < NX; ++x) y_place[x] = tr_place_swizzled<T, DX, SM::PY>(xt + x, lane);
+      const int z_place = tr_place<T>(SM::PZ, lane) + 16 * zt;
       int at = 0;  // it modulo NB
       for (int it = 0; it < n; ++it) {
-        const T* y0 = &sm.Y[at][0][0] + y_place;
+        const T* y0 = &sm.Y[at][0][0];
         const T* z0 = &sm.Z[at][0][0] + z_place;
         const float dec = sm.dec[it & 1];
         // b z: the lane's eight tokens of every 32, as tr_at has them
@@ -639,7 +660,7 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-          for (int x = 0; x < NX; ++x) y[kk][x] = tr_at<T, SM::PY>(y0 + 32 * kk * SM::PY + 16 * x);
+          for (int x = 0; x < NX; ++x) y[kk][x] = tr_at<T, SM::PY>(y0 + y_place[x] + 32 * kk * SM::PY);
         at = at + 1 == SM::NB ? 0 : at + 1;
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
@@ -689,7 +710,7 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
   }
 
   if (n <= 0) return;
-  if (wave >= NO + 4) {
+  if (wave >= NO + 4 && wave < NO + 6) {
     // ---------------------------------------------------------------- the loads
     // the first wave y and the gates, the second z and x
     auto load_chunks = [&](auto issue, auto count) {
@@ -710,7 +731,7 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
     };
     if (wave == NO + 4) {
       const UniformPtr yb = uniform_ptr(rows_of<T>(ro.y, ro.ys, ro.y_share, a, sp, b, h));
-      const RowLoads<T, DX, SM::PY> yl(lane, ro.ys.t);
+      const RowLoads<T, DX, SM::PY, SM::SW> yl(lane, ro.ys.t);
       const int64_t la0 = (a.offsets ? sp.row0 * a.ls.t : b * a.ls.b) + h * a.ls.h;
       auto gates = [&](int it) {
         const int c = chunk_at(it);
@@ -726,34 +747,34 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
             gates(min(it + 1, n - 1));
             yl.load(sm.Y[it % SM::NB], yb + (int64_t)c * kL * ro.ys.t * (int)sizeof(T), sp.len - c * kL, lane);
           },
-          std::integral_constant<int, RowLoads<T, DX, SM::PY>::U>{});
+          std::integral_constant<int, RowLoads<T, DX, SM::PY, SM::SW>::U>{});
     } else {
       const UniformPtr zb = uniform_ptr(rows_of<T>(ro.z, ro.zs, ro.z_share, a, sp, b, h) + slice * ZS);
-      const RowLoads<T, ZS, SM::PZ> zl(lane, ro.zs.t);
+      const RowLoads<T, ZS, SM::PZ, false> zl(lane, ro.zs.t);
       lds_barrier();
       if constexpr (!SUMMARY && SM::XL) {
         const UniformPtr xb = uniform_ptr(rows_of<T>(ro.x, ro.xs, ro.x_share, a, sp, b, h));
-        const RowLoads<T, DX, SM::PY> xl(lane, ro.xs.t);
+        const RowLoads<T, DX, SM::PY, SM::SW> xl(lane, ro.xs.t);
         load_chunks(
             [&](int it) {
               const int c = chunk_at(it);
               zl.load(sm.Z[it % SM::NB], zb + (int64_t)c * kL * ro.zs.t * (int)sizeof(T), sp.len - c * kL, lane);
               xl.load(sm.X[it % SM::NB], xb + (int64_t)c * kL * ro.xs.t * (int)sizeof(T), sp.len - c * kL, lane);
             },
-            std::integral_constant<int, RowLoads<T, ZS, SM::PZ>::U + RowLoads<T, DX, SM::PY>::U>{});
+            std::integral_constant<int, RowLoads<T, ZS, SM::PZ, false>::U + RowLoads<T, DX, SM::PY, SM::SW>::U>{});
       } else {
         load_chunks(
             [&](int it) {
               const int c = chunk_at(it);
               zl.load(sm.Z[it % SM::NB], zb + (int64_t)c * kL * ro.zs.t * (int)sizeof(T), sp.len - c * kL, lane);
             },
-            std::integral_constant<int, RowLoads<T, ZS, SM::PZ>::U>{});
+            std::integral_constant<int, RowLoads<T, ZS, SM::PZ, false>::U>{});
       }
     }
     return;
   }
   // ---------------------------------------------------------------- the outputs, and the gates
-  if constexpr (SUMMARY) {
+  if (SUMMARY || wave == NO + 6) {
     Gates<REV, SM> gates(a, ro, sm, sp, c_lo, c_hi, lane);
     lds_barrier();
     gates.template form<0>(0);
@@ -766,8 +787,10 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
         lds_barrier();
       }
     }
-    if (slice == 0 && lane == 0) ro.slot_log[(size_t)chain * a.segments + seg] = gates.total;
-  } else {
+    if (SUMMARY && slice == 0 && lane == 0) ro.slot_log[(size_t)chain * a.segments + seg] = gates.total;
+    return;
+  }
+  if constexpr (!SUMMARY) {
     if (wave == 0) walk_outputs<T, DX, SPLIT, REV, 0>(a, ro, chain, slice, sp, c_lo, c_hi, lane, sm);
     else if (wave == 1) walk_outputs<T, DX, SPLIT, REV, 1>(a, ro, chain, slice, sp, c_lo, c_hi, lane, sm);
     else if (wave == 2) walk_outputs<T, DX, SPLIT, REV, 2>(a, ro, chain, slice, sp, c_lo, c_hi, lane, sm);
@@ -775,12 +798,11 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
   }
 }
 
-constexpr int walk_threads(bool summary) { return summary ? 448 : 640; }
+constexpr int walk_threads(bool summary) { return summary ? 448 : 704; }
 
-// Workgroups of a launch: along x, eight chains at a time, one on each XCD, with the roles and slices of a chain (which
-// share its rows) next to each other; along y the segments.  An XCD takes an eighth of the chains in order: heads that
-// lie side by side in a token's row, and with them on the channels of its L2.  (Every eighth chain, two heads of sixteen on
-// an XCD, whose rows 12 KB apart all fell on two channels: 109 against XX us at B4 T4096.)
+// Workgroups of a launch: along x, eight chains at a time, one on each XCD, with the roles and slices of a chain next to
+// each other, so that rows which they share come into one L2 once; along y the segments.  An XCD takes an eighth of the
+// chains in order.
 template <typename T, int DX, bool SPLIT, bool SUMMARY>
 __global__ __launch_bounds__(walk_threads(SUMMARY)) void la_walk_kernel(Args a) {
   __shared__ __align__(16) Smem<T, DX, SPLIT, SUMMARY> sm;
@@ -876,8 +898,11 @@ __global__ __launch_bounds__(kThreads) void la_sum_kernel(SumArgs a) {
   }
 }
 
-// dlog alpha of one chain: the sums from the end of rq - rk (over the slices), plus the state's product, in 64 bits.
-constexpr int kGateThreads = 1024;
+// dlog alpha of one chain: the sums from the end of rq - rk (over the slices), plus the state's product, in 64 bits.  A
+// thread takes four tokens that follow each other, so that a few thousand tokens are one round of loads and one scan
+// (one token a thread: 24 us for 64 chains of 4096, now 17).
+constexpr int kGateThreads = 1024, kGateRun = 4;
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
 struct GateArgs {
   Args a;
   const float *rq, *rk, *dot;  // [slices][chains][T], the same, [chains][dot_slices] or null
@@ -904,28 +929,40 @@ __global__ __launch_bounds__(kGateThreads) void la_gate_kernel(GateArgs q) {
     behind = s;
   }
   __syncthreads();
-  for (int last = sp.len; last > 0; last -= kGateThreads) {  // thread 0 the last token of the stretch
-    const int t = last - 1 - tid;
-    double r = 0.0;
-    if (t >= 0) {
-      for (int s = 0; s < q.q_slices; ++s) r += (double)q.rq[((size_t)s * a.chains + chain) * a.T + t];
-      for (int s = 0; s < q.k_slices; ++s) r -= (double)q.rk[((size_t)s * a.chains + chain) * a.T + t];
-    }
+  for (int last = sp.len; last > 0; last -= kGateThreads * kGateRun) {  // thread 0 the last tokens of the stretch
+    const int t0 = last - kGateRun * (tid + 1);                          // may be below 0
+    unsigned bits[kGateRun];
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const double up = __shfl_up(r, off, 64);
-      if (lane >= off) r += up;
-    }
-    if (lane == 63) tops[w] = r;
+    for (int i = 0; i < kGateRun; ++i) bits[i] = t0 + i >= 0 ? gate_bits(a, la0 + (int64_t)(t0 + i) * a.ls.t) : 0u;
+    double r[kGateRun] = {0.0, 0.0, 0.0, 0.0};
+    auto add = [&](const float* p, int slices, double sign) {
+      for (int s = 0; s < slices; ++s, p += (size_t)a.chains * a.T) {
+        if (t0 >= 0) {
+          const f32x4_any v = *reinterpret_cast<const f32x4_any*>(p + t0);
+#pragma unroll
+          for (int i = 0; i < kGateRun; ++i) r[i] += sign * (double)v[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < kGateRun; ++i)
+            if (t0 + i >= 0) r[i] += sign * (double)p[t0 + i];
+        }
+      }
+    };
+    add(q.rq + (size_t)chain * a.T, q.q_slices, 1.0);
+    add(q.rk + (size_t)chain * a.T, q.k_slices, -1.0);
+#pragma unroll
+    for (int i = kGateRun - 2; i >= 0; --i) r[i] += r[i + 1];
+    double sum = wave_running(r[0]);
+    const double before = sum - r[0];
+    if (lane == 63) tops[w] = sum;
     __syncthreads();
-    for (int i = 0; i < w; ++i) r += tops[i];
-    const double sum = r + behind;
-    if (t >= 0) {
-      const bool dropped = exp2_fast((float)gate_of(a, la0 + (int64_t)t * a.ls.t)) == 0.f;
-      store(t, dropped ? 0.f : (float)sum);
-    }
+    double base = before + behind;
+    for (int i = 0; i < w; ++i) base += tops[i];
+#pragma unroll
+    for (int i = 0; i < kGateRun; ++i)
+      if (t0 + i >= 0) store(t0 + i, exp2_fast((float)gate_value(a, bits[i])) == 0.f ? 0.f : (float)(r[i] + base));
     __syncthreads();
-    if (tid == kGateThreads - 1) behind = sum;
+    if (tid == kGateThreads - 1) behind = base + r[0];
     __syncthreads();
   }
   if (a.offsets == nullptr)
@@ -950,14 +987,26 @@ struct Space {
 
 constexpr int kStepTokens = 8;
 
-// Segments: enough workgroups for the card, of at least four chunks each.
+// Segments of a sequence.  A workgroup has a CU to itself, so `groups` of them (chains, roles and slices) take
+// ceil(groups / 256) turns of all its chunks; cut in P they take turns of a P-th, behind a summary, which takes about
+// half as long for a chunk, two to a CU, and a launch that costs some six chunks.  The P with the least of these.  (One sequence of
+// 20,480 tokens, 16 heads of 128: 355 us whole, 169 with 4; 42 chains of up to 777 tokens in fp32: 45 whole, 59 with 2.)
 void split_of(const ccq_linear_attn_params& p, int groups, int* segments, int* per) {
   const int nc = (p.T - 1) / kL + 1;
-  int want = (256 + groups - 1) / groups;
-  want = want < 1 ? 1 : (want > 32 ? 32 : want);
-  if (want > nc / 4) want = nc / 4 < 1 ? 1 : nc / 4;
-  *per = (nc + want - 1) / want;
-  *segments = (nc + *per - 1) / *per;
+  *segments = 1;
+  *per = nc;
+  int64_t least = 0;
+  for (int s = 1; s <= 32 && s <= nc; ++s) {
+    const int each = (nc + s - 1) / s;
+    if (s > 1 && (s - 1) * each >= nc) continue;  // the last one would be empty
+    int64_t cost = 2 * (((int64_t)groups * s + 255) / 256) * each;
+    if (s > 1) cost += 12 + (((int64_t)groups * (s - 1) + 511) / 512) * each * 2 + s;
+    if (s == 1 || cost < least) {
+      least = cost;
+      *segments = s;
+      *per = each;
+    }
+  }
 }
 
 Args base_of(const ccq_linear_attn_params& p) {
