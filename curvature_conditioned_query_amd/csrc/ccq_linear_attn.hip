@@ -800,16 +800,18 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
 
 constexpr int walk_threads(bool summary) { return summary ? 448 : 704; }
 
+constexpr unsigned kGridX = 1u << 22;  // a launch has less than 2^32 threads along x; what is more lies along z
+
 // Workgroups of a launch: along x, eight chains at a time, one on each XCD, with the roles and slices of a chain next to
 // each other, so that rows which they share come into one L2 once; along y the segments.  An XCD takes an eighth of the
 // chains in order.
 template <typename T, int DX, bool SPLIT, bool SUMMARY>
 __global__ __launch_bounds__(walk_threads(SUMMARY)) void la_walk_kernel(Args a) {
   __shared__ __align__(16) Smem<T, DX, SPLIT, SUMMARY> sm;
-  const int at = blockIdx.x / 8, group = at / a.slots_per_group;
+  const int block = blockIdx.z * kGridX + blockIdx.x, at = block / 8, group = at / a.slots_per_group;
   int k = at - group * a.slots_per_group, role = 0;
-  const int chain = (int)(blockIdx.x % 8) * ((a.chains + 7) / 8) + group;
-  if (chain >= a.chains) return;
+  const int each = (a.chains + 7) / 8, chain = block % 8 * each + group;
+  if (group >= each || chain >= a.chains) return;
   while (role + 1 < a.roles && k >= a.role[role].slices) k -= a.role[role++].slices;
   const Role& ro = a.role[role];
   const bool rev = ro.reverse != 0;
@@ -1072,8 +1074,9 @@ char* plan_forward(const ccq_linear_attn_params& p, Args& a, void* workspace) {
 template <typename T, int DX, bool SPLIT>
 hipError_t run_walk(const Args& a, hipStream_t stream) {
   const unsigned groups = (unsigned)((a.chains + 7) / 8 * 8) * a.slots_per_group;
-  if (a.segments > 1) la_walk_kernel<T, DX, false, true><<<dim3(groups, a.segments - 1), walk_threads(true), 0, stream>>>(a);
-  la_walk_kernel<T, DX, SPLIT, false><<<dim3(groups, a.segments), walk_threads(false), 0, stream>>>(a);
+  const unsigned x = groups < kGridX ? groups : kGridX, z = (groups - 1) / kGridX + 1;
+  if (a.segments > 1) la_walk_kernel<T, DX, false, true><<<dim3(x, a.segments - 1, z), walk_threads(true), 0, stream>>>(a);
+  la_walk_kernel<T, DX, SPLIT, false><<<dim3(x, a.segments, z), walk_threads(false), 0, stream>>>(a);
   return hipGetLastError();
 }
 

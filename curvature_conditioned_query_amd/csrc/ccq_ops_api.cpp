@@ -481,7 +481,10 @@ int validate_adjust(const ccq_logits_adjust_params* p) {
                      {p->bias_token, rows * p->n_bias * 4},
                      {p->bias_value, rows * p->n_bias * 4},
                      {p->allowed, rows * (((size_t)p->V + 31) / 32) * 4}};
-  if (any_misaligned(r) || misaligned(p->logits)) return CCQ_ERR_MISALIGNED;
+  // rows may stand anywhere, so each tensor needs its elements' alignment only
+  if (((reinterpret_cast<uintptr_t>(p->logits) | reinterpret_cast<uintptr_t>(p->out)) & (E - 1)) != 0) return CCQ_ERR_MISALIGNED;
+  for (size_t i = 2; i < sizeof(r) / sizeof(r[0]); ++i)
+    if ((reinterpret_cast<uintptr_t>(r[i].p) & 3u) != 0) return CCQ_ERR_MISALIGNED;
   if (written_overlaps(r, 11, 1)) return CCQ_ERR_INVALID_ARG;
   return CCQ_OK;
 }

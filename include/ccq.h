@@ -673,7 +673,8 @@ typedef struct {
  *   x = x - frequency c - presence [c > 0] + the sum of v's biases, in the list's order;
  *   out[v] = x if v is allowed, else -INFINITY (whatever x is).
  * The arithmetic is fp32; the result is rounded once; a logit that nothing touches stays as it is, a NaN
- * or infinity too.  repetition must be above 0 (a row's own is taken as it stands).  V <= 2^24, L <= 2^24,
+ * or infinity too.  repetition must be above 0 (a row's own is taken as it stands).  Every pointer needs the
+ * alignment of its elements only, so rows of a larger batch can be given as they are.  V <= 2^24, L <= 2^24,
  * R (V / 4096 + 1) < 2^24 (CCQ_ERR_UNSUPPORTED beyond).  Returns a ccq_status.
  */
 int ccq_logits_adjust(const ccq_logits_adjust_params *p, void *hip_stream);

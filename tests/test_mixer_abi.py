@@ -65,14 +65,14 @@ LA_BAD = [
     (dict(v=None), INVALID), (dict(rows=5), INVALID), (dict(offsets=BASE + 40 * GIB, rows=2000), INVALID),
     (dict(lengths=None, offsets=BASE + 40 * GIB), INVALID), (dict(lengths=None, offsets=BASE + 40 * GIB, rows=1 << 31), UNSUPPORTED),
     (dict(lengths=None, offsets=BASE + 40 * GIB, rows=-1), INVALID),
-    (dict(q_stride_t=-8), INVALID), (dict(k_stride_b=1 << 60), INVALID), (dict(v_stride_h=130), MISALIGNED),
+    (dict(q_stride_t=-8), INVALID), (dict(q_stride_t=1 << 24), UNSUPPORTED), (dict(k_stride_b=1 << 60), INVALID), (dict(v_stride_h=130), MISALIGNED),
     (dict(q_stride_t=132), MISALIGNED), (dict(la_stride_t=-1), INVALID), (dict(q=BASE + 2), MISALIGNED),
     (dict(gate_dtype=0, log_alpha=at("log_alpha") + 2), MISALIGNED), (dict(lengths=at("lengths") + 4), MISALIGNED),
 ]
 
 
 @pytest.mark.parametrize("kw,code", LA_BAD + [
-    (dict(o=None), INVALID), (dict(o_stride_t=256), INVALID), (dict(o_stride_h=0), INVALID), (dict(o_stride_t=516), MISALIGNED),
+    (dict(o=None), INVALID), (dict(o_stride_t=1 << 24, o_stride_b=1 << 36), UNSUPPORTED), (dict(o_stride_t=256), INVALID), (dict(o_stride_h=0), INVALID), (dict(o_stride_t=516), MISALIGNED),
     (dict(o=BASE), INVALID), (dict(o=at("v") + 256), INVALID), (dict(S_out=at("S0") + 16), INVALID), (dict(S_out=at("k")), INVALID),
     (dict(workspace=at("o")), INVALID), (dict(o=at("log_alpha")), INVALID), (dict(o=at("S0")), INVALID), (dict(o=at("lengths")), INVALID),
     (dict(S_out=at("S_out") + 4), MISALIGNED), (dict(T=30000, o=at("S0")), INVALID)])
@@ -114,7 +114,8 @@ def _lab(**kw):
 @pytest.mark.parametrize("kw,code", [({"fwd." + k: v for k, v in kw.items()}, c) for kw, c in LA_BAD] + [
     (dict(grad_dtype=2), INVALID), ({"fwd.dtype": 0, "grad_dtype": 1}, INVALID), (dict(d_o=None), INVALID), (dict(dq=None), INVALID),
     (dict(dk=None), INVALID), (dict(dv=None), INVALID), ({"fwd.log_alpha": None}, INVALID), (dict(do_stride_t=-8), INVALID),
-    (dict(do_stride_h=60), MISALIGNED), (dict(dq_stride_t=64), INVALID), (dict(dk_stride_t=0), INVALID), (dict(dv_stride_h=4), MISALIGNED),
+    (dict(do_stride_h=60), MISALIGNED), (dict(dq_stride_t=64), INVALID), (dict(dq_stride_t=1 << 24, dq_stride_b=1 << 36), UNSUPPORTED),
+    (dict(dk_stride_t=0), INVALID), (dict(dv_stride_h=4), MISALIGNED),
     (dict(dq=bat("dk")), INVALID), (dict(dq=bat("dv") + 16), INVALID), (dict(dq=bat("d_o")), INVALID), (dict(dv=at("q")), INVALID),
     (dict(dS0=bat("dS_out")), INVALID), (dict(dS0=at("S0")), INVALID), (dict(dlog_alpha=at("log_alpha")), INVALID),
     (dict(dlog_alpha=bat("dq") + 64), INVALID), (dict(workspace=bat("dq")), INVALID), (dict(workspace=None), WORKSPACE),
@@ -209,8 +210,8 @@ def _adj(**kw):
     (dict(presence=float("inf")), INVALID), (dict(frequency=float("nan")), INVALID), (dict(n_bias=1025), UNSUPPORTED),
     (dict(V=(1 << 24) + 1, logits_stride=1 << 25, out_stride=1 << 25), UNSUPPORTED), (dict(L=(1 << 24) + 1), UNSUPPORTED),
     (dict(R=1 << 24), UNSUPPORTED), (dict(R=1 << 12, V=1 << 24, logits_stride=1 << 24, out_stride=1 << 24), UNSUPPORTED),
-    (dict(logits=None), INVALID), (dict(out=None), INVALID), (dict(logits=BASE + 2), MISALIGNED),
-    (dict(history=aat("history") + 4), MISALIGNED), (dict(out=aat("out") + 8), MISALIGNED), (dict(out=BASE, out_stride=1002), INVALID),
+    (dict(logits=None), INVALID), (dict(out=None), INVALID), (dict(logits=BASE + 1), MISALIGNED),
+    (dict(dtype=0, logits=BASE + 2), MISALIGNED), (dict(history=aat("history") + 2), MISALIGNED), (dict(out=aat("out") + 1), MISALIGNED), (dict(out=BASE, out_stride=1002), INVALID),
     (dict(out=BASE + 16), INVALID), (dict(out=aat("allowed")), INVALID), (dict(out=aat("lengths")), INVALID)])
 def test_logits_adjust_refusals(lib, kw, code):
     assert lib.ccq_logits_adjust(_adj(**kw), None) == code
