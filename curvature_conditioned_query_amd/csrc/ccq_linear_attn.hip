@@ -532,6 +532,8 @@ __device__ __forceinline__ void walk_outputs(const Args& a, const Role& ro, int 
   else store_rows(weights[1], n - 1);
 }
 
+constexpr int walk_threads(bool summary) { return summary ? 448 : 704; }
+
 // One chain, slice and segment.  Waves 0 .. 3 form the outputs (SUMMARY: one wave, for the gates alone), the four
 // behind them carry the state, one forms the gates, two load (where the other waves issued the loads, 44 KB a chunk at 64 bytes a clock,
 // they stood still for a third of their time), and a chunk has one barrier.  SUMMARY: the state alone, from zeros, into
@@ -560,7 +562,7 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
     if (ro.zero_tail && a.offsets == nullptr) {  // rows of no token
       const int64_t ob = b * ro.os.b + h * ro.os.h + slice * ZS;
       const int last = seg == a.segments - 1 ? a.T : min(a.T, (c_lo + a.chunks_per_segment) * kL);
-      for (int t = max(sp.len, c_lo * kL) + tid / (ZS / 4); t < last; t += 704 / (ZS / 4))
+      for (int t = max(sp.len, c_lo * kL) + tid / (ZS / 4); t < last; t += walk_threads(false) / (ZS / 4))
         store_out<T>(ro.out, ob + (int64_t)t * ro.os.t + 4 * (tid % (ZS / 4)), zero4(), ro.out_f32);
     }
   }
@@ -797,8 +799,6 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
     else walk_outputs<T, DX, SPLIT, REV, 3>(a, ro, chain, slice, sp, c_lo, c_hi, lane, sm);
   }
 }
-
-constexpr int walk_threads(bool summary) { return summary ? 448 : 704; }
 
 constexpr unsigned kGridX = 1u << 22;  // a launch has less than 2^32 threads along x; what is more lies along z
 
