@@ -5,9 +5,9 @@
 // lane, twice that where d > 512.  A thread keeps its group and channels while it walks over tokens, so the weights
 // stay in registers and the weights' gradients gather there; consecutive rows of a workgroup are `groups` groups of a
 // token and then the next token.
-// 16,384 tokens of 16 groups of 128 in bf16, gated: 40 us, 5.0 TB/s (45 with twice the workgroups, whose weights are
-// loaded as often; 46 with two rows of a thread in flight, which fewer waves then fit).  Gradient of 6,141 tokens of 12
-// groups of 80 in fp32: 25 us with the sum of the weights' gradients.
+// 16,384 tokens of 16 groups of 128 in bf16, gated: 37 us, 5.5 TB/s (45 with twice the workgroups, whose weights are
+// loaded as often, and one row of 256 bytes a workgroup; 46 with two rows of a thread in flight, which fewer waves then
+// fit).  Gradient of 6,141 tokens of 12 groups of 80 in fp32: 23 us with the sum of the weights' gradients.
 #include <type_traits>
 
 #include "ccq_device.hpp"

@@ -152,8 +152,8 @@ __global__ __launch_bounds__(kThreads) void logits_adjust_kernel(ccq_logits_adju
   }
   __syncthreads();
   auto count = [&](int i, int v) {
+    if (i >= n || v < base || v >= end) return;
     const int at = v - base;
-    if (i >= n || at < 0 || at >= end - base) return;
     if (i < prompt) atomicOr(&table[at], kSeen);
     else atomicAdd(&table[at], 1u);
   };
