@@ -149,3 +149,29 @@ def test_binding_refusals_on_device(gpu_lib):
             ccq_logits_adjust(**{**c, **kw})
     with pytest.raises(CcqError):
         ccq_logits_adjust(c["logits"], repetition=0.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("L", [32767, 32768])
+def test_one_token_all_along_a_history(gpu_lib, L, dtype):
+    """The largest counts of 16-bit entries and the first beyond them, beside neighbours that stand there once, with biases
+    at a stretch's first and last tokens."""
+    import torch
+    from curvature_conditioned_query_amd import ccq_logits_adjust
+    c = _case(4, 20001, L, 6, dtype, mask=False, lengths=False, prompts=False, seed=2)
+    h = c["history"]
+    h[:2], h[2:] = 16383, 8192
+    h[1, 5], h[1, 6], h[3, 7], h[3, 8] = 16382, 16384, 8193, 8191
+    c["prompt_lengths"] = torch.tensor([0, 1, L, L - 1], dtype=torch.int32, device="cuda")
+    c["bias_token"][:, :4] = torch.tensor([16383, 16384, 8191, 0], dtype=torch.int32, device="cuda")
+    c["frequency"] = 2.0 ** -10
+    _check(ccq_logits_adjust(**c), c, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_of_a_larger_batch(gpu_lib, dtype):
+    """Parts that begin anywhere: only the elements' alignment is asked for."""
+    from curvature_conditioned_query_amd import ccq_logits_adjust
+    c = _case(5, 1003, 51, 5, dtype, seed=3)
+    part = ccq_logits_adjust(**{m: t[1:4] for m, t in c.items()})
+    _check(part, {m: t[1:4] for m, t in c.items()}, dtype)
