@@ -209,7 +209,7 @@ __device__ __forceinline__ int swizzle(int r) { return D == 128 ? r & 15 : (r >>
 
 // A chunk's rows of COLS entries straight into an LDS tile of pitch P by one wave, rows behind the sequence's end as
 // row 0 (their weights are 0).  Each lane's places are worked out once.  The U loads are not the compiler's: the caller
-// waits.
+// waits, and the s_nop is the wait state that a load into LDS needs behind a write of M0.
 template <typename T, int COLS, int P, bool SWIZZLED>
 struct RowLoads {
   static constexpr int U = P * (int)sizeof(T) / 16, DU = COLS * (int)sizeof(T) / 16;
@@ -228,7 +228,7 @@ struct RowLoads {
       unsigned o = off[j];
       if (live < kL) o = (64 * j + lane) / U < live ? o : 0u;
       const unsigned m0 = __builtin_amdgcn_readfirstlane(base + 1024u * (unsigned)j);
-      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m0), "v"(o), "s"(src) : "memory", "m0");
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m0), "v"(o), "s"(src) : "memory", "m0");
     }
   }
 };
@@ -334,10 +334,10 @@ __device__ __forceinline__ void load_gates(const Args& a, uint32_t* dst, int64_t
   const int64_t own = at + (lane < live ? lane * a.ls.t : 0);
   if (a.gate_bf16) {
     const uint16_t* p = static_cast<const uint16_t*>(a.la) + own;
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_ushort %1, off" ::"s"(m0), "v"(p) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ushort %1, off" ::"s"(m0), "v"(p) : "memory", "m0");
   } else {
     const uint32_t* p = static_cast<const uint32_t*>(a.la) + own;
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(m0), "v"(p) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(m0), "v"(p) : "memory", "m0");
   }
 }
 

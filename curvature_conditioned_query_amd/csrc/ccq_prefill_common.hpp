@@ -187,7 +187,8 @@ __device__ __forceinline__ int tri_col(int idx) {
 // disjoint from the (runtime-selected) destination wait for the load.  Callers therefore
 // wait themselves: s_waitcnt vmcnt(0), then a barrier, before the tile is read.  Loads the
 // compiler does issue are still waited for correctly (the counter drains in order, so loads
-// it does not know about only make its own waits stricter).
+// it does not know about only make its own waits stricter).  Nor does it put the wait state there that a
+// load into LDS needs behind a write of M0: the s_nop does.
 // Instruction j (0 <= j < PQ * sizeof(T) / 16) of such a tile load; does nothing for larger j.
 template <int D, typename T, int PQ>
 __device__ __forceinline__ void dma_unit(T (*dst)[PQ], const T* src, int Lc, int j, int lane) {
@@ -200,7 +201,7 @@ __device__ __forceinline__ void dma_unit(T (*dst)[PQ], const T* src, int Lc, int
   const bool ok = row < Lc && slot < DU;
   const T* p = src + (ok ? row * D + slot * EPU : 0);
   const unsigned m0 = __builtin_amdgcn_readfirstlane(base + 1024u * (unsigned)j);
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(m0), "v"(p) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(m0), "v"(p) : "memory", "m0");
 }
 
 template <int D, typename T, int PQ>
@@ -223,7 +224,7 @@ __device__ __forceinline__ void dma_block(T (*dst)[PQ], const T* src, int w, int
       const int row = u / U, slot = u - row * U;
       const T* p = src + (slot < DU ? row * D + slot * EPU : 0);
       const unsigned m0 = __builtin_amdgcn_readfirstlane(base + 1024u * (unsigned)j);
-      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(m0), "v"(p) : "memory", "m0");
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(m0), "v"(p) : "memory", "m0");
     }
   }
 }
@@ -234,7 +235,7 @@ template <typename T>
 __device__ __forceinline__ void dma_lane(T* dst, const T* p) {
   const unsigned base = (unsigned)(uintptr_t)(__attribute__((address_space(3))) T*)dst;
   const unsigned m0 = __builtin_amdgcn_readfirstlane(base);
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(m0), "v"(p) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(m0), "v"(p) : "memory", "m0");
 }
 
 // The same tile loads with the lane's part of every instruction worked out once: instruction
@@ -263,7 +264,7 @@ struct DmaPlan {
     const unsigned base = (unsigned)(uintptr_t)(__attribute__((address_space(3))) T*)&dst[0][0];
     const T* p = src + (row[m] < Lc ? off[m] : 0);
     const unsigned m0 = __builtin_amdgcn_readfirstlane(base + 1024u * (unsigned)j);
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(m0), "v"(p) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(m0), "v"(p) : "memory", "m0");
   }
   __device__ __forceinline__ void load(T (*dst)[PQ], const T* src, int Lc, int w) const {
 #pragma unroll

@@ -83,7 +83,7 @@ struct PipeDma {
       const unsigned base = (unsigned)(uintptr_t)(__attribute__((address_space(3))) T*)&dst[0][0];
       const void* p = off[m] < Lc * D ? static_cast<const void*>(src + off[m]) : static_cast<const void*>(g_zero16);
       const unsigned m0 = __builtin_amdgcn_readfirstlane(base + 1024u * (unsigned)j);
-      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(m0), "v"(p) : "memory", "m0");
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(m0), "v"(p) : "memory", "m0");
     }
   }
 };
