@@ -39,6 +39,7 @@ constexpr int kSlice = 32;             // columns of z that a workgroup owns
 constexpr int kStepRows = 32;          // rows of a state that a workgroup owns in a step of single tokens
 constexpr double kLog2e = 1.4426950408889634074;
 constexpr float kGateFloor = -1.0e4f;  // log decays below count as this: e^-10000 is 0, sums of 64 stay exact enough
+constexpr double kReset = -126.0;      // log2 of a decay below which it is 0, fp32's least normal number: a reset
 
 struct Strides {
   int64_t b, t, h;
@@ -65,7 +66,7 @@ struct Role {
   float in_scale, out_scale;
   int reverse, slices, dz;
   float* slots;                   // summaries of segments, or null with one segment
-  double* slot_log;               // [chains][segments] their log decays, in units of log 2
+  double* slot_log;               // [chains][segments] their log decays, in units of log 2; -inf with a reset among them
 };
 
 struct Args {
@@ -149,6 +150,7 @@ struct Smem {
   // the state behind, and e^(its sum to the end of its 16 tokens), or from their beginning.
   float bh[2][kL], bl[2][kL], aw[2][kL], bw[2][kL], cf[2][kL];
   float dec[2];
+  int first[2], last[2];       // the chunk's first and last token whose decay is 0: kL and -1 if there is none
   uint32_t raw[NB + 1][kL];    // gates as stored
 };
 
@@ -170,19 +172,31 @@ __device__ __forceinline__ double wave_running(double x) {
 }
 
 // The weights of a chunk's 64 tokens into buffer `buf`; one wave, lane t token t, g its log2 decay (0 behind the
-// end).  Returns the chunk's log2 decay.
+// end).  Returns the chunk's log2 decay, -inf with a reset.  What a reset cuts off from the state has a weight of 0 whatever stands
+// among the other decays, NaN too: sums to the chunk's end begin behind the last reset.
 template <bool REV, typename SM>
 __device__ __forceinline__ double form_gates(SM& sm, int buf, double g, bool live, float in_scale, int lane) {
   const double s = wave_running(g), all = __shfl(s, 63, 64), near = __shfl(s, REV ? lane & 48 : lane | 15, 64);
+  const uint64_t resets = __ballot(g < kReset);
+  const int first = resets ? __builtin_ctzll(resets) : kL, last = 63 - __builtin_clzll(resets | 1) - (resets == 0);
+  double rest = all - s;
+  if (resets) {
+    const double r = wave_running(lane > last ? g : 0.0);
+    rest = __shfl(r, 63, 64) - r;
+  }
   const float hi = (float)s;
   sm.bh[buf][lane] = hi;
   sm.bl[buf][lane] = (float)(s - (double)hi);
-  const float up = exp2_fast((float)s), down = exp2_fast((float)(all - s));
+  const float up = exp2_fast((float)s), down = exp2_fast((float)rest);
   sm.aw[buf][lane] = REV ? down : up;
-  sm.bw[buf][lane] = live ? (REV ? up : down) * in_scale : 0.f;
+  sm.bw[buf][lane] = live && (REV ? lane < first : lane >= last) ? (REV ? up : down) * in_scale : 0.f;
   sm.cf[buf][lane] = live ? exp2_fast((float)(REV ? s - near : near - s)) * in_scale : 0.f;
-  if (lane == 0) sm.dec[buf] = exp2_fast((float)all);
-  return all;
+  if (lane == 0) {
+    sm.dec[buf] = exp2_fast((float)all);
+    sm.first[buf] = first;
+    sm.last[buf] = last;
+  }
+  return resets ? -INFINITY : all;
 }
 
 // An address that is the same in all lanes, in scalar registers, and vectors at byte offsets from it.  (Made of an
@@ -314,14 +328,17 @@ struct Gates {
   int len, c_lo, c_hi, lane, at;
   float in_scale;
   double total;
+  bool reset;
   __device__ __forceinline__ Gates(const Args& a, const Role& ro, SM& sm, const Span& sp, int c_lo, int c_hi, int lane)
-      : a(a), sm(sm), len(sp.len), c_lo(c_lo), c_hi(c_hi), lane(lane), at(0), in_scale(ro.in_scale), total(0.0) {}
+      : a(a), sm(sm), len(sp.len), c_lo(c_lo), c_hi(c_hi), lane(lane), at(0), in_scale(ro.in_scale), total(0.0), reset(false) {}
   // chunk it, into buffer BUF
   template <int BUF>
   __device__ __forceinline__ void form(int it) {
     if (it < c_hi - c_lo) {
       const bool live = (REV ? c_hi - 1 - it : c_lo + it) * kL + lane < len;
-      total += form_gates<REV>(sm, BUF, live && a.la ? gate_value(a, sm.raw[at][lane]) : 0.0, live, in_scale, lane);
+      const double one = form_gates<REV>(sm, BUF, live && a.la ? gate_value(a, sm.raw[at][lane]) : 0.0, live, in_scale, lane);
+      total += one;
+      reset = reset || one == -INFINITY;
     }
     at = at == SM::NB ? 0 : at + 1;
   }
@@ -468,7 +485,8 @@ __device__ __forceinline__ void walk_outputs(const Args& a, const Role& ro, int 
       if (ro.r) load_w(weights[1 - GB], it + 1);
       const T* st = &sm.St[GB][0][0][0];
       const T* z0 = &sm.Z[at][0][0] + z_place;
-      const float aw = sm.aw[GB][own], dec = sm.dec[GB];
+      const float aw = sm.aw[GB][own];
+      const int edge = REV ? sm.last[GB] : sm.first[GB];
       // far: the state before the chunk
       f32x4 acc[NZ], P[4];
 #pragma unroll
@@ -483,11 +501,13 @@ __device__ __forceinline__ void walk_outputs(const Args& a, const Role& ro, int 
       if constexpr (!SM::XL) {
         if (it + 1 < n) load_own(it + 1);
       }
-      if (dec == 0.f) {  // a gate of 0: the state before counts for nothing, whatever it holds
+      // (one loop with a select made the scheduler's block longer and the gradient 440 us for 360)
+      if (REV ? edge >= 0 : edge < kL) {  // a reset stands between the state and some tokens, whatever the state holds
+        const bool cut = REV ? (int)own < edge : (int)own >= edge;
 #pragma unroll
         for (int z = 0; z < NZ; ++z)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[z][r] = aw == 0.f ? 0.f : acc[z][r] * aw;
+          for (int r = 0; r < 4; ++r) acc[z][r] = cut ? 0.f : acc[z][r] * aw;
       } else {
 #pragma unroll
         for (int z = 0; z < NZ; ++z)
@@ -588,8 +608,8 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
 #pragma unroll
       for (int x = 0; x < NX; ++x) *reinterpret_cast<f32x4*>(p + x * 256) = S[x];
     };
-    auto decay_by = [&](float d) {
-      if (d == 0.f) {  // whatever the state holds
+    auto decay_by = [&](float d, bool reset) {
+      if (reset) {  // whatever the state holds
 #pragma unroll
         for (int x = 0; x < NX; ++x) S[x] = zero4();
       } else {
@@ -617,7 +637,8 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
         take_in();
       }
       for (int i = REV ? nseg - 1 : 0; REV ? i > seg : i < seg; i += REV ? -1 : 1) {
-        decay_by(exp2_fast((float)ro.slot_log[(size_t)chain * a.segments + i]));
+        const double d = ro.slot_log[(size_t)chain * a.segments + i];
+        decay_by(exp2_fast((float)d), d == -INFINITY);
         const float* p = slot_of(i);
 #pragma unroll
         for (int x = 0; x < NX; ++x) S[x] += *reinterpret_cast<const f32x4*>(p + x * 256);
@@ -649,6 +670,7 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
         const T* y0 = &sm.Y[at][0][0];
         const T* z0 = &sm.Z[at][0][0] + z_place;
         const float dec = sm.dec[it & 1];
+        const int first = sm.first[it & 1];
         // b z: the lane's eight tokens of every 32, as tr_at has them
         Frag<T> y[2][NX], zf[2][SM::NH];
         Frag<T> z[2];
@@ -664,26 +686,46 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
 #pragma unroll
           for (int x = 0; x < NX; ++x) y[kk][x] = tr_at<T, SM::PY>(y0 + y_place[x] + 32 * kk * SM::PY);
         at = at + 1 == SM::NB ? 0 : at + 1;
+        auto update = [&](bool reset) {
+          if (reset) {
+            // rows that the reset cuts off may hold anything, and so may the chunk's first, which rows behind the end repeat
+            const int lo = REV ? 0 : sm.last[it & 1], hi = min(REV ? first : kL, sp.len - chunk_at(it) * kL);
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-          float v[8];
+            for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = (float)z[kk].v[e] * bw[kk][e >> 2][e & 3];
+              for (int e = 0; e < 8; ++e) {
+                const int j = 32 * kk + 16 * (e >> 2) + 4 * g + (e & 3);
+                if (j >= lo && j < hi) continue;
+                z[kk].v[e] = (T)0.f;
 #pragma unroll
-          for (int p = 0; p < SM::NH; ++p)
+                for (int x = 0; x < NX; ++x) y[kk][x].v[e] = (T)0.f;
+              }
+          }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              zf[kk][p].v[e] = (T)v[e];
-              if (p + 1 < SM::NH) v[e] -= (float)zf[kk][p].v[e];
-            }
-        }
-        decay_by(dec);
+          for (int kk = 0; kk < 2; ++kk) {
+            float v[8];
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
+            for (int e = 0; e < 8; ++e) v[e] = (float)z[kk].v[e] * bw[kk][e >> 2][e & 3];
 #pragma unroll
-          for (int p = 0; p < SM::NH; ++p)
+            for (int p = 0; p < SM::NH; ++p)
 #pragma unroll
-            for (int x = 0; x < NX; ++x) mma(S[x], y[kk][x], zf[kk][p]);
+              for (int e = 0; e < 8; ++e) {
+                zf[kk][p].v[e] = (T)v[e];
+                if (p + 1 < SM::NH) v[e] -= (float)zf[kk][p].v[e];
+              }
+          }
+          decay_by(dec, reset);
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int p = 0; p < SM::NH; ++p)
+#pragma unroll
+              for (int x = 0; x < NX; ++x) mma(S[x], y[kk][x], zf[kk][p]);
+        };
+        // chunks without a reset have code of their own, which a summary does not gain from (20,480 tokens: 172 against 184 us)
+        if (SUMMARY) update(first < kL);
+        else if (first < kL) update(true);
+        else update(false);
         if constexpr (!SUMMARY) store_copy(it + 1);
         lds_barrier();
       }
@@ -789,7 +831,7 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
         lds_barrier();
       }
     }
-    if (SUMMARY && slice == 0 && lane == 0) ro.slot_log[(size_t)chain * a.segments + seg] = gates.total;
+    if (SUMMARY && slice == 0 && lane == 0) ro.slot_log[(size_t)chain * a.segments + seg] = gates.reset ? -INFINITY : gates.total;
     return;
   }
   if constexpr (!SUMMARY) {
@@ -848,14 +890,16 @@ __global__ __launch_bounds__(kThreads) void la_step_kernel(Args a) {
   }
   for (int t = 0; t < sp.len; ++t) {
     const f32x4 x = ld4(xb + t * ro.xs.t), y = ld4(yb + t * ro.ys.t);
-    const float d = exp2_fast((float)gate_of(a, la0 + (int64_t)t * a.ls.t));
+    const double gate = gate_of(a, la0 + (int64_t)t * a.ls.t);
+    const bool reset = gate < kReset;
+    const float d = exp2_fast((float)gate);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const float z = to_f32(zb[t * ro.zs.t + i * RPP]);
       float o = 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        S[i][e] = (d == 0.f ? 0.f : S[i][e] * d) + z * y[e];
+        S[i][e] = (reset ? 0.f : S[i][e] * d) + z * y[e];
         o += S[i][e] * x[e];
       }
       o = group_sum<LPR>(o);
@@ -962,7 +1006,7 @@ __global__ __launch_bounds__(kGateThreads) void la_gate_kernel(GateArgs q) {
     for (int i = 0; i < w; ++i) base += tops[i];
 #pragma unroll
     for (int i = 0; i < kGateRun; ++i)
-      if (t0 + i >= 0) store(t0 + i, exp2_fast((float)gate_value(a, bits[i])) == 0.f ? 0.f : (float)(r[i] + base));
+      if (t0 + i >= 0) store(t0 + i, gate_value(a, bits[i]) < kReset ? 0.f : (float)(r[i] + base));
     __syncthreads();
     if (tid == kGateThreads - 1) behind = base + r[0];
     __syncthreads();

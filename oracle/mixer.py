@@ -16,9 +16,12 @@ def _shared(x, H):
     return np.repeat(np.asarray(x, np.float64), H // x.shape[2], axis=2)
 
 
+RESET = -126.0 * np.log(2.0)  # a log decay below this counts as a decay of 0: fp32's least normal number
+
+
 def _gates(log_alpha, B, T, H):
     g = np.zeros((B, T, H)) if log_alpha is None else np.asarray(log_alpha, np.float64)
-    return np.exp(g)
+    return np.where(g < RESET, 0.0, np.exp(g))
 
 
 def _decayed(S, a):
