@@ -944,7 +944,8 @@ __global__ __launch_bounds__(kThreads) void la_sum_kernel(SumArgs a) {
   }
 }
 
-// dlog alpha of one chain: the sums from the end of rq - rk (over the slices), plus the state's product, in 64 bits.  A
+// dlog alpha of one chain: the sums from the end of rq - rk (over the slices), plus the state's product, in 64 bits.  They
+// begin anew at a reset: what stands behind it sums up to 0, but for its roundings and for what is infinite or NaN.  A
 // thread takes four tokens that follow each other, so that a few thousand tokens are one round of loads and one scan
 // (one token a thread: 24 us for 64 chains of 4096, now 17).
 constexpr int kGateThreads = 1024, kGateRun = 4;
@@ -961,6 +962,7 @@ __global__ __launch_bounds__(kGateThreads) void la_gate_kernel(GateArgs q) {
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const Span sp = span_of(a, b);
   __shared__ double tops[kGateThreads / 64];
+  __shared__ int cut[kGateThreads / 64];  // a reset among a wave's tokens
   __shared__ double behind;
   const int64_t la0 = (a.offsets ? sp.row0 * a.ls.t : b * a.ls.b) + h * a.ls.h;
   auto store = [&](int t, float v) {
@@ -996,19 +998,46 @@ __global__ __launch_bounds__(kGateThreads) void la_gate_kernel(GateArgs q) {
     };
     add(q.rq + (size_t)chain * a.T, q.q_slices, 1.0);
     add(q.rk + (size_t)chain * a.T, q.k_slices, -1.0);
+    bool reset[kGateRun], any = false;
 #pragma unroll
-    for (int i = kGateRun - 2; i >= 0; --i) r[i] += r[i + 1];
-    double sum = wave_running(r[0]);
-    const double before = sum - r[0];
-    if (lane == 63) tops[w] = sum;
-    __syncthreads();
-    double base = before + behind;
-    for (int i = 0; i < w; ++i) base += tops[i];
+    for (int i = 0; i < kGateRun; ++i) {
+      reset[i] = gate_value(a, bits[i]) < kReset;
+      any = any || reset[i];
+    }
 #pragma unroll
-    for (int i = 0; i < kGateRun; ++i)
-      if (t0 + i >= 0) store(t0 + i, gate_value(a, bits[i]) < kReset ? 0.f : (float)(r[i] + base));
+    for (int i = kGateRun - 2; i >= 0; --i) r[i] += reset[i + 1] ? 0.0 : r[i + 1];
+    // over the lanes, whose tokens come before those of the lanes below: each lane's sum since the last reset
+    const double own = reset[0] ? 0.0 : r[0];
+    const uint64_t resets = __ballot(any);
+    const bool cut_before = (resets & ((1ull << lane) - 1)) != 0;
+    double sum = own;
+    if (resets == 0) {
+      sum = wave_running(own);
+    } else {
+      const int since = cut_before || any ? 63 - __builtin_clzll(resets & (~0ull >> (63 - lane))) : 0;  // the sum's first lane
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const double o = __shfl_up(sum, d, 64);
+        if (lane - d >= since) sum += o;
+      }
+    }
+    const double up = __shfl_up(sum, 1, 64);
+    if (lane == 63) {
+      tops[w] = sum;
+      cut[w] = resets != 0;
+    }
     __syncthreads();
-    if (tid == kGateThreads - 1) behind = base + r[0];
+    double base = behind;
+    for (int i = 0; i < w; ++i) base = (cut[i] ? 0.0 : base) + tops[i];
+    if (cut_before) base = 0.0;
+    if (lane > 0) base += up;
+#pragma unroll
+    for (int i = kGateRun - 1; i >= 0; --i) {
+      if (t0 + i >= 0) store(t0 + i, reset[i] ? 0.f : (float)(r[i] + base));
+      if (reset[i]) base = 0.0;
+    }
+    __syncthreads();
+    if (tid == kGateThreads - 1) behind = base + own;
     __syncthreads();
   }
   if (a.offsets == nullptr)

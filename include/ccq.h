@@ -588,7 +588,9 @@ typedef struct {
 /* Gradient of ccq_linear_attn.  With the adjoint A_t = scale d_o_t q_t^T + alpha_{t+1} A_{t+1} (dS_out
  * behind the last token): dq_t = scale S_t^T d_o_t, dk_t = A_t^T v_t, dv_t = A_t k_t,
  * dlog_alpha_t = alpha_t <A_t, S_{t-1}>, which is formed as the sum over i >= t of
- * q_i . dq_i - k_i . dk_i, plus <dS_out, S_out>; 0 where alpha_t is 0.  Sums over shared heads go in a
+ * q_i . dq_i - k_i . dk_i, plus <dS_out, S_out>, or, where an alpha behind t is 0, over the tokens before that
+ * one alone; 0 where alpha_t is 0.  What is infinite or NaN in a chunk may so reach the dlog_alpha of earlier
+ * chunks too, as far back as the last alpha of 0 before its chunk.  Sums over shared heads go in a
  * fixed order: two calls give the same bits.  Returns a ccq_status. */
 int ccq_linear_attn_backward(const ccq_linear_attn_bwd_params *p, void *hip_stream);
 size_t ccq_linear_attn_backward_workspace_bytes(const ccq_linear_attn_bwd_params *p);

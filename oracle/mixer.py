@@ -89,6 +89,7 @@ def linear_attn_backward(q, k, v, d_o, log_alpha=None, scale=1.0, S0=None, dS_ou
             out["dlog_alpha"][b, t] = np.where(a[b, t] == 0, 0.0, dg)
             size["dlog_alpha"][b, t] = np.where(a[b, t] == 0, 0.0, gs)
             A, As = _decayed(A, a[b, t]), _decayed(As, a[b, t])
+            gs = np.where(a[b, t] == 0, 0.0, gs)
         out["dS0"][b], size["dS0"][b] = A, As
     for d in (out, size):
         for m, share in zip(("dq", "dk", "dv"), shares):

@@ -122,3 +122,31 @@ def test_an_infinite_state_lasts_without_a_reset(gpu_lib, T):
             assert not o.isfinite().any() and not S.isfinite().any()
         else:
             assert o[0, 7:].isfinite().all() and S.isfinite().all()
+
+
+@pytest.mark.filterwarnings("ignore:invalid value", "ignore:overflow")
+@pytest.mark.parametrize("T,resets,bad", [
+    (100, [70], False), (300, [1, 2, 63, 64, 65, 131], False), (300, [1, 2, 63, 64, 65, 131], True), (600, list(range(3, 600, 7)), False),
+    (5000, [903, 904, 950, 4700], False), (5000, [903, 904, 950, 4700], True), (5000, [10, 1000], False), (5000, [10, 1000], True)])
+def test_gradient_of_decays_before_a_reset(gpu_lib, T, resets, bad):
+    """The decays of a sequence take nothing from the sequence behind a reset: not the roundings of its large rows, and not its
+    NaN (in another chunk)."""
+    import torch
+    from curvature_conditioned_query_amd import ccq_linear_attn_backward
+    H, d = 2, 64
+    x = _inputs(1, T, H, H, H, H, d, d, "f32", gate="f32", seed=25, mild=8.0)
+    g = torch.Generator().manual_seed(2)
+    d_o, dS = torch.randn(1, T, H, d, generator=g).cuda(), torch.randn(1, H, d, d, generator=g).cuda()
+    x["log_alpha"][:, resets] = -INF
+    last = resets[-1]
+    for t in (x["q"], x["v"], d_o):
+        t[:, last:] *= 1e4
+    if bad:
+        d_o[:, T - 1, :, 1] = NAN
+    got = ccq_linear_attn_backward(**x, d_o=d_o, dS_out=dS)["dlog_alpha"]
+    want, size = mixer.linear_attn_backward(*(_np(x[m]) for m in "qkv"), _np(d_o), _np(x["log_alpha"]), x["scale"], _np(x["S0"]),
+                                            _np(dS))
+    want, size = want["dlog_alpha"], size["dlog_alpha"]
+    assert np.isfinite(want[:, :last]).all()
+    _close(_np(got), want, size, (T + 2 * d + 16) * U, U, "dlog_alpha")
+    assert (got[:, resets] == 0).all()
