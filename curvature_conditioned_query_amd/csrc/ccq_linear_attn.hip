@@ -911,7 +911,8 @@ __global__ __launch_bounds__(kThreads) void la_step_kernel(Args a) {
     for (int i = 0; i < NP; ++i) __builtin_nontemporal_store(S[i], reinterpret_cast<f32x4*>(ro.s_out + s0 + (size_t)i * RPP * DX));
 }
 
-// Gradient rows that several heads share: the sum of their parts, in order.  Parts are [rows][H][d] fp32.
+// Gradient rows that several heads share: the sum of their parts, in order.  Parts are [H][rows][d] fp32: the walk tells a chunk's
+// rows apart by 32-bit offsets, which H d between them would pass with many heads.
 struct Shared {
   const float* part;
   void* out;
@@ -921,7 +922,7 @@ struct Shared {
 struct SumArgs {
   int B, T, H;
   const int32_t *lengths, *offsets;
-  int64_t rows;
+  int64_t rows, part_rows;
   Shared side[3];
 };
 __global__ __launch_bounds__(kThreads) void la_sum_kernel(SumArgs a) {
@@ -936,8 +937,8 @@ __global__ __launch_bounds__(kThreads) void la_sum_kernel(SumArgs a) {
     if (t >= sp.len && a.offsets) continue;
     f32x4 v = zero4();
     if (t < sp.len) {
-      const float* p = s.part + ((a.offsets ? sp.row0 + t : bt) * a.H + (int64_t)hh * s.share) * s.d + c;
-      for (int i = 0; i < s.share; ++i) v += *reinterpret_cast<const f32x4*>(p + (size_t)i * s.d);
+      const float* p = s.part + ((int64_t)hh * s.share * a.part_rows + (a.offsets ? sp.row0 + t : bt)) * s.d + c;
+      for (int i = 0; i < s.share; ++i) v += *reinterpret_cast<const f32x4*>(p + i * a.part_rows * s.d);
     }
     const int64_t o = (a.offsets ? (sp.row0 + t) * s.os.t : b * s.os.b + t * s.os.t) + hh * s.os.h + c;
     store_out<__bf16>(s.out, o, v, s.f32);
@@ -1045,8 +1046,6 @@ __global__ __launch_bounds__(kGateThreads) void la_gate_kernel(GateArgs q) {
 }
 
 // ---------------------------------------------------------------- host
-
-Strides dense(int64_t T, int64_t H, int64_t d) { return Strides{T * H * d, H * d, d}; }
 
 // Where a call's parts of the workspace lie; base null: sizes alone.
 struct Space {
@@ -1207,7 +1206,7 @@ BackPlan plan_backward(const ccq_linear_attn_bwd_params& q) {
     if (share[i] > 1) {
       float* part = sp.take<float>(rows * p.H * dim[i]);
       r.out = part;
-      r.os = dense(p.T, p.H, dim[i]);
+      r.os = Strides{(int64_t)p.T * dim[i], dim[i], (int64_t)rows * dim[i]};
       r.out_f32 = 1;
       Shared& s = bp.sum.side[bp.sums++];
       s = Shared{part, out[i], gs[i], p.H / share[i], share[i], dim[i], grad_f32};
@@ -1251,6 +1250,7 @@ BackPlan plan_backward(const ccq_linear_attn_bwd_params& q) {
   bp.sum.lengths = p.lengths;
   bp.sum.offsets = p.offsets;
   bp.sum.rows = p.rows;
+  bp.sum.part_rows = (int64_t)rows;
   bp.gate.a = base_of(p);
   bp.gate.rq = role[0].r;
   bp.gate.rk = role[1].r;
