@@ -1101,7 +1101,7 @@ def ccq_linear_attn_backward(q, k, v, d_o, log_alpha=None, scale: float = 1.0, S
     of o (a strided view is fine); dS_out [B, H, d_v, d_k] fp32: gradient of S_out, or None.  Returns a dict: dq, dk,
     dv (the shapes of q, k, v; of grad_dtype, torch.float32 or q's, which None means; into the given views if any),
     dlog_alpha ([B, T, H], log_alpha's dtype, with log_alpha: one entry a token, also where tokens share a gate) and,
-    with want_dS0, dS0 fp32."""
+    with want_dS0, dS0 fp32.  Rows of no token (behind a length, outside packed sequences) are zeros."""
     ops, dev = _ops(), q.device
     with ops.place(dev, stream):
         f, n0, n1 = _la_params(ops, q, k, v, log_alpha, scale, S0, lengths, offsets, max_length, dev)

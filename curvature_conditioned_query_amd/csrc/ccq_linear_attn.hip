@@ -53,7 +53,7 @@ struct Role {
   void* out;                      // [B, T, H, 32 slices]
   Strides os;
   int out_f32;
-  int zero_tail;                  // rows behind a sequence's end are set to 0
+  int zero_idle;                  // rows of no token are set to 0
   const void* w;                  // gradient: rows of the slice's columns, whose products with the outputs are summed
   Strides ws;
   int w_share;
@@ -99,6 +99,17 @@ __device__ __forceinline__ Span span_of(const int32_t* lengths, const int32_t* o
   return s;
 }
 __device__ __forceinline__ Span span_of(const Args& a, int b) { return span_of(a.lengths, a.offsets, a.rows, a.T, b); }
+
+// Rows of no token that sequence b answers for, 0 .. front - 1 and from .. to - 1: those behind its end, counted from its own first
+// row; packed, those up to the next sequence's first row, and before the first sequence, counted over all rows.
+struct Idle {
+  int64_t front, from, to;
+};
+__device__ __forceinline__ Idle idle_of(const Args& a, const Span& s, int b) {
+  if (a.offsets == nullptr) return Idle{0, s.len, a.T};
+  const int64_t next = b + 1 < a.B ? (int64_t)a.offsets[b + 1] : a.rows;
+  return Idle{b == 0 ? s.row0 : 0, s.row0 + s.len, next < a.rows ? next : a.rows};
+}
 
 template <typename T>
 __device__ __forceinline__ T* rows_of(const void* p, const Strides& s, int share, const Args& a, const Span& sp, int b, int h) {
@@ -579,11 +590,13 @@ __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, i
   };
 
   if constexpr (!SUMMARY) {
-    if (ro.zero_tail && a.offsets == nullptr) {  // rows of no token
-      const int64_t ob = b * ro.os.b + h * ro.os.h + slice * ZS;
-      const int last = seg == a.segments - 1 ? a.T : min(a.T, (c_lo + a.chunks_per_segment) * kL);
-      for (int t = max(sp.len, c_lo * kL) + tid / (ZS / 4); t < last; t += walk_threads(false) / (ZS / 4))
-        store_out<T>(ro.out, ob + (int64_t)t * ro.os.t + 4 * (tid % (ZS / 4)), zero4(), ro.out_f32);
+    if (ro.zero_idle) {
+      const Idle idle = idle_of(a, sp, b);
+      const int64_t ob = (a.offsets ? 0 : b * ro.os.b) + h * ro.os.h + slice * ZS + 4 * (tid % (ZS / 4));
+      constexpr int kRows = walk_threads(false) / (ZS / 4);
+      const int64_t own = (int64_t)seg * kRows + tid / (ZS / 4), step = (int64_t)a.segments * kRows;
+      for (int64_t t = own; t < idle.front; t += step) store_out<T>(ro.out, ob + t * ro.os.t, zero4(), ro.out_f32);
+      for (int64_t t = idle.from + own; t < idle.to; t += step) store_out<T>(ro.out, ob + t * ro.os.t, zero4(), ro.out_f32);
     }
   }
 
@@ -920,28 +933,20 @@ struct Shared {
   int heads, share, d, f32;
 };
 struct SumArgs {
-  int B, T, H;
-  const int32_t *lengths, *offsets;
-  int64_t rows, part_rows;
+  int64_t rows, T;  // of all sequences, and of one (packed: as if of one sequence)
   Shared side[3];
 };
 __global__ __launch_bounds__(kThreads) void la_sum_kernel(SumArgs a) {
   const Shared& s = a.side[blockIdx.y];
   const int quads = s.d / 4;
-  const int64_t per = (int64_t)s.heads * quads, all = per * a.B * a.T;
+  const int64_t per = (int64_t)s.heads * quads, all = per * a.rows;
   for (int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x; at < all; at += (int64_t)gridDim.x * kThreads) {
-    const int64_t bt = at / per;
-    const int rest = (int)(at - bt * per), hh = rest / quads, c = 4 * (rest - hh * quads);
-    const int b = (int)(bt / a.T), t = (int)(bt - (int64_t)b * a.T);
-    const Span sp = span_of(a.lengths, a.offsets, a.rows, a.T, b);
-    if (t >= sp.len && a.offsets) continue;
+    const int64_t row = at / per, b = row / a.T, t = row - b * a.T;
+    const int rest = (int)(at - row * per), hh = rest / quads, c = 4 * (rest - hh * quads);
+    const float* p = s.part + ((int64_t)hh * s.share * a.rows + row) * s.d + c;
     f32x4 v = zero4();
-    if (t < sp.len) {
-      const float* p = s.part + ((int64_t)hh * s.share * a.part_rows + (a.offsets ? sp.row0 + t : bt)) * s.d + c;
-      for (int i = 0; i < s.share; ++i) v += *reinterpret_cast<const f32x4*>(p + i * a.part_rows * s.d);
-    }
-    const int64_t o = (a.offsets ? (sp.row0 + t) * s.os.t : b * s.os.b + t * s.os.t) + hh * s.os.h + c;
-    store_out<__bf16>(s.out, o, v, s.f32);
+    for (int i = 0; i < s.share; ++i) v += *reinterpret_cast<const f32x4*>(p + i * a.rows * s.d);
+    store_out<__bf16>(s.out, b * s.os.b + t * s.os.t + hh * s.os.h + c, v, s.f32);
   }
 }
 
@@ -966,8 +971,9 @@ __global__ __launch_bounds__(kGateThreads) void la_gate_kernel(GateArgs q) {
   __shared__ int cut[kGateThreads / 64];  // a reset among a wave's tokens
   __shared__ double behind;
   const int64_t la0 = (a.offsets ? sp.row0 * a.ls.t : b * a.ls.b) + h * a.ls.h;
-  auto store = [&](int t, float v) {
-    const int64_t at = ((a.offsets ? sp.row0 : (int64_t)b * a.T) + t) * a.H + h;
+  const int64_t row0 = a.offsets ? 0 : (int64_t)b * a.T;
+  auto store = [&](int64_t row, float v) {
+    const int64_t at = row * a.H + h;
     if (a.gate_bf16) static_cast<__bf16*>(q.out)[at] = (__bf16)v;
     else static_cast<float*>(q.out)[at] = v;
   };
@@ -1034,15 +1040,16 @@ __global__ __launch_bounds__(kGateThreads) void la_gate_kernel(GateArgs q) {
     if (lane > 0) base += up;
 #pragma unroll
     for (int i = kGateRun - 1; i >= 0; --i) {
-      if (t0 + i >= 0) store(t0 + i, reset[i] ? 0.f : (float)(r[i] + base));
+      if (t0 + i >= 0) store(row0 + sp.row0 + t0 + i, reset[i] ? 0.f : (float)(r[i] + base));
       if (reset[i]) base = 0.0;
     }
     __syncthreads();
     if (tid == kGateThreads - 1) behind = base + own;
     __syncthreads();
   }
-  if (a.offsets == nullptr)
-    for (int t = sp.len + tid; t < a.T; t += kGateThreads) store(t, 0.f);
+  const Idle idle = idle_of(a, sp, b);
+  for (int64_t t = tid; t < idle.front; t += kGateThreads) store(row0 + t, 0.f);
+  for (int64_t t = idle.from + tid; t < idle.to; t += kGateThreads) store(row0 + t, 0.f);
 }
 
 // ---------------------------------------------------------------- host
@@ -1216,8 +1223,8 @@ BackPlan plan_backward(const ccq_linear_attn_bwd_params& q) {
       r.out = out[i];
       r.os = gs[i];
       r.out_f32 = grad_f32;
-      r.zero_tail = 1;
     }
+    r.zero_idle = 1;
     if (q.dlog_alpha && i < 2) {
       r.w = in[i];
       r.ws = xs[i];
@@ -1244,13 +1251,8 @@ BackPlan plan_backward(const ccq_linear_attn_bwd_params& q) {
     split_of(p, a.chains * a.slots_per_group, &a.segments, &a.chunks_per_segment);
     space_for_segments(a, bp.dx[i], sp);
   }
-  bp.sum.B = p.B;
-  bp.sum.T = p.T;
-  bp.sum.H = p.H;
-  bp.sum.lengths = p.lengths;
-  bp.sum.offsets = p.offsets;
-  bp.sum.rows = p.rows;
-  bp.sum.part_rows = (int64_t)rows;
+  bp.sum.rows = (int64_t)rows;
+  bp.sum.T = p.offsets ? p.rows : p.T;
   bp.gate.a = base_of(p);
   bp.gate.rq = role[0].r;
   bp.gate.rk = role[1].r;
@@ -1265,7 +1267,7 @@ BackPlan plan_backward(const ccq_linear_attn_bwd_params& q) {
 
 // Workgroups of the sum over shared heads.
 unsigned sum_blocks(const BackPlan& bp) {
-  const uint64_t n = ((uint64_t)bp.most * bp.sum.B * bp.sum.T + kThreads - 1) / kThreads;
+  const uint64_t n = ((uint64_t)bp.most * bp.sum.rows + kThreads - 1) / kThreads;
   return (unsigned)(n < 8192 ? n : 8192);
 }
 

@@ -534,8 +534,8 @@ typedef struct {
   const int32_t *lengths;    /* [B] tokens of each sequence (taken into 0 .. T), or NULL            */
   const int32_t *offsets;    /* [B + 1], or NULL.  Packed sequences: the tensors have one row for each of
                                 `rows` tokens, sequence b those from offsets[b] to offsets[b + 1] - 1 (the
-                                first T of them, if there are more); strides over b are not read.  Not
-                                with lengths                                                        */
+                                first T of them, if there are more), never falling; strides over b are
+                                not read.  Not with lengths                                         */
   int64_t rows;              /* with offsets: rows of the packed tensors; else 0                    */
   const float *S0;           /* [B, H, d_v, d_k] state before the first token, or NULL: zeros       */
   void *o;                   /* [B, T, H, d_v] dtype, strides below, written; rows of no token are left as they were */
@@ -572,14 +572,14 @@ typedef struct {
   int64_t do_stride_b, do_stride_t, do_stride_h; /* >= 0                                            */
   const float *dS_out;       /* [B, H, d_v, d_k] gradient of S_out, or NULL: zeros                  */
   void *dq, *dk, *dv;        /* grad_dtype, the shapes of q, k and v, strides below, written: summed over
-                                the heads that share a row; zeros at t >= length (packed rows of no
-                                sequence are left as they were)                                     */
+                                the heads that share a row; zeros in rows of no token: at t >= length,
+                                before, between and behind packed sequences, past the first T of one */
   int64_t dq_stride_b, dq_stride_t, dq_stride_h; /* no two rows may overlap                         */
   int64_t dk_stride_b, dk_stride_t, dk_stride_h;
   int64_t dv_stride_b, dv_stride_t, dv_stride_h;
   void *dlog_alpha;          /* [B, T, H] (packed: [rows, H]) gate_dtype, dense, written, or NULL: one entry
                                 for each token whatever the strides of log_alpha: a gate that tokens
-                                share has their sum as its gradient                                 */
+                                share has their sum as its gradient; zeros in rows of no token       */
   float *dS0;                /* [B, H, d_v, d_k], written, or NULL                                  */
   void *workspace;           /* ccq_linear_attn_backward_workspace_bytes(p) bytes                   */
   size_t workspace_bytes;

@@ -26,3 +26,37 @@ def test_shared_heads_of_the_most_chains(gpu_lib, H, T, share):
         want = ccq_linear_attn_backward(q[:, :, few], k[:, :, few], v[:, :, many], d_o[:, :, many], la[:, :, many].contiguous())
         for m, part in (("dq", few), ("dk", few), ("dv", many), ("dlog_alpha", many)):
             assert torch.equal(got[m][:, :, part], want[m]), (m, at)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shares,dk,dv", [((1, 1, 1), 64, 64), ((2, 2, 1), 64, 128), ((1, 4, 2), 128, 64)])
+@pytest.mark.parametrize("at,most", [([3, 3, 133, 134, 300], 200), ([3, 3, 133, 134, 300], 70), ([0, 0, 0], 90), ([310, 310], 5),
+                                     ([200, 210], 400), ([0, 310], 310)])
+def test_packed_rows_of_no_sequence_have_a_gradient_of_zero(gpu_lib, at, most, shares, dk, dv, dtype):
+    """Before, between and behind the sequences, and past max_length, whatever the gradients' memory and the inputs held there;
+    the sequences' rows have the bits of calls on one sequence each."""
+    import torch
+    from curvature_conditioned_query_amd import ccq_linear_attn_backward
+    rows, H = 310, 4
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator().manual_seed(6)
+    rn = lambda h, d: torch.randn(1, rows, h, d, generator=g).to(dt).cuda()  # noqa: E731
+    x = dict(q=rn(H // shares[0], dk), k=rn(H // shares[1], dk), v=rn(H // shares[2], dv), d_o=rn(H, dv),
+             log_alpha=-torch.rand(1, rows, H, generator=g).to(dt).cuda())
+    spans = [(a, min(b - a, most)) for a, b in zip(at, at[1:])]
+    idle = torch.ones(rows, dtype=torch.bool)
+    for a, n in spans:
+        idle[a:a + n] = False
+    for t in x.values():
+        t[:, idle] = float("nan")
+    grads = {"d" + m: torch.full_like(x[m], float("nan")) for m in "qkv"}
+    junk = torch.full_like(x["log_alpha"], float("nan"))
+    del junk  # memory that the decays' gradient is likely to get
+    got = ccq_linear_attn_backward(**x, **grads, offsets=torch.tensor(at, dtype=torch.int32, device="cuda"), max_length=most)
+    assert all(got[m] is grads[m] for m in grads)
+    for m in got:
+        assert (got[m][:, idle] == 0).all(), m
+    for a, n in spans:
+        if n:
+            one = ccq_linear_attn_backward(**{m: t[:, a:a + n].contiguous() for m, t in x.items()})
+            assert all(torch.equal(got[m][:, a:a + n], one[m]) for m in one)
