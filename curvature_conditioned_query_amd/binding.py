@@ -1082,11 +1082,14 @@ def ccq_linear_attn(q, k, v, log_alpha=None, scale: float = 1.0, S0=None, S_out=
     [B, H, d_v, d_k] fp32 (S_out may be S0: the serving step is T = 1); lengths [B] int32.  Packed sequences:
     tensors [1, rows, ..] with offsets [B + 1] int32, not falling, and max_length, no sequence being longer.
     Returns o [B, T, H, d_v]: rows of no token are left as they were, which in an o allocated here (o=None) is
-    whatever the memory held."""
+    zeros, so that what follows, and its gradient, may take them in."""
     ops, dev = _ops(), q.device
     with ops.place(dev, stream):
         p, n0, n1 = _la_params(ops, q, k, v, log_alpha, scale, S0, lengths, offsets, max_length, dev)
+        fresh = o is None
         o, st = _view_into(ops, "o", o, dev, q.dtype, (n0, n1, p.H, p.d_v))
+        if fresh and (lengths is not None or offsets is not None):
+            o.zero_()
         p.o = o.data_ptr()
         p.o_stride_b, p.o_stride_t, p.o_stride_h = st
         p.S_out = _dense("S_out", S_out, dev, ops.f32, (p.B, p.H, p.d_v, p.d_k))
