@@ -38,8 +38,9 @@ constexpr int kThreads = 256;
 constexpr int kSlice = 32;             // columns of z that a workgroup owns
 constexpr int kStepRows = 32;          // rows of a state that a workgroup owns in a step of single tokens
 constexpr double kLog2e = 1.4426950408889634074;
-constexpr float kGateFloor = -1.0e4f;  // log decays below count as this: e^-10000 is 0, sums of 64 stay exact enough
-constexpr double kReset = -126.0;      // log2 of a decay below which it is 0, fp32's least normal number: a reset
+constexpr double kReset = -126.0;    // log2 of a decay below which it is 0, fp32's least normal number: a reset
+constexpr double kGateFloor = -1.5e4;  // and what it counts as in sums, so that growth behind it brings nothing back: 2^-15000 is 0, sums
+                                       // of 64 stay exact enough
 
 struct Strides {
   int64_t b, t, h;
@@ -123,9 +124,8 @@ __device__ __forceinline__ unsigned gate_bits(const Args& a, int64_t at) {
   return static_cast<const uint32_t*>(a.la)[at];
 }
 __device__ __forceinline__ double gate_value(const Args& a, unsigned bits) {
-  float g = __builtin_bit_cast(float, a.gate_bf16 ? bits << 16 : bits);
-  g = g < kGateFloor ? kGateFloor : g;  // NaN stays
-  return (double)g * kLog2e;
+  const double g = (double)__builtin_bit_cast(float, a.gate_bf16 ? bits << 16 : bits) * kLog2e;
+  return g < kReset ? kGateFloor : g;  // NaN stays
 }
 __device__ __forceinline__ double gate_of(const Args& a, int64_t at) { return gate_value(a, gate_bits(a, at)); }
 

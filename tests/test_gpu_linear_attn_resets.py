@@ -150,3 +150,27 @@ def test_gradient_of_decays_before_a_reset(gpu_lib, T, resets, bad):
     assert np.isfinite(want[:, :last]).all()
     _close(_np(got), want, size, (T + 2 * d + 16) * U, U, "dlog_alpha")
     assert (got[:, resets] == 0).all()
+
+
+@pytest.mark.parametrize("zero", [-88.0, -100.0, -INF])
+@pytest.mark.parametrize("T", [7, 60, 130])
+def test_growth_behind_a_reset_brings_nothing_back(gpu_lib, T, zero):
+    """A decay just below the limit is 0, also where the decays behind it are above 1: large rows before it leave no trace."""
+    import torch
+    from curvature_conditioned_query_amd import ccq_linear_attn, ccq_linear_attn_backward
+    H, d, at = 1, 64, 3
+    x = _inputs(1, T, H, H, H, H, d, d, "f32", gate="f32", seed=26)
+    x["log_alpha"].fill_(0.6)
+    x["log_alpha"][:, at] = zero
+    x["v"][:, :at] *= 1e35
+    x["S0"].mul_(1e35)
+    d_o = torch.randn(1, T, H, d, generator=torch.Generator().manual_seed(3)).cuda()
+    S = torch.empty_like(x["S0"])
+    o = ccq_linear_attn(**x, S_out=S)
+    dq = ccq_linear_attn_backward(**x, d_o=d_o)["dq"]
+    want, last, os, ss = mixer.linear_attn(*(_np(x[m]) for m in "qkv"), _np(x["log_alpha"]), x["scale"], _np(x["S0"]))
+    back, size = mixer.linear_attn_backward(*(_np(x[m]) for m in "qkv"), _np(d_o), _np(x["log_alpha"]), x["scale"], _np(x["S0"]))
+    # a product of growing gates is a power of two of the sum of its logs: an error of a unit of a sum of up to 0.6 T log2 e, and ln 2 of that
+    tol = (2 * T + d + 16) * U
+    for got, w, sz in ((o, want, os), (S, last, ss), (dq, back["dq"], size["dq"])):
+        _close(_np(got), w, sz, tol, U, "behind")
