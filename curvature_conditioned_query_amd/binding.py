@@ -1093,7 +1093,7 @@ def ccq_linear_attn(q, k, v, log_alpha=None, scale: float = 1.0, S0=None, S_out=
         p.o = o.data_ptr()
         p.o_stride_b, p.o_stride_t, p.o_stride_h = st
         p.S_out = _dense("S_out", S_out, dev, ops.f32, (p.B, p.H, p.d_v, p.d_k))
-        _launch(ops, "linear_attn", ops.linear_attn, p, dev, ops.linear_attn_workspace_bytes if p.T > 8 else None, workspace)
+        _launch(ops, "linear_attn", ops.linear_attn, p, dev, ops.linear_attn_workspace_bytes if p.T > 1 else None, workspace)
     return o
 
 

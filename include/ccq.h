@@ -561,7 +561,7 @@ typedef struct {
  * (CCQ_ERR_UNSUPPORTED beyond, and for other d).  Returns a ccq_status.
  */
 int ccq_linear_attn(const ccq_linear_attn_params *p, void *hip_stream);
-/* Bytes of device workspace that call needs (0 if none and for invalid p): depends on the sizes alone. */
+/* Bytes of device workspace that call needs (0 if none, so for T = 1, and for invalid p): depends on the sizes alone. */
 size_t ccq_linear_attn_workspace_bytes(const ccq_linear_attn_params *p);
 
 /* Arguments of ccq_linear_attn_backward.  Zero-initialise, then fill in. */
