@@ -22,9 +22,11 @@
 //   four hold the state, wave w a quarter of d_x:
 //     update   S^T = e^{B_L} S^T + Y^T (b z), b z as a sum of three bf16 where the inputs have 16 bits: what enters a
 //              state, which later tokens and calls build on, is right to 2^-24; and the copy St for the next chunk.
-// What bounds it: the slices of a chain read the same rows, and four workgroups that do so take at most 13.6 TB/s from
-// their L2, 3.4 TB/s of rows; with that alone B4 T4096, 16 heads of 128 takes 87 us, the arithmetic alone 80, both 92.
-// A slice of 64 columns would halve the reading, but its tiles need 174 KB of LDS.
+// What bounds it: nothing alone.  B4 T4096, 16 heads of 128 takes 94 to 99 us; without the rows' loads 84, without the outputs 78,
+// without the state 86, the loads and decays alone 69 (36 KB a chunk and workgroup, 604 MB, 8.8 TB/s from the L2s), the decays and
+// barriers alone 24.  A chunk is a chain of LDS reads, products and a barrier for one workgroup of 11 waves a CU, each of which
+// waits for a part of it.  A slice of 64 columns would halve the reading and share the scores; laid out as now its tiles need 174 KB
+// of LDS (about 149 with two tiles of x and outputs staged in 16 bits, which was not tried).
 // Weights of pairs, not e^{B_i} e^{-B_j}: nothing leaves fp32's range whatever the decay.  Running sums are
 // formed in 64 bits and kept as two floats, in units of log 2.
 #include <type_traits>
@@ -566,8 +568,8 @@ __device__ __forceinline__ void walk_outputs(const Args& a, const Role& ro, int 
 constexpr int walk_threads(bool summary) { return summary ? 448 : 704; }
 
 // One chain, slice and segment.  Waves 0 .. 3 form the outputs (SUMMARY: one wave, for the gates alone), the four
-// behind them carry the state, one forms the gates, two load (where the other waves issued the loads, 44 KB a chunk at 64 bytes a clock,
-// they stood still for a third of their time), and a chunk has one barrier.  SUMMARY: the state alone, from zeros, into
+// behind them carry the state, one forms the gates, two load (where the other waves issued the loads, 36 KB a chunk, they stood
+// still for a third of their time), and a chunk has one barrier.  SUMMARY: the state alone, from zeros, into
 // the segment's slot.
 template <typename T, int DX, bool SPLIT, bool REV, bool SUMMARY>
 __device__ __forceinline__ void walk(const Args& a, const Role& ro, int chain, int slice, int seg, Smem<T, DX, SPLIT, SUMMARY>& sm) {
@@ -1071,7 +1073,8 @@ constexpr int kStepTokens = 8;
 // Segments of a sequence.  A workgroup has a CU to itself, so `groups` of them (chains, roles and slices) take
 // ceil(groups / 256) turns of all its chunks; cut in P they take turns of a P-th, behind a summary, which takes about
 // half as long for a chunk, two to a CU, and a launch that costs some six chunks.  The P with the least of these.  (One sequence of
-// 20,480 tokens, 16 heads of 128: 355 us whole, 169 with 4; 42 chains of up to 777 tokens in fp32: 45 whole, 59 with 2.)
+// 20,480 tokens, 16 heads of 128: 8 segments, 172 us; 4 take the same, 2 316, the whole 385.  42 chains of up to 777 tokens in fp32: 45 whole,
+// 59 with 2.  One of 4096 tokens, 16 heads: 8 segments, 50 us, though 4 would take 44.)
 void split_of(const ccq_linear_attn_params& p, int groups, int* segments, int* per) {
   const int nc = (p.T - 1) / kL + 1;
   *segments = 1;
@@ -1292,6 +1295,9 @@ hipError_t launch_linear_attn(const ccq_linear_attn_params& p, hipStream_t strea
     }
     return hipGetLastError();
   }
+  // 16-bit inputs: scores and the state's copy in one part of 2^-8 each on the way to o, which is rounded to 2^-8 itself; the state stays fp32.
+  // o is 2.35e-3 off (relative, over all of it) where its own rounding alone is 1.66e-3; two parts, as in the gradient, leave just that
+  // and take 112 us for 99, and 190 for 172 over 20,480 tokens.
   return run_walk<false>(a, p.dtype, p.d_k, stream);
 }
 

@@ -4,7 +4,7 @@
 // the history is counted into a table in LDS (integer atomics: their order changes nothing), the few tokens with a bias
 // are formed by one thread each and left in the table, and the logits are then finished in registers and written.
 // Bound by memory, and by the chain of loads, counts and stores of a workgroup: 256 rows of 131,071 bf16 logits with up to
-// 4096 tokens seen take 37 us, 3.8 TB/s (stretches of 4096 tokens 41, of 16,384 tokens 41 to 45).
+// 4096 tokens seen take 41 us, 3.4 TB/s (where this took 42, stretches of 4096 tokens took 44, of 16,384 tokens 44 to 49).
 #include <type_traits>
 
 #include "ccq_device.hpp"
@@ -223,6 +223,7 @@ __global__ __launch_bounds__(kThreads) void logits_adjust_kernel(ccq_logits_adju
 
 }  // namespace
 
+// The header's limit, which counts stretches half as long as these: a launch could take twice as many.
 bool logits_adjust_grid_fits(const ccq_logits_adjust_params& p) {
   return (uint64_t)p.R * (p.V / 4096 + 1) < 1u << 24;
 }

@@ -553,7 +553,7 @@ typedef struct {
  * serving step.  The state is fp32 throughout.  Where the inputs have 16 bits and T > 8, a chunk's scores
  * and the state are rounded to 16 bits once on the way to o.  Gates are taken as they are, above 1 too, as
  * long as the product of consecutive gates stays inside the range of fp32; where alpha_t is 0 (below 2^-126,
- * log_alpha_t below about -87.3366) the state before token t is dropped, whatever it holds and whatever entered
+ * log_alpha_t below about -87.3365) the state before token t is dropped, whatever it holds and whatever entered
  * it.  An input that is infinite or NaN may reach the outputs of all tokens of its 64-token chunk, earlier ones
  * too, and beyond it what the formula says; what stands in rows of no token reaches nothing.
  * Long sequences with few heads are cut along T and the pieces joined in a fixed order: two calls give
@@ -622,7 +622,8 @@ typedef struct {
  *   y = act(z)        without a gate,
  *   y = z act(gate)   with one.
  * It takes the heads of a linear-attention or read-step output (head-major through its strides) to the
- * output projection (token-major).  The arithmetic is fp32; the result is rounded once.  Fewer than 2^31
+ * output projection (token-major).  The arithmetic is fp32 (a group's sum of squares must stay inside its range);
+ * the result is rounded once.  Fewer than 2^31
  * groups B T G, G < 2^16 (CCQ_ERR_UNSUPPORTED beyond, and for other d).  Returns a ccq_status.
  */
 int ccq_group_norm(const ccq_group_norm_params *p, void *hip_stream);
