@@ -40,9 +40,9 @@ constexpr int kThreads = 256;
 constexpr int kSlice = 32;             // columns of z that a workgroup owns
 constexpr int kStepRows = 32;          // rows of a state that a workgroup owns in a step of single tokens
 constexpr double kLog2e = 1.4426950408889634074;
-constexpr double kReset = -126.0;    // log2 of a decay below which it is 0, fp32's least normal number: a reset
-constexpr double kGateFloor = -1.5e4;  // and what it counts as in sums, so that growth behind it brings nothing back: 2^-15000 is 0, sums
-                                       // of 64 stay exact enough
+constexpr double kReset = -126.0;      // log2 of a decay below which it is 0, fp32's least normal number: a reset
+constexpr double kGateFloor = -1.5e4;  // and what it counts as in sums, so that growth behind it brings nothing back: 2^-15000 is 0,
+                                       // sums of 64 stay exact enough
 
 struct Strides {
   int64_t b, t, h;

@@ -552,9 +552,9 @@ typedef struct {
  * cleaning of the query.  A prompt is worked on in chunks of 64 tokens; T = 1 with S_out == S0 is the
  * serving step.  The state is fp32 throughout.  Where the inputs have 16 bits and T > 8, a chunk's scores
  * and the state are rounded to 16 bits once on the way to o.  Gates are taken as they are, above 1 too, as
- * long as the product of consecutive gates stays inside the range of fp32; where alpha_t is 0 (below 2^-126,
- * log_alpha_t below about -87.3365) the state before token t is dropped, whatever it holds and whatever entered
- * it.  An input that is infinite or NaN may reach the outputs of all tokens of its 64-token chunk, earlier ones
+ * long as the product of consecutive gates, and S q with the state before a chunk, stay inside the range of
+ * fp32; where alpha_t is 0 (below 2^-126, log_alpha_t below about -87.3365) the state before token t is dropped,
+ * whatever it holds and whatever entered it.  An input that is infinite or NaN may reach the outputs of all tokens of its 64-token chunk, earlier ones
  * too, and beyond it what the formula says; what stands in rows of no token reaches nothing.
  * Long sequences with few heads are cut along T and the pieces joined in a fixed order: two calls give
  * the same bits.  B H <= 2^20, B T <= 2^30, rows < 2^31, strides over tokens below 2^24
